@@ -34,3 +34,15 @@ from ._binding import (  # noqa: F401
     lib,
     library_path,
 )
+from ._ffn import (  # noqa: F401
+    MoePlan,
+    gemm_act,
+    gemm_act_backward,
+    gemm_act_backward_workspace_size,
+    gemm_act_workspace_size,
+    moe_experts,
+    moe_experts_backward,
+    moe_plan,
+    moe_route,
+    moe_route_backward,
+)

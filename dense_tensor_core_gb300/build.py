@@ -31,7 +31,7 @@ def nvcc() -> str:
 
 
 def _inputs():
-    files = sources() + [os.path.join(INCLUDE, "dtc_gemm.h")]
+    files = sources() + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
     files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     return files
 

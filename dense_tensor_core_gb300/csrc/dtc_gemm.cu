@@ -59,6 +59,10 @@ static __device__ __align__(256) unsigned char g_static_ws[kStaticWsBytes];
 constexpr int kMaxDevices = 64;
 DeviceInfo g_dev[kMaxDevices];
 
+}  // namespace
+
+namespace dtc_host {
+
 // Looks up (once per device) the compute capability, the SM count and the status word's address
 // on the current device.
 int current_device(int* dev_out, DeviceInfo** info_out) {
@@ -111,6 +115,10 @@ const DevModel& device_model(DeviceInfo* d) {
     return d->model;
 }
 
+}  // namespace dtc_host
+
+namespace {
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     static std::once_flag once;
@@ -146,6 +154,29 @@ int make_tmap(CUtensorMap* m, CUtensorMapDataType dt, int elem_bytes, const void
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         return fail(GEMM_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with CUresult %d", name, (int)r);
+    return GEMM_OK;
+}
+
+// A 16-bit tensor of 3 or 4 dimensions (dims[0] contiguous, strides in bytes from dims[1] on),
+// 128-byte swizzle (box[0] = 64 elements), zero fill.
+int make_tmap16_nd(CUtensorMap* m, CUtensorMapDataType dt, const void* ptr, int rank,
+                   const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
+                   const char* name) {
+    auto fn = encode_fn();
+    if (!fn) return fail(GEMM_ERR_CUDA, "cuTensorMapEncodeTiled entry point not available");
+    cuuint64_t d[4], st[3];
+    cuuint32_t b[4], estr[4] = {1, 1, 1, 1};
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        if (i) st[i - 1] = strides[i - 1];
+    }
+    CUresult r = fn(m, dt, rank, const_cast<void*>(ptr), d, st, b, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(GEMM_ERR_CUDA, "cuTensorMapEncodeTiled(%s, %d-D) failed with CUresult %d", name,
+                    rank, (int)r);
     return GEMM_OK;
 }
 
@@ -390,6 +421,10 @@ int validate(int dtype, const void* A, const void* B, const void* sfA, const voi
     return GEMM_OK;
 }
 
+}  // namespace
+
+namespace dtc_host {
+
 // The kernels read and write through tensor maps of the current device: every buffer must be
 // device memory of that device (or managed memory). A pointer into another GPU's memory, or into
 // host memory, is refused here rather than read over a link.
@@ -408,6 +443,10 @@ int check_device_ptr(const void* p, int dev, const char* name) {
                     name, a.device, dev);
     return fail(GEMM_ERR_INVALID_ARG, "%s is not device memory (memory type %d)", name, (int)a.type);
 }
+
+}  // namespace dtc_host
+
+namespace {
 
 // Busy time of the slowest cluster, in tile-width units, when every tile costs time proportional
 // to its width: (waves of tiles over the resident units) x (tile width).
@@ -806,6 +845,21 @@ int run(int dtype, const void* A, const void* B, const void* sfA, const void* sf
     if (rc) return rc;
     return launch_prepared(r, dtype, M, N, K, o, stream);
 }
+
+}  // namespace
+
+namespace dtc_host {
+
+int product16(int dtype, const void* A, const void* B, void* C, int64_t M, int64_t N, int64_t K,
+              int layout, const gemm_options* o, cudaStream_t stream) {
+    return run(dtype, A, B, nullptr, nullptr, C, M, N, K, layout, o, stream);
+}
+
+void clear_error() { g_err[0] = '\0'; }
+
+}  // namespace dtc_host
+
+namespace {
 
 void fill_info(const Plan& p, gemm_plan_info* info) {
     info->variant = p.variant;

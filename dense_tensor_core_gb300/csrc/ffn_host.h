@@ -1,0 +1,89 @@
+// ffn_host.h -- host-side pieces of the feed-forward operators (include/dtc_ffn.h): the launchers of
+// their kernels, one translation unit per family.
+#pragma once
+
+#include "dtc_ffn.h"
+#include "gemm16_ffn.cuh"
+#include "host.h"
+
+namespace dtc_host {
+
+// A product of gemm16_ffn.cuh. Sizes in elements; args carries the epilogue.
+struct FfnCall {
+    bool bf16 = true;
+    int mode = 0;  // dtc::ffn::Mode
+    bool p_mn = false, q_mn = false, gated = false;
+    const void* P = nullptr;  // features
+    const void* Q = nullptr;  // rows
+    int64_t ldp = 0, ldq = 0;
+    int64_t red = 0;       // reduction length (kRed: the rows both operands hold)
+    int64_t q_rows = 0;    // rows of Q (kRed: its columns)
+    int experts = 1;
+    int grid = 0;
+    bool dependent = false;
+    dtc::FfnArgs args = {};
+};
+int launch_ffn_rows(const FfnCall& c, DeviceInfo* dev, cudaStream_t stream);
+int launch_ffn_experts(const FfnCall& c, DeviceInfo* dev, cudaStream_t stream);
+int ffn_tmaps(const FfnCall& c, CUtensorMap* p, CUtensorMap* q);
+
+template <bool kBF16, int kMode, bool kPMN, bool kQMN, bool kGated>
+int launch_ffn(const FfnCall& c, DeviceInfo* dev, cudaStream_t stream) {
+    CUtensorMap tp = {}, tq = {};
+    int rc = ffn_tmaps(c, &tp, &tq);
+    if (rc) return rc;
+    auto kern = dtc::gemm16_ffn_kernel<kBF16, kMode, kPMN, kQMN, kGated>;
+    if ((rc = ensure_smem_attr(kern, dtc::ffn::kSmemBytes, dev))) return rc;
+    return launch_chain(kern, dim3(c.grid), dtc::ffn::kThreads, dtc::ffn::kSmemBytes, 2, c.dependent,
+                        stream, tp, tq, c.args);
+}
+
+// dZ of gemm_act and its column sums (act_backward.cuh). dz may be NULL (sums only), dbias too.
+struct ActBackwardCall {
+    bool bf16;
+    const void* dC;
+    const void* z;
+    void* dz;
+    float* dbias;
+    int64_t M, N, ldc, ldz;
+    int act;
+    uint32_t* counters;  // act_backward_col_blocks words, zero between calls
+    float* partial;      // act_backward_partial_floats
+};
+int64_t act_backward_col_blocks(int64_t width);
+int64_t act_backward_partial_floats(int64_t M, int64_t width, int sms);
+int launch_act_backward(const ActBackwardCall& c, DeviceInfo* dev, cudaStream_t stream);
+
+// moe.cuh
+struct RouteCall {
+    int dtype;
+    const void* logits;
+    int64_t ld;
+    const float* bias;
+    int64_t T, E;
+    moe_route_options o;
+    float* weights;
+    int* indices;
+    const float* dweights;    // backward
+    const int* chosen;        // backward
+    void* dlogits;            // backward
+};
+int launch_moe_route(const RouteCall& c, DeviceInfo* dev, cudaStream_t stream);
+int launch_moe_route_backward(const RouteCall& c, DeviceInfo* dev, cudaStream_t stream);
+int launch_moe_plan(const int* indices, int64_t T, int k, int64_t E, int32_t* plan,
+                    const moe_plan_info& l, DeviceInfo* dev, cudaStream_t stream);
+// rows of x in expert order, gap rows zero; also clears `zero_words` words of counters
+int launch_moe_gather(const void* x, const int32_t* plan, const moe_plan_info& l, int k, int64_t E,
+                      int64_t H, void* out, uint32_t* zero, int zero_words, DeviceInfo* dev,
+                      cudaStream_t stream);
+// dys = w * dy rows in expert order, gap rows zero; dweights = dy . ys
+int launch_moe_spread(bool bf16, int wdtype, const void* dy, const void* ys, const void* weights,
+                      const int32_t* plan, const moe_plan_info& l, int64_t T, int k, int64_t E,
+                      int64_t H, void* dys, void* dweights, uint32_t* zero, int zero_words,
+                      DeviceInfo* dev, cudaStream_t stream);
+// out[t] = residual[t] + sum_j w[t,j] rows[slot[t,j]] (weights NULL: 1)
+int launch_moe_join(bool bf16, int wdtype, const void* rows, const void* weights,
+                    const int32_t* slots, const void* residual, void* out, int64_t T, int k,
+                    int64_t H, DeviceInfo* dev, cudaStream_t stream);
+
+}  // namespace dtc_host

@@ -101,7 +101,21 @@ struct Launch {
     cudaStream_t stream;
 };
 
+// The current device's state (probed once per device), its model (resident clusters asked on
+// first use), and the check that a buffer is memory of that device.
+int current_device(int* dev_out, DeviceInfo** info_out);
+const DevModel& device_model(DeviceInfo* d);
+int check_device_ptr(const void* p, int dev, const char* name);
+void clear_error();
+
+// gemm_ex for the 16-bit products, for the operators that take one as a part.
+int product16(int dtype, const void* A, const void* B, void* C, int64_t M, int64_t N, int64_t K,
+              int layout, const gemm_options* o, cudaStream_t stream);
+
 // Tensor maps (cuTensorMapEncodeTiled through the runtime's driver entry point).
+int make_tmap16_nd(CUtensorMap* m, CUtensorMapDataType dt, const void* ptr, int rank,
+                   const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
+                   const char* name);
 int make_tmap(CUtensorMap* m, CUtensorMapDataType dt, int elem_bytes, const void* ptr,
               uint64_t inner, uint64_t outer, uint64_t ld, uint32_t box_inner, uint32_t box_outer,
               CUtensorMapSwizzle swz, const char* name);
@@ -171,6 +185,34 @@ int launch_dependent(Kern kern, int grid, int threads, int smem, cudaStream_t st
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, params...);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "kernel launch");
+    return GEMM_OK;
+}
+
+// A cluster launch that may also begin early behind the stream's previous kernel (`dependent`; the
+// kernel then waits in griddepcontrol.wait before it touches what that kernel reads or writes).
+template <typename Kern, typename... Params>
+int launch_chain(Kern kern, dim3 grid, int threads, int smem, int cluster, bool dependent,
+                 cudaStream_t stream, const Params&... params) {
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    if (cluster > 1) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attr[cfg.numAttrs].val.clusterDim.x = cluster;
+        attr[cfg.numAttrs].val.clusterDim.y = 1;
+        attr[cfg.numAttrs++].val.clusterDim.z = 1;
+    }
+    if (dependent) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
     cudaError_t e = cudaLaunchKernelEx(&cfg, kern, params...);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "kernel launch");

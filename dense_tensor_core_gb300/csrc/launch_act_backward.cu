@@ -1,0 +1,45 @@
+// launch_act_backward.cu -- launcher of the activation's backward pass with the bias gradient.
+#include "act_backward.cuh"
+#include "ffn_host.h"
+
+namespace dtc_host {
+
+namespace {
+// Row blocks: enough blocks for 8 per SM (the SM's 2048 threads), each with at least 32 rows.
+int row_blocks(int64_t M, int64_t N, int sms) {
+    const int64_t gx = (N + dtc::kActBackCols - 1) / dtc::kActBackCols;
+    return (int)std::max<int64_t>(1, std::min<int64_t>((M + 31) / 32, (int64_t)sms * 8 / gx));
+}
+}  // namespace
+
+int64_t act_backward_col_blocks(int64_t N) {
+    return (N + dtc::kActBackCols - 1) / dtc::kActBackCols;
+}
+
+int64_t act_backward_partial_floats(int64_t M, int64_t N, int sms) {
+    return 2 * N * row_blocks(M, N, sms);
+}
+
+int launch_act_backward(const ActBackwardCall& c, DeviceInfo* dev, cudaStream_t stream) {
+    const bool gated = dtc::act_gated(c.act);
+    const int gy = row_blocks(c.M, c.N, dev->model.sms);
+    dtc::ActBackArgs a;
+    a.dC = static_cast<const uint16_t*>(c.dC);
+    a.z = static_cast<const uint16_t*>(c.z);
+    a.dz = static_cast<uint16_t*>(c.dz);
+    a.dbias = c.dbias;
+    a.M = c.M;
+    a.N = c.N;
+    a.ldc = c.ldc;
+    a.ldz = c.ldz;
+    a.act = c.act;
+    a.rows_per_block = (int)((c.M + gy - 1) / gy);
+    a.counters = c.counters;
+    a.partial = c.partial;
+    const dim3 grid((unsigned)act_backward_col_blocks(c.N), gy);
+    auto kern = c.bf16 ? (gated ? dtc::act_backward_kernel<true, true> : dtc::act_backward_kernel<true, false>)
+                       : (gated ? dtc::act_backward_kernel<false, true> : dtc::act_backward_kernel<false, false>);
+    return launch_chain(kern, grid, dtc::kActBackThreads, 0, 1, false, stream, a);
+}
+
+}  // namespace dtc_host

@@ -1,0 +1,71 @@
+// launch_ffn_rows.cu -- tensor maps of the feed-forward products, and the one-matrix products
+// (gemm_act) in their four layouts and the gated form.
+#include "ffn_host.h"
+
+namespace dtc_host {
+
+// P: the features' operand, Q: the rows' (gemm16_ffn.cuh). K-major operands are read as boxes of
+// {64 elements, rows, 2 chunks} where the reduction is whole 64-element chunks (one instruction a
+// stage), else as two boxes of one chunk each, which the tensor map zero-fills past the end.
+int ffn_tmaps(const FfnCall& c, CUtensorMap* p, CUtensorMap* q) {
+    const CUtensorMapDataType dt =
+        c.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    if (c.red == 0) return GEMM_OK;  // the kernel loads nothing
+    const uint64_t feats = c.args.feats, red = c.red, E = c.experts;
+    int rc;
+    if (c.p_mn) {
+        // stored [experts][reduction][features]; the reduction's end is the map's, so a K-block
+        // that reaches past it reads zeros, not the next expert's matrix
+        const uint64_t dims[3] = {feats, red, E};
+        const uint64_t st[2] = {(uint64_t)c.ldp * 2, red * (uint64_t)c.ldp * 2};
+        const uint32_t box[3] = {64, dtc::ffn::kBK, 1};
+        rc = make_tmap16_nd(p, dt, c.P, 3, dims, st, box, "features");
+    } else if (c.gated) {
+        // gate and up rows alternate: dimension 1 steps from a gate row to its up row
+        const uint64_t span = E * 2 * feats - feats;
+        const uint64_t row = (uint64_t)c.ldp * 2;
+        if (c.args.p_deep) {
+            const uint64_t dims[4] = {64, 2, span, red / 64};
+            const uint64_t st[3] = {feats * row, row, 128};
+            const uint32_t box[4] = {64, 2, 64, 2};
+            rc = make_tmap16_nd(p, dt, c.P, 4, dims, st, box, "features");
+        } else {
+            const uint64_t dims[3] = {red, 2, span};
+            const uint64_t st[2] = {feats * row, row};
+            const uint32_t box[3] = {64, 2, 64};
+            rc = make_tmap16_nd(p, dt, c.P, 3, dims, st, box, "features");
+        }
+    } else if (c.args.p_deep) {
+        rc = make_tmap_kchunks(p, dt, 2, c.P, red, E * feats, c.ldp, 128, "features");
+    } else {
+        rc = make_tmap(p, dt, 2, c.P, red, E * feats, c.ldp, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B,
+                       "features");
+    }
+    if (rc) return rc;
+    if (c.q_mn)
+        return make_tmap(q, dt, 2, c.Q, c.q_rows, red, c.ldq, 64, dtc::ffn::kBK,
+                         CU_TENSOR_MAP_SWIZZLE_128B, "rows");
+    if (c.args.q_deep)
+        return make_tmap_kchunks(q, dt, 2, c.Q, red, c.q_rows, c.ldq, c.args.q_box, "rows");
+    return make_tmap(q, dt, 2, c.Q, red, c.q_rows, c.ldq, 64, c.args.q_box,
+                     CU_TENSOR_MAP_SWIZZLE_128B, "rows");
+}
+
+namespace {
+template <bool kBF16>
+int rows_of(const FfnCall& c, DeviceInfo* dev, cudaStream_t s) {
+    using namespace dtc::ffn;
+    if (c.gated) return launch_ffn<kBF16, kRows, false, false, true>(c, dev, s);
+    if (c.p_mn)
+        return c.q_mn ? launch_ffn<kBF16, kRows, true, true, false>(c, dev, s)
+                      : launch_ffn<kBF16, kRows, true, false, false>(c, dev, s);
+    return c.q_mn ? launch_ffn<kBF16, kRows, false, true, false>(c, dev, s)
+                  : launch_ffn<kBF16, kRows, false, false, false>(c, dev, s);
+}
+}  // namespace
+
+int launch_ffn_rows(const FfnCall& c, DeviceInfo* dev, cudaStream_t stream) {
+    return c.bf16 ? rows_of<true>(c, dev, stream) : rows_of<false>(c, dev, stream);
+}
+
+}  // namespace dtc_host

@@ -1,0 +1,161 @@
+// launch_moe.cu -- launchers of the routing, plan, gather, spread and join kernels.
+#include "ffn_host.h"
+#include "moe.cuh"
+
+namespace dtc_host {
+
+namespace {
+
+dtc::RouteArgs route_args(const RouteCall& c) {
+    dtc::RouteArgs a = {};
+    a.logits = c.logits;
+    a.ld = c.ld;
+    a.bias = c.bias;
+    a.T = c.T;
+    a.E = (int)c.E;
+    a.k = c.o.top_k;
+    a.groups = c.o.groups;
+    a.per_group = (int)c.E / c.o.groups;
+    a.top_groups = c.o.top_groups;
+    a.div_magic = ((1u << 20) + a.per_group - 1) / a.per_group;
+    a.sigmoid = c.o.scoring == MOE_SIGMOID;
+    a.renorm = c.o.renormalize != 0;
+    a.scale = c.o.scale;
+    a.weights = c.weights;
+    a.indices = c.indices;
+    a.dweights = c.dweights;
+    a.chosen = c.chosen;
+    a.dlogits = c.dlogits;
+    return a;
+}
+
+// Experts per lane: the smallest instantiation that holds E.
+template <int kType, bool kBack>
+int route_by_size(const dtc::RouteArgs& a, cudaStream_t s) {
+    const dim3 grid((unsigned)((a.T + dtc::kRouteWarps - 1) / dtc::kRouteWarps));
+    const int threads = dtc::kRouteWarps * 32;
+    auto go = [&](auto kern) { return launch_chain(kern, grid, threads, 0, 1, false, s, a); };
+    const int v = (a.E + 31) / 32;
+#define DTC_ROUTE(N)                                             \
+    if (v <= N) {                                                \
+        if constexpr (kBack)                                     \
+            return go(dtc::moe_route_backward_kernel<kType, N>); \
+        else                                                     \
+            return go(dtc::moe_route_kernel<kType, N>);          \
+    }
+    DTC_ROUTE(1)
+    DTC_ROUTE(2)
+    DTC_ROUTE(4)
+    DTC_ROUTE(8)
+    DTC_ROUTE(16)
+    DTC_ROUTE(32)
+#undef DTC_ROUTE
+    return fail(GEMM_ERR_INVALID_ARG, "too many experts");
+}
+
+template <bool kBack>
+int route_any(const RouteCall& c, cudaStream_t s) {
+    const dtc::RouteArgs a = route_args(c);
+    if (c.dtype == 0) return route_by_size<0, kBack>(a, s);
+    if (c.dtype == 1) return route_by_size<1, kBack>(a, s);
+    return route_by_size<2, kBack>(a, s);
+}
+
+// One warp per row: as many blocks as fill the device's threads, at most one per 8 rows.
+int rows_grid(int64_t warps, DeviceInfo* dev) {
+    const int64_t per = dtc::kRowsThreads / 32;
+    return (int)std::max<int64_t>(1, std::min<int64_t>((warps + per - 1) / per, (int64_t)dev->model.sms * 8));
+}
+
+}  // namespace
+
+int launch_moe_route(const RouteCall& c, DeviceInfo*, cudaStream_t stream) {
+    return route_any<false>(c, stream);
+}
+int launch_moe_route_backward(const RouteCall& c, DeviceInfo*, cudaStream_t stream) {
+    return route_any<true>(c, stream);
+}
+
+int launch_moe_plan(const int* indices, int64_t T, int k, int64_t E, int32_t* plan,
+                    const moe_plan_info& l, DeviceInfo* dev, cudaStream_t stream) {
+    dtc::PlanArgs a;
+    a.indices = indices;
+    a.n = (int)(T * k);
+    a.E = (int)E;
+    // a CTA's 32 warps take 32 choices each at least; more CTAs only when that leaves work for them
+    int ctas = 1;
+    while (ctas < dtc::kPlanMaxCtas && (int64_t)ctas * dtc::kPlanThreads < a.n) ctas *= 2;
+    const int per_warp = ceil_div(a.n, (int64_t)ctas * dtc::kPlanWarps);
+    a.run = (per_warp + 31) / 32 * 32;
+    a.num_tiles = plan;
+    a.tiles = reinterpret_cast<dtc::FfnTile*>(plan + l.tiles);
+    a.offsets = plan + l.offsets;
+    a.counts = plan + l.counts;
+    a.slots = plan + l.slots;
+    a.rows = plan + l.rows;
+    const int smem = (int)((dtc::kPlanWarps + 2) * E * 4);
+    int rc = ensure_smem_attr(dtc::moe_plan_kernel, (dtc::kPlanWarps + 2) * dtc::ffn::kMaxExperts * 4, dev);
+    if (rc) return rc;
+    return launch_chain(dtc::moe_plan_kernel, dim3(ctas), dtc::kPlanThreads, smem, ctas, false, stream, a);
+}
+
+int launch_moe_gather(const void* x, const int32_t* plan, const moe_plan_info& l, int k, int64_t E,
+                      int64_t H, void* out, uint32_t* zero, int zero_words, DeviceInfo* dev,
+                      cudaStream_t stream) {
+    dtc::RowsArgs a = {};
+    a.in = static_cast<const uint16_t*>(x);
+    a.out = static_cast<uint16_t*>(out);
+    a.rows = plan + l.rows;
+    a.slots = plan + l.slots;
+    a.end = plan + l.offsets + E;
+    a.k = k;
+    a.H8 = (int)(H / 8);
+    a.zero = zero;
+    a.zero_words = zero_words;
+    return launch_chain(dtc::moe_gather_kernel, dim3(rows_grid(l.capacity, dev)), dtc::kRowsThreads, 0,
+                        1, false, stream, a);
+}
+
+int launch_moe_spread(bool bf16, int wdtype, const void* dy, const void* ys, const void* weights,
+                      const int32_t* plan, const moe_plan_info& l, int64_t T, int k, int64_t E,
+                      int64_t H, void* dys, void* dweights, uint32_t* zero, int zero_words,
+                      DeviceInfo* dev, cudaStream_t stream) {
+    dtc::RowsArgs a = {};
+    a.in = static_cast<const uint16_t*>(dy);
+    a.out = static_cast<uint16_t*>(dys);
+    a.rows = plan + l.rows;
+    a.slots = plan + l.slots;
+    a.end = plan + l.offsets + E;
+    a.T = T;
+    a.k = k;
+    a.H8 = (int)(H / 8);
+    a.y = static_cast<const uint16_t*>(ys);
+    a.weights = weights;
+    a.dweights = dweights;
+    a.wtype = wdtype;
+    a.zero = zero;
+    a.zero_words = zero_words;
+    const dim3 grid(rows_grid(l.capacity, dev));
+    return bf16 ? launch_chain(dtc::moe_spread_kernel<true>, grid, dtc::kRowsThreads, 0, 1, false, stream, a)
+                : launch_chain(dtc::moe_spread_kernel<false>, grid, dtc::kRowsThreads, 0, 1, false, stream, a);
+}
+
+int launch_moe_join(bool bf16, int wdtype, const void* rows, const void* weights,
+                    const int32_t* slots, const void* residual, void* out, int64_t T, int k,
+                    int64_t H, DeviceInfo* dev, cudaStream_t stream) {
+    dtc::JoinArgs a;
+    a.rows = static_cast<const uint16_t*>(rows);
+    a.weights = weights;
+    a.wtype = wdtype;
+    a.slots = slots;
+    a.residual = static_cast<const uint16_t*>(residual);
+    a.out = static_cast<uint16_t*>(out);
+    a.T = T;
+    a.k = k;
+    a.H8 = (int)(H / 8);
+    const dim3 grid(rows_grid(T * ((a.H8 + 31) / 32), dev));
+    return bf16 ? launch_chain(dtc::moe_join_kernel<true>, grid, dtc::kRowsThreads, 0, 1, false, stream, a)
+                : launch_chain(dtc::moe_join_kernel<false>, grid, dtc::kRowsThreads, 0, 1, false, stream, a);
+}
+
+}  // namespace dtc_host

@@ -1,0 +1,565 @@
+// moe.cuh -- routing of tokens to experts and the movement of rows into expert order and back.
+#pragma once
+
+#include <math_constants.h>
+
+#include "gemm16_ffn.cuh"
+
+namespace dtc {
+
+constexpr unsigned kFull = 0xffffffffu;
+
+// ------------------------------------------------------------------------------------------------
+// Elements of a 16- or 32-bit float type by code: 0 bf16, 1 fp16, 2 fp32
+// ------------------------------------------------------------------------------------------------
+template <int kType>
+__device__ __forceinline__ float load_f(const void* p, int64_t i) {
+    if constexpr (kType == 0) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+    else if constexpr (kType == 1) return __half2float(static_cast<const __half*>(p)[i]);
+    else return static_cast<const float*>(p)[i];
+}
+template <int kType>
+__device__ __forceinline__ void store_f(void* p, int64_t i, float v) {
+    if constexpr (kType == 0) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+    else if constexpr (kType == 1) static_cast<__half*>(p)[i] = __float2half_rn(v);
+    else static_cast<float*>(p)[i] = v;
+}
+__device__ __forceinline__ float load_w(const void* p, int64_t i, int type) {
+    return type == 0 ? load_f<0>(p, i) : type == 1 ? load_f<1>(p, i) : load_f<2>(p, i);
+}
+__device__ __forceinline__ void store_w(void* p, int64_t i, float v, int type) {
+    if (type == 0) store_f<0>(p, i, v);
+    else if (type == 1) store_f<1>(p, i, v);
+    else store_f<2>(p, i, v);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+    return v;
+}
+
+// ------------------------------------------------------------------------------------------------
+// moe_route: a warp per token, the token's logits in registers (expert e = lane + 32 j).
+//
+// The choice compares keys as unsigned integers in the order of their floats, so a round of the
+// top-k is one local maximum, one warp reduction of the key and one of the index (lowest on ties);
+// 0 stands for "cannot be chosen" and is below every key. Keys are computed with the correctly
+// rounded operations and the standard exponential (not the fast forms), so that a choice between
+// near-equal keys does not depend on an approximation.
+//
+// Bound by instructions more than by HBM for large k: about 2 VPL + 20 per choice and token.
+// ------------------------------------------------------------------------------------------------
+struct RouteArgs {
+    const void* logits;
+    int64_t ld;
+    const float* bias;
+    int64_t T;
+    int E, k, groups, per_group, top_groups;
+    uint32_t div_magic;  // (e * div_magic) >> 20 = e / per_group for e < 1024
+    bool sigmoid, renorm;
+    float scale;
+    float* weights;
+    int* indices;
+    // backward
+    const float* dweights;
+    const int* chosen;
+    void* dlogits;
+};
+
+constexpr int kRouteWarps = 4;
+
+// Floats in the order of unsigned integers; both zeros alike. -infinity and above give > 0.
+__device__ __forceinline__ uint32_t order_key(float f) {
+    const uint32_t u = __float_as_uint(f == 0.0f ? 0.0f : f);
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float from_key(uint32_t k) {
+    return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+
+__device__ __forceinline__ float sigmoid_exact(float z) { return __fdiv_rn(1.0f, 1.0f + expf(-z)); }
+
+template <int kType, int kVPL>
+__global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const RouteArgs a) {
+    __shared__ uint32_t group_keys[kRouteWarps][kVPL * 32];
+    grid_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
+    if (t >= a.T) return;
+    const int64_t row = t * a.ld;
+    float z[kVPL];
+    uint32_t key[kVPL];
+#pragma unroll
+    for (int j = 0; j < kVPL; ++j) {
+        const int e = lane + 32 * j;
+        z[j] = e < a.E ? load_f<kType>(a.logits, row + e) : -CUDART_INF_F;
+    }
+#pragma unroll
+    for (int j = 0; j < kVPL; ++j) {
+        const int e = lane + 32 * j;
+        float s = a.sigmoid ? sigmoid_exact(z[j]) : z[j];
+        if (a.bias && e < a.E) s = s + __ldg(a.bias + e);
+        // masked: -infinity or NaN, in the logit or in the key
+        key[j] = (z[j] > -CUDART_INF_F && s > -CUDART_INF_F) ? order_key(s) : 0u;
+    }
+    if (a.groups > 1) {
+        uint32_t* const keys = group_keys[warp];
+#pragma unroll
+        for (int j = 0; j < kVPL; ++j) keys[lane + 32 * j] = key[j];
+        __syncwarp();
+        // lanes_per lanes scan a group for its two largest keys, then join
+        int lanes_per = 32;
+        while (lanes_per * a.groups > 32) lanes_per >>= 1;
+        const int g = lane / lanes_per, sub = lane - g * lanes_per;
+        uint32_t m1 = 0, m2 = 0;
+        if (g < a.groups)
+            for (int i = sub; i < a.per_group; i += lanes_per) {
+                const uint32_t v = keys[g * a.per_group + i];
+                m2 = max(m2, min(m1, v));
+                m1 = max(m1, v);
+            }
+        for (int o = lanes_per >> 1; o; o >>= 1) {
+            const uint32_t n1 = __shfl_xor_sync(kFull, m1, o), n2 = __shfl_xor_sync(kFull, m2, o);
+            m2 = max(max(m2, n2), min(m1, n1));
+            m1 = max(m1, n1);
+        }
+        uint32_t score = 0;
+        if (sub == 0 && m1) score = order_key(from_key(m1) + (a.sigmoid && m2 ? from_key(m2) : 0.0f));
+        uint32_t keep = 0;
+        for (int i = 0; i < a.top_groups; ++i) {
+            const uint32_t best = __reduce_max_sync(kFull, score);
+            if (best == 0) break;
+            const unsigned at = __reduce_min_sync(kFull, score == best ? (unsigned)g : 64u);
+            keep |= 1u << at;
+            if (g == (int)at) score = 0;
+        }
+#pragma unroll
+        for (int j = 0; j < kVPL; ++j) {
+            const uint32_t eg = ((uint32_t)(lane + 32 * j) * a.div_magic) >> 20;
+            if (eg >= 32u || !((keep >> eg) & 1u)) key[j] = 0;
+        }
+    }
+    // the k largest keys; lane i keeps the i-th choice
+    int mine = -1;
+    for (int i = 0; i < a.k; ++i) {
+        uint32_t m = key[0];
+#pragma unroll
+        for (int j = 1; j < kVPL; ++j) m = max(m, key[j]);
+        const uint32_t best = __reduce_max_sync(kFull, m);
+        if (best == 0) break;
+        unsigned at = 0xffffu;
+#pragma unroll
+        for (int j = kVPL - 1; j >= 0; --j)
+            if (key[j] == best) at = lane + 32 * j;
+        at = __reduce_min_sync(kFull, at);
+        if (lane == i) mine = (int)at;
+#pragma unroll
+        for (int j = 0; j < kVPL; ++j)
+            if (lane + 32 * j == (int)at) key[j] = 0;
+    }
+    const bool got = mine >= 0;
+    const float zi = got ? load_f<kType>(a.logits, row + mine) : -CUDART_INF_F;
+    float w = 0.0f;
+    if (a.sigmoid) {
+        w = got ? sigmoid_exact(zi) : 0.0f;
+        if (a.renorm) {
+            const float total = warp_sum(w);
+            w = total > 0.0f ? w / total : 0.0f;
+        }
+    } else if (a.renorm) {
+        const float m = warp_max(zi);
+        const float e = got ? expf(zi - m) : 0.0f;
+        const float total = warp_sum(e);
+        w = got ? e / total : 0.0f;
+    } else {
+        float m = -CUDART_INF_F;
+#pragma unroll
+        for (int j = 0; j < kVPL; ++j) m = fmaxf(m, z[j]);  // (fmaxf passes over NaN)
+        m = warp_max(m);
+        float total = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kVPL; ++j)
+            if (z[j] > -CUDART_INF_F) total += expf(z[j] - m);
+        total = warp_sum(total);
+        w = got ? expf(zi - m) / total : 0.0f;
+    }
+    if (lane < a.k) {
+        a.weights[t * a.k + lane] = w * a.scale;
+        a.indices[t * a.k + lane] = mine;
+    }
+}
+
+// moe_route_backward: a warp per token, the dense row of the gradient written once. With p the
+// chosen scores and g = scale * dweights:
+//   softmax, renormalized      d_i = p_i (g_i - sum g p)        on the choices
+//   softmax over all           d_j = p_j ([j chosen] g_j - sum g p)
+//   sigmoid                    d_i = g_i s_i (1 - s_i);  renormalized: g_i -> (g_i - sum g s / S) / S
+template <int kType, int kVPL>
+__global__ void __launch_bounds__(kRouteWarps * 32) moe_route_backward_kernel(const RouteArgs a) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
+    if (t >= a.T) return;
+    const int64_t row = t * a.ld;
+    int mine = -1;
+    float g = 0.0f;
+    if (lane < a.k) {
+        mine = a.chosen[t * a.k + lane];
+        if (mine < 0 || mine >= a.E) mine = -1;
+        if (mine >= 0) g = a.dweights[t * a.k + lane] * a.scale;
+    }
+    const float zi = mine >= 0 ? load_f<kType>(a.logits, row + mine) : -CUDART_INF_F;
+    const bool got = zi > -CUDART_INF_F;
+    if (!got) {
+        mine = -1;
+        g = 0.0f;
+    }
+    float d = 0.0f, dot = 0.0f, m = 0.0f, inv = 0.0f;
+    float z[kVPL];
+    const bool full = !a.sigmoid && !a.renorm;
+    if (a.sigmoid) {
+        const float s = got ? sigmoid_exact(zi) : 0.0f;
+        if (a.renorm) {
+            const float total = warp_sum(s);
+            const float mean = total > 0.0f ? warp_sum(g * s) / total : 0.0f;
+            g = total > 0.0f && got ? (g - mean) / total : 0.0f;
+        }
+        d = g * s * (1.0f - s);
+    } else if (!full) {
+        m = warp_max(zi);
+        const float e = got ? expf(zi - m) : 0.0f;
+        const float total = warp_sum(e);
+        const float p = got ? e / total : 0.0f;
+        d = p * (g - warp_sum(g * p));
+    } else {
+        m = -CUDART_INF_F;
+#pragma unroll
+        for (int j = 0; j < kVPL; ++j) {
+            const int e = lane + 32 * j;
+            z[j] = e < a.E ? load_f<kType>(a.logits, row + e) : -CUDART_INF_F;
+            m = fmaxf(m, z[j]);
+        }
+        m = warp_max(m);
+        float total = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kVPL; ++j)
+            if (z[j] > -CUDART_INF_F) total += expf(z[j] - m);
+        total = warp_sum(total);
+        inv = total;
+        const float p = got ? expf(zi - m) / total : 0.0f;
+        d = g * p;
+        dot = warp_sum(d);
+    }
+    float out[kVPL];
+#pragma unroll
+    for (int j = 0; j < kVPL; ++j)
+        out[j] = full && z[j] > -CUDART_INF_F ? -(expf(z[j] - m) / inv) * dot : 0.0f;
+    for (int i = 0; i < a.k; ++i) {
+        const int e = __shfl_sync(kFull, mine, i);
+        const float v = __shfl_sync(kFull, d, i);
+#pragma unroll
+        for (int j = 0; j < kVPL; ++j)
+            if (lane + 32 * j == e) out[j] += v;
+    }
+#pragma unroll
+    for (int j = 0; j < kVPL; ++j) {
+        const int e = lane + 32 * j;
+        if (e < a.E) store_f<kType>(a.dlogits, t * a.E + e, out[j]);
+    }
+}
+
+// ------------------------------------------------------------------------------------------------
+// moe_plan: a stable counting sort of the choices by expert in one launch. The warps of a cluster
+// (1 to 8 CTAs of 32 warps) take consecutive runs of the choices. (1) Each warp counts its run per
+// expert in shared memory. (2) Counts become exclusive prefixes over the warps of a CTA, the CTAs
+// read each other's totals through distributed shared memory, and every CTA scans the experts'
+// padded totals. (3) Each warp walks its run again, 32 choices at a time: a choice's row is its
+// expert's start plus the warp's running count plus its rank among the equal choices of its 32.
+// One launch, because for few tokens the launches would take longer than the work.
+// ------------------------------------------------------------------------------------------------
+constexpr int kPlanThreads = 1024, kPlanWarps = 32, kPlanMaxCtas = 8;
+
+struct PlanArgs {
+    const int* indices;
+    int n;  // choices
+    int E;
+    int run;  // choices per warp, a multiple of 32
+    int* num_tiles;
+    FfnTile* tiles;
+    int* offsets;
+    int* counts;
+    int* slots;
+    int* rows;
+};
+
+__device__ __forceinline__ int ld_shared_cluster_s32(uint32_t addr) {
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// Exclusive prefix over the block's threads of a pair of sums (< 2^31 each).
+__device__ __forceinline__ int2 block_exclusive(int2 v, int2* warp_sums, int2& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int2 s = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(kFull, s.x, o), y = __shfl_up_sync(kFull, s.y, o);
+        if (lane >= o) {
+            s.x += x;
+            s.y += y;
+        }
+    }
+    if (lane == 31) warp_sums[warp] = s;
+    __syncthreads();
+    if (warp == 0) {
+        int2 w = warp_sums[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(kFull, w.x, o), y = __shfl_up_sync(kFull, w.y, o);
+            if (lane >= o) {
+                w.x += x;
+                w.y += y;
+            }
+        }
+        warp_sums[lane] = w;
+    }
+    __syncthreads();
+    total = warp_sums[kPlanWarps - 1];
+    const int2 before = warp ? warp_sums[warp - 1] : make_int2(0, 0);
+    return make_int2(before.x + s.x - v.x, before.y + s.y - v.y);
+}
+
+__global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_kernel(const PlanArgs a) {
+    extern __shared__ int plan_smem[];
+    int* const hist = plan_smem;                   // [32 warps][E]
+    int* const base = hist + kPlanWarps * a.E;     // [E]
+    int* const totals = base + a.E;                // [E], read by the other CTAs
+    __shared__ int2 warp_sums[kPlanWarps];
+    grid_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int rank = (int)cluster_ctarank(), ctas = (int)gridDim.x;
+    for (int i = threadIdx.x; i < kPlanWarps * a.E; i += kPlanThreads) hist[i] = 0;
+    __syncthreads();
+    grid_dependency_wait();
+    const int64_t r0 = (int64_t)(rank * kPlanWarps + warp) * a.run;
+    const int64_t r1 = min((int64_t)a.n, r0 + a.run);
+    int* const my = hist + warp * a.E;
+#pragma unroll 4
+    for (int64_t i = r0 + lane; i < r1; i += 32) {
+        const int e = a.indices[i];
+        if (e >= 0 && e < a.E) atomicAdd(my + e, 1);
+    }
+    __syncthreads();
+    const int e = threadIdx.x;
+    if (e < a.E) {
+        int s = 0;
+#pragma unroll 8
+        for (int w = 0; w < kPlanWarps; ++w) {
+            const int c = hist[w * a.E + e];
+            hist[w * a.E + e] = s;
+            s += c;
+        }
+        totals[e] = s;
+    }
+    cluster_sync();
+    int count = 0, below = 0;
+    if (e < a.E) {
+        const uint32_t at = smem_u32(totals + e);
+        for (int c = 0; c < ctas; ++c) {
+            const int v = ld_shared_cluster_s32(map_to_cta(at, c));
+            if (c < rank) below += v;
+            count += v;
+        }
+    }
+    const int padded = (count + ffn::kSegAlign - 1) / ffn::kSegAlign * ffn::kSegAlign;
+    const int nt = (count + ffn::kMaxRows - 1) / ffn::kMaxRows;
+    int2 total;
+    const int2 start = block_exclusive(make_int2(padded, nt), warp_sums, total);
+    if (e < a.E) {
+        base[e] = start.x + below;
+        if (rank == 0) {
+            a.offsets[e] = start.x;
+            a.counts[e] = count;
+            for (int r = count; r < padded; ++r) a.rows[start.x + r] = -1;
+            // equal tiles, in steps of the MMA's 32 rows
+            const int per = nt ? ((count + nt - 1) / nt + 31) & ~31 : 0;
+            for (int i = 0; i < nt; ++i)
+                a.tiles[start.y + i] =
+                    FfnTile{e, start.x + i * per, min(per, count - i * per), i == nt - 1 ? 1 : 0};
+        }
+    }
+    if (rank == 0 && threadIdx.x == 0) {
+        a.offsets[a.E] = total.x;
+        *a.num_tiles = total.y;
+    }
+    __syncthreads();
+    const unsigned below_me = (1u << lane) - 1u;
+    for (int64_t i0 = r0; i0 < r1; i0 += 32) {
+        const int64_t i = i0 + lane;
+        int x = i < r1 ? a.indices[i] : -1;
+        const bool ok = x >= 0 && x < a.E;
+        if (!ok) x = -1;
+        const unsigned same = __match_any_sync(kFull, x);
+        int at = -1;
+        if (ok) at = base[x] + my[x] + __popc(same & below_me);
+        __syncwarp();
+        if (ok && (same & below_me) == 0) my[x] += __popc(same);
+        __syncwarp();
+        if (i < r1) {
+            a.slots[i] = at;
+            if (ok) a.rows[at] = (int)i;
+        }
+    }
+    cluster_sync();  // no CTA leaves while another may still read its totals
+}
+
+// ------------------------------------------------------------------------------------------------
+// Movement of rows, bound by HBM. A warp per row, 16 bytes a lane.
+// ------------------------------------------------------------------------------------------------
+struct RowsArgs {
+    const uint16_t* in;   // gather: x [T,H]; spread: dy [T,H]
+    uint16_t* out;        // rows in expert order
+    const int* rows;
+    const int* slots;
+    const int* end;       // offsets[E]
+    int64_t T;
+    int k;
+    int H8;               // 16-byte pieces of a row
+    // spread
+    const uint16_t* y;    // the second product's rows
+    const void* weights;
+    void* dweights;
+    int wtype;
+    // counters to clear for the products behind this kernel
+    uint32_t* zero;
+    int zero_words;
+};
+
+constexpr int kRowsThreads = 256;
+
+__global__ void __launch_bounds__(kRowsThreads) moe_gather_kernel(const RowsArgs a) {
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int64_t tid = (int64_t)blockIdx.x * kRowsThreads + threadIdx.x;
+    for (int64_t i = tid; i < a.zero_words; i += (int64_t)gridDim.x * kRowsThreads) a.zero[i] = 0u;
+    const int lane = threadIdx.x & 31;
+    const int64_t warps = (int64_t)gridDim.x * (kRowsThreads / 32);
+    const int64_t end = __ldg(a.end);
+    for (int64_t r = tid >> 5; r < end; r += warps) {
+        const int i = __ldg(a.rows + r);
+        uint4* const d = reinterpret_cast<uint4*>(a.out) + r * a.H8;
+        if (i < 0) {
+            for (int c = lane; c < a.H8; c += 32) d[c] = make_uint4(0, 0, 0, 0);
+            continue;
+        }
+        const uint4* const s = reinterpret_cast<const uint4*>(a.in) + (int64_t)(i / a.k) * a.H8;
+#pragma unroll 8
+        for (int c = lane; c < a.H8; c += 32) d[c] = __ldg(s + c);
+    }
+}
+
+template <bool kBF16>
+__global__ void __launch_bounds__(kRowsThreads) moe_spread_kernel(const RowsArgs a) {
+    using namespace ffn;
+    const int64_t tid = (int64_t)blockIdx.x * kRowsThreads + threadIdx.x;
+    const int64_t threads = (int64_t)gridDim.x * kRowsThreads;
+    for (int64_t i = tid; i < a.zero_words; i += threads) a.zero[i] = 0u;
+    for (int64_t i = tid; i < a.T * a.k; i += threads)  // choices that are none
+        if (a.slots[i] < 0) store_w(a.dweights, i, 0.0f, a.wtype);
+    const int lane = threadIdx.x & 31;
+    const int64_t end = __ldg(a.end);
+    for (int64_t r = tid >> 5; r < end; r += threads >> 5) {
+        const int i = __ldg(a.rows + r);
+        uint4* const d = reinterpret_cast<uint4*>(a.out) + r * a.H8;
+        if (i < 0) {
+            for (int c = lane; c < a.H8; c += 32) d[c] = make_uint4(0, 0, 0, 0);
+            continue;
+        }
+        const uint4* const g = reinterpret_cast<const uint4*>(a.in) + (int64_t)(i / a.k) * a.H8;
+        const uint4* const y = reinterpret_cast<const uint4*>(a.y) + r * a.H8;
+        const float w = load_w(a.weights, i, a.wtype);
+        float dot = 0.0f;
+#pragma unroll 4
+        for (int c = lane; c < a.H8; c += 32) {
+            float u[8], v[8];
+            unpack8<kBF16>(__ldg(g + c), u);
+            unpack8<kBF16>(__ldcs(y + c), v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                dot = fmaf(u[j], v[j], dot);
+                u[j] *= w;
+            }
+            d[c] = pack8<kBF16>(u);
+        }
+        dot = warp_sum(dot);
+        if (lane == 0) store_w(a.dweights, i, dot, a.wtype);
+    }
+}
+
+struct JoinArgs {
+    const uint16_t* rows;
+    const void* weights;  // NULL: 1
+    int wtype;
+    const int* slots;
+    const uint16_t* residual;
+    uint16_t* out;
+    int64_t T;
+    int k;
+    int H8;
+};
+
+// out[t] = residual[t] + sum_j w_j rows[slot_j], in the order of j, fp32, one rounding. A warp
+// takes a run of 32 x 8 columns of a token; lane j holds choice j's row and weight and hands them
+// round. Four rows' pieces are in flight at a time.
+template <bool kBF16>
+__global__ void __launch_bounds__(kRowsThreads) moe_join_kernel(const JoinArgs a) {
+    using namespace ffn;
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int lane = threadIdx.x & 31;
+    const int pieces = (a.H8 + 31) / 32;
+    const int64_t items = a.T * pieces;
+    const int64_t warps = (int64_t)gridDim.x * (kRowsThreads / 32);
+    for (int64_t it = ((int64_t)blockIdx.x * kRowsThreads + threadIdx.x) >> 5; it < items; it += warps) {
+        const int64_t t = it / pieces;
+        const int c = (int)(it - t * pieces) * 32 + lane;
+        int slot = -1;
+        float w = 0.0f;
+        if (lane < a.k) {
+            slot = a.slots[t * a.k + lane];
+            if (slot >= 0) w = a.weights ? load_w(a.weights, t * a.k + lane, a.wtype) : 1.0f;
+        }
+        float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (a.residual && c < a.H8)
+            unpack8<kBF16>(__ldg(reinterpret_cast<const uint4*>(a.residual) + t * a.H8 + c), s);
+        for (int j0 = 0; j0 < a.k; j0 += 4) {
+            uint4 v[4];
+            float wj[4];
+            bool on[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int src = __shfl_sync(kFull, slot, (j0 + j) & 31);
+                wj[j] = __shfl_sync(kFull, w, (j0 + j) & 31);
+                on[j] = j0 + j < a.k && src >= 0 && c < a.H8;
+                if (on[j]) v[j] = __ldcs(reinterpret_cast<const uint4*>(a.rows) + (int64_t)src * a.H8 + c);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (!on[j]) continue;
+                float x[8];
+                unpack8<kBF16>(v[j], x);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s[i] = fmaf(wj[j], x[i], s[i]);
+            }
+        }
+        if (c < a.H8) reinterpret_cast<uint4*>(a.out)[t * a.H8 + c] = pack8<kBF16>(s);
+    }
+}
+
+}  // namespace dtc
