@@ -42,7 +42,7 @@ class moe_experts_options(ctypes.Structure):
 
 
 class moe_experts_info(ctypes.Structure):
-    _fields_ = [(n, _u64) for n in ("bytes", "x", "z", "h", "y", "split")]
+    _fields_ = [(n, _u64) for n in ("bytes", "x", "z", "h", "scale", "y", "split")]
 
 
 _lib = None

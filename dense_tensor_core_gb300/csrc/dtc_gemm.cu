@@ -157,15 +157,15 @@ int make_tmap(CUtensorMap* m, CUtensorMapDataType dt, int elem_bytes, const void
     return GEMM_OK;
 }
 
-// A 16-bit tensor of 3 or 4 dimensions (dims[0] contiguous, strides in bytes from dims[1] on),
+// A 16-bit tensor of 3 to 5 dimensions (dims[0] contiguous, strides in bytes from dims[1] on),
 // 128-byte swizzle (box[0] = 64 elements), zero fill.
 int make_tmap16_nd(CUtensorMap* m, CUtensorMapDataType dt, const void* ptr, int rank,
                    const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
                    const char* name) {
     auto fn = encode_fn();
     if (!fn) return fail(GEMM_ERR_CUDA, "cuTensorMapEncodeTiled entry point not available");
-    cuuint64_t d[4], st[3];
-    cuuint32_t b[4], estr[4] = {1, 1, 1, 1};
+    cuuint64_t d[5], st[4];
+    cuuint32_t b[5], estr[5] = {1, 1, 1, 1, 1};
     for (int i = 0; i < rank; ++i) {
         d[i] = dims[i];
         b[i] = box[i];

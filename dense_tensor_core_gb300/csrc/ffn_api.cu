@@ -27,7 +27,7 @@ int num_feature_tiles(int64_t feats, bool gated) { return ceil_div(feats, gated 
 
 void size_split(FfnPlan* p) {
     if (p->splits <= 1) return;
-    p->counter_bytes = up256((uint64_t)p->tiles * 8 * 4);
+    p->counter_bytes = up256((uint64_t)p->tiles * 2 * dtc::ffn::kEpWarps * 4);
     p->bytes = p->counter_bytes + (uint64_t)p->tiles * p->splits * p->tile_n * 1024;
 }
 
@@ -250,7 +250,6 @@ int gemm_act(int dtype, const void* A, const void* B, void* C, int64_t M, int64_
     a.experts = 1;
     a.p_deep = a.q_deep = K % 64 == 0;
     a.q_box = p.tile_n / 2;
-    a.epi = dtc::ffn::kEpiForward;
     a.act = o.activation;
     a.out = C;
     a.ld_out = o.ldc;
@@ -640,12 +639,15 @@ void seg_call(const ExpertSizes& s, bool bf16, const int32_t* plan, const moe_ex
     a.status = info->status;
 }
 
-// A product over the experts' rows: out[row, f] = epilogue(rows[row, :] . P_e[f, :]).
+// A product over the experts' rows: out[row, f] = epilogue(rows[row, :] . P_e[f, :]). `e` holds the
+// epilogue's part of the arguments.
 int seg_product(const ExpertSizes& s, bool bf16, const int32_t* plan, const moe_experts_options& o,
                 DeviceInfo* info, const FfnPlan& p, void* counters, void* partial, const void* rows,
-                int64_t red, const void* weights, bool weights_mn, int64_t feats, bool gated, int epi,
-                int act, void* out, int64_t ld_out, void* preact, int64_t ld_pre, cudaStream_t st) {
+                int64_t red, const void* weights, bool weights_mn, int64_t feats, bool gated, bool back,
+                const dtc::FfnArgs& e, cudaStream_t st) {
     FfnCall c;
+    c.back = back;
+    c.args = e;
     seg_call(s, bf16, plan, o, info, &c);
     c.mode = dtc::ffn::kSeg;
     c.p_mn = weights_mn;
@@ -661,12 +663,6 @@ int seg_product(const ExpertSizes& s, bool bf16, const int32_t* plan, const moe_
     a.red = (int)red;
     a.p_deep = red % 64 == 0;
     a.p_expert_rows = (int)(gated ? 2 * feats : feats);
-    a.epi = epi;
-    a.act = act;
-    a.out = out;
-    a.ld_out = ld_out;
-    a.preact = preact;
-    a.ld_pre = ld_pre;
     apply_plan(p, nullptr, &c);
     if (p.splits > 1) {
         a.counters = static_cast<uint32_t*>(counters);
@@ -695,7 +691,6 @@ int red_product(const ExpertSizes& s, bool bf16, const int32_t* plan, const moe_
     a.feats = (int)width_r;
     a.rows = (int)width_l;
     a.red = (int)s.plan.capacity;
-    a.epi = dtc::ffn::kEpiForward;
     a.act = dtc::kActNone;
     a.out = out;
     a.ld_out = width_r;
@@ -708,8 +703,9 @@ int experts_layout(const ExpertSizes& s, int train, int pairs, moe_experts_info*
     const uint64_t R = s.plan.capacity;
     l->x = 0;
     l->z = up256(R * s.H * 2);
-    l->h = l->z + (train && s.act != GEMM_ACT_NONE ? up256(R * s.Fz * 2) : 0);
-    l->y = l->h + up256(R * s.F * 2);
+    l->h = l->z + (train ? up256(R * s.Fz * 2) : 0);
+    l->scale = l->h + up256(R * s.F * 2);
+    l->y = l->scale + up256(R * 4);
     l->split = l->y + up256(R * s.H * 2);
     const SplitScratch x = split_scratch(seg_plan(s, s.F, s.gated, s.H, pairs),
                                          seg_plan(s, s.H, false, s.F, pairs));
@@ -777,36 +773,49 @@ int moe_experts(int dtype, const void* x, const void* w_in, const void* w_out, c
     const int32_t* const pl = static_cast<const int32_t*>(plan);
     const cudaStream_t st = (cudaStream_t)stream;
     const bool bf16 = dtype == 0;
-    if ((rc = launch_moe_gather(x, pl, s.plan, k, E, H, b + l.x, reinterpret_cast<uint32_t*>(split),
-                                (int)(sc.partial / 4), info, st)))
-        return rc;
-    void* const z = train && s.act != GEMM_ACT_NONE ? b + l.z : nullptr;
+    const GatherCall g{x, b + l.x, weights, o.weights_dtype, reinterpret_cast<float*>(b + l.scale),
+                       reinterpret_cast<uint32_t*>(split), (int)(sc.partial / 4)};
+    if ((rc = launch_moe_gather(g, pl, s.plan, k, E, H, info, st))) return rc;
+    // h = weight * act(z): the weight goes in here, in fp32 before h's one rounding, so the join
+    // is a plain sum and the backward pass needs no product of the weights with rounded rows
+    dtc::FfnArgs e = {};
+    e.act = s.act;
+    e.row_scale = reinterpret_cast<const float*>(b + l.scale);
+    e.out = b + l.h;
+    e.ld_out = F;
+    e.preact = train ? b + l.z : nullptr;
+    e.ld_pre = s.Fz;
     if ((rc = seg_product(s, bf16, pl, o, info, p1, split, split + sc.partial, b + l.x, H, w_in, false,
-                          F, s.gated, dtc::ffn::kEpiForward, s.act, b + l.h, F, z, s.Fz, st)))
+                          F, s.gated, false, e, st)))
         return rc;
+    e = {};
+    e.out = b + l.y;
+    e.ld_out = H;
     if ((rc = seg_product(s, bf16, pl, o, info, p2, split + sc.second, split + sc.partial, b + l.h, F,
-                          w_out, false, H, false, dtc::ffn::kEpiForward, dtc::kActNone, b + l.y, H,
-                          nullptr, 0, st)))
+                          w_out, false, H, false, false, e, st)))
         return rc;
-    return launch_moe_join(bf16, o.weights_dtype, b + l.y, weights, pl + s.plan.slots, o.residual, y, T,
-                           k, H, info, st);
+    const JoinCall j{b + l.y, o.residual, y, nullptr, 0, nullptr, 0};
+    return launch_moe_join(bf16, j, pl, s.plan, T, k, E, H, info, st);
 }
 
 }  // extern "C"
 
 namespace {
 
-// Scratch of the backward pass: the gradients of the second product's rows, of z and of the
-// gathered rows, and the split products'.
+// Scratch of the backward pass: dy's rows in expert order, the gradients of z and of the gathered
+// rows, the pieces of the weights' gradient, and the split products'.
 struct ExpertsBackLayout {
-    uint64_t dy, dz, dx, split, bytes;
+    uint64_t dy, dz, dx, dots, split, bytes;
+    int parts;  // pieces per row: one per 32 features
 };
 void experts_back_layout(const ExpertSizes& s, int pairs, ExpertsBackLayout* l) {
     const uint64_t R = s.plan.capacity;
     l->dy = 0;
     l->dz = up256(R * s.H * 2);
     l->dx = l->dz + up256(R * s.Fz * 2);
-    l->split = l->dx + up256(R * s.H * 2);
+    l->dots = l->dx + up256(R * s.H * 2);
+    l->parts = num_feature_tiles(s.F, false) * 8;
+    l->split = l->dots + up256(R * l->parts * 4);
     const SplitScratch x = split_scratch(seg_plan(s, s.F, false, s.H, pairs),
                                          seg_plan(s, s.H, false, s.Fz, pairs));
     l->bytes = l->split + up256(x.bytes);
@@ -891,26 +900,37 @@ int moe_experts_backward(int dtype, const void* dy, const void* w_in, const void
     char* const split = ws + w.split;
     const int32_t* const pl = static_cast<const int32_t*>(plan);
     const bool bf16 = dtype == 0;
-    if ((rc = launch_moe_spread(bf16, o.weights_dtype, dy, b + l.y, weights, pl, s.plan, T, k, E, H,
-                                ws + w.dy, dweights, reinterpret_cast<uint32_t*>(split),
-                                (int)(sc.partial / 4), info, st)))
-        return rc;
-    // dz = (dy rows . w_out) * act'(z), in the product's epilogue
+    const GatherCall g{dy, ws + w.dy, nullptr, 0, nullptr, reinterpret_cast<uint32_t*>(split),
+                       (int)(sc.partial / 4)};
+    if ((rc = launch_moe_gather(g, pl, s.plan, k, E, H, info, st))) return rc;
+    // dz = weight * (dy rows . w_out) * act'(z) and the rows' dot products, in the epilogue
+    dtc::FfnArgs e = {};
+    e.act = s.act;
+    e.row_scale = reinterpret_cast<const float*>(b + l.scale);
+    e.row_dot = reinterpret_cast<float*>(ws + w.dots);
+    e.row_dot_ld = (int64_t)s.plan.capacity;
+    e.out = ws + w.dz;
+    e.ld_out = s.Fz;
+    e.preact = const_cast<char*>(b) + l.z;
+    e.ld_pre = s.Fz;
     if ((rc = seg_product(s, bf16, pl, o, info, ph, split, split + sc.partial, ws + w.dy, H, w_out, true, F,
-                          false, dtc::ffn::kEpiBackward, s.act, ws + w.dz, s.Fz,
-                          const_cast<char*>(b) + l.z, s.Fz, st)))
+                          false, true, e, st)))
         return rc;
     if (dw_in) {
         if ((rc = red_product(s, bf16, pl, o, info, pairs, ws + w.dy, H, b + l.h, F, dw_out, st))) return rc;
         if ((rc = red_product(s, bf16, pl, o, info, pairs, ws + w.dz, s.Fz, b + l.x, H, dw_in, st))) return rc;
     }
-    if (!dx) return GEMM_OK;
-    if ((rc = seg_product(s, bf16, pl, o, info, px, split + sc.second, split + sc.partial, ws + w.dz, s.Fz,
-                          w_in, true, H, false, dtc::ffn::kEpiForward, dtc::kActNone, ws + w.dx, H, nullptr,
-                          0, st)))
-        return rc;
-    return launch_moe_join(bf16, o.weights_dtype, ws + w.dx, nullptr, pl + s.plan.slots, nullptr, dx, T, k, H,
-                           info, st);
+    if (dx) {
+        e = {};
+        e.out = ws + w.dx;
+        e.ld_out = H;
+        if ((rc = seg_product(s, bf16, pl, o, info, px, split + sc.second, split + sc.partial, ws + w.dz,
+                              s.Fz, w_in, true, H, false, false, e, st)))
+            return rc;
+    }
+    const JoinCall j{ws + w.dx, nullptr, dx, reinterpret_cast<const float*>(ws + w.dots), w.parts, dweights,
+                     o.weights_dtype};
+    return launch_moe_join(bf16, j, pl, s.plan, T, k, E, H, info, st);
 }
 
 }  // extern "C"

@@ -12,7 +12,7 @@ namespace dtc_host {
 struct FfnCall {
     bool bf16 = true;
     int mode = 0;  // dtc::ffn::Mode
-    bool p_mn = false, q_mn = false, gated = false;
+    bool p_mn = false, q_mn = false, gated = false, back = false;
     const void* P = nullptr;  // features
     const void* Q = nullptr;  // rows
     int64_t ldp = 0, ldq = 0;
@@ -27,12 +27,12 @@ int launch_ffn_rows(const FfnCall& c, DeviceInfo* dev, cudaStream_t stream);
 int launch_ffn_experts(const FfnCall& c, DeviceInfo* dev, cudaStream_t stream);
 int ffn_tmaps(const FfnCall& c, CUtensorMap* p, CUtensorMap* q);
 
-template <bool kBF16, int kMode, bool kPMN, bool kQMN, bool kGated>
+template <bool kBF16, int kMode, bool kPMN, bool kQMN, bool kGated, bool kBack = false>
 int launch_ffn(const FfnCall& c, DeviceInfo* dev, cudaStream_t stream) {
     CUtensorMap tp = {}, tq = {};
     int rc = ffn_tmaps(c, &tp, &tq);
     if (rc) return rc;
-    auto kern = dtc::gemm16_ffn_kernel<kBF16, kMode, kPMN, kQMN, kGated>;
+    auto kern = dtc::gemm16_ffn_kernel<kBF16, kMode, kPMN, kQMN, kGated, kBack>;
     if ((rc = ensure_smem_attr(kern, dtc::ffn::kSmemBytes, dev))) return rc;
     return launch_chain(kern, dim3(c.grid), dtc::ffn::kThreads, dtc::ffn::kSmemBytes, 2, c.dependent,
                         stream, tp, tq, c.args);
@@ -72,18 +72,31 @@ int launch_moe_route(const RouteCall& c, DeviceInfo* dev, cudaStream_t stream);
 int launch_moe_route_backward(const RouteCall& c, DeviceInfo* dev, cudaStream_t stream);
 int launch_moe_plan(const int* indices, int64_t T, int k, int64_t E, int32_t* plan,
                     const moe_plan_info& l, DeviceInfo* dev, cudaStream_t stream);
-// rows of x in expert order, gap rows zero; also clears `zero_words` words of counters
-int launch_moe_gather(const void* x, const int32_t* plan, const moe_plan_info& l, int k, int64_t E,
-                      int64_t H, void* out, uint32_t* zero, int zero_words, DeviceInfo* dev,
-                      cudaStream_t stream);
-// dys = w * dy rows in expert order, gap rows zero; dweights = dy . ys
-int launch_moe_spread(bool bf16, int wdtype, const void* dy, const void* ys, const void* weights,
-                      const int32_t* plan, const moe_plan_info& l, int64_t T, int k, int64_t E,
-                      int64_t H, void* dys, void* dweights, uint32_t* zero, int zero_words,
-                      DeviceInfo* dev, cudaStream_t stream);
-// out[t] = residual[t] + sum_j w[t,j] rows[slot[t,j]] (weights NULL: 1)
-int launch_moe_join(bool bf16, int wdtype, const void* rows, const void* weights,
-                    const int32_t* slots, const void* residual, void* out, int64_t T, int k,
-                    int64_t H, DeviceInfo* dev, cudaStream_t stream);
+// Rows of x [T,H] in expert order, gap rows zero; with weights [T,k] also each row's weight in
+// `scale`; also clears `zero_words` words of counters.
+struct GatherCall {
+    const void* x;
+    void* out;
+    const void* weights;
+    int wtype;
+    float* scale;
+    uint32_t* zero;
+    int zero_words;
+};
+int launch_moe_gather(const GatherCall& c, const int32_t* plan, const moe_plan_info& l, int k, int64_t E,
+                      int64_t H, DeviceInfo* dev, cudaStream_t stream);
+// out[t] = residual[t] + sum_j rows[slot[t,j]] (out NULL: no join); dweights from the pieces of the
+// rows' dot products (dweights NULL: none).
+struct JoinCall {
+    const void* rows;
+    const void* residual;
+    void* out;
+    const float* dots;
+    int parts;
+    void* dweights;
+    int wtype;
+};
+int launch_moe_join(bool bf16, const JoinCall& c, const int32_t* plan, const moe_plan_info& l, int64_t T,
+                    int k, int64_t E, int64_t H, DeviceInfo* dev, cudaStream_t stream);
 
 }  // namespace dtc_host

@@ -17,19 +17,24 @@
 // tensor pipe).
 //
 // The two accumulator lanes of a gate and its up value must meet in one thread: the gated form
-// loads feature rows alternately from the gate half and the up half of P (one tensor-map dimension
-// of extent 2 between K and the features), so lanes 2i and 2i + 1 hold feature i's pair.
+// loads feature rows in octets, 8 of the gate half of P and then the same 8 of its up half (a
+// tensor-map dimension of extent 2 between the octets' rows and the octets), so that lanes l and
+// l + 8 hold a feature's pair, which the fragment layout below puts into one thread.
 //
 // Roles as in the pair kernel of the plain product: warp 0 loads (TMA, 3 stages of 128-deep
-// K-blocks, 64 KB a stage), warp 1 of the leader issues the MMAs, warps 2-5 of both CTAs run the
+// K-blocks, 64 KB a stage), warp 1 of the leader issues the MMAs, warps 2-9 of both CTAs run the
 // epilogue on one of two accumulators while the next tile is multiplied into the other. Every wait
 // is bounded (wait_bounded) and a wait that gives up releases Tensor Memory and returns.
 //
-// Epilogue: the accumulator arrives with a feature per lane and rows in registers. A warp passes
-// 32 x 32 blocks through 4 KB of its own shared memory (32 conflict-free 4-byte stores, 8
-// conflict-free 16-byte loads per thread), after which a thread holds 8 consecutive features of a
-// row: bias is one register set per tile, residual and results move as 16-byte accesses, four
-// lanes to a 64-byte row piece (whole sectors). No value is rounded before the one store.
+// Epilogue: two warps share each quarter of the accumulator lanes and take its 32-row blocks in
+// turn. A 32 x 32 block is read from Tensor Memory in the matrix-fragment layout (a thread: 4
+// features x 8 rows), finished in fp32, packed, and transposed to rows of consecutive features by
+// four stmatrix.trans into 2 KB of the warp's own shared memory, from where it leaves as 16-byte
+// stores (64 contiguous bytes per row). Residuals and kept activations come in the opposite way
+// (16-byte loads issued a block ahead, ldmatrix.trans). No value is rounded before the one store.
+// Against an earlier form that passed fp32 blocks through shared memory with 4 warps this halves
+// the shared-memory traffic, which the MMA's operand reads compete for, and it is what bounds the
+// products with a short reduction.
 //
 // splits > 1 (few tiles, e.g. single tokens): the K-blocks of a tile are shared out over `splits`
 // items. Each epilogue warp writes its fp32 partial sums to the workspace and raises a counter; the
@@ -44,13 +49,15 @@
 namespace dtc {
 
 namespace ffn {
-constexpr int kThreads = 192;
+constexpr int kEpWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpWarps;
 constexpr int kBK = 128;
 constexpr int kStages = 3;
 constexpr int kPStage = 128 * kBK * 2;
 constexpr int kQStage = 128 * kBK * 2;
 constexpr int kStageBytes = kPStage + kQStage;
-constexpr int kEpBytes = 4 * 4096;  // one 32 x 32 fp32 block per epilogue warp
+constexpr int kSlot = 2048;                    // one 32 x 32 16-bit block
+constexpr int kEpBytes = kEpWarps * 2 * kSlot;  // two per epilogue warp
 constexpr int kSmemBytes = kStages * kStageBytes + kEpBytes + 1024;
 constexpr int kTmemCols = 512;
 constexpr int kAccStride = 256;
@@ -63,7 +70,6 @@ constexpr uint64_t kPeerSettleNs = 1000ull * 1000;
 static_assert(kSmemBytes <= 227 * 1024 - 256, "shared memory budget");
 
 enum Mode { kRows = 0, kSeg = 1, kRed = 2 };
-enum Epi { kEpiForward = 0, kEpiBackward = 1 };
 }  // namespace ffn
 
 // One tile of an expert's rows: rows row0 .. row0 + valid - 1 of the expert order.
@@ -87,9 +93,12 @@ struct FfnArgs {
     const int* counts;
     int p_expert_rows;      // K-major P: rows between experts' matrices
     // epilogue
-    int epi, act;
+    int act;
     void* out;
     int64_t ld_out, expert_out;  // elements between rows, and (kRed) between experts' matrices
+    const float* row_scale;      // factor of each row, after the activation
+    float* row_dot;              // backward: [num_ft * 8][row_dot_ld] pieces of sum_f x act(z)
+    int64_t row_dot_ld;
     const void* bias;            // [feats] (gated [2 feats])
     const void* residual;
     int64_t ld_res;
@@ -187,18 +196,11 @@ __device__ __forceinline__ void unpack8(uint4 u, float (&v)[8]) {
     }
 }
 template <bool kBF16>
-__device__ __forceinline__ void unpack4(uint2 u, float (&v)[4]) {
-    const uint32_t w[2] = {u.x, u.y};
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        float2 f;
-        if constexpr (kBF16)
-            f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
-        else
-            f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
-    }
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+    if constexpr (kBF16)
+        return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+    else
+        return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 template <bool kBF16>
 __device__ __forceinline__ uint32_t packf2(float a, float b) {
@@ -209,105 +211,302 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
     return make_uint4(packf2<kBF16>(v[0], v[1]), packf2<kBF16>(v[2], v[3]),
                       packf2<kBF16>(v[4], v[5]), packf2<kBF16>(v[6], v[7]));
 }
-template <bool kBF16>
-__device__ __forceinline__ uint2 pack4(const float (&v)[4]) {
-    return make_uint2(packf2<kBF16>(v[0], v[1]), packf2<kBF16>(v[2], v[3]));
-}
 
-// The epilogue of one row's 8 accumulator features `x` (ungated: features f .. f + 7; gated: the
-// pairs of features f .. f + 3). `row` counts rows of the result. `b`: the bias of the 8.
-template <bool kBF16, bool kGated>
-__device__ __forceinline__ void finish8(const FfnArgs& a, float (&x)[8], const float (&b)[8],
-                                        int64_t row, int f, int64_t out_base) {
-    uint16_t* const out = static_cast<uint16_t*>(a.out) + out_base + row * a.ld_out + f;
-    if constexpr (kGated) {
-        float g[4], u[4];
+// ------------------------------------------------------------------------------------------------
+// 32-row blocks of 8 kOct features between fragments (v[o][2 b + i]: feature 8 o + t / 4, row
+// 8 b + 2 (t % 4) + i) and row-major 16-bit memory, through one of the warp's slots. In the slot a
+// row takes 16 kOct bytes and its 16-byte piece j stands at j ^ s(row), s so chosen that the 8 rows
+// of an stmatrix and the 8 lanes of a 16-byte access cover all banks.
+// ------------------------------------------------------------------------------------------------
+template <int kOct>
+struct Block {
+    static_assert(kOct == 4 || kOct == 2, "32 or 16 features");
+    static constexpr int kRowBytes = 16 * kOct;
+    static constexpr int kPerPass = 32 / kOct;       // rows per 16-byte access of the warp
+    static constexpr int kPasses = 32 / kPerPass;
+    uint32_t matrix;  // this lane's stmatrix / ldmatrix address
+    uint32_t piece;   // this lane's 16-byte address
+    int row, col;     // and its row and first feature
+
+    __device__ __forceinline__ Block(uint32_t slot, int lane) {
+        const int m = lane >> 3, r = lane & 7;
+        if constexpr (kOct == 4)
+            matrix = slot + r * 64 + ((m ^ ((r >> 1) & 3)) << 4);
+        else
+            matrix = slot + (8 * (m >> 1) + r) * 32 + (((m & 1) ^ ((r >> 2) & 1)) << 4);
+        row = lane / kOct;
+        const int j = lane % kOct;
+        col = 8 * j;
+        piece = slot + row * kRowBytes + ((j ^ (kOct == 4 ? (row >> 1) & 3 : (row >> 2) & 1)) << 4);
+    }
+    // rows 0 .. rows - 1 of the block to memory at `out` (the block's first row and feature)
+    template <bool kBF16, typename V>
+    __device__ __forceinline__ void store(V v, uint16_t* out, int64_t ld, int rows, int feats) const {
+        __syncwarp();  // the slot has been read
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            g[i] = x[2 * i] + b[2 * i];
-            u[i] = x[2 * i + 1] + b[2 * i + 1];
-        }
-        if (a.preact) {
-            uint16_t* const z = static_cast<uint16_t*>(a.preact) + row * a.ld_pre + f;
-            *reinterpret_cast<uint2*>(z) = pack4<kBF16>(g);
-            *reinterpret_cast<uint2*>(z + a.feats) = pack4<kBF16>(u);
-        }
-        act_forward(g, act_of_gate(a.act));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) g[i] *= u[i];
-        if (a.residual) {
-            float r[4];
-            unpack4<kBF16>(*reinterpret_cast<const uint2*>(
-                               static_cast<const uint16_t*>(a.residual) + row * a.ld_res + f), r);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) g[i] += r[i];
-        }
-        *reinterpret_cast<uint2*>(out) = pack4<kBF16>(g);
-    } else if (a.epi == kEpiForward) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] += b[i];
-        if (a.preact)
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.preact) + row * a.ld_pre + f) =
-                pack8<kBF16>(x);
-        act_forward(x, a.act);
-        if (a.residual) {
-            float r[8];
-            unpack8<kBF16>(*reinterpret_cast<const uint4*>(
-                               static_cast<const uint16_t*>(a.residual) + row * a.ld_res + f), r);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] += r[i];
-        }
-        *reinterpret_cast<uint4*>(out) = pack8<kBF16>(x);
-    } else {
-        // x is the gradient of the activation's output; the result is that of z (gated: both
-        // halves, feats apart)
-        if (a.act == kActNone) {
-            *reinterpret_cast<uint4*>(out) = pack8<kBF16>(x);
-            return;
-        }
-        const uint16_t* const z = static_cast<const uint16_t*>(a.preact) + row * a.ld_pre + f;
-        float v[8], d[8];
-        unpack8<kBF16>(__ldg(reinterpret_cast<const uint4*>(z)), v);
-        act_both(v, d, act_of_gate(a.act));
-        if (act_gated(a.act)) {
-            float u[8];
-            unpack8<kBF16>(__ldg(reinterpret_cast<const uint4*>(z + a.feats)), u);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                v[i] *= x[i];
-                x[i] *= u[i] * d[i];
+        for (int b = 0; b < 4; ++b) {
+            if constexpr (kOct == 4) {
+                stmatrix_x4_trans(matrix + b * 512, packf2<kBF16>(v(0, 2 * b), v(0, 2 * b + 1)),
+                                  packf2<kBF16>(v(1, 2 * b), v(1, 2 * b + 1)),
+                                  packf2<kBF16>(v(2, 2 * b), v(2, 2 * b + 1)),
+                                  packf2<kBF16>(v(3, 2 * b), v(3, 2 * b + 1)));
+            } else if (b % 2 == 0) {
+                stmatrix_x4_trans(matrix + b * 256, packf2<kBF16>(v(0, 2 * b), v(0, 2 * b + 1)),
+                                  packf2<kBF16>(v(1, 2 * b), v(1, 2 * b + 1)),
+                                  packf2<kBF16>(v(0, 2 * b + 2), v(0, 2 * b + 3)),
+                                  packf2<kBF16>(v(1, 2 * b + 2), v(1, 2 * b + 3)));
             }
-            *reinterpret_cast<uint4*>(out + a.feats) = pack8<kBF16>(v);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] *= d[i];
         }
-        *reinterpret_cast<uint4*>(out) = pack8<kBF16>(x);
+        __syncwarp();
+        flush(out, ld, rows, feats);
+    }
+    // the slot's rows to memory
+    __device__ __forceinline__ void flush(uint16_t* out, int64_t ld, int rows, int feats) const {
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int r = row + i * kPerPass;
+            const uint4 x = ld_shared_u4(piece + i * kPerPass * kRowBytes);
+            if (r < rows && col < feats) *reinterpret_cast<uint4*>(out + r * ld + col) = x;
+        }
+    }
+    // The same the other way in three steps: fetch issues the loads, put writes them to the slot,
+    // take (after a __syncwarp) hands the fragments over.
+    __device__ __forceinline__ void fetch(uint4 (&x)[kPasses], const uint16_t* in, int64_t ld, int rows,
+                                          int feats) const {
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int r = row + i * kPerPass;
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (r < rows && col < feats) x[i] = *reinterpret_cast<const uint4*>(in + r * ld + col);
+        }
+    }
+    __device__ __forceinline__ void put(const uint4 (&x)[kPasses]) const {
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i)
+            st_shared_u4(piece + i * kPerPass * kRowBytes, x[i].x, x[i].y, x[i].z, x[i].w);
+    }
+    template <bool kBF16, typename F>
+    __device__ __forceinline__ void take(F f) const {
+#pragma unroll
+        for (int b = 0; b < 4; b += kOct == 4 ? 1 : 2) {
+            uint32_t r[4];
+            ldmatrix_x4_trans(matrix + b * (kOct == 4 ? 512 : 256), r);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const float2 p = unpack2<kBF16>(r[m]);
+                const int o = kOct == 4 ? m : m & 1, bb = kOct == 4 ? b : b + (m >> 1);
+                f(o, 2 * bb, p.x);
+                f(o, 2 * bb + 1, p.y);
+            }
+        }
+    }
+};
+
+// What a block's epilogue reads from memory, fetched ahead of its sums: the residual, or in the
+// backward form z.
+template <bool kGated, bool kBack>
+struct Ahead {
+    uint4 a[kGated ? 2 : 4], b[kBack ? 4 : 1];
+};
+
+// Where a warp's block lies: first row of the result, first feature, rows that hold sums, rows that
+// are written (more by an expert's gap rows, as zeros).
+struct Place {
+    int64_t row, out_base;
+    int f;        // first feature of the block (32, gated 16, features wide)
+    int valid, rows;
+    int piece;    // backward: number of the features' piece in row_dot
+};
+
+template <bool kGated, bool kBack>
+__device__ __forceinline__ void fetch_ahead(const FfnArgs& a, const Place& p, uint32_t slot, int lane,
+                                            Ahead<kGated, kBack>& x) {
+    const int left = a.feats - p.f;
+    const Block<kGated ? 2 : 4> blk(slot, lane);
+    if constexpr (!kBack) {
+        if (a.residual)
+            blk.fetch(x.a, static_cast<const uint16_t*>(a.residual) + p.row * a.ld_res + p.f, a.ld_res,
+                      p.valid, left);
+    } else {
+        const uint16_t* const z = static_cast<const uint16_t*>(a.preact) + p.row * a.ld_pre + p.f;
+        blk.fetch(x.a, z, a.ld_pre, p.valid, left);
+        if (act_gated(a.act)) blk.fetch(x.b, z + a.feats, a.ld_pre, p.valid, left);
     }
 }
 
-// An expert's gap rows (up to 15 behind its last row) are written as zeros wherever results are:
-// the weight gradients then reduce over whole 16-row steps without a mask.
-template <bool kGated>
-__device__ __forceinline__ void zero8(const FfnArgs& a, int64_t row, int f) {
-    uint16_t* const out = static_cast<uint16_t*>(a.out) + row * a.ld_out + f;
-    const uint4 z4 = make_uint4(0, 0, 0, 0);
-    if constexpr (kGated) {
-        *reinterpret_cast<uint2*>(out) = make_uint2(0, 0);
+// Finishes one block: v holds the sums. `bias`: of the thread's 4 accumulator lanes. `x` goes into
+// the slots first, then `refill` may fetch the next block's into it.
+template <bool kBF16, bool kGated, bool kBack, typename Refill>
+__device__ __forceinline__ void finish_block(const FfnArgs& a, float (&v)[4][8], const float (&bias)[4],
+                                             const Place& p, Ahead<kGated, kBack>& x, uint32_t slot,
+                                             int lane, Refill refill) {
+    const int left = a.feats - p.f;
+    uint16_t* const out = static_cast<uint16_t*>(a.out) + p.out_base + p.row * a.ld_out + p.f;
+    const int tr = 2 * (lane & 3);  // the thread's rows: 8 b + tr + i
+    __syncwarp();  // the slots have been read
+    if constexpr (kBack) {
+        Block<4>(slot, lane).put(x.a);
+        if (act_gated(a.act)) Block<4>(slot + kSlot, lane).put(x.b);
+    } else if (a.residual) {
+        Block<kGated ? 2 : 4>(slot + kSlot, lane).put(x.a);
+    }
+    refill();
+    __syncwarp();
+    float scale[8];
+    if (a.row_scale) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            float2 s = make_float2(0.0f, 0.0f);  // (rows come in multiples of 16, so pairs are whole)
+            if (8 * b + tr < p.rows) s = __ldg(reinterpret_cast<const float2*>(a.row_scale + p.row + 8 * b + tr));
+            scale[2 * b] = s.x;
+            scale[2 * b + 1] = s.y;
+        }
+    }
+    auto past = [&](int k) { return 8 * (k >> 1) + tr + (k & 1) >= p.valid; };
+    if constexpr (!kBack) {
+#pragma unroll
+        for (int o = 0; o < 4; ++o)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[o][k] += bias[o];
+        if constexpr (kGated) {
+            const Block<2> blk(slot, lane);
+            if (a.preact) {
+                uint16_t* const z = static_cast<uint16_t*>(a.preact) + p.row * a.ld_pre + p.f;
+                blk.template store<kBF16>([&](int o, int k) { return v[2 * o][k]; }, z, a.ld_pre, p.valid, left);
+                blk.template store<kBF16>([&](int o, int k) { return v[2 * o + 1][k]; }, z + a.feats, a.ld_pre,
+                                 p.valid, left);
+            }
+#pragma unroll
+            for (int o = 0; o < 4; o += 2) {
+                act_forward(v[o], act_of_gate(a.act));
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[o][k] *= v[o + 1][k];
+            }
+            if (a.row_scale) {
+#pragma unroll
+                for (int o = 0; o < 4; o += 2)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[o][k] *= scale[k];
+            }
+            if (a.residual)
+                Block<2>(slot + kSlot, lane).template take<kBF16>([&](int o, int k, float r) { v[2 * o][k] += r; });
+            if (p.rows > p.valid) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (past(k)) v[0][k] = v[2][k] = 0.0f;
+            }
+            blk.template store<kBF16>([&](int o, int k) { return v[2 * o][k]; }, out, a.ld_out, p.rows, left);
+        } else {
+            const Block<4> blk(slot, lane);
+            auto val = [&](int o, int k) { return v[o][k]; };
+            if (a.preact)
+                blk.template store<kBF16>(val, static_cast<uint16_t*>(a.preact) + p.row * a.ld_pre + p.f, a.ld_pre,
+                                 p.valid, left);
+#pragma unroll
+            for (int o = 0; o < 4; ++o) act_forward(v[o], a.act);
+            if (a.row_scale) {
+#pragma unroll
+                for (int o = 0; o < 4; ++o)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[o][k] *= scale[k];
+            }
+            if (a.residual)
+                Block<4>(slot + kSlot, lane).template take<kBF16>([&](int o, int k, float r) { v[o][k] += r; });
+            if (p.rows > p.valid) {
+#pragma unroll
+                for (int o = 0; o < 4; ++o)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (past(k)) v[o][k] = 0.0f;
+            }
+            blk.template store<kBF16>(val, out, a.ld_out, p.rows, left);
+        }
     } else {
-        *reinterpret_cast<uint4*>(out) = z4;
-        if (a.epi == kEpiBackward && act_gated(a.act)) *reinterpret_cast<uint4*>(out + a.feats) = z4;
+        // v is the gradient of the activation's output without the row's factor; the result is that
+        // of z (gated: both halves, feats apart), and the row's dot product with the activation is
+        // the gradient of its factor
+        // (gated: both halves' slots). Eight rows at a time, each slot rewritten in place.
+        const Block<4> blk(slot, lane), blk2(slot + kSlot, lane);
+        const bool gated = act_gated(a.act);
+        float dot[8];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            uint32_t rz[4], ru[4] = {0, 0, 0, 0};
+            ldmatrix_x4_trans(blk.matrix + b * 512, rz);
+            if (gated) ldmatrix_x4_trans(blk2.matrix + b * 512, ru);
+            float z[8], d[8], up[8];  // [2 o + i]
+#pragma unroll
+            for (int o = 0; o < 4; ++o) {
+                const float2 zz = unpack2<kBF16>(rz[o]), uu = unpack2<kBF16>(ru[o]);
+                z[2 * o] = zz.x;
+                z[2 * o + 1] = zz.y;
+                up[2 * o] = uu.x;
+                up[2 * o + 1] = uu.y;
+            }
+            act_both(z, d, act_of_gate(a.act));
+            dot[2 * b] = dot[2 * b + 1] = 0.0f;
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                const int k = 2 * b + (n & 1);
+                const float g = v[n >> 1][k];
+                const float t = p.rows > p.valid && past(k) ? 0.0f : a.row_scale ? g * scale[k] : g;
+                if (gated) {
+                    dot[k] = fmaf(g, z[n] * up[n], dot[k]);
+                    d[n] = t * up[n] * d[n];
+                    up[n] = t * z[n];
+                } else {
+                    dot[k] = fmaf(g, z[n], dot[k]);
+                    d[n] = t * d[n];
+                }
+            }
+            __syncwarp();
+            stmatrix_x4_trans(blk.matrix + b * 512, packf2<kBF16>(d[0], d[1]), packf2<kBF16>(d[2], d[3]),
+                              packf2<kBF16>(d[4], d[5]), packf2<kBF16>(d[6], d[7]));
+            if (gated)
+                stmatrix_x4_trans(blk2.matrix + b * 512, packf2<kBF16>(up[0], up[1]),
+                                  packf2<kBF16>(up[2], up[3]), packf2<kBF16>(up[4], up[5]),
+                                  packf2<kBF16>(up[6], up[7]));
+        }
+        __syncwarp();
+        blk.flush(out, a.ld_out, p.rows, left);
+        if (gated) blk2.flush(out + a.feats, a.ld_out, p.rows, left);
+        if (a.row_dot) {
+            // sum over the 8 lanes that hold other features of the same rows, halving the rows a
+            // lane keeps at each step: lane bits 4, 3, 2 end up selecting bits 2, 1, 0 of k
+            float h[4], q[2], e;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const bool hi = lane & 16;
+                const float keep = hi ? dot[k + 4] : dot[k], give = hi ? dot[k] : dot[k + 4];
+                h[k] = keep + __shfl_xor_sync(0xffffffffu, give, 16);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const bool hi = lane & 8;
+                const float keep = hi ? h[k + 2] : h[k], give = hi ? h[k] : h[k + 2];
+                q[k] = keep + __shfl_xor_sync(0xffffffffu, give, 8);
+            }
+            {
+                const bool hi = lane & 4;
+                const float keep = hi ? q[1] : q[0], give = hi ? q[0] : q[1];
+                e = keep + __shfl_xor_sync(0xffffffffu, give, 4);
+            }
+            const int k = ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1);
+            const int r = 8 * (k >> 1) + tr + (k & 1);
+            if (r < p.valid) a.row_dot[p.piece * a.row_dot_ld + p.row + r] = e;
+        }
     }
 }
 
 }  // namespace ffn
 
-template <bool kBF16, int kMode, bool kPMN, bool kQMN, bool kGated>
+template <bool kBF16, int kMode, bool kPMN, bool kQMN, bool kGated, bool kBack>
 __global__ void __launch_bounds__(ffn::kThreads, 1)
     gemm16_ffn_kernel(const __grid_constant__ CUtensorMap tmP,
                       const __grid_constant__ CUtensorMap tmQ, const FfnArgs args) {
     using namespace ffn;
     static_assert(!kGated || (!kPMN && !kQMN), "the gated form takes K-major operands");
+    static_assert(!kBack || (kMode == kSeg && !kGated), "the backward epilogue: rows of experts");
     static_assert(kMode != kRed || (kPMN && kQMN), "the reduction over rows reads stored rows");
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bar_full[kStages];
@@ -336,7 +535,7 @@ __global__ void __launch_bounds__(ffn::kThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&bar_tfull[b]), 1);
-            mbar_init(smem_u32(&bar_tempty[b]), 8);  // 4 epilogue warps in each CTA
+            mbar_init(smem_u32(&bar_tempty[b]), 2 * kEpWarps);  // of both CTAs
         }
         mbar_init(smem_u32(&bar_drain), 1);
         abort_flag = 0;
@@ -394,12 +593,12 @@ __global__ void __launch_bounds__(ffn::kThreads, 1)
                             tma_load_3d_pair(p + j * (64 * kBK * 2), &tmP, full, f_row + j * 64,
                                              w.krow + kb * kBK, kMode == kSeg ? w.expert : 0);
                     } else if constexpr (kGated) {
-                        const int row = w.expert * args.p_expert_rows + f_row;
+                        const int oct = (w.expert * args.p_expert_rows + f_row) / 8;
                         if (args.p_deep) {
-                            tma_load_4d_pair(p, &tmP, full, 0, 0, row, kb * 2);
+                            tma_load_5d_pair(p, &tmP, full, 0, 0, 0, oct, kb * 2);
                         } else {
-                            tma_load_3d_pair(p, &tmP, full, kb * kBK, 0, row);
-                            tma_load_3d_pair(p + kPStage / 2, &tmP, full, kb * kBK + 64, 0, row);
+                            tma_load_4d_pair(p, &tmP, full, kb * kBK, 0, 0, oct);
+                            tma_load_4d_pair(p + kPStage / 2, &tmP, full, kb * kBK + 64, 0, 0, oct);
                         }
                     } else {
                         const int row = w.expert * args.p_expert_rows + f_row;
@@ -502,42 +701,41 @@ __global__ void __launch_bounds__(ffn::kThreads, 1)
             }
         }
     } else {
-        // ------------------------------ epilogue (warps 2..5, both CTAs) ---------------------
-        const int q = warp & 3;
-        float* const stage = reinterpret_cast<float*>(
-            smem_raw + (base - smem_u32(smem_raw)) + kStages * kStageBytes + q * 4096);
-        const uint32_t stage_a = smem_u32(stage);
-        // after the transposition: thread holds accumulator features 8 cg .. 8 cg + 7 of rows
-        // 8 i + lr of a block
-        const int cg = lane & 3, lr = lane >> 2;
-        const int half = (lr & 1) * 4;  // which 16 bytes of the 32 are read first: conflict-free
+        // ------------------------------ epilogue (warps 2..9, both CTAs) ---------------------
+        const int q = warp & 3, turn = (warp - 2) >> 2;
+        const uint32_t slot = base + kStages * kStageBytes + (uint32_t)(warp - 2) * (2 * kSlot);
         uint32_t acc = 0;
         Item w;
         for (int t = pair; get_item<kMode, kGated>(args, t, seg_tiles, w); t += num_pairs) {
             const uint32_t b = acc & 1u, aph = (acc >> 1) & 1u;
             ++acc;
-            // feature of x[0] and whether the thread's features exist (feats is a multiple of 8)
-            const int f = kGated ? w.f0 + (int)rank * 64 + q * 16 + cg * 4
-                                 : w.f0 + (int)rank * 128 + q * 32 + cg * 8;
-            const bool f_ok = f < args.feats;
-            const int64_t out_base = kMode == kRed ? (int64_t)w.expert * args.expert_out : 0;
-            float bias[8];
+            const int total = w.valid + w.zeros;  // (gap rows share the last block)
+            const int chunks = (total + 31) / 32;
+            Place place;
+            place.f = kGated ? w.f0 + (int)rank * 64 + q * 16 : w.f0 + (int)rank * 128 + q * 32;
+            place.out_base = kMode == kRed ? (int64_t)w.expert * args.expert_out : 0;
+            place.piece = (w.f0 / 256 * 2 + (int)rank) * 4 + q;
+            auto at_chunk = [&](int c) {
+                place.row = (int64_t)w.r0 + c * 32;
+                place.valid = min(32, w.valid - c * 32);
+                place.rows = min(32, total - c * 32);
+            };
+            // bias of the thread's 4 lanes (feats is a multiple of 8, so octets are whole)
+            float bias[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) bias[i] = 0.0f;
-            if (args.bias && f_ok) {
-                const uint16_t* const bp = static_cast<const uint16_t*>(args.bias) + f;
-                if constexpr (kGated) {
-                    float g[4], u[4];
-                    unpack4<kBF16>(__ldg(reinterpret_cast<const uint2*>(bp)), g);
-                    unpack4<kBF16>(__ldg(reinterpret_cast<const uint2*>(bp + args.feats)), u);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        bias[2 * i] = g[i];
-                        bias[2 * i + 1] = u[i];
-                    }
-                } else {
-                    unpack8<kBF16>(__ldg(reinterpret_cast<const uint4*>(bp)), bias);
+            for (int o = 0; o < 4; ++o) {
+                bias[o] = 0.0f;
+                const int f = place.f + (lane >> 2) + (kGated ? (o >> 1) * 8 : o * 8);
+                if (args.bias && f < args.feats) {
+                    const int64_t at = f + (kGated && (o & 1) ? args.feats : 0);
+                    bias[o] = unpack2<kBF16>(static_cast<const uint16_t*>(args.bias)[at]).x;
                 }
+            }
+            Ahead<kGated, kBack> ahead;
+            const bool whole = args.splits <= 1;
+            if (whole && turn < chunks) {
+                at_chunk(turn);
+                fetch_ahead<kGated, kBack>(args, place, slot, lane, ahead);
             }
             int ok = 1;
             if (lane == 0)
@@ -546,84 +744,87 @@ __global__ void __launch_bounds__(ffn::kThreads, 1)
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) break;
             tc_fence_after_sync();
+            auto hand_back = [&]() {  // accumulator read: back to the MMA issuer
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(map_to_cta(smem_u32(&bar_tempty[b]), 0));
+            };
+            if (turn >= chunks) hand_back();
             const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + b * kAccStride;
             const bool empty = w.kb0 == w.kb1;  // no K-block: the sum is zero
-            const int chunks = (w.valid + 31) / 32;
-            // split-K: this warp's slice of the tile in the workspace, [rows][32 features]
-            const int64_t slice = ((int64_t)w.tile * 2 + rank) * 4 + q;
-            const int64_t slice_elems = (int64_t)args.tile_n * 32;
-            float* const mine =
-                args.splits > 1 ? args.partial + (slice * args.splits + w.split) * slice_elems : nullptr;
+            // split-K: the blocks of this quarter in the workspace, 1024 floats each, in the
+            // order [split][block]
+            const int blocks = args.tile_n / 32;
+            const int64_t quarter = ((int64_t)w.tile * 2 + rank) * 4 + q;
 #pragma unroll 1
-            for (int c = 0; c < chunks; ++c) {
-                {
-                    uint32_t v[32];
-                    tmem_load_32cols(taddr + c * 32, v);
-                    if (c == chunks - 1) {  // accumulator read: back to the MMA issuer
-                        tc_fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(map_to_cta(smem_u32(&bar_tempty[b]), 0));
-                    }
-                    __syncwarp();  // the block before has been read
+            for (int c = turn; c < chunks; c += 2) {
+                float v[4][8];
+                tmem_load_fragment32(taddr + c * 32, v);
+                if (c + 2 >= chunks) hand_back();
+                if (empty) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        stage[j * 32 + lane] = empty ? 0.0f : __uint_as_float(v[j]);
-                    __syncwarp();
+                    for (int i = 0; i < 32; ++i) v[i / 8][i % 8] = 0.0f;
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = c * 32 + i * 8 + lr;
-                    if (r < w.valid && f_ok) {
-                        const uint32_t at = stage_a + (i * 8 + lr) * 128 + cg * 32;
-                        const float4 x0 = ld_shared_f4(at + half * 4);
-                        const float4 x1 = ld_shared_f4(at + (4 - half) * 4);
-                        const float4 lo = half ? x1 : x0, hi = half ? x0 : x1;
-                        if (mine) {
-                            float4* const d = reinterpret_cast<float4*>(mine + r * 32 + cg * 8);
-                            d[0] = lo;
-                            d[1] = hi;
-                        } else {
-                            float x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-                            finish8<kBF16, kGated>(args, x, bias, (int64_t)w.r0 + r, f, out_base);
+                at_chunk(c);
+                if (whole) {
+                    const Place here = place;
+                    finish_block<kBF16, kGated, kBack>(args, v, bias, here, ahead, slot, lane, [&]() {
+                        if (c + 2 < chunks) {
+                            at_chunk(c + 2);
+                            fetch_ahead<kGated, kBack>(args, place, slot, lane, ahead);
                         }
-                    }
+                    });
+                } else {
+                    float4* const d = reinterpret_cast<float4*>(
+                        args.partial + ((quarter * args.splits + w.split) * blocks + c) * 1024) + lane;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (8 * k < place.valid) {
+                            d[(2 * k) * 32] = make_float4(v[0][2 * k], v[0][2 * k + 1], v[1][2 * k], v[1][2 * k + 1]);
+                            d[(2 * k + 1) * 32] = make_float4(v[2][2 * k], v[2][2 * k + 1], v[3][2 * k], v[3][2 * k + 1]);
+                        }
                 }
             }
-            bool finish = mine == nullptr;
-            if (mine) {
+            if (!whole && turn < chunks) {
+                uint32_t* const counter = args.counters + ((int64_t)w.tile * 2 + rank) * kEpWarps + (warp - 2);
                 __threadfence();  // this lane's pieces are visible before the count
                 __syncwarp();
                 uint32_t before = 0;
-                if (lane == 0) before = atomicAdd(args.counters + slice, 1u);
+                if (lane == 0) before = atomicAdd(counter, 1u);
                 before = __shfl_sync(0xffffffffu, before, 0);
                 if (before == (uint32_t)args.splits - 1) {
                     __threadfence();  // and the others' before this warp reads them
-                    if (lane == 0) args.counters[slice] = 0u;
-                    finish = true;
-                    const float* const all = args.partial + slice * args.splits * slice_elems;
-                    for (int r = lr; r < w.valid && f_ok; r += 8) {
-                        float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                        const float* p = all + r * 32 + cg * 8;
+                    if (lane == 0) *counter = 0u;
+#pragma unroll 1
+                    for (int c = turn; c < chunks; c += 2) {
+                        at_chunk(c);
+                        fetch_ahead<kGated, kBack>(args, place, slot, lane, ahead);
+                        float v[4][8];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i / 8][i % 8] = 0.0f;
+                        const float4* d = reinterpret_cast<const float4*>(
+                            args.partial + (quarter * args.splits * blocks + c) * 1024) + lane;
 #pragma unroll 4
-                        for (int k = 0; k < args.splits; ++k, p += slice_elems) {
-                            const float4 lo = ld_global_cg_f4(reinterpret_cast<const float4*>(p));
-                            const float4 hi = ld_global_cg_f4(reinterpret_cast<const float4*>(p) + 1);
-                            x[0] += lo.x;
-                            x[1] += lo.y;
-                            x[2] += lo.z;
-                            x[3] += lo.w;
-                            x[4] += hi.x;
-                            x[5] += hi.y;
-                            x[6] += hi.z;
-                            x[7] += hi.w;
+                        for (int s = 0; s < args.splits; ++s, d += blocks * 256) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (8 * k < place.valid) {
+                                    const float4 lo = ld_global_cg_f4(d + (2 * k) * 32);
+                                    const float4 hi = ld_global_cg_f4(d + (2 * k + 1) * 32);
+                                    v[0][2 * k] += lo.x;
+                                    v[0][2 * k + 1] += lo.y;
+                                    v[1][2 * k] += lo.z;
+                                    v[1][2 * k + 1] += lo.w;
+                                    v[2][2 * k] += hi.x;
+                                    v[2][2 * k + 1] += hi.y;
+                                    v[3][2 * k] += hi.z;
+                                    v[3][2 * k + 1] += hi.w;
+                                }
                         }
-                        finish8<kBF16, kGated>(args, x, bias, (int64_t)w.r0 + r, f, out_base);
+                        finish_block<kBF16, kGated, kBack>(args, v, bias, place, ahead, slot, lane, [] {});
                     }
                 }
             }
-            if (kMode == kSeg && finish && f_ok)
-                for (int r = lr; r < w.zeros; r += 8)
-                    zero8<kGated>(args, (int64_t)w.r0 + w.valid + r, f);
         }
     }
 

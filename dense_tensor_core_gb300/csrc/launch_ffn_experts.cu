@@ -10,6 +10,7 @@ int experts_of(const FfnCall& c, DeviceInfo* dev, cudaStream_t s) {
     using namespace dtc::ffn;
     if (c.mode == kRed) return launch_ffn<kBF16, kRed, true, true, false>(c, dev, s);
     if (c.gated) return launch_ffn<kBF16, kSeg, false, false, true>(c, dev, s);
+    if (c.back) return launch_ffn<kBF16, kSeg, true, false, false, true>(c, dev, s);
     return c.p_mn ? launch_ffn<kBF16, kSeg, true, false, false>(c, dev, s)
                   : launch_ffn<kBF16, kSeg, false, false, false>(c, dev, s);
 }

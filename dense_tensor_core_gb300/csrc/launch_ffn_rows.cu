@@ -21,20 +21,13 @@ int ffn_tmaps(const FfnCall& c, CUtensorMap* p, CUtensorMap* q) {
         const uint32_t box[3] = {64, dtc::ffn::kBK, 1};
         rc = make_tmap16_nd(p, dt, c.P, 3, dims, st, box, "features");
     } else if (c.gated) {
-        // gate and up rows alternate: dimension 1 steps from a gate row to its up row
-        const uint64_t span = E * 2 * feats - feats;
+        // octets of gate rows and of up rows alternate: {K, 8 rows, gate or up, octets, K-chunks}
+        const uint64_t octets = (E * 2 * feats - feats) / 8;
         const uint64_t row = (uint64_t)c.ldp * 2;
-        if (c.args.p_deep) {
-            const uint64_t dims[4] = {64, 2, span, red / 64};
-            const uint64_t st[3] = {feats * row, row, 128};
-            const uint32_t box[4] = {64, 2, 64, 2};
-            rc = make_tmap16_nd(p, dt, c.P, 4, dims, st, box, "features");
-        } else {
-            const uint64_t dims[3] = {red, 2, span};
-            const uint64_t st[2] = {feats * row, row};
-            const uint32_t box[3] = {64, 2, 64};
-            rc = make_tmap16_nd(p, dt, c.P, 3, dims, st, box, "features");
-        }
+        const uint64_t dims[5] = {c.args.p_deep ? 64 : red, 8, 2, octets, red / 64};
+        const uint64_t st[4] = {row, feats * row, 8 * row, 128};
+        const uint32_t box[5] = {64, 8, 2, 8, 2};
+        rc = make_tmap16_nd(p, dt, c.P, c.args.p_deep ? 5 : 4, dims, st, box, "features");
     } else if (c.args.p_deep) {
         rc = make_tmap_kchunks(p, dt, 2, c.P, red, E * feats, c.ldp, 128, "features");
     } else {

@@ -99,63 +99,45 @@ int launch_moe_plan(const int* indices, int64_t T, int k, int64_t E, int32_t* pl
     return launch_chain(dtc::moe_plan_kernel, dim3(ctas), dtc::kPlanThreads, smem, ctas, false, stream, a);
 }
 
-int launch_moe_gather(const void* x, const int32_t* plan, const moe_plan_info& l, int k, int64_t E,
-                      int64_t H, void* out, uint32_t* zero, int zero_words, DeviceInfo* dev,
-                      cudaStream_t stream) {
-    dtc::RowsArgs a = {};
-    a.in = static_cast<const uint16_t*>(x);
-    a.out = static_cast<uint16_t*>(out);
+int launch_moe_gather(const GatherCall& c, const int32_t* plan, const moe_plan_info& l, int k, int64_t E,
+                      int64_t H, DeviceInfo* dev, cudaStream_t stream) {
+    dtc::RowsArgs a;
+    a.in = static_cast<const uint16_t*>(c.x);
+    a.out = static_cast<uint16_t*>(c.out);
     a.rows = plan + l.rows;
-    a.slots = plan + l.slots;
     a.end = plan + l.offsets + E;
     a.k = k;
     a.H8 = (int)(H / 8);
-    a.zero = zero;
-    a.zero_words = zero_words;
+    a.weights = c.weights;
+    a.wtype = c.wtype;
+    a.scale = c.scale;
+    a.zero = c.zero;
+    a.zero_words = c.zero_words;
     return launch_chain(dtc::moe_gather_kernel, dim3(rows_grid(l.capacity, dev)), dtc::kRowsThreads, 0,
                         1, false, stream, a);
 }
 
-int launch_moe_spread(bool bf16, int wdtype, const void* dy, const void* ys, const void* weights,
-                      const int32_t* plan, const moe_plan_info& l, int64_t T, int k, int64_t E,
-                      int64_t H, void* dys, void* dweights, uint32_t* zero, int zero_words,
-                      DeviceInfo* dev, cudaStream_t stream) {
-    dtc::RowsArgs a = {};
-    a.in = static_cast<const uint16_t*>(dy);
-    a.out = static_cast<uint16_t*>(dys);
-    a.rows = plan + l.rows;
-    a.slots = plan + l.slots;
-    a.end = plan + l.offsets + E;
-    a.T = T;
-    a.k = k;
-    a.H8 = (int)(H / 8);
-    a.y = static_cast<const uint16_t*>(ys);
-    a.weights = weights;
-    a.dweights = dweights;
-    a.wtype = wdtype;
-    a.zero = zero;
-    a.zero_words = zero_words;
-    const dim3 grid(rows_grid(l.capacity, dev));
-    return bf16 ? launch_chain(dtc::moe_spread_kernel<true>, grid, dtc::kRowsThreads, 0, 1, false, stream, a)
-                : launch_chain(dtc::moe_spread_kernel<false>, grid, dtc::kRowsThreads, 0, 1, false, stream, a);
-}
-
-int launch_moe_join(bool bf16, int wdtype, const void* rows, const void* weights,
-                    const int32_t* slots, const void* residual, void* out, int64_t T, int k,
-                    int64_t H, DeviceInfo* dev, cudaStream_t stream) {
+int launch_moe_join(bool bf16, const JoinCall& c, const int32_t* plan, const moe_plan_info& l, int64_t T,
+                    int k, int64_t E, int64_t H, DeviceInfo* dev, cudaStream_t stream) {
     dtc::JoinArgs a;
-    a.rows = static_cast<const uint16_t*>(rows);
-    a.weights = weights;
-    a.wtype = wdtype;
-    a.slots = slots;
-    a.residual = static_cast<const uint16_t*>(residual);
-    a.out = static_cast<uint16_t*>(out);
+    a.rows = static_cast<const uint16_t*>(c.rows);
+    a.slots = plan + l.slots;
+    a.residual = static_cast<const uint16_t*>(c.residual);
+    a.out = static_cast<uint16_t*>(c.out);
     a.T = T;
     a.k = k;
     a.H8 = (int)(H / 8);
-    const dim3 grid(rows_grid(T * ((a.H8 + 31) / 32), dev));
-    return bf16 ? launch_chain(dtc::moe_join_kernel<true>, grid, dtc::kRowsThreads, 0, 1, false, stream, a)
-                : launch_chain(dtc::moe_join_kernel<false>, grid, dtc::kRowsThreads, 0, 1, false, stream, a);
+    a.items = c.out ? T * ((a.H8 + 31) / 32) : 0;
+    a.dots = c.dots;
+    a.parts = c.parts;
+    a.ld = l.capacity;
+    a.choice = plan + l.rows;
+    a.end = plan + l.offsets + E;
+    a.dweights = c.dweights;
+    a.wtype = c.wtype;
+    const dim3 grid(rows_grid(std::max<int64_t>(a.items, c.dweights ? (l.capacity + 31) / 32 : 0), dev));
+    return bf16 ? launch_chain(dtc::moe_join_kernel<true>, grid, dtc::kRowsThreads, 0, 1, true, stream, a)
+                : launch_chain(dtc::moe_join_kernel<false>, grid, dtc::kRowsThreads, 0, 1, true, stream, a);
 }
 
 }  // namespace dtc_host

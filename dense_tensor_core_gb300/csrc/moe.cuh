@@ -423,19 +423,15 @@ __global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_kernel(const PlanArg
 // Movement of rows, bound by HBM. A warp per row, 16 bytes a lane.
 // ------------------------------------------------------------------------------------------------
 struct RowsArgs {
-    const uint16_t* in;   // gather: x [T,H]; spread: dy [T,H]
+    const uint16_t* in;   // [T,H]
     uint16_t* out;        // rows in expert order
     const int* rows;
-    const int* slots;
     const int* end;       // offsets[E]
-    int64_t T;
     int k;
     int H8;               // 16-byte pieces of a row
-    // spread
-    const uint16_t* y;    // the second product's rows
-    const void* weights;
-    void* dweights;
+    const void* weights;  // [T,k]; NULL: no scale
     int wtype;
+    float* scale;         // [rows]: each row's weight, 0 in gap rows
     // counters to clear for the products behind this kernel
     uint32_t* zero;
     int zero_words;
@@ -453,6 +449,7 @@ __global__ void __launch_bounds__(kRowsThreads) moe_gather_kernel(const RowsArgs
     const int64_t end = __ldg(a.end);
     for (int64_t r = tid >> 5; r < end; r += warps) {
         const int i = __ldg(a.rows + r);
+        if (a.weights && lane == 0) a.scale[r] = i < 0 ? 0.0f : load_w(a.weights, i, a.wtype);
         uint4* const d = reinterpret_cast<uint4*>(a.out) + r * a.H8;
         if (i < 0) {
             for (int c = lane; c < a.H8; c += 32) d[c] = make_uint4(0, 0, 0, 0);
@@ -464,59 +461,29 @@ __global__ void __launch_bounds__(kRowsThreads) moe_gather_kernel(const RowsArgs
     }
 }
 
-template <bool kBF16>
-__global__ void __launch_bounds__(kRowsThreads) moe_spread_kernel(const RowsArgs a) {
-    using namespace ffn;
-    const int64_t tid = (int64_t)blockIdx.x * kRowsThreads + threadIdx.x;
-    const int64_t threads = (int64_t)gridDim.x * kRowsThreads;
-    for (int64_t i = tid; i < a.zero_words; i += threads) a.zero[i] = 0u;
-    for (int64_t i = tid; i < a.T * a.k; i += threads)  // choices that are none
-        if (a.slots[i] < 0) store_w(a.dweights, i, 0.0f, a.wtype);
-    const int lane = threadIdx.x & 31;
-    const int64_t end = __ldg(a.end);
-    for (int64_t r = tid >> 5; r < end; r += threads >> 5) {
-        const int i = __ldg(a.rows + r);
-        uint4* const d = reinterpret_cast<uint4*>(a.out) + r * a.H8;
-        if (i < 0) {
-            for (int c = lane; c < a.H8; c += 32) d[c] = make_uint4(0, 0, 0, 0);
-            continue;
-        }
-        const uint4* const g = reinterpret_cast<const uint4*>(a.in) + (int64_t)(i / a.k) * a.H8;
-        const uint4* const y = reinterpret_cast<const uint4*>(a.y) + r * a.H8;
-        const float w = load_w(a.weights, i, a.wtype);
-        float dot = 0.0f;
-#pragma unroll 4
-        for (int c = lane; c < a.H8; c += 32) {
-            float u[8], v[8];
-            unpack8<kBF16>(__ldg(g + c), u);
-            unpack8<kBF16>(__ldcs(y + c), v);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                dot = fmaf(u[j], v[j], dot);
-                u[j] *= w;
-            }
-            d[c] = pack8<kBF16>(u);
-        }
-        dot = warp_sum(dot);
-        if (lane == 0) store_w(a.dweights, i, dot, a.wtype);
-    }
-}
-
 struct JoinArgs {
     const uint16_t* rows;
-    const void* weights;  // NULL: 1
-    int wtype;
     const int* slots;
     const uint16_t* residual;
     uint16_t* out;
     int64_t T;
+    int64_t items;   // 256-column pieces of all tokens; 0: no join
     int k;
     int H8;
+    // gradient of the weights: pieces of each row's dot product, [parts][ld]
+    const float* dots;
+    int parts;
+    int64_t ld;
+    const int* choice;  // the plan's rows
+    const int* end;
+    void* dweights;
+    int wtype;
 };
 
-// out[t] = residual[t] + sum_j w_j rows[slot_j], in the order of j, fp32, one rounding. A warp
-// takes a run of 32 x 8 columns of a token; lane j holds choice j's row and weight and hands them
-// round. Four rows' pieces are in flight at a time.
+// out[t] = residual[t] + sum_j rows[slot_j], in the order of j, fp32, one rounding. A warp takes
+// 256 columns of a token; lane j holds choice j's row and hands it round. Four rows' pieces are in
+// flight at a time. In the backward pass the kernel also adds up the weights' gradients, whose
+// pieces the products' epilogues left per row.
 template <bool kBF16>
 __global__ void __launch_bounds__(kRowsThreads) moe_join_kernel(const JoinArgs a) {
     using namespace ffn;
@@ -524,28 +491,34 @@ __global__ void __launch_bounds__(kRowsThreads) moe_join_kernel(const JoinArgs a
     grid_dependency_wait();
     const int lane = threadIdx.x & 31;
     const int pieces = (a.H8 + 31) / 32;
-    const int64_t items = a.T * pieces;
-    const int64_t warps = (int64_t)gridDim.x * (kRowsThreads / 32);
-    for (int64_t it = ((int64_t)blockIdx.x * kRowsThreads + threadIdx.x) >> 5; it < items; it += warps) {
+    const int64_t tid = (int64_t)blockIdx.x * kRowsThreads + threadIdx.x;
+    const int64_t threads = (int64_t)gridDim.x * kRowsThreads;
+    if (a.dweights) {
+        for (int64_t i = tid; i < a.T * a.k; i += threads)  // choices that are none
+            if (a.slots[i] < 0) store_w(a.dweights, i, 0.0f, a.wtype);
+        const int64_t end = __ldg(a.end);
+        for (int64_t r = tid; r < end; r += threads) {
+            const int i = a.choice[r];
+            if (i < 0) continue;
+            float s = 0.0f;
+#pragma unroll 8
+            for (int p = 0; p < a.parts; ++p) s += __ldg(a.dots + p * a.ld + r);
+            store_w(a.dweights, i, s, a.wtype);
+        }
+    }
+    for (int64_t it = tid >> 5; it < a.items; it += threads >> 5) {
         const int64_t t = it / pieces;
         const int c = (int)(it - t * pieces) * 32 + lane;
-        int slot = -1;
-        float w = 0.0f;
-        if (lane < a.k) {
-            slot = a.slots[t * a.k + lane];
-            if (slot >= 0) w = a.weights ? load_w(a.weights, t * a.k + lane, a.wtype) : 1.0f;
-        }
+        const int slot = lane < a.k ? a.slots[t * a.k + lane] : -1;
         float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         if (a.residual && c < a.H8)
             unpack8<kBF16>(__ldg(reinterpret_cast<const uint4*>(a.residual) + t * a.H8 + c), s);
         for (int j0 = 0; j0 < a.k; j0 += 4) {
             uint4 v[4];
-            float wj[4];
             bool on[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int src = __shfl_sync(kFull, slot, (j0 + j) & 31);
-                wj[j] = __shfl_sync(kFull, w, (j0 + j) & 31);
                 on[j] = j0 + j < a.k && src >= 0 && c < a.H8;
                 if (on[j]) v[j] = __ldcs(reinterpret_cast<const uint4*>(a.rows) + (int64_t)src * a.H8 + c);
             }
@@ -555,7 +528,7 @@ __global__ void __launch_bounds__(kRowsThreads) moe_join_kernel(const JoinArgs a
                 float x[8];
                 unpack8<kBF16>(v[j], x);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) s[i] = fmaf(wj[j], x[i], s[i]);
+                for (int i = 0; i < 8; ++i) s[i] += x[i];
             }
         }
         if (c < a.H8) reinterpret_cast<uint4*>(a.out)[t * a.H8 + c] = pack8<kBF16>(s);

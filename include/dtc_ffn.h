@@ -171,7 +171,8 @@ typedef struct {
     uint64_t bytes;  /* size of the buffer */
     uint64_t x;      /* [capacity, H]: the tokens' rows */
     uint64_t z;      /* [capacity, F or 2F]: the first product (training only) */
-    uint64_t h;      /* [capacity, F]: its activation */
+    uint64_t h;      /* [capacity, F]: its activation times the row's weight */
+    uint64_t scale;  /* [capacity] fp32: each row's weight */
     uint64_t y;      /* [capacity, H]: the second product */
     uint64_t split;  /* counters and partial sums of split products */
 } moe_experts_info;
@@ -189,8 +190,9 @@ int moe_experts_layout(int dtype, int64_t T, int k, int64_t E, int64_t H, int64_
  * [T,k]; plan as moe_plan wrote it for the indices. The rows are gathered into expert order, both
  * products run over each expert's rows (experts without rows cost nothing), and the join sums a
  * token's k rows in the order of j. `buffer` (moe_experts_layout bytes, 16-byte aligned, no initial
- * contents needed) holds the rows; with train non-zero moe_experts_backward reads it. The rows of
- * the activation and of the second product are rounded to the operands' type.
+ * contents needed) holds the rows; with train non-zero moe_experts_backward reads it. A choice's
+ * weight multiplies its activation in fp32; that product and the rows of the second product are
+ * rounded to the operands' type (the tensor cores' operand, and half the bytes of fp32 rows).
  * A choice with index -1 adds nothing; T == 0 does nothing. INVALID_ARG as moe_experts_layout, for
  * missing or misaligned pointers. The pages have no counterpart.
  */
