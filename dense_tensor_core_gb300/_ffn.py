@@ -7,8 +7,7 @@ import functools
 import torch
 
 from . import _binding
-from ._binding import (_check, _check_tensor, _DTYPE, _layout_code, _layout_name, _ld, _ptr,
-                       _same_device, _stream_handle)
+from ._binding import _check, _check_tensor, _DTYPE, _layout_code, _layout_name, _ld
 
 _ACT = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "swiglu": 5, "geglu": 6}
 _GATED = ("swiglu", "geglu")
@@ -33,7 +32,7 @@ class moe_route_options(ctypes.Structure):
 
 class moe_plan_info(ctypes.Structure):
     _fields_ = [(n, _i64) for n in ("words", "offsets", "counts", "slots", "rows", "tiles",
-                                    "capacity", "max_tiles")]
+                                    "scratch", "capacity", "max_tiles")]
 
 
 class moe_experts_options(ctypes.Structure):
@@ -80,15 +79,42 @@ def _L():
     return _lib
 
 
-def _call(dev, stream, name, *args):
+# The current stream's handle without building a Stream object (several microseconds).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call(dev, stream, f, *args):
     """The C call on `dev` (made current where it is not) and the given or current stream, which
     is the last argument of every entry point that enqueues work."""
-    f = getattr(_L(), name)
-    if torch.cuda.current_device() == dev.index:
-        _check(f(*args, _stream_handle(stream, dev)))
+    index = dev.index
+    handle = _raw_stream(index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        status = f(*args, handle)
     else:
         with torch.cuda.device(dev):
-            _check(f(*args, _stream_handle(stream, dev)))
+            status = f(*args, handle)
+    if status:
+        _check(status)
+
+
+def _mat(t, dt, name, dev):
+    """Checks a 2-D operand that may be rows of a larger row-major array; its leading dimension (0:
+    dense)."""
+    if t.dtype is not dt or t.device != dev or not t.is_contiguous() or not t.is_cuda:
+        _check_tensor(t, dt, name, True)
+        if t.device != dev:
+            raise ValueError(f"all tensors must be on one CUDA device, got {name} on {t.device} "
+                             f"and others on {dev}")
+        return _ld(t)
+    return 0
+
+
+def _dense(t, dt, name, dev):
+    if t.dtype is not dt or t.device != dev or not t.is_contiguous() or not t.is_cuda:
+        _check_tensor(t, dt, name)
+        raise ValueError(f"all tensors must be on one CUDA device, got {name} on {t.device} and "
+                         f"others on {dev}")
 
 
 def _act_code(activation):
@@ -104,29 +130,41 @@ def _kind_dtype(kind):
 
 
 def _shape(t, shape, name):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
 
 
+# layout: (code, A stored [K,M], B stored [N,K])
+_LAYOUT = {"NT": (0, False, True), "NN": (1, False, False), "TN": (2, True, False),
+           "TT": (3, True, True)}
+
+
 def _act_shapes(A, B, layout, gated):
-    """(M, N, K, stored columns of Bop) of a gemm_act call."""
+    """(layout code, M, N, K, stored columns of Bop) of a gemm_act call."""
     if A.dim() != 2 or B.dim() != 2:
         raise ValueError("A and B must be 2-D")
-    name = _layout_name(layout)
-    K, M = A.shape if name[0] == "T" else A.shape[::-1]
-    Nb, Kb = B.shape if name[1] == "T" else B.shape[::-1]
+    found = _LAYOUT.get(layout)
+    if found is None:
+        found = _LAYOUT[_layout_name(layout)]
+    code, a_t, b_t = found
+    M, K = A.shape
+    if a_t:
+        M, K = K, M
+    Nb, Kb = B.shape
+    if not b_t:
+        Nb, Kb = Kb, Nb
     if Kb != K:
-        raise ValueError(f"inner sizes differ: A is {tuple(A.shape)}, B is {tuple(B.shape)} ({name})")
+        raise ValueError(f"inner sizes differ: A is {tuple(A.shape)}, B is {tuple(B.shape)} ({layout})")
     if gated and Nb % 2:
         raise ValueError(f"a gated activation needs an even number of columns, got {Nb}")
-    return M, Nb // 2 if gated else Nb, K, Nb
+    return code, M, Nb // 2 if gated else Nb, K, Nb
 
 
-def _ws(workspace):
+def _ws(workspace, dev):
     if workspace is None:
         return None, 0
-    if not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor of the operands' device")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -154,29 +192,33 @@ def gemm_act(kind, A, B, C=None, layout="NT", bias=None, residual=None, activati
     residual."""
     dt = _kind_dtype(kind)
     act = _act_code(activation)
-    _check_tensor(A, dt, "A", True)
-    _check_tensor(B, dt, "B", True)
-    M, N, K, Nb = _act_shapes(A, B, layout, activation in _GATED)
+    dev = A.device
+    lda, ldb = _mat(A, dt, "A", dev), _mat(B, dt, "B", dev)
+    code, M, N, K, Nb = _act_shapes(A, B, layout, activation in _GATED)
+    ldc = ldr = ldz = 0
+    bias_p = res_p = pre_p = None
     if C is None:
-        C = torch.empty((M, N), dtype=dt, device=A.device)
+        C = torch.empty((M, N), dtype=dt, device=dev)
     else:
-        _check_tensor(C, dt, "C", True)
+        ldc = _mat(C, dt, "C", dev)
         _shape(C, (M, N), "C")
     if bias is not None:
-        _check_tensor(bias, dt, "bias")
+        _dense(bias, dt, "bias", dev)
         _shape(bias, (Nb,), "bias")
+        bias_p = _addr(bias)
     if residual is not None:
-        _check_tensor(residual, dt, "residual", True)
+        ldr = _mat(residual, dt, "residual", dev)
         _shape(residual, (M, N), "residual")
+        res_p = _addr(residual)
     if preact is not None:
-        _check_tensor(preact, dt, "preact", True)
+        ldz = _mat(preact, dt, "preact", dev)
         _shape(preact, (M, Nb), "preact")
-    ws, ws_bytes = _ws(workspace)
-    o = gemm_act_options(act, _addr(bias), _addr(residual), _addr(preact), _ld(A), _ld(B), _ld(C),
-                         _ld(residual), _ld(preact), ws, ws_bytes, timeout_ns, fault_inject)
-    dev = _same_device(A, B, C, bias, residual, preact, workspace)
-    _call(dev, stream, "gemm_act", _DTYPE[kind], _ptr(A), _ptr(B), _ptr(C), M, N, K,
-          _layout_code(layout), ctypes.byref(o))
+        pre_p = _addr(preact)
+    ws, ws_bytes = _ws(workspace, dev)
+    o = gemm_act_options(act, bias_p, res_p, pre_p, lda, ldb, ldc, ldr, ldz, ws, ws_bytes,
+                         timeout_ns, fault_inject)
+    _call(dev, stream, _L().gemm_act, _DTYPE[kind], _addr(A), _addr(B), _addr(C), M, N, K, code,
+          ctypes.byref(o))
     return C
 
 
@@ -196,30 +238,28 @@ def gemm_act_backward(kind, dC, A, B, preact=None, layout="NT", activation="none
     gemm_act_backward_workspace_size bytes; allocated here when not given."""
     dt = _kind_dtype(kind)
     act = _act_code(activation)
-    for t, name in ((dC, "dC"), (A, "A"), (B, "B")):
-        _check_tensor(t, dt, name, True)
-    M, N, K, Nb = _act_shapes(A, B, layout, activation in _GATED)
+    dev = dC.device
+    ldc, lda, ldb = (_mat(t, dt, name, dev) for t, name in ((dC, "dC"), (A, "A"), (B, "B")))
+    code, M, N, K, Nb = _act_shapes(A, B, layout, activation in _GATED)
     _shape(dC, (M, N), "dC")
+    pre_p, ldz = None, 0
     if act:
         if preact is None:
             raise ValueError(f"the gradient of {activation} needs preact")
-        _check_tensor(preact, dt, "preact", True)
+        ldz = _mat(preact, dt, "preact", dev)
         _shape(preact, (M, Nb), "preact")
-    else:
-        preact = None
-    dev = _same_device(dC, A, B, preact, workspace)
+        pre_p = _addr(preact)
     if workspace is None:
         with torch.cuda.device(dev):
             n = gemm_act_backward_workspace_size(kind, M, N, K, layout, activation)
         workspace = torch.zeros(max(n, 16), dtype=torch.uint8, device=dev)
-    ws, ws_bytes = _ws(workspace)
+    ws, ws_bytes = _ws(workspace, dev)
     dA = torch.empty(A.shape, dtype=dt, device=dev) if need[0] else None
     dB = torch.empty(B.shape, dtype=dt, device=dev) if need[1] else None
     db = torch.empty((Nb,), dtype=torch.float32, device=dev) if need[2] else None
-    o = gemm_act_options(act, None, None, _addr(preact), _ld(A), _ld(B), _ld(dC), 0, _ld(preact),
-                         ws, ws_bytes, timeout_ns, 0)
-    _call(dev, stream, "gemm_act_backward", _DTYPE[kind], _ptr(dC), _ptr(A), _ptr(B), _ptr(dA),
-          _ptr(dB), _ptr(db), M, N, K, _layout_code(layout), ctypes.byref(o))
+    o = gemm_act_options(act, None, None, pre_p, lda, ldb, ldc, 0, ldz, ws, ws_bytes, timeout_ns, 0)
+    _call(dev, stream, _L().gemm_act_backward, _DTYPE[kind], _addr(dC), _addr(A), _addr(B),
+          _addr(dA), _addr(dB), _addr(db), M, N, K, code, ctypes.byref(o))
     return dA, dB, db
 
 
@@ -227,15 +267,15 @@ def gemm_act_backward(kind, dC, A, B, preact=None, layout="NT", activation="none
 # routing
 # ------------------------------------------------------------------------------------------------
 def _route_args(logits, top_k, scoring, groups, top_groups, renormalize, scale):
-    if logits.dtype not in _FLOAT_CODE:
+    code = _FLOAT_CODE.get(logits.dtype)
+    if code is None:
         raise TypeError(f"logits must be bf16, fp16 or fp32, got {logits.dtype}")
     if logits.dim() != 2:
         raise ValueError("logits must be [T, E]")
-    _check_tensor(logits, logits.dtype, "logits", True)
     if scoring not in _SCORING:
         raise ValueError(f"unknown scoring {scoring!r}: softmax or sigmoid")
-    return moe_route_options(top_k, _SCORING[scoring], groups, top_groups, int(bool(renormalize)),
-                             scale)
+    return code, _mat(logits, logits.dtype, "logits", logits.device), moe_route_options(
+        top_k, _SCORING[scoring], groups, top_groups, 1 if renormalize else 0, scale)
 
 
 def moe_route(logits, top_k, bias=None, scoring="softmax", groups=1, top_groups=1,
@@ -246,24 +286,24 @@ def moe_route(logits, top_k, bias=None, scoring="softmax", groups=1, top_groups=
     the lowest index; weights come from the logits alone, over the choices (renormalize) or over all
     experts, times scale. Logits of -infinity or NaN are masked; where fewer than k experts can be
     chosen the rest are index -1 with weight 0."""
-    o = _route_args(logits, top_k, scoring, groups, top_groups, renormalize, scale)
+    code, ld, o = _route_args(logits, top_k, scoring, groups, top_groups, renormalize, scale)
     T, E = logits.shape
+    dev = logits.device
     if bias is not None:
-        _check_tensor(bias, torch.float32, "bias")
+        _dense(bias, torch.float32, "bias", dev)
         _shape(bias, (E,), "bias")
     if weights is None:
-        weights = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
+        weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
     else:
-        _check_tensor(weights, torch.float32, "weights")
+        _dense(weights, torch.float32, "weights", dev)
         _shape(weights, (T, top_k), "weights")
     if indices is None:
-        indices = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
+        indices = torch.empty((T, top_k), dtype=torch.int32, device=dev)
     else:
-        _check_tensor(indices, torch.int32, "indices")
+        _dense(indices, torch.int32, "indices", dev)
         _shape(indices, (T, top_k), "indices")
-    dev = _same_device(logits, bias, weights, indices)
-    _call(dev, stream, "moe_route", _FLOAT_CODE[logits.dtype], _ptr(logits), _ld(logits),
-          _ptr(bias), T, E, ctypes.byref(o), _ptr(weights), _ptr(indices))
+    _call(dev, stream, _L().moe_route, code, _addr(logits), ld, _addr(bias), T, E, ctypes.byref(o),
+          _addr(weights), _addr(indices))
     return weights, indices
 
 
@@ -274,16 +314,16 @@ def moe_route_backward(dweights, logits, indices, scoring="softmax", renormalize
     if indices.dim() != 2:
         raise ValueError("indices must be [T, k]")
     k = indices.shape[1]
-    o = _route_args(logits, k, scoring, 1, 1, renormalize, scale)
+    code, ld, o = _route_args(logits, k, scoring, 1, 1, renormalize, scale)
     T, E = logits.shape
-    _check_tensor(indices, torch.int32, "indices")
-    _check_tensor(dweights, torch.float32, "dweights")
+    dev = logits.device
+    _dense(indices, torch.int32, "indices", dev)
+    _dense(dweights, torch.float32, "dweights", dev)
     _shape(indices, (T, k), "indices")
     _shape(dweights, (T, k), "dweights")
-    dev = _same_device(dweights, logits, indices)
     out = torch.empty((T, E), dtype=logits.dtype, device=dev)
-    _call(dev, stream, "moe_route_backward", _FLOAT_CODE[logits.dtype], _ptr(dweights),
-          _ptr(logits), _ld(logits), _ptr(indices), T, E, ctypes.byref(o), _ptr(out))
+    _call(dev, stream, _L().moe_route_backward, code, _addr(dweights), _addr(logits), ld,
+          _addr(indices), T, E, ctypes.byref(o), _addr(out))
     return out
 
 
@@ -332,13 +372,14 @@ class MoePlan:
 def moe_plan(indices, experts, stream=None):
     """Puts the choices [T,k] int32 (outside 0 .. experts-1: no choice) in expert order, stable in
     the order of the tokens: a MoePlan."""
-    _check_tensor(indices, torch.int32, "indices")
+    dev = indices.device
+    _dense(indices, torch.int32, "indices", dev)
     if indices.dim() != 2:
         raise ValueError("indices must be [T, k]")
     T, k = indices.shape
     layout = _plan_layout(T, k, experts)
-    data = torch.empty(layout.words, dtype=torch.int32, device=indices.device)
-    _call(indices.device, stream, "moe_plan", _ptr(indices), T, k, experts, data.data_ptr())
+    data = torch.empty(layout.words, dtype=torch.int32, device=dev)
+    _call(dev, stream, _L().moe_plan, _addr(indices), T, k, experts, data.data_ptr())
     return MoePlan(data, layout, T, k, experts)
 
 
@@ -360,9 +401,10 @@ def _experts_layout(device_index, dtype, T, k, E, H, F, act, train):
 def _experts_args(kind, x, w_in, w_out, weights, plan, activation, name):
     dt = _kind_dtype(kind)
     act = _act_code(activation)
-    _check_tensor(x, dt, name)
-    _check_tensor(w_in, dt, "w_in")
-    _check_tensor(w_out, dt, "w_out")
+    dev = x.device
+    _dense(x, dt, name, dev)
+    _dense(w_in, dt, "w_in", dev)
+    _dense(w_out, dt, "w_out", dev)
     if x.dim() != 2 or w_in.dim() != 3 or w_out.dim() != 3:
         raise ValueError(f"{name} must be [T, H], w_in [E, F, H] (gated [E, 2F, H]), w_out [E, H, F]")
     T, H = x.shape
@@ -372,11 +414,14 @@ def _experts_args(kind, x, w_in, w_out, weights, plan, activation, name):
     if plan.tokens != T or plan.experts != E:
         raise ValueError(f"the plan is for {plan.tokens} tokens and {plan.experts} experts, not "
                          f"{T} and {E}")
-    if weights.dtype not in _FLOAT_CODE:
+    wcode = _FLOAT_CODE.get(weights.dtype)
+    if wcode is None:
         raise TypeError(f"weights must be bf16, fp16 or fp32, got {weights.dtype}")
-    _check_tensor(weights, weights.dtype, "weights")
+    _dense(weights, weights.dtype, "weights", dev)
     _shape(weights, (T, plan.top_k), "weights")
-    return dt, act, T, E, H, F
+    if plan.data.device != dev:
+        raise ValueError(f"the plan is on {plan.data.device}, the tensors on {dev}")
+    return dt, dev, act, wcode, T, E, H, F
 
 
 def moe_experts(kind, x, w_in, w_out, weights, plan, activation="swiglu", residual=None, out=None,
@@ -385,22 +430,21 @@ def moe_experts(kind, x, w_in, w_out, weights, plan, activation="swiglu", residu
     token t in `plan` (moe_plan). x [T,H]; w_in [E, F, H] (gated: [E, 2F, H], gate rows first);
     w_out [E, H, F]; weights [T,k] bf16, fp16 or fp32. Experts without tokens cost nothing. With
     save, returns (y, saved) where saved is what moe_experts_backward needs."""
-    dt, act, T, E, H, F = _experts_args(kind, x, w_in, w_out, weights, plan, activation, "x")
+    dt, dev, act, wcode, T, E, H, F = _experts_args(kind, x, w_in, w_out, weights, plan, activation,
+                                                    "x")
     if residual is not None:
-        _check_tensor(residual, dt, "residual")
+        _dense(residual, dt, "residual", dev)
         _shape(residual, (T, H), "residual")
     if out is None:
-        out = torch.empty((T, H), dtype=dt, device=x.device)
+        out = torch.empty((T, H), dtype=dt, device=dev)
     else:
-        _check_tensor(out, dt, "out")
+        _dense(out, dt, "out", dev)
         _shape(out, (T, H), "out")
-    dev = _same_device(x, w_in, w_out, weights, plan.data, residual, out)
     nbytes, _ = _experts_layout(dev.index, _DTYPE[kind], T, plan.top_k, E, H, F, act, int(save))
     buffer = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    o = moe_experts_options(act, _FLOAT_CODE[weights.dtype], _addr(residual), timeout_ns,
-                            fault_inject)
-    _call(dev, stream, "moe_experts", _DTYPE[kind], _ptr(x), _ptr(w_in), _ptr(w_out), _ptr(weights),
-          plan.data.data_ptr(), _ptr(out), T, plan.top_k, E, H, F, ctypes.byref(o), int(save),
+    o = moe_experts_options(act, wcode, _addr(residual), timeout_ns, fault_inject)
+    _call(dev, stream, _L().moe_experts, _DTYPE[kind], _addr(x), _addr(w_in), _addr(w_out),
+          _addr(weights), plan.data.data_ptr(), _addr(out), T, plan.top_k, E, H, F, ctypes.byref(o), int(save),
           buffer.data_ptr())
     return (out, buffer) if save else out
 
@@ -409,18 +453,18 @@ def moe_experts_backward(kind, dy, w_in, w_out, weights, plan, saved, activation
                          need_weights=True, need_x=True, timeout_ns=0, stream=None):
     """(dx, dw_in, dw_out, dweights) of moe_experts from dy [T,H] and what it saved; dw_in and
     dw_out are None without need_weights, dx without need_x. The gradient of a residual is dy."""
-    dt, act, T, E, H, F = _experts_args(kind, dy, w_in, w_out, weights, plan, activation, "dy")
-    dev = _same_device(dy, w_in, w_out, weights, plan.data, saved)
+    dt, dev, act, wcode, T, E, H, F = _experts_args(kind, dy, w_in, w_out, weights, plan, activation,
+                                                    "dy")
     nbytes, back = _experts_layout(dev.index, _DTYPE[kind], T, plan.top_k, E, H, F, act, 1)
-    if saved.dtype != torch.uint8 or saved.numel() != nbytes:
+    if saved.dtype != torch.uint8 or saved.numel() != nbytes or saved.device != dev:
         raise ValueError("saved is not what moe_experts returned for these sizes with save=True")
     ws = torch.empty(back, dtype=torch.uint8, device=dev)
     dx = torch.empty((T, H), dtype=dt, device=dev) if need_x else None
     dwi = torch.empty(w_in.shape, dtype=dt, device=dev) if need_weights else None
     dwo = torch.empty(w_out.shape, dtype=dt, device=dev) if need_weights else None
     dw = torch.empty(weights.shape, dtype=weights.dtype, device=dev)
-    o = moe_experts_options(act, _FLOAT_CODE[weights.dtype], None, timeout_ns, 0)
-    _call(dev, stream, "moe_experts_backward", _DTYPE[kind], _ptr(dy), _ptr(w_in), _ptr(w_out),
-          _ptr(weights), plan.data.data_ptr(), saved.data_ptr(), _ptr(dx), _ptr(dwi), _ptr(dwo),
-          _ptr(dw), T, plan.top_k, E, H, F, ctypes.byref(o), ws.data_ptr(), back)
+    o = moe_experts_options(act, wcode, None, timeout_ns, 0)
+    _call(dev, stream, _L().moe_experts_backward, _DTYPE[kind], _addr(dy), _addr(w_in), _addr(w_out),
+          _addr(weights), plan.data.data_ptr(), _addr(saved), _addr(dx), _addr(dwi), _addr(dwo),
+          _addr(dw), T, plan.top_k, E, H, F, ctypes.byref(o), ws.data_ptr(), back)
     return dx, dwi, dwo, dw

@@ -44,33 +44,46 @@ __global__ void __launch_bounds__(kActBackThreads) act_backward_kernel(const Act
 #pragma unroll
     for (int i = 0; i < 8 * kSets; ++i) s[i / 8][i % 8] = 0.0f;
     if (on) {
-#pragma unroll 2
-        for (int64_t r = r0 + rl; r < r1; r += kActBackLanes) {
-            float x[8];
-            unpack8<kBF16>(__ldcs(reinterpret_cast<const uint4*>(a.dC + r * a.ldc + col)), x);
-            if (a.z) {
-                float v[8], d[8];
-                unpack8<kBF16>(__ldcs(reinterpret_cast<const uint4*>(a.z + r * a.ldz + col)), v);
-                act_both(v, d, act_of_gate(a.act));
-                if constexpr (kGated) {
-                    float u[8];
-                    unpack8<kBF16>(
-                        __ldcs(reinterpret_cast<const uint4*>(a.z + r * a.ldz + a.N + col)), u);
+        for (int64_t r = r0 + rl; r < r1; r += 2 * kActBackLanes) {
+            // both rows' loads first: the stores of dz could alias them for all the compiler knows
+            uint4 cx[2], cz[2], cu[2];
+            const bool two = r + kActBackLanes < r1;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        v[i] *= x[i];
-                        x[i] *= u[i] * d[i];
-                        s[1][i] += v[i];
-                    }
-                    *reinterpret_cast<uint4*>(a.dz + r * width + a.N + col) = pack8<kBF16>(v);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] *= d[i];
-                }
-                *reinterpret_cast<uint4*>(a.dz + r * width + col) = pack8<kBF16>(x);
+            for (int n = 0; n < 2; ++n) {
+                const int64_t rr = r + (n && two ? kActBackLanes : 0);
+                cx[n] = __ldcs(reinterpret_cast<const uint4*>(a.dC + rr * a.ldc + col));
+                if (a.z) cz[n] = __ldcs(reinterpret_cast<const uint4*>(a.z + rr * a.ldz + col));
+                if (kGated && a.z) cu[n] = __ldcs(reinterpret_cast<const uint4*>(a.z + rr * a.ldz + a.N + col));
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s[0][i] += x[i];
+            for (int n = 0; n < 2; ++n) {
+                if (n && !two) break;
+                const int64_t rr = r + n * kActBackLanes;
+                float x[8];
+                unpack8<kBF16>(cx[n], x);
+                if (a.z) {
+                    float v[8], d[8];
+                    unpack8<kBF16>(cz[n], v);
+                    act_both(v, d, act_of_gate(a.act));
+                    if constexpr (kGated) {
+                        float u[8];
+                        unpack8<kBF16>(cu[n], u);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            v[i] *= x[i];
+                            x[i] *= u[i] * d[i];
+                            s[1][i] += v[i];
+                        }
+                        *reinterpret_cast<uint4*>(a.dz + rr * width + a.N + col) = pack8<kBF16>(v);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] *= d[i];
+                    }
+                    *reinterpret_cast<uint4*>(a.dz + rr * width + col) = pack8<kBF16>(x);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s[0][i] += x[i];
+            }
         }
     }
     if (!a.dbias) return;

@@ -537,7 +537,8 @@ int moe_plan_layout(int64_t T, int k, int64_t E, moe_plan_info* info) {
     info->counts = info->offsets + E + 1;
     info->slots = info->counts + E;
     info->rows = info->slots + n;
-    info->words = info->rows + info->capacity;
+    info->scratch = info->rows + info->capacity;
+    info->words = info->scratch + moe_plan_scratch_words(n, E);
     return GEMM_OK;
 }
 

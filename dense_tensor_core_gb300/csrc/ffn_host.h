@@ -72,6 +72,7 @@ int launch_moe_route(const RouteCall& c, DeviceInfo* dev, cudaStream_t stream);
 int launch_moe_route_backward(const RouteCall& c, DeviceInfo* dev, cudaStream_t stream);
 int launch_moe_plan(const int* indices, int64_t T, int k, int64_t E, int32_t* plan,
                     const moe_plan_info& l, DeviceInfo* dev, cudaStream_t stream);
+int64_t moe_plan_scratch_words(int64_t choices, int64_t E);
 // Rows of x [T,H] in expert order, gap rows zero; with weights [T,k] also each row's weight in
 // `scale`; also clears `zero_words` words of counters.
 struct GatherCall {

@@ -82,21 +82,36 @@ int launch_moe_plan(const int* indices, int64_t T, int k, int64_t E, int32_t* pl
     a.indices = indices;
     a.n = (int)(T * k);
     a.E = (int)E;
-    // a CTA's 32 warps take 32 choices each at least; more CTAs only when that leaves work for them
-    int ctas = 1;
-    while (ctas < dtc::kPlanMaxCtas && (int64_t)ctas * dtc::kPlanThreads < a.n) ctas *= 2;
-    const int per_warp = ceil_div(a.n, (int64_t)ctas * dtc::kPlanWarps);
-    a.run = (per_warp + 31) / 32 * 32;
     a.num_tiles = plan;
     a.tiles = reinterpret_cast<dtc::FfnTile*>(plan + l.tiles);
     a.offsets = plan + l.offsets;
     a.counts = plan + l.counts;
     a.slots = plan + l.slots;
     a.rows = plan + l.rows;
-    const int smem = (int)((dtc::kPlanWarps + 2) * E * 4);
-    int rc = ensure_smem_attr(dtc::moe_plan_kernel, (dtc::kPlanWarps + 2) * dtc::ffn::kMaxExperts * 4, dev);
-    if (rc) return rc;
-    return launch_chain(dtc::moe_plan_kernel, dim3(ctas), dtc::kPlanThreads, smem, ctas, false, stream, a);
+    a.block_counts = plan + l.scratch;
+    // a block's 32 warps take 32 choices each at least; more blocks only when that leaves work
+    const bool few = a.n <= dtc::kPlanFew;
+    const int most = few ? dtc::kPlanMaxCtas : dtc::kPlanBlocks;
+    int blocks = 1;
+    while (blocks < most && (int64_t)blocks * dtc::kPlanThreads < a.n) blocks *= 2;
+    a.run = (ceil_div(a.n, (int64_t)blocks * dtc::kPlanWarps) + 31) / 32 * 32;
+    const int words = dtc::kPlanWarps + 3;  // of shared memory per expert
+    int rc;
+    if (few) {
+        if ((rc = ensure_smem_attr(dtc::moe_plan_kernel, words * dtc::ffn::kMaxExperts * 4, dev))) return rc;
+        return launch_chain(dtc::moe_plan_kernel, dim3(blocks), dtc::kPlanThreads, words * (int)E * 4, blocks,
+                            false, stream, a);
+    }
+    if ((rc = ensure_smem_attr(dtc::moe_plan_place_kernel, words * dtc::ffn::kMaxExperts * 4, dev))) return rc;
+    if ((rc = launch_chain(dtc::moe_plan_count_kernel, dim3(blocks), dtc::kPlanThreads, (int)E * 4, 1, false,
+                           stream, a)))
+        return rc;
+    return launch_chain(dtc::moe_plan_place_kernel, dim3(blocks), dtc::kPlanThreads, words * (int)E * 4, 1, true,
+                        stream, a);
+}
+
+int64_t moe_plan_scratch_words(int64_t choices, int64_t E) {
+    return choices > dtc::kPlanFew ? (int64_t)dtc::kPlanBlocks * E : 0;
 }
 
 int launch_moe_gather(const GatherCall& c, const int32_t* plan, const moe_plan_info& l, int k, int64_t E,

@@ -47,13 +47,18 @@ __device__ __forceinline__ float warp_max(float v) {
 // ------------------------------------------------------------------------------------------------
 // moe_route: a warp per token, the token's logits in registers (expert e = lane + 32 j).
 //
-// The choice compares keys as unsigned integers in the order of their floats, so a round of the
-// top-k is one local maximum, one warp reduction of the key and one of the index (lowest on ties);
-// 0 stands for "cannot be chosen" and is below every key. Keys are computed with the correctly
-// rounded operations and the standard exponential (not the fast forms), so that a choice between
-// near-equal keys does not depend on an approximation.
+// The choice compares keys as unsigned integers in the order of their floats; 0 stands for "cannot
+// be chosen" and is below every key. Keys are computed with the correctly rounded operations and
+// the standard exponential (not the fast forms), so that a choice between near-equal keys does not
+// depend on an approximation.
 //
-// Bound by instructions more than by HBM for large k: about 2 VPL + 20 per choice and token.
+// Top-k in two steps. The k-th largest of the 32 lanes' maxima is a lower bound of the k-th largest
+// key, and usually only a few more than k keys reach it: those are compacted, in index order, to
+// one per lane, and k rounds of one warp maximum and one ballot pick them in order (the lowest lane
+// of the ballot is the lowest index). Where ties leave more than 32, k rounds over all keys do.
+//
+// Bound by the issue of instructions, not by HBM: for 256 experts about half of them are the 8
+// exact logistic functions a lane computes.
 // ------------------------------------------------------------------------------------------------
 struct RouteArgs {
     const void* logits;
@@ -83,11 +88,13 @@ __device__ __forceinline__ float from_key(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
-__device__ __forceinline__ float sigmoid_exact(float z) { return __fdiv_rn(1.0f, 1.0f + expf(-z)); }
+__device__ __forceinline__ float sigmoid_exact(float z) { return __frcp_rn(1.0f + expf(-z)); }
 
 template <int kType, int kVPL>
 __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const RouteArgs a) {
     __shared__ uint32_t group_keys[kRouteWarps][kVPL * 32];
+    __shared__ uint32_t cands[kRouteWarps][32];
+    __shared__ uint16_t cands_at[kRouteWarps][32];
     grid_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
@@ -145,23 +152,74 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
             if (eg >= 32u || !((keep >> eg) & 1u)) key[j] = 0;
         }
     }
-    // the k largest keys; lane i keeps the i-th choice
-    int mine = -1;
-    for (int i = 0; i < a.k; ++i) {
+    // the k largest keys: lane with mine >= 0 holds choice number `place`
+    int mine = -1, place = -1, found = 0;
+    uint32_t cand = key[0];
+    int cand_at = lane;
+    bool few = true;
+    if constexpr (kVPL > 1) {
         uint32_t m = key[0];
 #pragma unroll
         for (int j = 1; j < kVPL; ++j) m = max(m, key[j]);
-        const uint32_t best = __reduce_max_sync(kFull, m);
-        if (best == 0) break;
-        unsigned at = 0xffffu;
+        uint32_t bound = 1;
+        for (int i = 0; i < a.k; ++i) {
+            const uint32_t best = __reduce_max_sync(kFull, m);
+            if (best == 0) {
+                bound = 1;
+                break;
+            }
+            bound = best;
+            if (lane == __ffs(__ballot_sync(kFull, m == best)) - 1) m = 0;
+        }
+        int n = 0;
 #pragma unroll
-        for (int j = kVPL - 1; j >= 0; --j)
-            if (key[j] == best) at = lane + 32 * j;
-        at = __reduce_min_sync(kFull, at);
-        if (lane == i) mine = (int)at;
+        for (int j = 0; j < kVPL; ++j) {
+            const bool in = key[j] >= bound;
+            const unsigned b = __ballot_sync(kFull, in);
+            const int at = n + __popc(b & ((1u << lane) - 1u));
+            if (in && at < 32) {
+                cands[warp][at] = key[j];
+                cands_at[warp][at] = (uint16_t)(lane + 32 * j);
+            }
+            n += __popc(b);
+        }
+        few = n <= 32;
+        __syncwarp();
+        cand = lane < n ? cands[warp][lane] : 0u;
+        cand_at = cands_at[warp][lane];
+    }
+    if (few) {
+        for (int i = 0; i < a.k; ++i) {
+            const uint32_t best = __reduce_max_sync(kFull, cand);
+            if (best == 0) break;
+            if (lane == __ffs(__ballot_sync(kFull, cand == best)) - 1) {
+                mine = cand_at;
+                place = i;
+                cand = 0;
+            }
+            ++found;
+        }
+    } else {
+        for (int i = 0; i < a.k; ++i) {
+            uint32_t m = key[0];
 #pragma unroll
-        for (int j = 0; j < kVPL; ++j)
-            if (lane + 32 * j == (int)at) key[j] = 0;
+            for (int j = 1; j < kVPL; ++j) m = max(m, key[j]);
+            const uint32_t best = __reduce_max_sync(kFull, m);
+            if (best == 0) break;
+            unsigned at = 0xffffu;
+#pragma unroll
+            for (int j = kVPL - 1; j >= 0; --j)
+                if (key[j] == best) at = lane + 32 * j;
+            at = __reduce_min_sync(kFull, at);
+            if (lane == i) {
+                mine = (int)at;
+                place = i;
+            }
+#pragma unroll
+            for (int j = 0; j < kVPL; ++j)
+                if (lane + 32 * j == (int)at) key[j] = 0;
+            ++found;
+        }
     }
     const bool got = mine >= 0;
     const float zi = got ? load_f<kType>(a.logits, row + mine) : -CUDART_INF_F;
@@ -189,9 +247,13 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
         total = warp_sum(total);
         w = got ? expf(zi - m) / total : 0.0f;
     }
-    if (lane < a.k) {
-        a.weights[t * a.k + lane] = w * a.scale;
-        a.indices[t * a.k + lane] = mine;
+    if (got) {
+        a.weights[t * a.k + place] = w * a.scale;
+        a.indices[t * a.k + place] = mine;
+    }
+    if (lane >= found && lane < a.k) {  // fewer than k could be chosen
+        a.weights[t * a.k + lane] = 0.0f;
+        a.indices[t * a.k + lane] = -1;
     }
 }
 
@@ -274,15 +336,21 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_backward_kernel(co
 }
 
 // ------------------------------------------------------------------------------------------------
-// moe_plan: a stable counting sort of the choices by expert in one launch. The warps of a cluster
-// (1 to 8 CTAs of 32 warps) take consecutive runs of the choices. (1) Each warp counts its run per
-// expert in shared memory. (2) Counts become exclusive prefixes over the warps of a CTA, the CTAs
-// read each other's totals through distributed shared memory, and every CTA scans the experts'
-// padded totals. (3) Each warp walks its run again, 32 choices at a time: a choice's row is its
-// expert's start plus the warp's running count plus its rank among the equal choices of its 32.
-// One launch, because for few tokens the launches would take longer than the work.
+// moe_plan: a stable counting sort of the choices by expert. Every block of 32 warps takes a
+// consecutive run of the choices and every warp a consecutive run of the block's. (1) The choices
+// are counted per expert and block. (2) The counts of the blocks before a block and of all blocks
+// give the block its first row of every expert, the padded totals of the experts their offsets.
+// (3) The block counts its run per warp, turns that into prefixes over the warps, and each warp
+// walks its run, 32 choices at a time: a choice's row is its expert's first row for the warp plus
+// the choice's rank among the equal choices of its 32.
+//
+// Few choices (up to kPlanFew): one launch of one cluster, whose blocks read each other's counts
+// through distributed shared memory: for few tokens a second launch would take longer than the
+// work. Many: a counting launch and a placing launch on up to 128 blocks, the counts in the plan's
+// scratch (524288 choices, 256 experts: 78 us on one cluster).
 // ------------------------------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024, kPlanWarps = 32, kPlanMaxCtas = 8;
+constexpr int kPlanFew = 8192, kPlanBlocks = 128;
 
 struct PlanArgs {
     const int* indices;
@@ -295,6 +363,7 @@ struct PlanArgs {
     int* counts;
     int* slots;
     int* rows;
+    int* block_counts;  // many choices: [blocks][E]
 };
 
 __device__ __forceinline__ int ld_shared_cluster_s32(uint32_t addr) {
@@ -335,55 +404,51 @@ __device__ __forceinline__ int2 block_exclusive(int2 v, int2* warp_sums, int2& t
     return make_int2(before.x + s.x - v.x, before.y + s.y - v.y);
 }
 
-__global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_kernel(const PlanArgs a) {
-    extern __shared__ int plan_smem[];
-    int* const hist = plan_smem;                   // [32 warps][E]
-    int* const base = hist + kPlanWarps * a.E;     // [E]
-    int* const totals = base + a.E;                // [E], read by the other CTAs
-    __shared__ int2 warp_sums[kPlanWarps];
-    grid_launch_dependents();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int rank = (int)cluster_ctarank(), ctas = (int)gridDim.x;
-    for (int i = threadIdx.x; i < kPlanWarps * a.E; i += kPlanThreads) hist[i] = 0;
-    __syncthreads();
-    grid_dependency_wait();
-    const int64_t r0 = (int64_t)(rank * kPlanWarps + warp) * a.run;
-    const int64_t r1 = min((int64_t)a.n, r0 + a.run);
-    int* const my = hist + warp * a.E;
-#pragma unroll 4
-    for (int64_t i = r0 + lane; i < r1; i += 32) {
-        const int e = a.indices[i];
-        if (e >= 0 && e < a.E) atomicAdd(my + e, 1);
+// The warp's run of choices.
+struct PlanRun {
+    int64_t r0, r1;
+    __device__ PlanRun(const PlanArgs& a, int block) {
+        r0 = ((int64_t)block * kPlanWarps + (threadIdx.x >> 5)) * a.run;
+        r1 = min((int64_t)a.n, r0 + a.run);
     }
-    __syncthreads();
+};
+
+// Counts the warp's run into `hist` (shared memory, [E], zero before).
+__device__ __forceinline__ void plan_count(const PlanArgs& a, const PlanRun& r, int* hist) {
+#pragma unroll 4
+    for (int64_t i = r.r0 + (threadIdx.x & 31); i < r.r1; i += 32) {
+        const int e = __ldg(a.indices + i);
+        if (e >= 0 && e < a.E) atomicAdd(hist + e, 1);
+    }
+}
+
+// Counts per warp to exclusive prefixes over the warps; the block's count of the thread's expert.
+__device__ __forceinline__ int plan_prefix(const PlanArgs& a, int* hist) {
     const int e = threadIdx.x;
+    int s = 0;
     if (e < a.E) {
-        int s = 0;
 #pragma unroll 8
         for (int w = 0; w < kPlanWarps; ++w) {
             const int c = hist[w * a.E + e];
             hist[w * a.E + e] = s;
             s += c;
         }
-        totals[e] = s;
     }
-    cluster_sync();
-    int count = 0, below = 0;
-    if (e < a.E) {
-        const uint32_t at = smem_u32(totals + e);
-        for (int c = 0; c < ctas; ++c) {
-            const int v = ld_shared_cluster_s32(map_to_cta(at, c));
-            if (c < rank) below += v;
-            count += v;
-        }
-    }
+    return s;
+}
+
+// From each expert's count and the count before this block (thread e: expert e) the block's first
+// rows; the first block writes the plan's arrays over the experts.
+__device__ __forceinline__ void plan_offsets(const PlanArgs& a, int count, int below, bool first, int* base,
+                                             int2* warp_sums) {
+    const int e = threadIdx.x;
     const int padded = (count + ffn::kSegAlign - 1) / ffn::kSegAlign * ffn::kSegAlign;
     const int nt = (count + ffn::kMaxRows - 1) / ffn::kMaxRows;
     int2 total;
     const int2 start = block_exclusive(make_int2(padded, nt), warp_sums, total);
     if (e < a.E) {
         base[e] = start.x + below;
-        if (rank == 0) {
+        if (first) {
             a.offsets[e] = start.x;
             a.counts[e] = count;
             for (int r = count; r < padded; ++r) a.rows[start.x + r] = -1;
@@ -394,15 +459,19 @@ __global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_kernel(const PlanArg
                     FfnTile{e, start.x + i * per, min(per, count - i * per), i == nt - 1 ? 1 : 0};
         }
     }
-    if (rank == 0 && threadIdx.x == 0) {
+    if (first && threadIdx.x == 0) {
         a.offsets[a.E] = total.x;
         *a.num_tiles = total.y;
     }
-    __syncthreads();
+}
+
+// Rows of the warp's run; `my`: the warp's prefixes, advanced as it goes.
+__device__ __forceinline__ void plan_place(const PlanArgs& a, const PlanRun& run, const int* base, int* my) {
+    const int lane = threadIdx.x & 31;
     const unsigned below_me = (1u << lane) - 1u;
-    for (int64_t i0 = r0; i0 < r1; i0 += 32) {
+    for (int64_t i0 = run.r0; i0 < run.r1; i0 += 32) {
         const int64_t i = i0 + lane;
-        int x = i < r1 ? a.indices[i] : -1;
+        int x = i < run.r1 ? __ldg(a.indices + i) : -1;
         const bool ok = x >= 0 && x < a.E;
         if (!ok) x = -1;
         const unsigned same = __match_any_sync(kFull, x);
@@ -411,12 +480,92 @@ __global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_kernel(const PlanArg
         __syncwarp();
         if (ok && (same & below_me) == 0) my[x] += __popc(same);
         __syncwarp();
-        if (i < r1) {
+        if (i < run.r1) {
             a.slots[i] = at;
             if (ok) a.rows[at] = (int)i;
         }
     }
+}
+
+__global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_kernel(const PlanArgs a) {
+    extern __shared__ int plan_smem[];
+    int* const hist = plan_smem;                   // [32 warps][E]
+    int* const base = hist + kPlanWarps * a.E;     // [E]
+    int* const totals = base + a.E;                // [E], read by the other CTAs
+    __shared__ int2 warp_sums[kPlanWarps];
+    const int rank = (int)cluster_ctarank(), ctas = (int)gridDim.x;
+    for (int i = threadIdx.x; i < kPlanWarps * a.E; i += kPlanThreads) hist[i] = 0;
+    __syncthreads();
+    const PlanRun run(a, rank);
+    int* const my = hist + (threadIdx.x >> 5) * a.E;
+    plan_count(a, run, my);
+    __syncthreads();
+    const int e = threadIdx.x;
+    const int mine = plan_prefix(a, hist);
+    if (e < a.E) totals[e] = mine;
+    cluster_sync();
+    int count = 0, below = 0;
+    if (e < a.E) {
+        const uint32_t at = smem_u32(totals + e);
+        for (int c = 0; c < ctas; ++c) {
+            const int v = ld_shared_cluster_s32(map_to_cta(at, c));
+            if (c < rank) below += v;
+            count += v;
+        }
+    }
+    plan_offsets(a, count, below, rank == 0, base, warp_sums);
+    __syncthreads();
+    plan_place(a, run, base, my);
     cluster_sync();  // no CTA leaves while another may still read its totals
+}
+
+__global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_count_kernel(const PlanArgs a) {
+    extern __shared__ int plan_smem[];  // [E]
+    grid_launch_dependents();
+    for (int i = threadIdx.x; i < a.E; i += kPlanThreads) plan_smem[i] = 0;
+    __syncthreads();
+    plan_count(a, PlanRun(a, blockIdx.x), plan_smem);
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.E; i += kPlanThreads)
+        a.block_counts[(int64_t)blockIdx.x * a.E + i] = plan_smem[i];
+}
+
+__global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_place_kernel(const PlanArgs a) {
+    extern __shared__ int plan_smem[];
+    int* const hist = plan_smem;                // [32 warps][E]
+    int* const base = hist + kPlanWarps * a.E;  // [E]
+    int* const sums = base + a.E;               // [2][E]
+    __shared__ int2 warp_sums[kPlanWarps];
+    for (int i = threadIdx.x; i < kPlanWarps * a.E; i += kPlanThreads) hist[i] = 0;
+    for (int i = threadIdx.x; i < 2 * a.E; i += kPlanThreads) sums[i] = 0;
+    __syncthreads();
+    const PlanRun run(a, blockIdx.x);
+    int* const my = hist + (threadIdx.x >> 5) * a.E;
+    plan_count(a, run, my);  // (reads the indices only)
+    __syncthreads();
+    plan_prefix(a, hist);
+    grid_dependency_wait();
+    // each expert's choices in all blocks and in those before this one: threads e, e + E, ... share
+    // an expert's blocks
+    const int e = threadIdx.x;
+    const int parts = max(1, kPlanThreads / a.E);
+    const int blocks = (int)gridDim.x;
+    if (threadIdx.x < parts * a.E) {
+        const int x = threadIdx.x % a.E;
+        int count = 0, below = 0;
+#pragma unroll 8
+        for (int b = threadIdx.x / a.E; b < blocks; b += parts) {
+            const int v = __ldcg(a.block_counts + (int64_t)b * a.E + x);
+            if (b < (int)blockIdx.x) below += v;
+            count += v;
+        }
+        atomicAdd(sums + x, count);  // whole numbers: any order gives the same sum
+        atomicAdd(sums + a.E + x, below);
+    }
+    __syncthreads();
+    plan_offsets(a, e < a.E ? sums[e] : 0, e < a.E ? sums[a.E + e] : 0, blockIdx.x == 0, base, warp_sums);
+    __syncthreads();
+    plan_place(a, run, base, my);
 }
 
 // ------------------------------------------------------------------------------------------------

@@ -141,6 +141,7 @@ typedef struct {
     int64_t rows;      /* [capacity]: the choice t * k + j in each row, -1 in gap rows; rows past
                           the end are not written */
     int64_t tiles;     /* private: tiles of rows (16-byte records) */
+    int64_t scratch;   /* private: counts per block of choices */
     int64_t capacity;  /* rows that a buffer in expert order needs, whatever the indices are */
     int64_t max_tiles;
 } moe_plan_info;
@@ -153,8 +154,7 @@ int moe_plan_layout(int64_t T, int k, int64_t E, moe_plan_info* info);
 /*
  * Puts the choices in expert order: each expert's rows are consecutive, in the order of the tokens
  * (stable), and start at a multiple of 16. indices [T,k]; an index outside 0 .. E-1 is no choice.
- * plan: device memory of moe_plan_layout's words, 16-byte aligned. One kernel on a cluster of up to
- * 8 CTAs. The pages have no counterpart.
+ * plan: device memory of moe_plan_layout's words, 16-byte aligned. The pages have no counterpart.
  */
 int moe_plan(const int* indices, int64_t T, int k, int64_t E, void* plan, dtc_stream_t stream);
 
