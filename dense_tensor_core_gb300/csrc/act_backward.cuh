@@ -34,6 +34,8 @@ __global__ void __launch_bounds__(kActBackThreads) act_backward_kernel(const Act
     constexpr int kSets = kGated ? 2 : 1;  // column sets a dC column feeds
     __shared__ float sums[kActBackLanes][kSets * kActBackCols];
     __shared__ bool is_last;
+    grid_launch_dependents();
+    grid_dependency_wait();
     const int ct = threadIdx.x & 31, rl = threadIdx.x >> 5;
     const int64_t col = (int64_t)blockIdx.x * kActBackCols + ct * 8;
     const bool on = col < a.N;  // N is a multiple of 8
@@ -51,9 +53,9 @@ __global__ void __launch_bounds__(kActBackThreads) act_backward_kernel(const Act
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 const int64_t rr = r + (n && two ? kActBackLanes : 0);
-                cx[n] = __ldcs(reinterpret_cast<const uint4*>(a.dC + rr * a.ldc + col));
-                if (a.z) cz[n] = __ldcs(reinterpret_cast<const uint4*>(a.z + rr * a.ldz + col));
-                if (kGated && a.z) cu[n] = __ldcs(reinterpret_cast<const uint4*>(a.z + rr * a.ldz + a.N + col));
+                cx[n] = *reinterpret_cast<const uint4*>(a.dC + rr * a.ldc + col);
+                if (a.z) cz[n] = *reinterpret_cast<const uint4*>(a.z + rr * a.ldz + col);
+                if (kGated && a.z) cu[n] = *reinterpret_cast<const uint4*>(a.z + rr * a.ldz + a.N + col);
             }
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
@@ -114,7 +116,7 @@ __global__ void __launch_bounds__(kActBackThreads) act_backward_kernel(const Act
         float t = 0.0f;
         const float* p = a.partial + k * a.N + c0;
 #pragma unroll 8
-        for (unsigned y = 0; y < gridDim.y; ++y) t += __ldcg(p + (int64_t)y * width);
+        for (unsigned y = 0; y < gridDim.y; ++y) t += p[(int64_t)y * width];
         a.dbias[k * a.N + c0] = t;
     }
 }

@@ -32,12 +32,17 @@ void size_split(FfnPlan* p) {
 }
 
 // Modelled time of a launch in SM cycles: whole waves of items over the pairs. A K-block of 128
-// costs 4 cycles per row of the tile (the tensor core's rate for 256 features) and at least 520
-// (its operands' delivery into shared memory); an item 200 more; the last tile's epilogue shows.
-// Split items write their sums and the last of a tile reads them all back.
-double item_cost(int64_t tiles, int splits, int kb_per, int n, int pairs) {
+// costs 4 cycles per row of the tile (the tensor core's rate for 256 features) or the delivery of
+// its operands, measured as about 1.6 cycles per 128-byte row piece that a CTA fetches (256 of the
+// features, one per row of the tile); a piece of rows that do not start on 128-byte lines spans two
+// lines and costs twice that. An item costs 200 more; the last tile's epilogue shows. Split items
+// write their sums and the last of a tile reads them all back.
+struct Delivery {
+    int p = 1, q = 1;  // lines per 128-byte piece of the features' and the rows' operand
+};
+double item_cost(int64_t tiles, int splits, int kb_per, int n, int pairs, Delivery d) {
     const double waves = (double)((tiles * splits + pairs - 1) / pairs);
-    double item = kb_per * std::max(4.0 * n, 520.0) + 200.0;
+    double item = kb_per * std::max(4.0 * n, 1.6 * (256.0 * d.p + n * d.q)) + 200.0;
     double end = 16.0 * n;
     if (splits > 1) {
         item += 6.0 * n;
@@ -46,9 +51,13 @@ double item_cost(int64_t tiles, int splits, int kb_per, int n, int pairs) {
     return waves * item + end;
 }
 
+int lines_of(const void* p, int64_t ld) {
+    return (reinterpret_cast<uintptr_t>(p) & 127) || ld % 64 ? 2 : 1;
+}
+
 // Tile rows and K splits of one matrix's product: the cheapest by item_cost.
 FfnPlan plan_rows(int64_t rows, int64_t feats, bool gated, int64_t red, bool q_mn, int pairs,
-                  uint64_t ws_bytes) {
+                  uint64_t ws_bytes, Delivery d) {
     FfnPlan best;
     double cost = 0;
     const int ft = num_feature_tiles(feats, gated);
@@ -70,7 +79,7 @@ FfnPlan plan_rows(int64_t rows, int64_t feats, bool gated, int64_t red, bool q_m
             p.counter_bytes = p.bytes = 0;
             size_split(&p);
             if (p.bytes > ws_bytes || p.bytes > (64ull << 20)) continue;
-            const double c = item_cost(p.tiles, s, p.kb_per_split, n, pairs);
+            const double c = item_cost(p.tiles, s, p.kb_per_split, n, pairs, d);
             if (best.num_ft == 0 || c < cost) {
                 best = p;
                 cost = c;
@@ -100,7 +109,7 @@ FfnPlan plan_seg(int64_t T, int k, int64_t E, int64_t max_tiles, int64_t feats, 
         for (int s = 1; s <= std::max(1, std::min(32, kb / 2)); ++s) {
             const int per = ceil_div(kb, s);
             if (s > 1 && ceil_div(kb, per) != s) continue;
-            const double c = item_cost(likely, s, per, expect, pairs);
+            const double c = item_cost(likely, s, per, expect, pairs, Delivery());
             if (s == 1 || c < cost) {
                 cost = c;
                 best = s;
@@ -228,7 +237,8 @@ int gemm_act(int dtype, const void* A, const void* B, void* C, int64_t M, int64_
     if (o.bias && (rc = check_device_ptr(o.bias, dev, "bias"))) return rc;
     if (o.residual && (rc = check_device_ptr(o.residual, dev, "residual"))) return rc;
     if (o.preact && (rc = check_device_ptr(o.preact, dev, "preact"))) return rc;
-    const FfnPlan p = plan_rows(M, N, gated, K, amn, pairs_of(info), o.workspace ? o.workspace_bytes : 0);
+    const FfnPlan p = plan_rows(M, N, gated, K, amn, pairs_of(info), o.workspace ? o.workspace_bytes : 0,
+                                Delivery{lines_of(B, o.ldb), lines_of(A, o.lda)});
     if (p.num_ft == 0) return fail(GEMM_ERR_UNSUPPORTED, "too many tiles");
     if (p.splits > 1 && (rc = check_device_ptr(o.workspace, dev, "the workspace"))) return rc;
     FfnCall c;
@@ -276,7 +286,9 @@ int gemm_act_workspace_size(int dtype, int64_t M, int64_t N, int64_t K, int layo
     int dev;
     DeviceInfo* info;
     if ((rc = current_device(&dev, &info))) return rc;
-    *bytes = plan_rows(M, N, dtc::act_gated(activation), K, a_is_mn(layout), pairs_of(info), ~0ull).bytes;
+    // for dense operands; other row pitches are planned within this size
+    const Delivery d{lines_of(nullptr, b_is_mn(layout) ? N : K), lines_of(nullptr, a_is_mn(layout) ? M : K)};
+    *bytes = plan_rows(M, N, dtc::act_gated(activation), K, a_is_mn(layout), pairs_of(info), ~0ull, d).bytes;
     return GEMM_OK;
 }
 
@@ -568,6 +580,9 @@ namespace {
 
 struct ExpertSizes {
     int64_t T, E, H, F, Fz;
+    // elements between the rows of the buffers in expert order: whole 128-byte lines, so that a
+    // 128-byte box row of a tensor-map load is one line of the L2 and not parts of two
+    int64_t ldH, ldF, ldFz;
     int k, act;
     bool gated;
     moe_plan_info plan;
@@ -588,6 +603,9 @@ int check_experts(int dtype, int64_t T, int k, int64_t E, int64_t H, int64_t F, 
     s->act = act;
     s->gated = dtc::act_gated(act);
     s->Fz = s->gated ? 2 * F : F;
+    s->ldH = (H + 63) / 64 * 64;
+    s->ldF = (F + 63) / 64 * 64;
+    s->ldFz = (s->Fz + 63) / 64 * 64;
     if (H < 8 || F < 8 || H % 8 || F % 8 || H > (1 << 24) || F > (1 << 24))
         return fail(GEMM_ERR_INVALID_ARG, "H=%lld and F=%lld must be multiples of 8 in [8, 2^24]",
                     (long long)H, (long long)F);
@@ -626,11 +644,12 @@ void seg_call(const ExpertSizes& s, bool bf16, const int32_t* plan, const moe_ex
               DeviceInfo* info, FfnCall* c) {
     c->bf16 = bf16;
     c->experts = (int)s.E;
-    c->dependent = true;
     dtc::FfnArgs& a = c->args;
     a.experts = (int)s.E;
     a.tiles = reinterpret_cast<const dtc::FfnTile*>(plan + s.plan.tiles);
     a.num_tiles = plan;
+    a.max_tiles = (int)s.plan.max_tiles;
+    a.rows = (int)s.plan.capacity;
     a.offsets = plan + s.plan.offsets;
     a.counts = plan + s.plan.counts;
     a.q_deep = false;
@@ -644,7 +663,7 @@ void seg_call(const ExpertSizes& s, bool bf16, const int32_t* plan, const moe_ex
 // epilogue's part of the arguments.
 int seg_product(const ExpertSizes& s, bool bf16, const int32_t* plan, const moe_experts_options& o,
                 DeviceInfo* info, const FfnPlan& p, void* counters, void* partial, const void* rows,
-                int64_t red, const void* weights, bool weights_mn, int64_t feats, bool gated, bool back,
+                int64_t ld_rows, int64_t red, const void* weights, bool weights_mn, int64_t feats, bool gated, bool back,
                 const dtc::FfnArgs& e, cudaStream_t st) {
     FfnCall c;
     c.back = back;
@@ -656,7 +675,7 @@ int seg_product(const ExpertSizes& s, bool bf16, const int32_t* plan, const moe_
     c.P = weights;
     c.ldp = weights_mn ? feats : red;
     c.Q = rows;
-    c.ldq = red;
+    c.ldq = ld_rows;
     c.red = red;
     c.q_rows = s.plan.capacity;
     dtc::FfnArgs& a = c.args;
@@ -674,8 +693,8 @@ int seg_product(const ExpertSizes& s, bool bf16, const int32_t* plan, const moe_
 
 // out[e] = the sum over expert e's rows of left[row, :]^T right[row, :], [width_l, width_r].
 int red_product(const ExpertSizes& s, bool bf16, const int32_t* plan, const moe_experts_options& o,
-                DeviceInfo* info, int pairs, const void* left, int64_t width_l, const void* right,
-                int64_t width_r, void* out, cudaStream_t st) {
+                DeviceInfo* info, int pairs, const void* left, int64_t ld_l, int64_t width_l,
+                const void* right, int64_t ld_r, int64_t width_r, void* out, cudaStream_t st) {
     FfnCall c;
     seg_call(s, bf16, plan, o, info, &c);
     const FfnPlan p = plan_red(s.E, width_l, width_r, pairs);
@@ -683,9 +702,9 @@ int red_product(const ExpertSizes& s, bool bf16, const int32_t* plan, const moe_
     c.p_mn = c.q_mn = true;
     c.experts = 1;
     c.P = right;
-    c.ldp = width_r;
+    c.ldp = ld_r;
     c.Q = left;
-    c.ldq = width_l;
+    c.ldq = ld_l;
     c.red = s.plan.capacity;
     c.q_rows = width_l;
     dtc::FfnArgs& a = c.args;
@@ -703,11 +722,11 @@ int red_product(const ExpertSizes& s, bool bf16, const int32_t* plan, const moe_
 int experts_layout(const ExpertSizes& s, int train, int pairs, moe_experts_info* l) {
     const uint64_t R = s.plan.capacity;
     l->x = 0;
-    l->z = up256(R * s.H * 2);
-    l->h = l->z + (train ? up256(R * s.Fz * 2) : 0);
-    l->scale = l->h + up256(R * s.F * 2);
+    l->z = up256(R * s.ldH * 2);
+    l->h = l->z + (train ? up256(R * s.ldFz * 2) : 0);
+    l->scale = l->h + up256(R * s.ldF * 2);
     l->y = l->scale + up256(R * 4);
-    l->split = l->y + up256(R * s.H * 2);
+    l->split = l->y + up256(R * s.ldH * 2);
     const SplitScratch x = split_scratch(seg_plan(s, s.F, s.gated, s.H, pairs),
                                          seg_plan(s, s.H, false, s.F, pairs));
     l->bytes = l->split + up256(x.bytes);
@@ -776,27 +795,27 @@ int moe_experts(int dtype, const void* x, const void* w_in, const void* w_out, c
     const bool bf16 = dtype == 0;
     const GatherCall g{x, b + l.x, weights, o.weights_dtype, reinterpret_cast<float*>(b + l.scale),
                        reinterpret_cast<uint32_t*>(split), (int)(sc.partial / 4)};
-    if ((rc = launch_moe_gather(g, pl, s.plan, k, E, H, info, st))) return rc;
+    if ((rc = launch_moe_gather(g, pl, s.plan, k, E, H, s.ldH, info, st))) return rc;
     // h = weight * act(z): the weight goes in here, in fp32 before h's one rounding, so the join
     // is a plain sum and the backward pass needs no product of the weights with rounded rows
     dtc::FfnArgs e = {};
     e.act = s.act;
     e.row_scale = reinterpret_cast<const float*>(b + l.scale);
     e.out = b + l.h;
-    e.ld_out = F;
+    e.ld_out = s.ldF;
     e.preact = train ? b + l.z : nullptr;
-    e.ld_pre = s.Fz;
-    if ((rc = seg_product(s, bf16, pl, o, info, p1, split, split + sc.partial, b + l.x, H, w_in, false,
+    e.ld_pre = s.ldFz;
+    if ((rc = seg_product(s, bf16, pl, o, info, p1, split, split + sc.partial, b + l.x, s.ldH, H, w_in, false,
                           F, s.gated, false, e, st)))
         return rc;
     e = {};
     e.out = b + l.y;
-    e.ld_out = H;
-    if ((rc = seg_product(s, bf16, pl, o, info, p2, split + sc.second, split + sc.partial, b + l.h, F,
+    e.ld_out = s.ldH;
+    if ((rc = seg_product(s, bf16, pl, o, info, p2, split + sc.second, split + sc.partial, b + l.h, s.ldF, F,
                           w_out, false, H, false, false, e, st)))
         return rc;
     const JoinCall j{b + l.y, o.residual, y, nullptr, 0, nullptr, 0};
-    return launch_moe_join(bf16, j, pl, s.plan, T, k, E, H, info, st);
+    return launch_moe_join(bf16, j, pl, s.plan, T, k, E, H, s.ldH, info, st);
 }
 
 }  // extern "C"
@@ -812,9 +831,9 @@ struct ExpertsBackLayout {
 void experts_back_layout(const ExpertSizes& s, int pairs, ExpertsBackLayout* l) {
     const uint64_t R = s.plan.capacity;
     l->dy = 0;
-    l->dz = up256(R * s.H * 2);
-    l->dx = l->dz + up256(R * s.Fz * 2);
-    l->dots = l->dx + up256(R * s.H * 2);
+    l->dz = up256(R * s.ldH * 2);
+    l->dx = l->dz + up256(R * s.ldFz * 2);
+    l->dots = l->dx + up256(R * s.ldH * 2);
     l->parts = num_feature_tiles(s.F, false) * 8;
     l->split = l->dots + up256(R * l->parts * 4);
     const SplitScratch x = split_scratch(seg_plan(s, s.F, false, s.H, pairs),
@@ -903,7 +922,7 @@ int moe_experts_backward(int dtype, const void* dy, const void* w_in, const void
     const bool bf16 = dtype == 0;
     const GatherCall g{dy, ws + w.dy, nullptr, 0, nullptr, reinterpret_cast<uint32_t*>(split),
                        (int)(sc.partial / 4)};
-    if ((rc = launch_moe_gather(g, pl, s.plan, k, E, H, info, st))) return rc;
+    if ((rc = launch_moe_gather(g, pl, s.plan, k, E, H, s.ldH, info, st))) return rc;
     // dz = weight * (dy rows . w_out) * act'(z) and the rows' dot products, in the epilogue
     dtc::FfnArgs e = {};
     e.act = s.act;
@@ -911,27 +930,29 @@ int moe_experts_backward(int dtype, const void* dy, const void* w_in, const void
     e.row_dot = reinterpret_cast<float*>(ws + w.dots);
     e.row_dot_ld = (int64_t)s.plan.capacity;
     e.out = ws + w.dz;
-    e.ld_out = s.Fz;
+    e.ld_out = s.ldFz;
     e.preact = const_cast<char*>(b) + l.z;
-    e.ld_pre = s.Fz;
-    if ((rc = seg_product(s, bf16, pl, o, info, ph, split, split + sc.partial, ws + w.dy, H, w_out, true, F,
-                          false, true, e, st)))
+    e.ld_pre = s.ldFz;
+    if ((rc = seg_product(s, bf16, pl, o, info, ph, split, split + sc.partial, ws + w.dy, s.ldH, H, w_out,
+                          true, F, false, true, e, st)))
         return rc;
     if (dw_in) {
-        if ((rc = red_product(s, bf16, pl, o, info, pairs, ws + w.dy, H, b + l.h, F, dw_out, st))) return rc;
-        if ((rc = red_product(s, bf16, pl, o, info, pairs, ws + w.dz, s.Fz, b + l.x, H, dw_in, st))) return rc;
+        if ((rc = red_product(s, bf16, pl, o, info, pairs, ws + w.dy, s.ldH, H, b + l.h, s.ldF, F, dw_out, st)))
+            return rc;
+        if ((rc = red_product(s, bf16, pl, o, info, pairs, ws + w.dz, s.ldFz, s.Fz, b + l.x, s.ldH, H, dw_in, st)))
+            return rc;
     }
     if (dx) {
         e = {};
         e.out = ws + w.dx;
-        e.ld_out = H;
+        e.ld_out = s.ldH;
         if ((rc = seg_product(s, bf16, pl, o, info, px, split + sc.second, split + sc.partial, ws + w.dz,
-                              s.Fz, w_in, true, H, false, false, e, st)))
+                              s.ldFz, s.Fz, w_in, true, H, false, false, e, st)))
             return rc;
     }
     const JoinCall j{ws + w.dx, nullptr, dx, reinterpret_cast<const float*>(ws + w.dots), w.parts, dweights,
                      o.weights_dtype};
-    return launch_moe_join(bf16, j, pl, s.plan, T, k, E, H, info, st);
+    return launch_moe_join(bf16, j, pl, s.plan, T, k, E, H, s.ldH, info, st);
 }
 
 }  // extern "C"

@@ -20,7 +20,6 @@ struct FfnCall {
     int64_t q_rows = 0;    // rows of Q (kRed: its columns)
     int experts = 1;
     int grid = 0;
-    bool dependent = false;
     dtc::FfnArgs args = {};
 };
 int launch_ffn_rows(const FfnCall& c, DeviceInfo* dev, cudaStream_t stream);
@@ -34,7 +33,7 @@ int launch_ffn(const FfnCall& c, DeviceInfo* dev, cudaStream_t stream) {
     if (rc) return rc;
     auto kern = dtc::gemm16_ffn_kernel<kBF16, kMode, kPMN, kQMN, kGated, kBack>;
     if ((rc = ensure_smem_attr(kern, dtc::ffn::kSmemBytes, dev))) return rc;
-    return launch_chain(kern, dim3(c.grid), dtc::ffn::kThreads, dtc::ffn::kSmemBytes, 2, c.dependent,
+    return launch_chain(kern, dim3(c.grid), dtc::ffn::kThreads, dtc::ffn::kSmemBytes, 2, true,
                         stream, tp, tq, c.args);
 }
 
@@ -85,7 +84,7 @@ struct GatherCall {
     int zero_words;
 };
 int launch_moe_gather(const GatherCall& c, const int32_t* plan, const moe_plan_info& l, int k, int64_t E,
-                      int64_t H, DeviceInfo* dev, cudaStream_t stream);
+                      int64_t H, int64_t ld_out, DeviceInfo* dev, cudaStream_t stream);
 // out[t] = residual[t] + sum_j rows[slot[t,j]] (out NULL: no join); dweights from the pieces of the
 // rows' dot products (dweights NULL: none).
 struct JoinCall {
@@ -98,6 +97,6 @@ struct JoinCall {
     int wtype;
 };
 int launch_moe_join(bool bf16, const JoinCall& c, const int32_t* plan, const moe_plan_info& l, int64_t T,
-                    int k, int64_t E, int64_t H, DeviceInfo* dev, cudaStream_t stream);
+                    int k, int64_t E, int64_t H, int64_t ld_rows, DeviceInfo* dev, cudaStream_t stream);
 
 }  // namespace dtc_host

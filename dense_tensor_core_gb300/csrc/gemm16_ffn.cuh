@@ -79,7 +79,8 @@ struct FfnTile {
 
 struct FfnArgs {
     int feats;    // output features of one matrix (gated: pairs)
-    int rows;     // kRows: rows; kRed: rows of one output matrix (Q's columns)
+    int rows;     // kRows: rows; kSeg: rows of the buffers; kRed: rows of one output matrix (Q's
+                  // columns)
     int red;      // reduction length (kRows, kSeg); kRed: the rows of the operands' buffers
     int tile_n;   // kRows, kRed: rows per tile (a multiple of 32)
     int num_ft, num_rt;
@@ -89,6 +90,7 @@ struct FfnArgs {
     int q_box;            // K-major Q: rows per box
     const FfnTile* tiles;   // kSeg
     const int* num_tiles;   // kSeg
+    int max_tiles;          // kSeg: records that the plan has room for
     const int* offsets;     // kRed: expert e's rows are offsets[e] .. offsets[e] + counts[e] - 1
     const int* counts;
     int p_expert_rows;      // K-major P: rows between experts' matrices
@@ -155,13 +157,18 @@ __device__ __forceinline__ bool get_item(const FfnArgs& a, int t, int seg_tiles,
     } else if constexpr (kMode == kSeg) {
         if (tile >= a.num_ft * seg_tiles) return false;
         const int rt = tile / a.num_ft;
-        const int4 s = __ldg(reinterpret_cast<const int4*>(a.tiles) + rt);
+        const int4 s = reinterpret_cast<const int4*>(a.tiles)[rt];
+        // a record that no plan of these sizes holds (a stale or foreign plan) ends the walk: the
+        // MMA's shape and the rows written come from it
+        if ((unsigned)s.x >= (unsigned)a.experts || s.z < 1 || s.z > kMaxRows || s.y < 0 ||
+            s.y > a.rows - s.z)
+            return false;
         w.f0 = (tile - rt * a.num_ft) * kFeats;
         w.expert = s.x;
         w.r0 = s.y;
         w.valid = s.z;
         w.n = round32(s.z);
-        if (s.w) w.zeros = (kSegAlign - (s.z & (kSegAlign - 1))) & (kSegAlign - 1);
+        if (s.w) w.zeros = min((kSegAlign - (s.z & (kSegAlign - 1))) & (kSegAlign - 1), a.rows - s.y - s.z);
     } else {
         const int per = a.num_ft * a.num_rt;
         if (tile >= per * a.experts) return false;
@@ -172,8 +179,8 @@ __device__ __forceinline__ bool get_item(const FfnArgs& a, int t, int seg_tiles,
         w.r0 = rt * a.tile_n;
         w.valid = min(a.tile_n, a.rows - w.r0);
         w.n = a.tile_n;
-        w.red = __ldg(a.counts + w.expert);
-        w.krow = __ldg(a.offsets + w.expert);
+        w.krow = min(max(a.offsets[w.expert], 0), a.red);
+        w.red = min(max(a.counts[w.expert], 0), a.red - w.krow);
     }
     const int kb = (w.red + kBK - 1) / kBK;
     w.kb0 = a.splits > 1 ? min(kb, split * a.kb_per_split) : 0;
@@ -357,7 +364,7 @@ __device__ __forceinline__ void finish_block(const FfnArgs& a, float (&v)[4][8],
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
             float2 s = make_float2(0.0f, 0.0f);  // (rows come in multiples of 16, so pairs are whole)
-            if (8 * b + tr < p.rows) s = __ldg(reinterpret_cast<const float2*>(a.row_scale + p.row + 8 * b + tr));
+            if (8 * b + tr < p.rows) s = *reinterpret_cast<const float2*>(a.row_scale + p.row + 8 * b + tr);
             scale[2 * b] = s.x;
             scale[2 * b + 1] = s.y;
         }
@@ -557,7 +564,9 @@ __global__ void __launch_bounds__(ffn::kThreads, 1)
     const uint32_t tmem_base = tmem_slot;
     grid_launch_dependents();
     grid_dependency_wait();  // the set-up above overlaps the tail of the kernel before
-    const int seg_tiles = kMode == kSeg ? __ldg(args.num_tiles) : 0;
+    // (Nothing behind the wait may be a read-only-cache load, __ldg: the compiler is free to move
+    // those, whose data must not change during the kernel, ahead of it.)
+    const int seg_tiles = kMode == kSeg ? min(*args.num_tiles, args.max_tiles) : 0;
 
     if (warp == 0) {
         // ------------------------------ TMA producer (both CTAs) ------------------------------

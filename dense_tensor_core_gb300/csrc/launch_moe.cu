@@ -34,7 +34,7 @@ template <int kType, bool kBack>
 int route_by_size(const dtc::RouteArgs& a, cudaStream_t s) {
     const dim3 grid((unsigned)((a.T + dtc::kRouteWarps - 1) / dtc::kRouteWarps));
     const int threads = dtc::kRouteWarps * 32;
-    auto go = [&](auto kern) { return launch_chain(kern, grid, threads, 0, 1, false, s, a); };
+    auto go = [&](auto kern) { return launch_chain(kern, grid, threads, 0, 1, true, s, a); };
     const int v = (a.E + 31) / 32;
 #define DTC_ROUTE(N)                                             \
     if (v <= N) {                                                \
@@ -100,10 +100,10 @@ int launch_moe_plan(const int* indices, int64_t T, int k, int64_t E, int32_t* pl
     if (few) {
         if ((rc = ensure_smem_attr(dtc::moe_plan_kernel, words * dtc::ffn::kMaxExperts * 4, dev))) return rc;
         return launch_chain(dtc::moe_plan_kernel, dim3(blocks), dtc::kPlanThreads, words * (int)E * 4, blocks,
-                            false, stream, a);
+                            true, stream, a);
     }
     if ((rc = ensure_smem_attr(dtc::moe_plan_place_kernel, words * dtc::ffn::kMaxExperts * 4, dev))) return rc;
-    if ((rc = launch_chain(dtc::moe_plan_count_kernel, dim3(blocks), dtc::kPlanThreads, (int)E * 4, 1, false,
+    if ((rc = launch_chain(dtc::moe_plan_count_kernel, dim3(blocks), dtc::kPlanThreads, (int)E * 4, 1, true,
                            stream, a)))
         return rc;
     return launch_chain(dtc::moe_plan_place_kernel, dim3(blocks), dtc::kPlanThreads, words * (int)E * 4, 1, true,
@@ -115,25 +115,28 @@ int64_t moe_plan_scratch_words(int64_t choices, int64_t E) {
 }
 
 int launch_moe_gather(const GatherCall& c, const int32_t* plan, const moe_plan_info& l, int k, int64_t E,
-                      int64_t H, DeviceInfo* dev, cudaStream_t stream) {
+                      int64_t H, int64_t ld_out, DeviceInfo* dev, cudaStream_t stream) {
     dtc::RowsArgs a;
     a.in = static_cast<const uint16_t*>(c.x);
     a.out = static_cast<uint16_t*>(c.out);
     a.rows = plan + l.rows;
     a.end = plan + l.offsets + E;
+    a.capacity = (int)l.capacity;
+    a.choices = (int)(l.rows - l.slots);
     a.k = k;
     a.H8 = (int)(H / 8);
+    a.ld8 = (int)(ld_out / 8);
     a.weights = c.weights;
     a.wtype = c.wtype;
     a.scale = c.scale;
     a.zero = c.zero;
     a.zero_words = c.zero_words;
     return launch_chain(dtc::moe_gather_kernel, dim3(rows_grid(l.capacity, dev)), dtc::kRowsThreads, 0,
-                        1, false, stream, a);
+                        1, true, stream, a);
 }
 
 int launch_moe_join(bool bf16, const JoinCall& c, const int32_t* plan, const moe_plan_info& l, int64_t T,
-                    int k, int64_t E, int64_t H, DeviceInfo* dev, cudaStream_t stream) {
+                    int k, int64_t E, int64_t H, int64_t ld_rows, DeviceInfo* dev, cudaStream_t stream) {
     dtc::JoinArgs a;
     a.rows = static_cast<const uint16_t*>(c.rows);
     a.slots = plan + l.slots;
@@ -142,10 +145,12 @@ int launch_moe_join(bool bf16, const JoinCall& c, const int32_t* plan, const moe
     a.T = T;
     a.k = k;
     a.H8 = (int)(H / 8);
+    a.ld8 = (int)(ld_rows / 8);
     a.items = c.out ? T * ((a.H8 + 31) / 32) : 0;
     a.dots = c.dots;
     a.parts = c.parts;
     a.ld = l.capacity;
+    a.capacity = (int)l.capacity;
     a.choice = plan + l.rows;
     a.end = plan + l.offsets + E;
     a.dweights = c.dweights;

@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
     __shared__ uint32_t cands[kRouteWarps][32];
     __shared__ uint16_t cands_at[kRouteWarps][32];
     grid_launch_dependents();
+    grid_dependency_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
     if (t >= a.T) return;
@@ -111,7 +112,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
     for (int j = 0; j < kVPL; ++j) {
         const int e = lane + 32 * j;
         float s = a.sigmoid ? sigmoid_exact(z[j]) : z[j];
-        if (a.bias && e < a.E) s = s + __ldg(a.bias + e);
+        if (a.bias && e < a.E) s = s + a.bias[e];
         // masked: -infinity or NaN, in the logit or in the key
         key[j] = (z[j] > -CUDART_INF_F && s > -CUDART_INF_F) ? order_key(s) : 0u;
     }
@@ -264,6 +265,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
 //   sigmoid                    d_i = g_i s_i (1 - s_i);  renormalized: g_i -> (g_i - sum g s / S) / S
 template <int kType, int kVPL>
 __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_backward_kernel(const RouteArgs a) {
+    grid_launch_dependents();
+    grid_dependency_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
     if (t >= a.T) return;
@@ -273,7 +276,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_backward_kernel(co
     if (lane < a.k) {
         mine = a.chosen[t * a.k + lane];
         if (mine < 0 || mine >= a.E) mine = -1;
-        if (mine >= 0) g = a.dweights[t * a.k + lane] * a.scale;
+        // (products rounded by themselves: fused into the differences below, one choice's gradient,
+        // which cancels, would come out as the rounding error of dweights * scale)
+        if (mine >= 0) g = __fmul_rn(a.dweights[t * a.k + lane], a.scale);
     }
     const float zi = mine >= 0 ? load_f<kType>(a.logits, row + mine) : -CUDART_INF_F;
     const bool got = zi > -CUDART_INF_F;
@@ -288,7 +293,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_backward_kernel(co
         const float s = got ? sigmoid_exact(zi) : 0.0f;
         if (a.renorm) {
             const float total = warp_sum(s);
-            const float mean = total > 0.0f ? warp_sum(g * s) / total : 0.0f;
+            const float mean = total > 0.0f ? warp_sum(__fmul_rn(g, s)) / total : 0.0f;
             g = total > 0.0f && got ? (g - mean) / total : 0.0f;
         }
         d = g * s * (1.0f - s);
@@ -297,7 +302,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_backward_kernel(co
         const float e = got ? expf(zi - m) : 0.0f;
         const float total = warp_sum(e);
         const float p = got ? e / total : 0.0f;
-        d = p * (g - warp_sum(g * p));
+        d = p * (g - warp_sum(__fmul_rn(g, p)));
     } else {
         m = -CUDART_INF_F;
 #pragma unroll
@@ -415,10 +420,13 @@ struct PlanRun {
 
 // Counts the warp's run into `hist` (shared memory, [E], zero before).
 __device__ __forceinline__ void plan_count(const PlanArgs& a, const PlanRun& r, int* hist) {
-#pragma unroll 4
-    for (int64_t i = r.r0 + (threadIdx.x & 31); i < r.r1; i += 32) {
-        const int e = __ldg(a.indices + i);
-        if (e >= 0 && e < a.E) atomicAdd(hist + e, 1);
+    for (int64_t i = r.r0 + (threadIdx.x & 31); i < r.r1; i += 128) {
+        int e[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) e[j] = i + 32 * j < r.r1 ? a.indices[i + 32 * j] : -1;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (e[j] >= 0 && e[j] < a.E) atomicAdd(hist + e[j], 1);
     }
 }
 
@@ -471,7 +479,7 @@ __device__ __forceinline__ void plan_place(const PlanArgs& a, const PlanRun& run
     const unsigned below_me = (1u << lane) - 1u;
     for (int64_t i0 = run.r0; i0 < run.r1; i0 += 32) {
         const int64_t i = i0 + lane;
-        int x = i < run.r1 ? __ldg(a.indices + i) : -1;
+        int x = i < run.r1 ? a.indices[i] : -1;
         const bool ok = x >= 0 && x < a.E;
         if (!ok) x = -1;
         const unsigned same = __match_any_sync(kFull, x);
@@ -494,8 +502,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_kernel(const PlanArg
     int* const totals = base + a.E;                // [E], read by the other CTAs
     __shared__ int2 warp_sums[kPlanWarps];
     const int rank = (int)cluster_ctarank(), ctas = (int)gridDim.x;
+    grid_launch_dependents();
     for (int i = threadIdx.x; i < kPlanWarps * a.E; i += kPlanThreads) hist[i] = 0;
     __syncthreads();
+    grid_dependency_wait();
     const PlanRun run(a, rank);
     int* const my = hist + (threadIdx.x >> 5) * a.E;
     plan_count(a, run, my);
@@ -524,6 +534,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_count_kernel(const P
     grid_launch_dependents();
     for (int i = threadIdx.x; i < a.E; i += kPlanThreads) plan_smem[i] = 0;
     __syncthreads();
+    grid_dependency_wait();
     plan_count(a, PlanRun(a, blockIdx.x), plan_smem);
     __syncthreads();
     for (int i = threadIdx.x; i < a.E; i += kPlanThreads)
@@ -539,12 +550,13 @@ __global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_place_kernel(const P
     for (int i = threadIdx.x; i < kPlanWarps * a.E; i += kPlanThreads) hist[i] = 0;
     for (int i = threadIdx.x; i < 2 * a.E; i += kPlanThreads) sums[i] = 0;
     __syncthreads();
+    grid_launch_dependents();
+    grid_dependency_wait();
     const PlanRun run(a, blockIdx.x);
     int* const my = hist + (threadIdx.x >> 5) * a.E;
-    plan_count(a, run, my);  // (reads the indices only)
+    plan_count(a, run, my);
     __syncthreads();
     plan_prefix(a, hist);
-    grid_dependency_wait();
     // each expert's choices in all blocks and in those before this one: threads e, e + E, ... share
     // an expert's blocks
     const int e = threadIdx.x;
@@ -555,7 +567,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_place_kernel(const P
         int count = 0, below = 0;
 #pragma unroll 8
         for (int b = threadIdx.x / a.E; b < blocks; b += parts) {
-            const int v = __ldcg(a.block_counts + (int64_t)b * a.E + x);
+            const int v = a.block_counts[(int64_t)b * a.E + x];
             if (b < (int)blockIdx.x) below += v;
             count += v;
         }
@@ -576,8 +588,9 @@ struct RowsArgs {
     uint16_t* out;        // rows in expert order
     const int* rows;
     const int* end;       // offsets[E]
+    int capacity, choices;  // bounds of the plan's rows and of what stands in them
     int k;
-    int H8;               // 16-byte pieces of a row
+    int H8, ld8;          // 16-byte pieces of a row, and between the rows of `out`
     const void* weights;  // [T,k]; NULL: no scale
     int wtype;
     float* scale;         // [rows]: each row's weight, 0 in gap rows
@@ -595,18 +608,26 @@ __global__ void __launch_bounds__(kRowsThreads) moe_gather_kernel(const RowsArgs
     for (int64_t i = tid; i < a.zero_words; i += (int64_t)gridDim.x * kRowsThreads) a.zero[i] = 0u;
     const int lane = threadIdx.x & 31;
     const int64_t warps = (int64_t)gridDim.x * (kRowsThreads / 32);
-    const int64_t end = __ldg(a.end);
+    const int64_t end = min(*a.end, a.capacity);
     for (int64_t r = tid >> 5; r < end; r += warps) {
-        const int i = __ldg(a.rows + r);
+        int i = a.rows[r];
+        if (i >= a.choices) i = -1;
         if (a.weights && lane == 0) a.scale[r] = i < 0 ? 0.0f : load_w(a.weights, i, a.wtype);
-        uint4* const d = reinterpret_cast<uint4*>(a.out) + r * a.H8;
+        uint4* const d = reinterpret_cast<uint4*>(a.out) + r * a.ld8;
         if (i < 0) {
             for (int c = lane; c < a.H8; c += 32) d[c] = make_uint4(0, 0, 0, 0);
             continue;
         }
         const uint4* const s = reinterpret_cast<const uint4*>(a.in) + (int64_t)(i / a.k) * a.H8;
-#pragma unroll 8
-        for (int c = lane; c < a.H8; c += 32) d[c] = __ldg(s + c);
+        for (int c0 = lane; c0 < a.H8; c0 += 256) {  // 8 loads in flight (4 KB of the row a warp)
+            uint4 x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c0 + 32 * j < a.H8) x[j] = s[c0 + 32 * j];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c0 + 32 * j < a.H8) d[c0 + 32 * j] = x[j];
+        }
     }
 }
 
@@ -618,11 +639,12 @@ struct JoinArgs {
     int64_t T;
     int64_t items;   // 256-column pieces of all tokens; 0: no join
     int k;
-    int H8;
+    int H8, ld8;     // 16-byte pieces of a row, and between the rows of `rows`
     // gradient of the weights: pieces of each row's dot product, [parts][ld]
     const float* dots;
     int parts;
     int64_t ld;
+    int capacity;    // rows that the buffers hold
     const int* choice;  // the plan's rows
     const int* end;
     void* dweights;
@@ -645,13 +667,13 @@ __global__ void __launch_bounds__(kRowsThreads) moe_join_kernel(const JoinArgs a
     if (a.dweights) {
         for (int64_t i = tid; i < a.T * a.k; i += threads)  // choices that are none
             if (a.slots[i] < 0) store_w(a.dweights, i, 0.0f, a.wtype);
-        const int64_t end = __ldg(a.end);
+        const int64_t end = min(*a.end, a.capacity);
         for (int64_t r = tid; r < end; r += threads) {
             const int i = a.choice[r];
-            if (i < 0) continue;
+            if (i < 0 || i >= a.T * a.k) continue;
             float s = 0.0f;
 #pragma unroll 8
-            for (int p = 0; p < a.parts; ++p) s += __ldg(a.dots + p * a.ld + r);
+            for (int p = 0; p < a.parts; ++p) s += a.dots[p * a.ld + r];
             store_w(a.dweights, i, s, a.wtype);
         }
     }
@@ -661,15 +683,15 @@ __global__ void __launch_bounds__(kRowsThreads) moe_join_kernel(const JoinArgs a
         const int slot = lane < a.k ? a.slots[t * a.k + lane] : -1;
         float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         if (a.residual && c < a.H8)
-            unpack8<kBF16>(__ldg(reinterpret_cast<const uint4*>(a.residual) + t * a.H8 + c), s);
+            unpack8<kBF16>(reinterpret_cast<const uint4*>(a.residual)[t * a.H8 + c], s);
         for (int j0 = 0; j0 < a.k; j0 += 4) {
             uint4 v[4];
             bool on[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int src = __shfl_sync(kFull, slot, (j0 + j) & 31);
-                on[j] = j0 + j < a.k && src >= 0 && c < a.H8;
-                if (on[j]) v[j] = __ldcs(reinterpret_cast<const uint4*>(a.rows) + (int64_t)src * a.H8 + c);
+                on[j] = j0 + j < a.k && src >= 0 && src < a.capacity && c < a.H8;
+                if (on[j]) v[j] = reinterpret_cast<const uint4*>(a.rows)[(int64_t)src * a.ld8 + c];
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
