@@ -122,19 +122,13 @@ FfnPlan plan_seg(int64_t T, int k, int64_t E, int64_t max_tiles, int64_t feats, 
     return p;
 }
 
-// Tiles of the weight gradients: the widest row tile that wastes least.
+// Tiles of the weight gradients: 256 rows of the result, or 128 where that wastes less. (A half
+// tile is whole 64-element chunks of the MN-major rows' operand.)
 FfnPlan plan_red(int64_t E, int64_t rows, int64_t feats, int pairs) {
     FfnPlan p;
     p.num_ft = num_feature_tiles(feats, false);
-    int64_t cost = 0;
-    for (int n = 64; n <= 256; n += 32) {
-        const int64_t c = (int64_t)ceil_div(rows, n) * (std::max(n, 128) + 16);
-        if (p.num_rt == 0 || c <= cost) {
-            cost = c;
-            p.tile_n = n;
-            p.num_rt = ceil_div(rows, n);
-        }
-    }
+    p.tile_n = ceil_div(rows, 256) * 256 * 0.8 > ceil_div(rows, 128) * 128 ? 128 : 256;
+    p.num_rt = ceil_div(rows, p.tile_n);
     p.tiles = E * p.num_ft * p.num_rt;
     p.grid = 2 * (int)std::min<int64_t>(p.tiles, pairs);
     return p;
@@ -258,7 +252,8 @@ int gemm_act(int dtype, const void* A, const void* B, void* C, int64_t M, int64_
     a.rows = (int)M;
     a.red = (int)K;
     a.experts = 1;
-    a.p_deep = a.q_deep = K % 64 == 0;
+    a.p_deep = (bmn ? N : K) % 64 == 0;
+    a.q_deep = amn ? M % 64 == 0 && p.tile_n % 128 == 0 : K % 64 == 0;
     a.q_box = p.tile_n / 2;
     a.act = o.activation;
     a.out = C;
@@ -631,15 +626,6 @@ SplitScratch split_scratch(const FfnPlan& a, const FfnPlan& b) {
     return s;
 }
 
-// Rows per box of the rows' operand: about half an average expert's rows (a CTA loads half a
-// tile), 16 to 64, so that small tiles do not fetch rows they do not multiply.
-int seg_box(const ExpertSizes& s) {
-    const int64_t half = (s.T * s.k / s.E + 1) / 2;
-    int box = 16;
-    while (box < 64 && box < half) box *= 2;
-    return box;
-}
-
 void seg_call(const ExpertSizes& s, bool bf16, const int32_t* plan, const moe_experts_options& o,
               DeviceInfo* info, FfnCall* c) {
     c->bf16 = bf16;
@@ -652,8 +638,6 @@ void seg_call(const ExpertSizes& s, bool bf16, const int32_t* plan, const moe_ex
     a.rows = (int)s.plan.capacity;
     a.offsets = plan + s.plan.offsets;
     a.counts = plan + s.plan.counts;
-    a.q_deep = false;
-    a.q_box = seg_box(s);
     a.timeout_ns = timeout_of(o.timeout_ns);
     a.fault = o.fault_inject;
     a.status = info->status;
@@ -681,7 +665,8 @@ int seg_product(const ExpertSizes& s, bool bf16, const int32_t* plan, const moe_
     dtc::FfnArgs& a = c.args;
     a.feats = (int)feats;
     a.red = (int)red;
-    a.p_deep = red % 64 == 0;
+    a.p_deep = (weights_mn ? feats : red) % 64 == 0;
+    a.q_deep = red % 64 == 0;
     a.p_expert_rows = (int)(gated ? 2 * feats : feats);
     apply_plan(p, nullptr, &c);
     if (p.splits > 1) {
@@ -711,6 +696,7 @@ int red_product(const ExpertSizes& s, bool bf16, const int32_t* plan, const moe_
     a.feats = (int)width_r;
     a.rows = (int)width_l;
     a.red = (int)s.plan.capacity;
+    a.p_deep = a.q_deep = true;  // (the buffers' rows are whole 64-element chunks)
     a.act = dtc::kActNone;
     a.out = out;
     a.ld_out = width_r;

@@ -24,11 +24,12 @@ struct FfnCall {
 };
 int launch_ffn_rows(const FfnCall& c, DeviceInfo* dev, cudaStream_t stream);
 int launch_ffn_experts(const FfnCall& c, DeviceInfo* dev, cudaStream_t stream);
-int ffn_tmaps(const FfnCall& c, CUtensorMap* p, CUtensorMap* q);
+int ffn_tmaps(const FfnCall& c, CUtensorMap* p, dtc::FfnQMaps* q);
 
 template <bool kBF16, int kMode, bool kPMN, bool kQMN, bool kGated, bool kBack = false>
 int launch_ffn(const FfnCall& c, DeviceInfo* dev, cudaStream_t stream) {
-    CUtensorMap tp = {}, tq = {};
+    CUtensorMap tp = {};
+    dtc::FfnQMaps tq = {};
     int rc = ffn_tmaps(c, &tp, &tq);
     if (rc) return rc;
     auto kern = dtc::gemm16_ffn_kernel<kBF16, kMode, kPMN, kQMN, kGated, kBack>;

@@ -49,6 +49,8 @@
 namespace dtc {
 
 namespace ffn {
+// Epilogue warps: two per quarter of the accumulator lanes. More (12, 16) did not finish tiles
+// faster: the accumulator and shared-memory reads of the MMA beside them set the pace.
 constexpr int kEpWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpWarps;
 constexpr int kBK = 128;
@@ -82,12 +84,13 @@ struct FfnArgs {
     int rows;     // kRows: rows; kSeg: rows of the buffers; kRed: rows of one output matrix (Q's
                   // columns)
     int red;      // reduction length (kRows, kSeg); kRed: the rows of the operands' buffers
-    int tile_n;   // kRows, kRed: rows per tile (a multiple of 32)
+    int tile_n;   // rows per tile (a multiple of 32; kSeg: at most)
     int num_ft, num_rt;
     int experts;
     int splits, kb_per_split;
-    bool p_deep, q_deep;  // operand loaded by one box of two 64-element K-chunks per stage
-    int q_box;            // K-major Q: rows per box
+    bool p_deep, q_deep;  // the operand's stage is one box (K-major: two 64-element K-chunks;
+                          // MN-major: all its 64-element chunks), else one box a chunk
+    int q_box;            // kRows, K-major Q: rows per box (half a tile)
     const FfnTile* tiles;   // kSeg
     const int* num_tiles;   // kSeg
     int max_tiles;          // kSeg: records that the plan has room for
@@ -115,7 +118,21 @@ struct FfnArgs {
     int* status;
 };
 
+// Tensor maps of the rows' operand. The rows of an expert's tile vary, and a box must be one
+// instruction (few large copies feed an SM faster than many small ones: 64 KB a stage as two boxes
+// streams at 81-83 bytes a cycle, as four at 57-64), so there is a map for each of five box heights
+// and a tile takes the lowest that holds its half. Others use the first map only.
+constexpr int kQMaps = 5;
+struct FfnQMaps {
+    CUtensorMap m[kQMaps];
+};
+
 namespace ffn {
+
+__host__ __device__ constexpr int box_rows(int i) { return i == 0 ? 16 : i == 1 ? 32 : 32 * i; }
+__device__ __forceinline__ int box_of(int half) {
+    return half <= 16 ? 0 : half <= 32 ? 1 : (half + 31) / 32;
+}
 
 struct Item {
     int f0;      // first feature of the pair tile
@@ -160,7 +177,7 @@ __device__ __forceinline__ bool get_item(const FfnArgs& a, int t, int seg_tiles,
         const int4 s = reinterpret_cast<const int4*>(a.tiles)[rt];
         // a record that no plan of these sizes holds (a stale or foreign plan) ends the walk: the
         // MMA's shape and the rows written come from it
-        if ((unsigned)s.x >= (unsigned)a.experts || s.z < 1 || s.z > kMaxRows || s.y < 0 ||
+        if ((unsigned)s.x >= (unsigned)a.experts || s.z < 1 || s.z > a.tile_n || s.y < 0 ||
             s.y > a.rows - s.z)
             return false;
         w.f0 = (tile - rt * a.num_ft) * kFeats;
@@ -510,7 +527,7 @@ __device__ __forceinline__ void finish_block(const FfnArgs& a, float (&v)[4][8],
 template <bool kBF16, int kMode, bool kPMN, bool kQMN, bool kGated, bool kBack>
 __global__ void __launch_bounds__(ffn::kThreads, 1)
     gemm16_ffn_kernel(const __grid_constant__ CUtensorMap tmP,
-                      const __grid_constant__ CUtensorMap tmQ, const FfnArgs args) {
+                      const __grid_constant__ FfnQMaps tmQ, const FfnArgs args) {
     using namespace ffn;
     static_assert(!kGated || (!kPMN && !kQMN), "the gated form takes K-major operands");
     static_assert(!kBack || (kMode == kSeg && !kGated), "the backward epilogue: rows of experts");
@@ -551,7 +568,7 @@ __global__ void __launch_bounds__(ffn::kThreads, 1)
     }
     if (warp == 0 && lane == 0 && args.red > 0) {  // (a product with K = 0 has no tensor maps)
         tma_prefetch_desc(&tmP);
-        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmQ.m[0]);
     }
     if (warp == 1) {
         tmem_alloc<2>(smem_u32(&tmem_slot), kTmemCols);
@@ -578,10 +595,12 @@ __global__ void __launch_bounds__(ffn::kThreads, 1)
                 const int nh = w.n / 2;  // rows of Q per CTA
                 const int q_row = w.r0 + (int)rank * nh;
                 const int f_row = (kGated ? w.f0 + (int)rank * 64 : w.f0 + (int)rank * 128);
-                // boxes of Q per stage (per K-chunk for K-major 2-D boxes) and their bytes
-                const int q_boxes = kQMN ? (nh + 63) / 64 : (nh + args.q_box - 1) / args.q_box;
-                const uint32_t q_bytes = kQMN ? q_boxes * (64u * kBK * 2u)
-                                              : (uint32_t)q_boxes * args.q_box * (kBK * 2u);
+                // Q: its map, the rows of a box (K-major) and the bytes of a stage
+                const int qi = kMode == kSeg ? box_of(nh) : 0;
+                const CUtensorMap* const q_map = &tmQ.m[qi];
+                const int q_rows = kMode == kSeg ? box_rows(qi) : args.q_box;
+                const int q_chunks = (nh + 63) / 64;  // MN-major
+                const uint32_t q_bytes = kQMN ? q_chunks * (64u * kBK * 2u) : (uint32_t)q_rows * (kBK * 2u);
                 for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
                     const uint32_t s = it % kStages, ph = (it / kStages) & 1u;
                     if (!wait_bounded(smem_u32(&bar_empty[s]), ph ^ 1u, abort, args.timeout_ns,
@@ -595,12 +614,15 @@ __global__ void __launch_bounds__(ffn::kThreads, 1)
                     if (leader) mbar_arrive_expect_tx(full_local, 2 * (kPStage + q_bytes));
                     const uint32_t p = sP + s * kPStage, q = sQ + s * kQStage;
                     if constexpr (kPMN) {
-                        // stored [reduction, features]: two boxes of 64 features x 128 rows; the
-                        // third coordinate is the expert's matrix
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            tma_load_3d_pair(p + j * (64 * kBK * 2), &tmP, full, f_row + j * 64,
-                                             w.krow + kb * kBK, kMode == kSeg ? w.expert : 0);
+                        // stored [reduction, features]: two chunks of 64 features x 128 rows; the
+                        // last coordinate is the expert's matrix
+                        const int e = kMode == kSeg ? w.expert : 0, k0 = w.krow + kb * kBK;
+                        if (args.p_deep) {
+                            tma_load_4d_pair(p, &tmP, full, 0, k0, f_row / 64, e);
+                        } else {
+                            tma_load_3d_pair(p, &tmP, full, f_row, k0, e);
+                            tma_load_3d_pair(p + kPStage / 2, &tmP, full, f_row + 64, k0, e);
+                        }
                     } else if constexpr (kGated) {
                         const int oct = (w.expert * args.p_expert_rows + f_row) / 8;
                         if (args.p_deep) {
@@ -619,18 +641,18 @@ __global__ void __launch_bounds__(ffn::kThreads, 1)
                         }
                     }
                     if constexpr (kQMN) {
-                        for (int j = 0; j < q_boxes; ++j)
-                            tma_load_2d_pair(q + j * (64 * kBK * 2), &tmQ, full, q_row + j * 64,
-                                             w.krow + kb * kBK);
-                    } else if (args.q_deep) {
-                        tma_load_3d_pair(q, &tmQ, full, 0, q_row, kb * 2);
-                    } else {
-                        for (int j = 0; j < q_boxes; ++j) {
-                            const int y = q_row + j * args.q_box;
-                            const uint32_t d = q + j * args.q_box * 128;
-                            tma_load_2d_pair(d, &tmQ, full, kb * kBK, y);
-                            tma_load_2d_pair(d + kQStage / 2, &tmQ, full, kb * kBK + 64, y);
+                        const int k0 = w.krow + kb * kBK;
+                        if (args.q_deep) {
+                            tma_load_3d_pair(q, q_map, full, 0, k0, q_row / 64);
+                        } else {
+                            for (int j = 0; j < q_chunks; ++j)
+                                tma_load_2d_pair(q + j * (64 * kBK * 2), q_map, full, q_row + j * 64, k0);
                         }
+                    } else if (args.q_deep) {
+                        tma_load_3d_pair(q, q_map, full, 0, q_row, kb * 2);
+                    } else {
+                        tma_load_2d_pair(q, q_map, full, kb * kBK, q_row);
+                        tma_load_2d_pair(q + q_rows * 128, q_map, full, kb * kBK + 64, q_row);
                     }
                 }
             }
@@ -668,7 +690,8 @@ __global__ void __launch_bounds__(ffn::kThreads, 1)
                 const uint32_t idesc = idesc_f16(kBF16, kQMN, 256, w.n, kPMN);
                 const uint32_t d_tmem = tmem_base + b * kAccStride;
                 // bytes from a K-major stage's first 64-element K-chunk of Q to its second
-                const uint32_t q_chunk = args.q_deep ? (uint32_t)(w.n / 2) * 128u : kQStage / 2;
+                const uint32_t q_chunk =
+                    (uint32_t)(kMode == kSeg ? box_rows(box_of(w.n / 2)) : args.q_box) * 128u;
                 for (int kb = w.kb0; kb < w.kb1; ++kb) {
                     if (!wait_bounded(smem_u32(&bar_full[s]), ph, abort, args.timeout_ns,
                                       args.status, 43)) {

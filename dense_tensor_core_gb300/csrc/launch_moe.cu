@@ -29,19 +29,31 @@ dtc::RouteArgs route_args(const RouteCall& c) {
     return a;
 }
 
-// Experts per lane: the smallest instantiation that holds E.
+// Experts per lane: the smallest instantiation that holds E. Lanes of consecutive experts where E
+// fills them, the groups are whole lanes (then 32 / groups of them) and the rows and the bias can be
+// read as vectors.
 template <int kType, bool kBack>
-int route_by_size(const dtc::RouteArgs& a, cudaStream_t s) {
-    const dim3 grid((unsigned)((a.T + dtc::kRouteWarps - 1) / dtc::kRouteWarps));
+int route_by_size(const dtc::RouteArgs& a, DeviceInfo* dev, cudaStream_t s) {
     const int threads = dtc::kRouteWarps * 32;
+    const int64_t want = (a.T + dtc::kRouteWarps - 1) / dtc::kRouteWarps;
+    // the forward kernel walks over tokens with the bias in registers: blocks for the device's
+    // threads; the backward one takes a token a warp
+    const dim3 grid((unsigned)(kBack ? want : std::min<int64_t>(want, (int64_t)dev->model.sms * 16)));
     auto go = [&](auto kern) { return launch_chain(kern, grid, threads, 0, 1, true, s, a); };
     const int v = (a.E + 31) / 32;
-#define DTC_ROUTE(N)                                             \
-    if (v <= N) {                                                \
-        if constexpr (kBack)                                     \
-            return go(dtc::moe_route_backward_kernel<kType, N>); \
-        else                                                     \
-            return go(dtc::moe_route_kernel<kType, N>);          \
+    const uintptr_t lane_bytes = std::min<uintptr_t>(16, (uintptr_t)v * (kType == 2 ? 4 : 2));
+    const bool run = a.E == 32 * v && (v & (v - 1)) == 0 && a.per_group % v == 0 &&
+                     (a.groups & (a.groups - 1)) == 0 &&
+                     (reinterpret_cast<uintptr_t>(a.logits) | (uintptr_t)a.ld * (kType == 2 ? 4 : 2)) % lane_bytes == 0 &&
+                     reinterpret_cast<uintptr_t>(a.bias) % std::min<uintptr_t>(16, (uintptr_t)v * 4) == 0;
+#define DTC_ROUTE(N)                                                      \
+    if (v <= N) {                                                         \
+        if constexpr (kBack) {                                            \
+            return go(dtc::moe_route_backward_kernel<kType, N>);          \
+        } else {                                                          \
+            return run && v == N ? go(dtc::moe_route_kernel<kType, N, true>) \
+                                 : go(dtc::moe_route_kernel<kType, N, false>); \
+        }                                                                 \
     }
     DTC_ROUTE(1)
     DTC_ROUTE(2)
@@ -54,11 +66,11 @@ int route_by_size(const dtc::RouteArgs& a, cudaStream_t s) {
 }
 
 template <bool kBack>
-int route_any(const RouteCall& c, cudaStream_t s) {
+int route_any(const RouteCall& c, DeviceInfo* dev, cudaStream_t s) {
     const dtc::RouteArgs a = route_args(c);
-    if (c.dtype == 0) return route_by_size<0, kBack>(a, s);
-    if (c.dtype == 1) return route_by_size<1, kBack>(a, s);
-    return route_by_size<2, kBack>(a, s);
+    if (c.dtype == 0) return route_by_size<0, kBack>(a, dev, s);
+    if (c.dtype == 1) return route_by_size<1, kBack>(a, dev, s);
+    return route_by_size<2, kBack>(a, dev, s);
 }
 
 // One warp per row: as many blocks as fill the device's threads, at most one per 8 rows.
@@ -69,11 +81,11 @@ int rows_grid(int64_t warps, DeviceInfo* dev) {
 
 }  // namespace
 
-int launch_moe_route(const RouteCall& c, DeviceInfo*, cudaStream_t stream) {
-    return route_any<false>(c, stream);
+int launch_moe_route(const RouteCall& c, DeviceInfo* dev, cudaStream_t stream) {
+    return route_any<false>(c, dev, stream);
 }
-int launch_moe_route_backward(const RouteCall& c, DeviceInfo*, cudaStream_t stream) {
-    return route_any<true>(c, stream);
+int launch_moe_route_backward(const RouteCall& c, DeviceInfo* dev, cudaStream_t stream) {
+    return route_any<true>(c, dev, stream);
 }
 
 int launch_moe_plan(const int* indices, int64_t T, int k, int64_t E, int32_t* plan,

@@ -45,20 +45,23 @@ __device__ __forceinline__ float warp_max(float v) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// moe_route: a warp per token, the token's logits in registers (expert e = lane + 32 j).
+// moe_route: a warp per token, the token's logits in registers. Where the sizes allow (E = 32 kVPL,
+// rows and bias aligned to 16 bytes or to a lane's kVPL elements) a lane holds consecutive experts
+// e = lane kVPL + j, which loads as vectors and puts a group of experts into whole lanes; else
+// e = lane + 32 j, with the groups scanned in shared memory.
 //
 // The choice compares keys as unsigned integers in the order of their floats; 0 stands for "cannot
 // be chosen" and is below every key. Keys are computed with the correctly rounded operations and
 // the standard exponential (not the fast forms), so that a choice between near-equal keys does not
 // depend on an approximation.
 //
-// Top-k in two steps. The k-th largest of the 32 lanes' maxima is a lower bound of the k-th largest
-// key, and usually only a few more than k keys reach it: those are compacted, in index order, to
-// one per lane, and k rounds of one warp maximum and one ballot pick them in order (the lowest lane
-// of the ballot is the lowest index). Where ties leave more than 32, k rounds over all keys do.
+// Top-k in two steps. The k-th largest of the 32 lanes' maxima (a bitonic sort) is a lower bound of
+// the k-th largest key, and usually only a few more than k keys reach it: those are compacted, in
+// index order, to one per lane, and each counts the candidates before it, which is its place. Where
+// ties leave more than 32, k rounds over all keys do.
 //
-// Bound by the issue of instructions, not by HBM: for 256 experts about half of them are the 8
-// exact logistic functions a lane computes.
+// Bound by the issue of instructions, not by HBM: for 256 experts a third of them are the 8 exact
+// logistic functions a lane computes.
 // ------------------------------------------------------------------------------------------------
 struct RouteArgs {
     const void* logits;
@@ -79,10 +82,11 @@ struct RouteArgs {
 
 constexpr int kRouteWarps = 4;
 
-// Floats in the order of unsigned integers; both zeros alike. -infinity and above give > 0.
+// Floats in the order of unsigned integers; both zeros alike (the sum below turns -0 into +0).
+// -infinity and above give > 0.
 __device__ __forceinline__ uint32_t order_key(float f) {
-    const uint32_t u = __float_as_uint(f == 0.0f ? 0.0f : f);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    const uint32_t u = __float_as_uint(__fadd_rn(f, 0.0f));
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float from_key(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
@@ -90,171 +94,255 @@ __device__ __forceinline__ float from_key(uint32_t k) {
 
 __device__ __forceinline__ float sigmoid_exact(float z) { return __frcp_rn(1.0f + expf(-z)); }
 
-template <int kType, int kVPL>
+// kN consecutive elements, aligned to the vector (16 bytes at most an access).
+template <int kType, int kN>
+__device__ __forceinline__ void load_run(const void* p, int64_t i, float (&v)[kN]) {
+    constexpr int kBytes = kN * (kType == 2 ? 4 : 2);
+    const char* const at = static_cast<const char*>(p) + i * (kType == 2 ? 4 : 2);
+    if constexpr (kBytes >= 4) {
+        uint32_t w[kBytes / 4];
+        if constexpr (kBytes >= 16) {
+#pragma unroll
+            for (int c = 0; c < kBytes / 16; ++c) {
+                const uint4 u = reinterpret_cast<const uint4*>(at)[c];
+                w[4 * c] = u.x;
+                w[4 * c + 1] = u.y;
+                w[4 * c + 2] = u.z;
+                w[4 * c + 3] = u.w;
+            }
+        } else if constexpr (kBytes == 8) {
+            const uint2 u = *reinterpret_cast<const uint2*>(at);
+            w[0] = u.x;
+            w[1] = u.y;
+        } else {
+            w[0] = *reinterpret_cast<const uint32_t*>(at);
+        }
+#pragma unroll
+        for (int j = 0; j < kN; ++j) {
+            if constexpr (kType == 2) {
+                v[j] = __uint_as_float(w[j]);
+            } else {
+                const float2 f = ffn::unpack2<kType == 0>(w[j / 2]);
+                v[j] = j & 1 ? f.y : f.x;
+            }
+        }
+    } else {
+        v[0] = load_f<kType>(p, i);
+    }
+}
+
+template <int kType, int kVPL, bool kRun>
 __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const RouteArgs a) {
-    __shared__ uint32_t group_keys[kRouteWarps][kVPL * 32];
+    __shared__ uint32_t group_keys[kRouteWarps][kRun ? 1 : kVPL * 32];
     __shared__ uint32_t cands[kRouteWarps][32];
     __shared__ uint16_t cands_at[kRouteWarps][32];
     grid_launch_dependents();
     grid_dependency_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
-    if (t >= a.T) return;
-    const int64_t row = t * a.ld;
-    float z[kVPL];
-    uint32_t key[kVPL];
+    const unsigned below_me = (1u << lane) - 1u;
+    auto expert = [&](int j) { return kRun ? lane * kVPL + j : lane + 32 * j; };
+    float bias[kVPL];
 #pragma unroll
-    for (int j = 0; j < kVPL; ++j) {
-        const int e = lane + 32 * j;
-        z[j] = e < a.E ? load_f<kType>(a.logits, row + e) : -CUDART_INF_F;
-    }
+    for (int j = 0; j < kVPL; ++j) bias[j] = 0.0f;
+    if (a.bias) {
+        if constexpr (kRun) {
+            load_run<2, kVPL>(a.bias, lane * kVPL, bias);
+        } else {
 #pragma unroll
-    for (int j = 0; j < kVPL; ++j) {
-        const int e = lane + 32 * j;
-        float s = a.sigmoid ? sigmoid_exact(z[j]) : z[j];
-        if (a.bias && e < a.E) s = s + a.bias[e];
-        // masked: -infinity or NaN, in the logit or in the key
-        key[j] = (z[j] > -CUDART_INF_F && s > -CUDART_INF_F) ? order_key(s) : 0u;
-    }
-    if (a.groups > 1) {
-        uint32_t* const keys = group_keys[warp];
-#pragma unroll
-        for (int j = 0; j < kVPL; ++j) keys[lane + 32 * j] = key[j];
-        __syncwarp();
-        // lanes_per lanes scan a group for its two largest keys, then join
-        int lanes_per = 32;
-        while (lanes_per * a.groups > 32) lanes_per >>= 1;
-        const int g = lane / lanes_per, sub = lane - g * lanes_per;
-        uint32_t m1 = 0, m2 = 0;
-        if (g < a.groups)
-            for (int i = sub; i < a.per_group; i += lanes_per) {
-                const uint32_t v = keys[g * a.per_group + i];
-                m2 = max(m2, min(m1, v));
-                m1 = max(m1, v);
-            }
-        for (int o = lanes_per >> 1; o; o >>= 1) {
-            const uint32_t n1 = __shfl_xor_sync(kFull, m1, o), n2 = __shfl_xor_sync(kFull, m2, o);
-            m2 = max(max(m2, n2), min(m1, n1));
-            m1 = max(m1, n1);
+            for (int j = 0; j < kVPL; ++j)
+                if (expert(j) < a.E) bias[j] = a.bias[expert(j)];
         }
-        uint32_t score = 0;
-        if (sub == 0 && m1) score = order_key(from_key(m1) + (a.sigmoid && m2 ? from_key(m2) : 0.0f));
-        uint32_t keep = 0;
-        for (int i = 0; i < a.top_groups; ++i) {
-            const uint32_t best = __reduce_max_sync(kFull, score);
-            if (best == 0) break;
-            const unsigned at = __reduce_min_sync(kFull, score == best ? (unsigned)g : 64u);
-            keep |= 1u << at;
-            if (g == (int)at) score = 0;
+    }
+    for (int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp; t < a.T; t += (int64_t)gridDim.x * kRouteWarps) {
+        const int64_t row = t * a.ld;
+        float z[kVPL];
+        uint32_t key[kVPL];
+        if constexpr (kRun) {
+            load_run<kType, kVPL>(a.logits, row + lane * kVPL, z);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kVPL; ++j)
+                z[j] = expert(j) < a.E ? load_f<kType>(a.logits, row + expert(j)) : -CUDART_INF_F;
         }
 #pragma unroll
         for (int j = 0; j < kVPL; ++j) {
-            const uint32_t eg = ((uint32_t)(lane + 32 * j) * a.div_magic) >> 20;
-            if (eg >= 32u || !((keep >> eg) & 1u)) key[j] = 0;
+            float s = a.sigmoid ? sigmoid_exact(z[j]) : z[j];
+            if (a.bias) s = __fadd_rn(s, bias[j]);
+            // masked: -infinity or NaN, in the logit or in the key
+            key[j] = (z[j] > -CUDART_INF_F && s > -CUDART_INF_F) ? order_key(s) : 0u;
         }
-    }
-    // the k largest keys: lane with mine >= 0 holds choice number `place`
-    int mine = -1, place = -1, found = 0;
-    uint32_t cand = key[0];
-    int cand_at = lane;
-    bool few = true;
-    if constexpr (kVPL > 1) {
-        uint32_t m = key[0];
+        if (a.groups > 1) {
+            // a group's two largest keys, from lanes_per lanes
+            uint32_t m1 = 0, m2 = 0;
+            int lanes_per = 32, g, sub;
+            if constexpr (kRun) {
+                lanes_per = a.per_group / kVPL;  // (32 / groups)
+                g = lane / lanes_per;
+                sub = lane - g * lanes_per;
 #pragma unroll
-        for (int j = 1; j < kVPL; ++j) m = max(m, key[j]);
-        uint32_t bound = 1;
-        for (int i = 0; i < a.k; ++i) {
-            const uint32_t best = __reduce_max_sync(kFull, m);
-            if (best == 0) {
-                bound = 1;
-                break;
-            }
-            bound = best;
-            if (lane == __ffs(__ballot_sync(kFull, m == best)) - 1) m = 0;
-        }
-        int n = 0;
+                for (int j = 0; j < kVPL; ++j) {
+                    m2 = max(m2, min(m1, key[j]));
+                    m1 = max(m1, key[j]);
+                }
+            } else {
+                uint32_t* const keys = group_keys[warp];
+                __syncwarp();
 #pragma unroll
-        for (int j = 0; j < kVPL; ++j) {
-            const bool in = key[j] >= bound;
-            const unsigned b = __ballot_sync(kFull, in);
-            const int at = n + __popc(b & ((1u << lane) - 1u));
-            if (in && at < 32) {
-                cands[warp][at] = key[j];
-                cands_at[warp][at] = (uint16_t)(lane + 32 * j);
+                for (int j = 0; j < kVPL; ++j) keys[lane + 32 * j] = key[j];
+                __syncwarp();
+                while (lanes_per * a.groups > 32) lanes_per >>= 1;
+                g = lane / lanes_per;
+                sub = lane - g * lanes_per;
+                if (g < a.groups)
+                    for (int i = sub; i < a.per_group; i += lanes_per) {
+                        const uint32_t v = keys[g * a.per_group + i];
+                        m2 = max(m2, min(m1, v));
+                        m1 = max(m1, v);
+                    }
             }
-            n += __popc(b);
-        }
-        few = n <= 32;
-        __syncwarp();
-        cand = lane < n ? cands[warp][lane] : 0u;
-        cand_at = cands_at[warp][lane];
-    }
-    if (few) {
-        for (int i = 0; i < a.k; ++i) {
-            const uint32_t best = __reduce_max_sync(kFull, cand);
-            if (best == 0) break;
-            if (lane == __ffs(__ballot_sync(kFull, cand == best)) - 1) {
-                mine = cand_at;
-                place = i;
-                cand = 0;
+            for (int o = lanes_per >> 1; o; o >>= 1) {
+                const uint32_t n1 = __shfl_xor_sync(kFull, m1, o), n2 = __shfl_xor_sync(kFull, m2, o);
+                m2 = max(max(m2, n2), min(m1, n1));
+                m1 = max(m1, n1);
             }
-            ++found;
+            uint32_t score = 0;
+            if (sub == 0 && m1)
+                score = order_key(__fadd_rn(from_key(m1), a.sigmoid && m2 ? from_key(m2) : 0.0f));
+            // a group stays if fewer than top_groups groups come before it (the lower one on ties)
+            int rank = 0;
+            for (int i = 0; i < 32; i += lanes_per) {
+                const uint32_t o = __shfl_sync(kFull, score, i);
+                rank += o > score || (o == score && i < lane) ? 1 : 0;
+            }
+            const unsigned heads = __ballot_sync(kFull, score != 0 && rank < a.top_groups);
+            if constexpr (kRun) {
+                if (!((heads >> (lane - sub)) & 1u)) {
+#pragma unroll
+                    for (int j = 0; j < kVPL; ++j) key[j] = 0;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < kVPL; ++j) {
+                    const uint32_t eg = ((uint32_t)expert(j) * a.div_magic) >> 20;
+                    if (eg >= (uint32_t)a.groups || !((heads >> (eg * lanes_per)) & 1u)) key[j] = 0;
+                }
+            }
         }
-    } else {
-        for (int i = 0; i < a.k; ++i) {
+        // the k largest keys: lane with mine >= 0 holds choice number `place`
+        int mine = -1, place = -1, found = 0;
+        uint32_t cand = key[0];
+        int cand_at = lane;
+        bool few = true;
+        if constexpr (kVPL > 1) {
             uint32_t m = key[0];
 #pragma unroll
             for (int j = 1; j < kVPL; ++j) m = max(m, key[j]);
-            const uint32_t best = __reduce_max_sync(kFull, m);
-            if (best == 0) break;
-            unsigned at = 0xffffu;
+            // the lanes' maxima in falling order (a bitonic sort), of which the k-th is the bound
 #pragma unroll
-            for (int j = kVPL - 1; j >= 0; --j)
-                if (key[j] == best) at = lane + 32 * j;
-            at = __reduce_min_sync(kFull, at);
-            if (lane == i) {
-                mine = (int)at;
-                place = i;
+            for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+                for (int o = size >> 1; o; o >>= 1) {
+                    const uint32_t other = __shfl_xor_sync(kFull, m, o);
+                    const bool larger = ((lane & o) == 0) == ((lane & size) == 0 || size == 32);
+                    m = larger ? max(m, other) : min(m, other);
+                }
+            const uint32_t bound = max(__shfl_sync(kFull, m, a.k - 1), 1u);
+            int n = 0, at = 0;  // all candidates; those before this lane's next one
+            unsigned in[kVPL];
+#pragma unroll
+            for (int j = 0; j < kVPL; ++j) {
+                in[j] = __ballot_sync(kFull, key[j] >= bound);
+                n += __popc(in[j]);
+                if (kRun) at += __popc(in[j] & below_me);
             }
+            few = n <= 32;
+            __syncwarp();  // the candidates of the token before have been read
+            if (few) {
+#pragma unroll
+                for (int j = 0; j < kVPL; ++j) {
+                    if (key[j] >= bound) {
+                        const int to = kRun ? at : at + __popc(in[j] & below_me);
+                        cands[warp][to] = key[j];
+                        cands_at[warp][to] = (uint16_t)expert(j);
+                        if (kRun) ++at;
+                    }
+                    if (!kRun) at += __popc(in[j]);
+                }
+            }
+            __syncwarp();
+            cand = lane < n ? cands[warp][lane] : 0u;
+            cand_at = cands_at[warp][lane];
+        }
+        if (few) {
+            // a candidate's place: how many come before it (they stand in the order of their index)
+            const unsigned live = __ballot_sync(kFull, cand != 0);
+            int rank = 0;
+            for (unsigned left = live; left; left &= left - 1) {
+                const int i = __ffs(left) - 1;
+                const uint32_t o = __shfl_sync(kFull, cand, i);
+                rank += o > cand || (o == cand && i < lane) ? 1 : 0;
+            }
+            found = min(__popc(live), a.k);
+            if (cand != 0 && rank < a.k) {
+                mine = cand_at;
+                place = rank;
+            }
+        } else {
+            for (int i = 0; i < a.k; ++i) {
+                uint32_t m = key[0];
+#pragma unroll
+                for (int j = 1; j < kVPL; ++j) m = max(m, key[j]);
+                const uint32_t best = __reduce_max_sync(kFull, m);
+                if (best == 0) break;
+                unsigned at = 0xffffu;
+#pragma unroll
+                for (int j = kVPL - 1; j >= 0; --j)
+                    if (key[j] == best) at = expert(j);
+                at = __reduce_min_sync(kFull, at);
+                if (lane == i) {
+                    mine = (int)at;
+                    place = i;
+                }
+#pragma unroll
+                for (int j = 0; j < kVPL; ++j)
+                    if (expert(j) == (int)at) key[j] = 0;
+                ++found;
+            }
+        }
+        const bool got = mine >= 0;
+        const float zi = got ? load_f<kType>(a.logits, row + mine) : -CUDART_INF_F;
+        float w = 0.0f;
+        if (a.sigmoid) {
+            w = got ? sigmoid_exact(zi) : 0.0f;
+            if (a.renorm) {
+                const float total = warp_sum(w);
+                w = total > 0.0f ? w / total : 0.0f;
+            }
+        } else if (a.renorm) {
+            const float m = warp_max(zi);
+            const float e = got ? expf(zi - m) : 0.0f;
+            const float total = warp_sum(e);
+            w = got ? e / total : 0.0f;
+        } else {
+            float m = -CUDART_INF_F;
+#pragma unroll
+            for (int j = 0; j < kVPL; ++j) m = fmaxf(m, z[j]);  // (fmaxf passes over NaN)
+            m = warp_max(m);
+            float total = 0.0f;
 #pragma unroll
             for (int j = 0; j < kVPL; ++j)
-                if (lane + 32 * j == (int)at) key[j] = 0;
-            ++found;
+                if (z[j] > -CUDART_INF_F) total += expf(z[j] - m);
+            total = warp_sum(total);
+            w = got ? expf(zi - m) / total : 0.0f;
         }
-    }
-    const bool got = mine >= 0;
-    const float zi = got ? load_f<kType>(a.logits, row + mine) : -CUDART_INF_F;
-    float w = 0.0f;
-    if (a.sigmoid) {
-        w = got ? sigmoid_exact(zi) : 0.0f;
-        if (a.renorm) {
-            const float total = warp_sum(w);
-            w = total > 0.0f ? w / total : 0.0f;
+        if (got) {
+            a.weights[t * a.k + place] = w * a.scale;
+            a.indices[t * a.k + place] = mine;
         }
-    } else if (a.renorm) {
-        const float m = warp_max(zi);
-        const float e = got ? expf(zi - m) : 0.0f;
-        const float total = warp_sum(e);
-        w = got ? e / total : 0.0f;
-    } else {
-        float m = -CUDART_INF_F;
-#pragma unroll
-        for (int j = 0; j < kVPL; ++j) m = fmaxf(m, z[j]);  // (fmaxf passes over NaN)
-        m = warp_max(m);
-        float total = 0.0f;
-#pragma unroll
-        for (int j = 0; j < kVPL; ++j)
-            if (z[j] > -CUDART_INF_F) total += expf(z[j] - m);
-        total = warp_sum(total);
-        w = got ? expf(zi - m) / total : 0.0f;
-    }
-    if (got) {
-        a.weights[t * a.k + place] = w * a.scale;
-        a.indices[t * a.k + place] = mine;
-    }
-    if (lane >= found && lane < a.k) {  // fewer than k could be chosen
-        a.weights[t * a.k + lane] = 0.0f;
-        a.indices[t * a.k + lane] = -1;
+        if (lane >= found && lane < a.k) {  // fewer than k could be chosen
+            a.weights[t * a.k + lane] = 0.0f;
+            a.indices[t * a.k + lane] = -1;
+        }
     }
 }
 
