@@ -214,11 +214,12 @@ int gemm_act(int dtype, const void* A, const void* B, void* C, int64_t M, int64_
     const bool amn = a_is_mn(layout), bmn = b_is_mn(layout);
     const int64_t Nb = gated ? 2 * N : N;
     if ((rc = check_workspace(o.workspace))) return rc;
-    if ((rc = check_rows("A", A, amn ? K : M, amn ? M : K, &o.lda, false)) ||
-        (rc = check_rows("B", B, bmn ? K : Nb, bmn ? N : K, &o.ldb, false)) ||
+    const bool any = M > 0 && N > 0;  // (an empty result needs no operands)
+    if ((rc = check_rows("A", A, any ? (amn ? K : M) : 0, amn ? M : K, &o.lda, false)) ||
+        (rc = check_rows("B", B, any ? (bmn ? K : Nb) : 0, bmn ? N : K, &o.ldb, false)) ||
         (rc = check_rows("C", C, M, N, &o.ldc)))
         return rc;
-    if (M == 0 || N == 0) return GEMM_OK;
+    if (!any) return GEMM_OK;
     if (o.residual && (rc = check_rows("residual", o.residual, M, N, &o.ld_residual))) return rc;
     if (o.preact && (rc = check_rows("preact", o.preact, M, Nb, &o.ld_preact))) return rc;
     if (o.bias && !aligned(o.bias, 16))

@@ -178,7 +178,7 @@ __device__ __forceinline__ bool get_item(const FfnArgs& a, int t, int seg_tiles,
         // a record that no plan of these sizes holds (a stale or foreign plan) ends the walk: the
         // MMA's shape and the rows written come from it
         if ((unsigned)s.x >= (unsigned)a.experts || s.z < 1 || s.z > a.tile_n || s.y < 0 ||
-            s.y > a.rows - s.z)
+            s.y > a.rows - s.z || (s.y & (kSegAlign - 1)))
             return false;
         w.f0 = (tile - rt * a.num_ft) * kFeats;
         w.expert = s.x;

@@ -228,8 +228,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
                 }
             }
         }
-        // the k largest keys: lane with mine >= 0 holds choice number `place`
-        int mine = -1, place = -1, found = 0;
+        // the k largest keys: lane i holds choice number i (so that sums over the choices run in
+        // their order, whatever the lanes' experts are)
+        int mine = -1;
         uint32_t cand = key[0];
         int cand_at = lane;
         bool few = true;
@@ -282,11 +283,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
                 const uint32_t o = __shfl_sync(kFull, cand, i);
                 rank += o > cand || (o == cand && i < lane) ? 1 : 0;
             }
-            found = min(__popc(live), a.k);
-            if (cand != 0 && rank < a.k) {
-                mine = cand_at;
-                place = rank;
-            }
+            __syncwarp();
+            if (cand != 0 && rank < a.k) cands_at[warp][rank] = (uint16_t)cand_at;
+            __syncwarp();
+            if (lane < min(__popc(live), a.k)) mine = cands_at[warp][lane];
         } else {
             for (int i = 0; i < a.k; ++i) {
                 uint32_t m = key[0];
@@ -299,14 +299,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
                 for (int j = kVPL - 1; j >= 0; --j)
                     if (key[j] == best) at = expert(j);
                 at = __reduce_min_sync(kFull, at);
-                if (lane == i) {
-                    mine = (int)at;
-                    place = i;
-                }
+                if (lane == i) mine = (int)at;
 #pragma unroll
                 for (int j = 0; j < kVPL; ++j)
                     if (expert(j) == (int)at) key[j] = 0;
-                ++found;
             }
         }
         const bool got = mine >= 0;
@@ -335,13 +331,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
             total = warp_sum(total);
             w = got ? expf(zi - m) / total : 0.0f;
         }
-        if (got) {
-            a.weights[t * a.k + place] = w * a.scale;
-            a.indices[t * a.k + place] = mine;
-        }
-        if (lane >= found && lane < a.k) {  // fewer than k could be chosen
-            a.weights[t * a.k + lane] = 0.0f;
-            a.indices[t * a.k + lane] = -1;
+        if (lane < a.k) {  // (weight 0 and index -1 where fewer than k could be chosen)
+            a.weights[t * a.k + lane] = w * a.scale;
+            a.indices[t * a.k + lane] = mine;
         }
     }
 }
