@@ -46,46 +46,60 @@ __global__ void __launch_bounds__(kActBackThreads) act_backward_kernel(const Act
 #pragma unroll
     for (int i = 0; i < 8 * kSets; ++i) s[i / 8][i % 8] = 0.0f;
     if (on) {
-        for (int64_t r = r0 + rl; r < r1; r += 2 * kActBackLanes) {
-            // both rows' loads first: the stores of dz could alias them for all the compiler knows
-            uint4 cx[2], cz[2], cu[2];
-            const bool two = r + kActBackLanes < r1;
+        // two rows at a time, the next two's loads issued before the current ones are worked on (the
+        // stores of dz could alias them for all the compiler knows, so it would not move them up)
+        uint4 x[2][2], z[2][2], u[2][2];
+        auto fetch = [&](int64_t r, uint4 (&cx)[2], uint4 (&cz)[2], uint4 (&cu)[2]) {
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-                const int64_t rr = r + (n && two ? kActBackLanes : 0);
+                const int64_t rr = min(r + n * kActBackLanes, r1 - 1);
                 cx[n] = *reinterpret_cast<const uint4*>(a.dC + rr * a.ldc + col);
                 if (a.z) cz[n] = *reinterpret_cast<const uint4*>(a.z + rr * a.ldz + col);
                 if (kGated && a.z) cu[n] = *reinterpret_cast<const uint4*>(a.z + rr * a.ldz + a.N + col);
             }
+        };
+        auto work = [&](int64_t r, const uint4 (&cx)[2], const uint4 (&cz)[2], const uint4 (&cu)[2]) {
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-                if (n && !two) break;
                 const int64_t rr = r + n * kActBackLanes;
-                float x[8];
-                unpack8<kBF16>(cx[n], x);
+                if (rr >= r1) return;
+                float g[8];
+                unpack8<kBF16>(cx[n], g);
                 if (a.z) {
                     float v[8], d[8];
                     unpack8<kBF16>(cz[n], v);
                     act_both(v, d, act_of_gate(a.act));
                     if constexpr (kGated) {
-                        float u[8];
-                        unpack8<kBF16>(cu[n], u);
+                        float w[8];
+                        unpack8<kBF16>(cu[n], w);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            v[i] *= x[i];
-                            x[i] *= u[i] * d[i];
+                            v[i] *= g[i];
+                            g[i] *= w[i] * d[i];
                             s[1][i] += v[i];
                         }
                         *reinterpret_cast<uint4*>(a.dz + rr * width + a.N + col) = pack8<kBF16>(v);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) x[i] *= d[i];
+                        for (int i = 0; i < 8; ++i) g[i] *= d[i];
                     }
-                    *reinterpret_cast<uint4*>(a.dz + rr * width + col) = pack8<kBF16>(x);
+                    *reinterpret_cast<uint4*>(a.dz + rr * width + col) = pack8<kBF16>(g);
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) s[0][i] += x[i];
+                for (int i = 0; i < 8; ++i) s[0][i] += g[i];
             }
+        };
+        constexpr int kStep = 2 * kActBackLanes;
+        int64_t r = r0 + rl;
+        if (r < r1) fetch(r, x[0], z[0], u[0]);
+        while (r < r1) {
+            if (r + kStep < r1) fetch(r + kStep, x[1], z[1], u[1]);
+            work(r, x[0], z[0], u[0]);
+            r += kStep;
+            if (r >= r1) break;
+            if (r + kStep < r1) fetch(r + kStep, x[0], z[0], u[0]);
+            work(r, x[1], z[1], u[1]);
+            r += kStep;
         }
     }
     if (!a.dbias) return;
@@ -115,7 +129,7 @@ __global__ void __launch_bounds__(kActBackThreads) act_backward_kernel(const Act
     for (int k = 0; k < kSets; ++k) {
         float t = 0.0f;
         const float* p = a.partial + k * a.N + c0;
-#pragma unroll 8
+#pragma unroll 16
         for (unsigned y = 0; y < gridDim.y; ++y) t += p[(int64_t)y * width];
         a.dbias[k * a.N + c0] = t;
     }

@@ -19,43 +19,51 @@ uint64_t up256(uint64_t v) { return (v + 255) & ~(uint64_t)255; }
 // ------------------------------------------------------------------------------------------------
 struct FfnPlan {
     int tile_n = 256, num_ft = 0, num_rt = 0, splits = 1, kb_per_split = 0, grid = 0;
+    int split_tiles = 0;  // the first tiles, of which each is split
     int64_t tiles = 0;
     uint64_t counter_bytes = 0, bytes = 0;  // split-K workspace: counters, then partial sums
+    int64_t items() const { return tiles + (int64_t)split_tiles * (splits - 1); }
 };
 
 int num_feature_tiles(int64_t feats, bool gated) { return ceil_div(feats, gated ? 128 : 256); }
 
 void size_split(FfnPlan* p) {
+    p->counter_bytes = p->bytes = 0;
     if (p->splits <= 1) return;
-    p->counter_bytes = up256((uint64_t)p->tiles * 2 * dtc::ffn::kEpWarps * 4);
-    p->bytes = p->counter_bytes + (uint64_t)p->tiles * p->splits * p->tile_n * 1024;
+    p->counter_bytes = up256((uint64_t)p->split_tiles * 2 * dtc::ffn::kEpWarps * 4);
+    p->bytes = p->counter_bytes + (uint64_t)p->split_tiles * p->splits * p->tile_n * 1024;
 }
 
-// Modelled time of a launch in SM cycles: whole waves of items over the pairs. A K-block of 128
-// costs 4 cycles per row of the tile (the tensor core's rate for 256 features) or the delivery of
-// its operands, measured as about 1.6 cycles per 128-byte row piece that a CTA fetches (256 of the
-// features, one per row of the tile); a piece of rows that do not start on 128-byte lines spans two
-// lines and costs twice that. An item costs 200 more; the last tile's epilogue shows. Split items
-// write their sums and the last of a tile reads them all back.
+// Modelled time of a launch in SM cycles. A K-block of 128 costs 4 cycles per row of the tile (the
+// tensor core's rate for 256 features) or the delivery of its operands, measured as about 1.6 cycles
+// per 128-byte row piece that a CTA fetches (256 of the features, one per row of the tile); a piece
+// of rows that do not start on 128-byte lines spans two lines and costs 2.4 times that (the 2.4 is
+// measured: 1111 x 4112 x 2040 at 3.9 cycles a piece). An item costs 200 more; the last tile's
+// epilogue shows. Split items write their sums and the last of a tile reads them all back.
 struct Delivery {
-    int p = 1, q = 1;  // lines per 128-byte piece of the features' and the rows' operand
+    double p = 1, q = 1;  // cost of a 128-byte piece of the features' and of the rows' operand
 };
-double item_cost(int64_t tiles, int splits, int kb_per, int n, int pairs, Delivery d) {
-    const double waves = (double)((tiles * splits + pairs - 1) / pairs);
-    double item = kb_per * std::max(4.0 * n, 1.6 * (256.0 * d.p + n * d.q)) + 200.0;
-    double end = 16.0 * n;
-    if (splits > 1) {
-        item += 6.0 * n;
-        end += 2000.0 + 6.0 * n * splits;
+double item_cost(const FfnPlan& p, int kb, int pairs, Delivery d) {
+    const double block = std::max(4.0 * p.tile_n, 1.6 * (256 * d.p + p.tile_n * d.q));
+    const int64_t split_items = (int64_t)p.split_tiles * p.splits, whole = p.tiles - p.split_tiles;
+    double cost = 16.0 * p.tile_n;
+    if (p.splits > 1) {
+        const double item = p.kb_per_split * block + 200.0 + 6.0 * p.tile_n;
+        cost += (double)((split_items + pairs - 1) / pairs) * item + 2000.0 + 6.0 * p.tile_n * p.splits;
+        cost += (double)((whole + pairs - 1) / pairs) * (kb * block + 200.0);
+    } else {
+        cost += (double)((p.tiles + pairs - 1) / pairs) * (kb * block + 200.0);
     }
-    return waves * item + end;
+    return cost;
 }
 
-int lines_of(const void* p, int64_t ld) {
-    return (reinterpret_cast<uintptr_t>(p) & 127) || ld % 64 ? 2 : 1;
+double piece_cost(const void* p, int64_t ld) {
+    return (reinterpret_cast<uintptr_t>(p) & 127) || ld % 64 ? 2.4 : 1.0;
 }
 
-// Tile rows and K splits of one matrix's product: the cheapest by item_cost.
+// Tile rows and K splits of one matrix's product: the cheapest by item_cost, among whole tiles, all
+// tiles split (when they are fewer than two waves) and the tiles beyond whole waves split over the
+// pairs.
 FfnPlan plan_rows(int64_t rows, int64_t feats, bool gated, int64_t red, bool q_mn, int pairs,
                   uint64_t ws_bytes, Delivery d) {
     FfnPlan best;
@@ -71,22 +79,26 @@ FfnPlan plan_rows(int64_t rows, int64_t feats, bool gated, int64_t red, bool q_m
         p.num_rt = ceil_div(rows, n);
         p.tiles = (int64_t)ft * p.num_rt;
         if (p.tiles > kMaxSize / 64) continue;
-        const int most = p.tiles < 2 * pairs ? std::max(1, std::min(32, kb / 2)) : 1;
-        for (int s = 1; s <= most; ++s) {
-            p.kb_per_split = ceil_div(std::max(kb, 1), s);
-            if (s > 1 && ceil_div(kb, p.kb_per_split) != s) continue;
-            p.splits = s;
-            p.counter_bytes = p.bytes = 0;
+        auto consider = [&](int splits, int64_t split_tiles) {
+            p.kb_per_split = ceil_div(std::max(kb, 1), splits);
+            if (splits > 1 && ceil_div(kb, p.kb_per_split) != splits) return;
+            p.splits = splits;
+            p.split_tiles = splits > 1 ? (int)split_tiles : 0;
             size_split(&p);
-            if (p.bytes > ws_bytes || p.bytes > (64ull << 20)) continue;
-            const double c = item_cost(p.tiles, s, p.kb_per_split, n, pairs, d);
+            if (p.bytes > ws_bytes || p.bytes > (64ull << 20)) return;
+            const double c = item_cost(p, kb, pairs, d);
             if (best.num_ft == 0 || c < cost) {
                 best = p;
                 cost = c;
             }
-        }
+        };
+        const int most = std::max(1, std::min(32, kb / 2));
+        for (int s = 1; s <= (p.tiles < 2 * pairs ? most : 1); ++s) consider(s, p.tiles);
+        const int64_t tail = p.tiles % pairs;
+        if (p.tiles > pairs && tail > 0)
+            for (int s = 2; s <= std::min<int64_t>(most, pairs / tail); ++s) consider(s, tail);
     }
-    best.grid = 2 * (int)std::min<int64_t>(best.tiles * best.splits, pairs);
+    best.grid = 2 * (int)std::min<int64_t>(best.items(), pairs);
     return best;
 }
 
@@ -102,23 +114,26 @@ FfnPlan plan_seg(int64_t T, int k, int64_t E, int64_t max_tiles, int64_t feats, 
     const int expect = (int)std::min<int64_t>(256, (T + 31) / 32 * 32);
     p.tiles = max_tiles * p.num_ft;
     const int kb = ceil_div(red, kBK);
-    const int64_t likely = std::min(T * k, E) * p.num_ft;
+    // priced with the tiles and the rows that are likely
+    FfnPlan q = p;
+    q.tiles = std::min(T * k, E) * p.num_ft;
+    q.tile_n = expect;
     double cost = 0;
-    int best = 1;
-    if (p.tiles < 2 * pairs)
-        for (int s = 1; s <= std::max(1, std::min(32, kb / 2)); ++s) {
-            const int per = ceil_div(kb, s);
-            if (s > 1 && ceil_div(kb, per) != s) continue;
-            const double c = item_cost(likely, s, per, expect, pairs, Delivery());
-            if (s == 1 || c < cost) {
-                cost = c;
-                best = s;
-            }
+    for (int s = 1; s <= (p.tiles < 2 * pairs ? std::max(1, std::min(32, kb / 2)) : 1); ++s) {
+        q.splits = s;
+        q.kb_per_split = ceil_div(kb, s);
+        if (s > 1 && ceil_div(kb, q.kb_per_split) != s) continue;
+        q.split_tiles = s > 1 ? (int)q.tiles : 0;
+        const double c = item_cost(q, kb, pairs, Delivery());
+        if (s == 1 || c < cost) {
+            cost = c;
+            p.splits = s;
+            p.kb_per_split = q.kb_per_split;
         }
-    p.splits = best;
-    p.kb_per_split = ceil_div(kb, best);
+    }
+    if (p.splits > 1) p.split_tiles = (int)p.tiles;
     size_split(&p);
-    p.grid = 2 * (int)std::min<int64_t>(p.tiles * p.splits, pairs);
+    p.grid = 2 * (int)std::min<int64_t>(p.items(), pairs);
     return p;
 }
 
@@ -146,6 +161,7 @@ void apply_plan(const FfnPlan& p, void* ws, FfnCall* c) {
     c->args.num_rt = p.num_rt;
     c->args.splits = p.splits;
     c->args.kb_per_split = p.kb_per_split;
+    c->args.split_tiles = p.split_tiles;
     if (p.splits > 1) {
         c->args.counters = static_cast<uint32_t*>(ws);
         c->args.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + p.counter_bytes);
@@ -233,7 +249,7 @@ int gemm_act(int dtype, const void* A, const void* B, void* C, int64_t M, int64_
     if (o.residual && (rc = check_device_ptr(o.residual, dev, "residual"))) return rc;
     if (o.preact && (rc = check_device_ptr(o.preact, dev, "preact"))) return rc;
     const FfnPlan p = plan_rows(M, N, gated, K, amn, pairs_of(info), o.workspace ? o.workspace_bytes : 0,
-                                Delivery{lines_of(B, o.ldb), lines_of(A, o.lda)});
+                                Delivery{piece_cost(B, o.ldb), piece_cost(A, o.lda)});
     if (p.num_ft == 0) return fail(GEMM_ERR_UNSUPPORTED, "too many tiles");
     if (p.splits > 1 && (rc = check_device_ptr(o.workspace, dev, "the workspace"))) return rc;
     FfnCall c;
@@ -283,7 +299,7 @@ int gemm_act_workspace_size(int dtype, int64_t M, int64_t N, int64_t K, int layo
     DeviceInfo* info;
     if ((rc = current_device(&dev, &info))) return rc;
     // for dense operands; other row pitches are planned within this size
-    const Delivery d{lines_of(nullptr, b_is_mn(layout) ? N : K), lines_of(nullptr, a_is_mn(layout) ? M : K)};
+    const Delivery d{piece_cost(nullptr, b_is_mn(layout) ? N : K), piece_cost(nullptr, a_is_mn(layout) ? M : K)};
     *bytes = plan_rows(M, N, dtc::act_gated(activation), K, a_is_mn(layout), pairs_of(info), ~0ull, d).bytes;
     return GEMM_OK;
 }

@@ -36,8 +36,9 @@
 // the shared-memory traffic, which the MMA's operand reads compete for, and it is what bounds the
 // products with a short reduction.
 //
-// splits > 1 (few tiles, e.g. single tokens): the K-blocks of a tile are shared out over `splits`
-// items. Each epilogue warp writes its fp32 partial sums to the workspace and raises a counter; the
+// splits > 1: the K-blocks of a tile are shared out over `splits` items, for all tiles where there
+// are few (single tokens), or for those that would not fill the last wave of pairs; split tiles come
+// first. Each epilogue warp writes its fp32 partial sums to the workspace and raises a counter; the
 // warp that arrives last adds all pieces in the order of K (the same order whichever warp that
 // is, so results repeat bit for bit), finishes the tile and sets the counter back to zero. No warp
 // waits for another.
@@ -88,6 +89,7 @@ struct FfnArgs {
     int num_ft, num_rt;
     int experts;
     int splits, kb_per_split;
+    int split_tiles;  // the first so many tiles are split
     bool p_deep, q_deep;  // the operand's stage is one box (K-major: two 64-element K-chunks;
                           // MN-major: all its 64-element chunks), else one box a chunk
     int q_box;            // kRows, K-major Q: rows per box (half a tile)
@@ -143,7 +145,7 @@ struct Item {
     int zeros;   // further rows written as zeros (an expert's gap rows)
     int kb0, kb1;
     int red, krow;  // reduction length, and (kRed) the first row of the reduction
-    int tile, split;
+    int tile, split;  // split: number of the tile's piece, -1 for the whole
 };
 
 __device__ __forceinline__ int round32(int v) { return (v + 31) & ~31; }
@@ -152,10 +154,13 @@ __device__ __forceinline__ int round32(int v) { return (v + 31) & ~31; }
 template <int kMode, bool kGated>
 __device__ __forceinline__ bool get_item(const FfnArgs& a, int t, int seg_tiles, Item& w) {
     constexpr int kFeats = kGated ? 128 : 256;
-    int tile = t, split = 0;
+    int tile = t, split = -1;  // (a whole tile)
     if (a.splits > 1) {
         tile = t / a.splits;
-        split = t - tile * a.splits;
+        if (tile < a.split_tiles)
+            split = t - tile * a.splits;
+        else
+            tile = t - a.split_tiles * (a.splits - 1);
     }
     w.tile = tile;
     w.split = split;
@@ -200,8 +205,8 @@ __device__ __forceinline__ bool get_item(const FfnArgs& a, int t, int seg_tiles,
         w.red = min(max(a.counts[w.expert], 0), a.red - w.krow);
     }
     const int kb = (w.red + kBK - 1) / kBK;
-    w.kb0 = a.splits > 1 ? min(kb, split * a.kb_per_split) : 0;
-    w.kb1 = a.splits > 1 ? min(kb, w.kb0 + a.kb_per_split) : kb;
+    w.kb0 = split >= 0 ? min(kb, split * a.kb_per_split) : 0;
+    w.kb1 = split >= 0 ? min(kb, w.kb0 + a.kb_per_split) : kb;
     return true;
 }
 
@@ -764,7 +769,7 @@ __global__ void __launch_bounds__(ffn::kThreads, 1)
                 }
             }
             Ahead<kGated, kBack> ahead;
-            const bool whole = args.splits <= 1;
+            const bool whole = w.split < 0;
             if (whole && turn < chunks) {
                 at_chunk(turn);
                 fetch_ahead<kGated, kBack>(args, place, slot, lane, ahead);

@@ -5,11 +5,11 @@
 namespace dtc_host {
 
 namespace {
-// Row blocks: about 3 blocks per SM in all (enough loads in flight for the copy bandwidth; more row
+// Row blocks: about 2 blocks per SM in all (enough loads in flight for the copy bandwidth; more row
 // blocks only lengthen the last block's sum over them), each with at least 32 rows.
 int row_blocks(int64_t M, int64_t N, int sms) {
     const int64_t gx = (N + dtc::kActBackCols - 1) / dtc::kActBackCols;
-    return (int)std::max<int64_t>(1, std::min<int64_t>((M + 31) / 32, (int64_t)sms * 3 / gx));
+    return (int)std::max<int64_t>(1, std::min<int64_t>((M + 31) / 32, (int64_t)sms * 2 / gx));
 }
 }  // namespace
 

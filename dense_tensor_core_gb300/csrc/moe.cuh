@@ -153,6 +153,23 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
                 if (expert(j) < a.E) bias[j] = a.bias[expert(j)];
         }
     }
+    // what does not depend on the token: the steps of the bitonic sort in which this lane keeps the
+    // larger value, the lanes that hold a group, this lane's group and its place in it
+    uint32_t keeps_larger = 0;
+    {
+        int step = 0;
+#pragma unroll
+        for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+            for (int o = size >> 1; o; o >>= 1, ++step)
+                if (((lane & o) == 0) == ((lane & size) == 0 || size == 32)) keeps_larger |= 1u << step;
+    }
+    int lanes_per = 32;
+    if (kRun)
+        lanes_per = a.per_group / kVPL;  // (32 / groups)
+    else
+        while (lanes_per * a.groups > 32) lanes_per >>= 1;
+    const int group = lane / lanes_per, sub = lane - group * lanes_per;
     for (int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp; t < a.T; t += (int64_t)gridDim.x * kRouteWarps) {
         const int64_t row = t * a.ld;
         float z[kVPL];
@@ -166,19 +183,17 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
         }
 #pragma unroll
         for (int j = 0; j < kVPL; ++j) {
-            float s = a.sigmoid ? sigmoid_exact(z[j]) : z[j];
+            // masked: -infinity or NaN, in the logit or in the key (a masked logit's sigmoid is taken
+            // at 0: infinities take the reciprocal's slow path)
+            const bool live = z[j] > -CUDART_INF_F;
+            float s = a.sigmoid ? sigmoid_exact(live ? z[j] : 0.0f) : z[j];
             if (a.bias) s = __fadd_rn(s, bias[j]);
-            // masked: -infinity or NaN, in the logit or in the key
-            key[j] = (z[j] > -CUDART_INF_F && s > -CUDART_INF_F) ? order_key(s) : 0u;
+            key[j] = (live && s > -CUDART_INF_F) ? order_key(s) : 0u;
         }
         if (a.groups > 1) {
             // a group's two largest keys, from lanes_per lanes
             uint32_t m1 = 0, m2 = 0;
-            int lanes_per = 32, g, sub;
             if constexpr (kRun) {
-                lanes_per = a.per_group / kVPL;  // (32 / groups)
-                g = lane / lanes_per;
-                sub = lane - g * lanes_per;
 #pragma unroll
                 for (int j = 0; j < kVPL; ++j) {
                     m2 = max(m2, min(m1, key[j]));
@@ -190,12 +205,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
 #pragma unroll
                 for (int j = 0; j < kVPL; ++j) keys[lane + 32 * j] = key[j];
                 __syncwarp();
-                while (lanes_per * a.groups > 32) lanes_per >>= 1;
-                g = lane / lanes_per;
-                sub = lane - g * lanes_per;
-                if (g < a.groups)
+                if (group < a.groups)
                     for (int i = sub; i < a.per_group; i += lanes_per) {
-                        const uint32_t v = keys[g * a.per_group + i];
+                        const uint32_t v = keys[group * a.per_group + i];
                         m2 = max(m2, min(m1, v));
                         m1 = max(m1, v);
                     }
@@ -239,13 +251,13 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
 #pragma unroll
             for (int j = 1; j < kVPL; ++j) m = max(m, key[j]);
             // the lanes' maxima in falling order (a bitonic sort), of which the k-th is the bound
+            int step = 0;
 #pragma unroll
             for (int size = 2; size <= 32; size <<= 1)
 #pragma unroll
-                for (int o = size >> 1; o; o >>= 1) {
+                for (int o = size >> 1; o; o >>= 1, ++step) {
                     const uint32_t other = __shfl_xor_sync(kFull, m, o);
-                    const bool larger = ((lane & o) == 0) == ((lane & size) == 0 || size == 32);
-                    m = larger ? max(m, other) : min(m, other);
+                    m = (keeps_larger >> step) & 1u ? max(m, other) : min(m, other);
                 }
             const uint32_t bound = max(__shfl_sync(kFull, m, a.k - 1), 1u);
             int n = 0, at = 0;  // all candidates; those before this lane's next one
@@ -307,18 +319,20 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
         }
         const bool got = mine >= 0;
         const float zi = got ? load_f<kType>(a.logits, row + mine) : -CUDART_INF_F;
+        // (divisions only in lanes that hold a choice: a zero numerator takes the slow path)
         float w = 0.0f;
         if (a.sigmoid) {
-            w = got ? sigmoid_exact(zi) : 0.0f;
+            if (got) w = sigmoid_exact(zi);
             if (a.renorm) {
                 const float total = warp_sum(w);
-                w = total > 0.0f ? w / total : 0.0f;
+                if (got) w = total > 0.0f ? w / total : 0.0f;
             }
         } else if (a.renorm) {
             const float m = warp_max(zi);
-            const float e = got ? expf(zi - m) : 0.0f;
+            float e = 0.0f;
+            if (got) e = expf(zi - m);
             const float total = warp_sum(e);
-            w = got ? e / total : 0.0f;
+            if (got) w = e / total;
         } else {
             float m = -CUDART_INF_F;
 #pragma unroll
@@ -329,7 +343,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
             for (int j = 0; j < kVPL; ++j)
                 if (z[j] > -CUDART_INF_F) total += expf(z[j] - m);
             total = warp_sum(total);
-            w = got ? expf(zi - m) / total : 0.0f;
+            if (got) w = expf(zi - m) / total;
         }
         if (lane < a.k) {  // (weight 0 and index -1 where fewer than k could be chosen)
             a.weights[t * a.k + lane] = w * a.scale;
@@ -370,18 +384,19 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_backward_kernel(co
     float z[kVPL];
     const bool full = !a.sigmoid && !a.renorm;
     if (a.sigmoid) {
-        const float s = got ? sigmoid_exact(zi) : 0.0f;
+        float s = 0.0f;
+        if (got) s = sigmoid_exact(zi);
         if (a.renorm) {
-            const float total = warp_sum(s);
-            const float mean = total > 0.0f ? warp_sum(__fmul_rn(g, s)) / total : 0.0f;
-            g = total > 0.0f && got ? (g - mean) / total : 0.0f;
+            const float total = warp_sum(s), sum = warp_sum(__fmul_rn(g, s));
+            g = got && total > 0.0f ? (g - sum / total) / total : 0.0f;
         }
         d = g * s * (1.0f - s);
     } else if (!full) {
         m = warp_max(zi);
-        const float e = got ? expf(zi - m) : 0.0f;
+        float e = 0.0f, p = 0.0f;
+        if (got) e = expf(zi - m);
         const float total = warp_sum(e);
-        const float p = got ? e / total : 0.0f;
+        if (got) p = e / total;
         d = p * (g - warp_sum(__fmul_rn(g, p)));
     } else {
         m = -CUDART_INF_F;
@@ -397,15 +412,16 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_backward_kernel(co
         for (int j = 0; j < kVPL; ++j)
             if (z[j] > -CUDART_INF_F) total += expf(z[j] - m);
         total = warp_sum(total);
-        inv = total;
-        const float p = got ? expf(zi - m) / total : 0.0f;
+        inv = total > 0.0f ? 1.0f / total : 0.0f;  // (0: the whole row is masked)
+        float p = 0.0f;
+        if (got) p = expf(zi - m) / total;
         d = g * p;
         dot = warp_sum(d);
     }
     float out[kVPL];
 #pragma unroll
     for (int j = 0; j < kVPL; ++j)
-        out[j] = full && z[j] > -CUDART_INF_F ? -(expf(z[j] - m) / inv) * dot : 0.0f;
+        out[j] = full && z[j] > -CUDART_INF_F ? -(expf(z[j] - m) * inv) * dot : 0.0f;
     for (int i = 0; i < a.k; ++i) {
         const int e = __shfl_sync(kFull, mine, i);
         const float v = __shfl_sync(kFull, d, i);
@@ -557,20 +573,30 @@ __device__ __forceinline__ void plan_offsets(const PlanArgs& a, int count, int b
 __device__ __forceinline__ void plan_place(const PlanArgs& a, const PlanRun& run, const int* base, int* my) {
     const int lane = threadIdx.x & 31;
     const unsigned below_me = (1u << lane) - 1u;
-    for (int64_t i0 = run.r0; i0 < run.r1; i0 += 32) {
-        const int64_t i = i0 + lane;
-        int x = i < run.r1 ? a.indices[i] : -1;
-        const bool ok = x >= 0 && x < a.E;
-        if (!ok) x = -1;
-        const unsigned same = __match_any_sync(kFull, x);
-        int at = -1;
-        if (ok) at = base[x] + my[x] + __popc(same & below_me);
-        __syncwarp();
-        if (ok && (same & below_me) == 0) my[x] += __popc(same);
-        __syncwarp();
-        if (i < run.r1) {
-            a.slots[i] = at;
-            if (ok) a.rows[at] = (int)i;
+    constexpr int kAhead = 8;  // loads in flight
+    for (int64_t i0 = run.r0; i0 < run.r1; i0 += 32 * kAhead) {
+        int ahead[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int64_t i = i0 + 32 * j + lane;
+            ahead[j] = i < run.r1 ? a.indices[i] : -1;
+            if (ahead[j] >= a.E) ahead[j] = -1;
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            if (i0 + 32 * j >= run.r1) break;
+            const int64_t i = i0 + 32 * j + lane;
+            const int x = ahead[j] < 0 ? -1 : ahead[j];
+            const unsigned same = __match_any_sync(kFull, x);
+            int at = -1;
+            if (x >= 0) at = base[x] + my[x] + __popc(same & below_me);
+            __syncwarp();
+            if (x >= 0 && (same & below_me) == 0) my[x] += __popc(same);
+            __syncwarp();
+            if (i < run.r1) {
+                a.slots[i] = at;
+                if (x >= 0) a.rows[at] = (int)i;
+            }
         }
     }
 }
@@ -645,11 +671,16 @@ __global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_place_kernel(const P
     if (threadIdx.x < parts * a.E) {
         const int x = threadIdx.x % a.E;
         int count = 0, below = 0;
-#pragma unroll 8
-        for (int b = threadIdx.x / a.E; b < blocks; b += parts) {
-            const int v = a.block_counts[(int64_t)b * a.E + x];
-            if (b < (int)blockIdx.x) below += v;
-            count += v;
+        for (int b0 = threadIdx.x / a.E; b0 < blocks; b0 += 32 * parts) {
+            int v[32];  // loads in flight
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                v[j] = b0 + j * parts < blocks ? a.block_counts[(int64_t)(b0 + j * parts) * a.E + x] : 0;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                if (b0 + j * parts < (int)blockIdx.x) below += v[j];
+                count += v[j];
+            }
         }
         atomicAdd(sums + x, count);  // whole numbers: any order gives the same sum
         atomicAdd(sums + a.E + x, below);
