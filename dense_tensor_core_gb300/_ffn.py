@@ -1,18 +1,20 @@
-"""ctypes binding of the feed-forward operators (include/dtc_ffn.h): argument marshalling only, in
-the manner of ``_binding``. Every arithmetic step runs in the library's kernels.
+"""The feed-forward operators (include/dtc_ffn.h): their Python signatures. The checks, the output
+allocation and the calls are in the native module ``_ffn_native`` (csrc/ffn_binding.cpp), which
+raises TypeError, ValueError or GemmError; sizes and layouts go through ctypes. Every arithmetic
+step runs in the library's kernels.
 """
 import ctypes
 import functools
+import os
 
 import torch
 
 from . import _binding
-from ._binding import _check, _check_tensor, _DTYPE, _layout_code, _layout_name, _ld
+from ._binding import GemmError, _check, _DTYPE, _layout_code
 
 _ACT = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "swiglu": 5, "geglu": 6}
-_GATED = ("swiglu", "geglu")
-_KIND = {"bf16": torch.bfloat16, "f16": torch.float16}
-_FLOAT_CODE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_KIND = {"bf16": 0, "f16": 1}
+_LAYOUT = {"NT": 0, "NN": 1, "TN": 2, "TT": 3}
 _SCORING = {"softmax": 0, "sigmoid": 1}
 
 _vp, _i64, _i32, _u64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint64
@@ -79,97 +81,38 @@ def _L():
     return _lib
 
 
-# The current stream's handle without building a Stream object (several microseconds).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_native = None
 
 
-def _call(dev, stream, f, *args):
-    """The C call on `dev` (made current where it is not) and the given or current stream, which
-    is the last argument of every entry point that enqueues work."""
-    index = dev.index
-    handle = _raw_stream(index) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == index:
-        status = f(*args, handle)
-    else:
-        with torch.cuda.device(dev):
-            status = f(*args, handle)
-    if status:
-        _check(status)
+def _N():
+    """The native module (raises if it has not been built)."""
+    global _native
+    if _native is None:
+        if not os.path.exists(os.path.join(_binding.HERE, "_ffn_native.so")):
+            raise RuntimeError("_ffn_native.so is missing: build it with "
+                               "dense_tensor_core_gb300.build.build()")
+        _L()  # the library it is linked against
+        from . import _ffn_native
+
+        _ffn_native.set_error(GemmError)
+        _native = _ffn_native
+    return _native
 
 
-def _mat(t, dt, name, dev):
-    """Checks a 2-D operand that may be rows of a larger row-major array; its leading dimension (0:
-    dense)."""
-    if t.dtype is not dt or t.device != dev or not t.is_contiguous() or not t.is_cuda:
-        _check_tensor(t, dt, name, True)
-        if t.device != dev:
-            raise ValueError(f"all tensors must be on one CUDA device, got {name} on {t.device} "
-                             f"and others on {dev}")
-        return _ld(t)
-    return 0
+def _code(table, key, what):
+    code = table.get(key)
+    if code is None:
+        raise ValueError(f"unknown {what} {key!r}: one of {', '.join(table)}")
+    return code
 
 
-def _dense(t, dt, name, dev):
-    if t.dtype is not dt or t.device != dev or not t.is_contiguous() or not t.is_cuda:
-        _check_tensor(t, dt, name)
-        raise ValueError(f"all tensors must be on one CUDA device, got {name} on {t.device} and "
-                         f"others on {dev}")
+def _layout(layout):
+    code = _LAYOUT.get(layout)
+    return _layout_code(layout) if code is None else code
 
 
-def _act_code(activation):
-    if activation not in _ACT:
-        raise ValueError(f"unknown activation {activation!r}: one of {', '.join(_ACT)}")
-    return _ACT[activation]
-
-
-def _kind_dtype(kind):
-    if kind not in _KIND:
-        raise ValueError(f"unknown kind {kind!r}: bf16 or f16")
-    return _KIND[kind]
-
-
-def _shape(t, shape, name):
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-
-
-# layout: (code, A stored [K,M], B stored [N,K])
-_LAYOUT = {"NT": (0, False, True), "NN": (1, False, False), "TN": (2, True, False),
-           "TT": (3, True, True)}
-
-
-def _act_shapes(A, B, layout, gated):
-    """(layout code, M, N, K, stored columns of Bop) of a gemm_act call."""
-    if A.dim() != 2 or B.dim() != 2:
-        raise ValueError("A and B must be 2-D")
-    found = _LAYOUT.get(layout)
-    if found is None:
-        found = _LAYOUT[_layout_name(layout)]
-    code, a_t, b_t = found
-    M, K = A.shape
-    if a_t:
-        M, K = K, M
-    Nb, Kb = B.shape
-    if not b_t:
-        Nb, Kb = Kb, Nb
-    if Kb != K:
-        raise ValueError(f"inner sizes differ: A is {tuple(A.shape)}, B is {tuple(B.shape)} ({layout})")
-    if gated and Nb % 2:
-        raise ValueError(f"a gated activation needs an even number of columns, got {Nb}")
-    return code, M, Nb // 2 if gated else Nb, K, Nb
-
-
-def _ws(workspace, dev):
-    if workspace is None:
-        return None, 0
-    if workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor of the operands' device")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
-
-
-def _addr(t):
-    return t.data_ptr() if t is not None and t.numel() > 0 else None
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def gemm_act_workspace_size(kind, M, N, K, layout="NT", activation="none"):
@@ -177,7 +120,7 @@ def gemm_act_workspace_size(kind, M, N, K, layout="NT", activation="none"):
     tokens); 0 when it would not."""
     out = _u64(0)
     _check(_L().gemm_act_workspace_size(_DTYPE[kind], M, N, K, _layout_code(layout),
-                                        _act_code(activation), ctypes.byref(out)))
+                                        _code(_ACT, activation, "activation"), ctypes.byref(out)))
     return out.value
 
 
@@ -190,43 +133,16 @@ def gemm_act(kind, A, B, C=None, layout="NT", bias=None, residual=None, activati
     the sum before the activation, for gemm_act_backward. workspace: a zero-filled CUDA tensor of
     gemm_act_workspace_size bytes, reusable by later calls of the same stream. C may be the
     residual."""
-    dt = _kind_dtype(kind)
-    act = _act_code(activation)
-    dev = A.device
-    lda, ldb = _mat(A, dt, "A", dev), _mat(B, dt, "B", dev)
-    code, M, N, K, Nb = _act_shapes(A, B, layout, activation in _GATED)
-    ldc = ldr = ldz = 0
-    bias_p = res_p = pre_p = None
-    if C is None:
-        C = torch.empty((M, N), dtype=dt, device=dev)
-    else:
-        ldc = _mat(C, dt, "C", dev)
-        _shape(C, (M, N), "C")
-    if bias is not None:
-        _dense(bias, dt, "bias", dev)
-        _shape(bias, (Nb,), "bias")
-        bias_p = _addr(bias)
-    if residual is not None:
-        ldr = _mat(residual, dt, "residual", dev)
-        _shape(residual, (M, N), "residual")
-        res_p = _addr(residual)
-    if preact is not None:
-        ldz = _mat(preact, dt, "preact", dev)
-        _shape(preact, (M, Nb), "preact")
-        pre_p = _addr(preact)
-    ws, ws_bytes = _ws(workspace, dev)
-    o = gemm_act_options(act, bias_p, res_p, pre_p, lda, ldb, ldc, ldr, ldz, ws, ws_bytes,
-                         timeout_ns, fault_inject)
-    _call(dev, stream, _L().gemm_act, _DTYPE[kind], _addr(A), _addr(B), _addr(C), M, N, K, code,
-          ctypes.byref(o))
-    return C
+    return _N().gemm_act(_code(_KIND, kind, "kind"), _code(_ACT, activation, "activation"),
+                         _layout(layout), A, B, C, bias, residual, preact, workspace, timeout_ns,
+                         fault_inject, _handle(stream))
 
 
 def gemm_act_backward_workspace_size(kind, M, N, K, layout="NT", activation="none"):
     """Bytes of workspace gemm_act_backward needs."""
     out = _u64(0)
     _check(_L().gemm_act_backward_workspace_size(_DTYPE[kind], M, N, K, _layout_code(layout),
-                                                 _act_code(activation), ctypes.byref(out)))
+                                                 _code(_ACT, activation, "activation"), ctypes.byref(out)))
     return out.value
 
 
@@ -236,48 +152,22 @@ def gemm_act_backward(kind, dC, A, B, preact=None, layout="NT", activation="none
     dA and dB stored as A and B are, dbias fp32. need: which of the three to compute (the others
     are None). The gradient of a residual is dC. workspace: a zero-filled CUDA tensor of
     gemm_act_backward_workspace_size bytes; allocated here when not given."""
-    dt = _kind_dtype(kind)
-    act = _act_code(activation)
-    dev = dC.device
-    ldc, lda, ldb = (_mat(t, dt, name, dev) for t, name in ((dC, "dC"), (A, "A"), (B, "B")))
-    code, M, N, K, Nb = _act_shapes(A, B, layout, activation in _GATED)
-    _shape(dC, (M, N), "dC")
-    pre_p, ldz = None, 0
-    if act:
-        if preact is None:
-            raise ValueError(f"the gradient of {activation} needs preact")
-        ldz = _mat(preact, dt, "preact", dev)
-        _shape(preact, (M, Nb), "preact")
-        pre_p = _addr(preact)
-    if workspace is None:
-        with torch.cuda.device(dev):
-            n = gemm_act_backward_workspace_size(kind, M, N, K, layout, activation)
-        workspace = torch.zeros(max(n, 16), dtype=torch.uint8, device=dev)
-    ws, ws_bytes = _ws(workspace, dev)
-    dA = torch.empty(A.shape, dtype=dt, device=dev) if need[0] else None
-    dB = torch.empty(B.shape, dtype=dt, device=dev) if need[1] else None
-    db = torch.empty((Nb,), dtype=torch.float32, device=dev) if need[2] else None
-    o = gemm_act_options(act, None, None, pre_p, lda, ldb, ldc, 0, ldz, ws, ws_bytes, timeout_ns, 0)
-    _call(dev, stream, _L().gemm_act_backward, _DTYPE[kind], _addr(dC), _addr(A), _addr(B),
-          _addr(dA), _addr(dB), _addr(db), M, N, K, code, ctypes.byref(o))
-    return dA, dB, db
+    act, code = _code(_ACT, activation, "activation"), _layout(layout)
+    if workspace is None and dC.is_cuda and A.dim() == 2 and B.dim() == 2:
+        K = A.shape[1 - code // 2]
+        Nb = B.shape[0 if code in (0, 3) else 1]
+        with torch.cuda.device(dC.device):
+            n = gemm_act_backward_workspace_size(kind, dC.shape[0], Nb // 2 if act >= 5 else Nb, K,
+                                                 layout, activation)
+        workspace = torch.zeros(max(n, 16), dtype=torch.uint8, device=dC.device)
+    return _N().gemm_act_backward(_code(_KIND, kind, "kind"), act, code, dC, A, B, preact,
+                                  bool(need[0]), bool(need[1]), bool(need[2]), workspace, timeout_ns,
+                                  _handle(stream))
 
 
 # ------------------------------------------------------------------------------------------------
 # routing
 # ------------------------------------------------------------------------------------------------
-def _route_args(logits, top_k, scoring, groups, top_groups, renormalize, scale):
-    code = _FLOAT_CODE.get(logits.dtype)
-    if code is None:
-        raise TypeError(f"logits must be bf16, fp16 or fp32, got {logits.dtype}")
-    if logits.dim() != 2:
-        raise ValueError("logits must be [T, E]")
-    if scoring not in _SCORING:
-        raise ValueError(f"unknown scoring {scoring!r}: softmax or sigmoid")
-    return code, _mat(logits, logits.dtype, "logits", logits.device), moe_route_options(
-        top_k, _SCORING[scoring], groups, top_groups, 1 if renormalize else 0, scale)
-
-
 def moe_route(logits, top_k, bias=None, scoring="softmax", groups=1, top_groups=1,
               renormalize=True, scale=1.0, weights=None, indices=None, stream=None):
     """Routes tokens to experts: logits [T,E] (bf16, fp16 or fp32, rows may be strided) to (weights
@@ -286,45 +176,16 @@ def moe_route(logits, top_k, bias=None, scoring="softmax", groups=1, top_groups=
     the lowest index; weights come from the logits alone, over the choices (renormalize) or over all
     experts, times scale. Logits of -infinity or NaN are masked; where fewer than k experts can be
     chosen the rest are index -1 with weight 0."""
-    code, ld, o = _route_args(logits, top_k, scoring, groups, top_groups, renormalize, scale)
-    T, E = logits.shape
-    dev = logits.device
-    if bias is not None:
-        _dense(bias, torch.float32, "bias", dev)
-        _shape(bias, (E,), "bias")
-    if weights is None:
-        weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
-    else:
-        _dense(weights, torch.float32, "weights", dev)
-        _shape(weights, (T, top_k), "weights")
-    if indices is None:
-        indices = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-    else:
-        _dense(indices, torch.int32, "indices", dev)
-        _shape(indices, (T, top_k), "indices")
-    _call(dev, stream, _L().moe_route, code, _addr(logits), ld, _addr(bias), T, E, ctypes.byref(o),
-          _addr(weights), _addr(indices))
-    return weights, indices
+    return _N().moe_route(logits, top_k, bias, _code(_SCORING, scoring, "scoring"), groups, top_groups,
+                          renormalize, scale, weights, indices, _handle(stream))
 
 
 def moe_route_backward(dweights, logits, indices, scoring="softmax", renormalize=True, scale=1.0,
                        stream=None):
     """The gradient of moe_route's weights with respect to the logits: dlogits [T,E] in the logits'
     type, from dweights [T,k] fp32 and the chosen indices."""
-    if indices.dim() != 2:
-        raise ValueError("indices must be [T, k]")
-    k = indices.shape[1]
-    code, ld, o = _route_args(logits, k, scoring, 1, 1, renormalize, scale)
-    T, E = logits.shape
-    dev = logits.device
-    _dense(indices, torch.int32, "indices", dev)
-    _dense(dweights, torch.float32, "dweights", dev)
-    _shape(indices, (T, k), "indices")
-    _shape(dweights, (T, k), "dweights")
-    out = torch.empty((T, E), dtype=logits.dtype, device=dev)
-    _call(dev, stream, _L().moe_route_backward, code, _addr(dweights), _addr(logits), ld,
-          _addr(indices), T, E, ctypes.byref(o), _addr(out))
-    return out
+    return _N().moe_route_backward(dweights, logits, indices, _code(_SCORING, scoring, "scoring"),
+                                   renormalize, scale, _handle(stream))
 
 
 @functools.lru_cache(maxsize=256)
@@ -349,37 +210,31 @@ class MoePlan:
         self.tokens, self.top_k, self.experts = tokens, top_k, experts
         self.capacity = layout.capacity
 
-    def _view(self, at, n):
-        return self.data[at:at + n]
-
     @property
     def offsets(self):
-        return self._view(self._layout.offsets, self.experts + 1)
+        return _N().plan_view(self.data, self._layout.offsets, self.experts + 1, 0)
 
     @property
     def counts(self):
-        return self._view(self._layout.counts, self.experts)
+        return _N().plan_view(self.data, self._layout.counts, self.experts, 0)
 
     @property
     def slots(self):
-        return self._view(self._layout.slots, self.tokens * self.top_k).view(self.tokens, self.top_k)
+        return _N().plan_view(self.data, self._layout.slots, self.tokens, self.top_k)
 
     @property
     def rows(self):
-        return self._view(self._layout.rows, self.capacity)
+        return _N().plan_view(self.data, self._layout.rows, self.capacity, 0)
 
 
 def moe_plan(indices, experts, stream=None):
     """Puts the choices [T,k] int32 (outside 0 .. experts-1: no choice) in expert order, stable in
     the order of the tokens: a MoePlan."""
-    dev = indices.device
-    _dense(indices, torch.int32, "indices", dev)
     if indices.dim() != 2:
         raise ValueError("indices must be [T, k]")
     T, k = indices.shape
     layout = _plan_layout(T, k, experts)
-    data = torch.empty(layout.words, dtype=torch.int32, device=dev)
-    _call(dev, stream, _L().moe_plan, _addr(indices), T, k, experts, data.data_ptr())
+    data = _N().moe_plan(indices, experts, layout.words, _handle(stream))
     return MoePlan(data, layout, T, k, experts)
 
 
@@ -398,30 +253,13 @@ def _experts_layout(device_index, dtype, T, k, E, H, F, act, train):
     return info.bytes, back.value
 
 
-def _experts_args(kind, x, w_in, w_out, weights, plan, activation, name):
-    dt = _kind_dtype(kind)
-    act = _act_code(activation)
-    dev = x.device
-    _dense(x, dt, name, dev)
-    _dense(w_in, dt, "w_in", dev)
-    _dense(w_out, dt, "w_out", dev)
-    if x.dim() != 2 or w_in.dim() != 3 or w_out.dim() != 3:
-        raise ValueError(f"{name} must be [T, H], w_in [E, F, H] (gated [E, 2F, H]), w_out [E, H, F]")
-    T, H = x.shape
-    E, _, F = w_out.shape
-    _shape(w_out, (E, H, F), "w_out")
-    _shape(w_in, (E, 2 * F if activation in _GATED else F, H), "w_in")
-    if plan.tokens != T or plan.experts != E:
-        raise ValueError(f"the plan is for {plan.tokens} tokens and {plan.experts} experts, not "
-                         f"{T} and {E}")
-    wcode = _FLOAT_CODE.get(weights.dtype)
-    if wcode is None:
-        raise TypeError(f"weights must be bf16, fp16 or fp32, got {weights.dtype}")
-    _dense(weights, weights.dtype, "weights", dev)
-    _shape(weights, (T, plan.top_k), "weights")
-    if plan.data.device != dev:
-        raise ValueError(f"the plan is on {plan.data.device}, the tensors on {dev}")
-    return dt, dev, act, wcode, T, E, H, F
+def _buffer_sizes(x, w_out, plan, code, act, train):
+    """Bytes of the buffer in expert order and of the backward pass's scratch (0, 0 where the shapes
+    are not those of a call: the native module says what is wrong)."""
+    if not x.is_cuda or w_out.dim() != 3:
+        return 0, 0
+    E, H, F = w_out.shape
+    return _experts_layout(x.device.index, code, plan.tokens, plan.top_k, E, H, F, act, train)
 
 
 def moe_experts(kind, x, w_in, w_out, weights, plan, activation="swiglu", residual=None, out=None,
@@ -430,41 +268,20 @@ def moe_experts(kind, x, w_in, w_out, weights, plan, activation="swiglu", residu
     token t in `plan` (moe_plan). x [T,H]; w_in [E, F, H] (gated: [E, 2F, H], gate rows first);
     w_out [E, H, F]; weights [T,k] bf16, fp16 or fp32. Experts without tokens cost nothing. With
     save, returns (y, saved) where saved is what moe_experts_backward needs."""
-    dt, dev, act, wcode, T, E, H, F = _experts_args(kind, x, w_in, w_out, weights, plan, activation,
-                                                    "x")
-    if residual is not None:
-        _dense(residual, dt, "residual", dev)
-        _shape(residual, (T, H), "residual")
-    if out is None:
-        out = torch.empty((T, H), dtype=dt, device=dev)
-    else:
-        _dense(out, dt, "out", dev)
-        _shape(out, (T, H), "out")
-    nbytes, _ = _experts_layout(dev.index, _DTYPE[kind], T, plan.top_k, E, H, F, act, int(save))
-    buffer = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    o = moe_experts_options(act, wcode, _addr(residual), timeout_ns, fault_inject)
-    _call(dev, stream, _L().moe_experts, _DTYPE[kind], _addr(x), _addr(w_in), _addr(w_out),
-          _addr(weights), plan.data.data_ptr(), _addr(out), T, plan.top_k, E, H, F, ctypes.byref(o), int(save),
-          buffer.data_ptr())
-    return (out, buffer) if save else out
+    code, act = _code(_KIND, kind, "kind"), _code(_ACT, activation, "activation")
+    save = bool(save)
+    nbytes, _ = _buffer_sizes(x, w_out, plan, code, act, save)
+    return _N().moe_experts(code, act, x, w_in, w_out, weights, plan.data, plan.tokens, plan.top_k,
+                            plan.experts, residual, out, save, nbytes, timeout_ns, fault_inject,
+                            _handle(stream))
 
 
 def moe_experts_backward(kind, dy, w_in, w_out, weights, plan, saved, activation="swiglu",
                          need_weights=True, need_x=True, timeout_ns=0, stream=None):
     """(dx, dw_in, dw_out, dweights) of moe_experts from dy [T,H] and what it saved; dw_in and
     dw_out are None without need_weights, dx without need_x. The gradient of a residual is dy."""
-    dt, dev, act, wcode, T, E, H, F = _experts_args(kind, dy, w_in, w_out, weights, plan, activation,
-                                                    "dy")
-    nbytes, back = _experts_layout(dev.index, _DTYPE[kind], T, plan.top_k, E, H, F, act, 1)
-    if saved.dtype != torch.uint8 or saved.numel() != nbytes or saved.device != dev:
-        raise ValueError("saved is not what moe_experts returned for these sizes with save=True")
-    ws = torch.empty(back, dtype=torch.uint8, device=dev)
-    dx = torch.empty((T, H), dtype=dt, device=dev) if need_x else None
-    dwi = torch.empty(w_in.shape, dtype=dt, device=dev) if need_weights else None
-    dwo = torch.empty(w_out.shape, dtype=dt, device=dev) if need_weights else None
-    dw = torch.empty(weights.shape, dtype=weights.dtype, device=dev)
-    o = moe_experts_options(act, wcode, None, timeout_ns, 0)
-    _call(dev, stream, _L().moe_experts_backward, _DTYPE[kind], _addr(dy), _addr(w_in), _addr(w_out),
-          _addr(weights), plan.data.data_ptr(), _addr(saved), _addr(dx), _addr(dwi), _addr(dwo),
-          _addr(dw), T, plan.top_k, E, H, F, ctypes.byref(o), ws.data_ptr(), back)
-    return dx, dwi, dwo, dw
+    code, act = _code(_KIND, kind, "kind"), _code(_ACT, activation, "activation")
+    nbytes, scratch = _buffer_sizes(dy, w_out, plan, code, act, True)
+    return _N().moe_experts_backward(code, act, dy, w_in, w_out, weights, plan.data, plan.tokens,
+                                     plan.top_k, plan.experts, saved, nbytes, scratch, bool(need_x),
+                                     bool(need_weights), timeout_ns, _handle(stream))

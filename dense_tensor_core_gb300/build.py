@@ -1,13 +1,17 @@
-"""Build the CUDA library in-tree: dense_tensor_core_gb300/libdtc_gemm.so (sm_103a only).
+"""Build the CUDA library in-tree: dense_tensor_core_gb300/libdtc_gemm.so (sm_103a only), and the
+native part of the Python binding, dense_tensor_core_gb300/_ffn_native.so.
 
 One translation unit per kernel family plus the API unit, compiled in parallel with nvcc (one
 -gencode), then linked into one shared library. The CUDA runtime is linked statically so the
-library loads without a GPU (the CPU tests check its exports) and carries no rpath.
+library loads without a GPU (the CPU tests check its exports) and carries no rpath. The binding
+module is host code against torch's headers, compiled beside the kernels (about 10 s) and linked
+against the library in its own folder.
 """
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
@@ -16,6 +20,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libdtc_gemm.so")
+NATIVE = os.path.join(HERE, "_ffn_native.so")
 OBJ_DIR = os.path.join(HERE, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -32,8 +37,35 @@ def nvcc() -> str:
 
 def _inputs():
     files = sources() + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
-    files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
+    files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h", ".cpp"))]
     return files
+
+
+def _compile_native(obj_dir):
+    """The binding module's object (no GPU code; torch's own headers and ABI)."""
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
+    dirs = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+            cuda, sysconfig.get_paths()["include"], INCLUDE]
+    obj = os.path.join(obj_dir, "ffn_binding.o")
+    subprocess.check_call(
+        [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+         "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch.compiled_with_cxx11_abi()]
+        + [x for d in dirs for x in ("-isystem" if "torch" in d else "-I", d)]
+        + ["-c", os.path.join(CSRC, "ffn_binding.cpp"), "-o", obj])
+    return obj
+
+
+def _link_native(obj, tmp):
+    import torch
+
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    subprocess.check_call(
+        [shutil.which("g++") or "g++", "-shared", obj, "-o", tmp, "-L" + HERE, "-ldtc_gemm",
+         "-Wl,-rpath,$ORIGIN", "-L" + torch_lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+         "-lc10_cuda"])
 
 
 def _compile(src, obj_dir, verbose_ptxas):
@@ -47,19 +79,23 @@ def _compile(src, obj_dir, verbose_ptxas):
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    if not force and os.path.exists(LIB):
+    if not force and os.path.exists(LIB) and os.path.exists(NATIVE):
         newest = max(os.path.getmtime(f) for f in _inputs())
-        if os.path.getmtime(LIB) >= newest:
+        if min(os.path.getmtime(LIB), os.path.getmtime(NATIVE)) >= newest:
             return LIB
     os.makedirs(OBJ_DIR, exist_ok=True)
     srcs = sources()
     # objects in a directory of this build's own, so concurrent builds cannot mix their files
     with tempfile.TemporaryDirectory(dir=OBJ_DIR) as obj_dir:
-        with ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+        with ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+            native = ex.submit(_compile_native, obj_dir)
             objs = list(ex.map(lambda s: _compile(s, obj_dir, verbose_ptxas), srcs))
         tmp = LIB + ".tmp%d" % os.getpid()
         subprocess.check_call([nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs])
-    os.replace(tmp, LIB)
+        os.replace(tmp, LIB)
+        tmp = NATIVE + ".tmp%d" % os.getpid()
+        _link_native(native.result(), tmp)
+        os.replace(tmp, NATIVE)
     return LIB
 
 
