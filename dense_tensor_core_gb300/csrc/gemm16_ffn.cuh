@@ -177,9 +177,11 @@ __device__ __forceinline__ bool get_item(const FfnArgs& a, int t, int seg_tiles,
         w.valid = min(a.tile_n, a.rows - w.r0);
         w.n = a.tile_n;
     } else if constexpr (kMode == kSeg) {
-        if (tile >= a.num_ft * seg_tiles) return false;
         const int rt = tile / a.num_ft;
+        if (rt >= a.max_tiles) return false;
+        // (read before the count is looked at: the two loads overlap)
         const int4 s = reinterpret_cast<const int4*>(a.tiles)[rt];
+        if (rt >= seg_tiles) return false;
         // a record that no plan of these sizes holds (a stale or foreign plan) ends the walk: the
         // MMA's shape and the rows written come from it
         if ((unsigned)s.x >= (unsigned)a.experts || s.z < 1 || s.z > a.tile_n || s.y < 0 ||
@@ -742,6 +744,7 @@ __global__ void __launch_bounds__(ffn::kThreads, 1)
         const int q = warp & 3, turn = (warp - 2) >> 2;
         const uint32_t slot = base + kStages * kStageBytes + (uint32_t)(warp - 2) * (2 * kSlot);
         uint32_t acc = 0;
+        bool warm = true;
         Item w;
         for (int t = pair; get_item<kMode, kGated>(args, t, seg_tiles, w); t += num_pairs) {
             const uint32_t b = acc & 1u, aph = (acc >> 1) & 1u;
@@ -769,80 +772,82 @@ __global__ void __launch_bounds__(ffn::kThreads, 1)
                 }
             }
             Ahead<kGated, kBack> ahead;
-            const bool whole = w.split < 0;
-            if (whole && turn < chunks) {
-                at_chunk(turn);
-                fetch_ahead<kGated, kBack>(args, place, slot, lane, ahead);
-            }
-            int ok = 1;
-            if (lane == 0)
-                ok = wait_bounded<false, true>(smem_u32(&bar_tfull[b]), aph, abort,
-                                               args.timeout_ns, args.status, 44);
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok) break;
-            tc_fence_after_sync();
             auto hand_back = [&]() {  // accumulator read: back to the MMA issuer
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(map_to_cta(smem_u32(&bar_tempty[b]), 0));
             };
-            if (turn >= chunks) hand_back();
             const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + b * kAccStride;
             const bool empty = w.kb0 == w.kb1;  // no K-block: the sum is zero
             // split-K: the blocks of this quarter in the workspace, 1024 floats each, in the
             // order [split][block]
             const int blocks = args.tile_n / 32;
             const int64_t quarter = ((int64_t)w.tile * 2 + rank) * 4 + q;
+            // What a pass over the warp's blocks does, through one copy of the code:
+            //   kWarm  before the launch's first tile: one block of no rows, which brings the
+            //          epilogue's instructions into the caches while the operands are still on
+            //          their way (a single token's tile: 4 us from the sums to the result without);
+            //   kWhole the sums of a whole tile, finished;
+            //   kPiece the sums of a piece of a split tile, written to the workspace;
+            //   kJoin  all pieces' sums, by the warp that came last, finished.
+            constexpr int kWarm = 0, kWhole = 1, kPiece = 2, kJoin = 3;
+            const int main_pass = w.split < 0 ? kWhole : kPiece;
+            int pass = warm ? kWarm : main_pass;
+            bool gave_up = false;
 #pragma unroll 1
-            for (int c = turn; c < chunks; c += 2) {
-                float v[4][8];
-                tmem_load_fragment32(taddr + c * 32, v);
-                if (c + 2 >= chunks) hand_back();
-                if (empty) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i / 8][i % 8] = 0.0f;
-                }
-                at_chunk(c);
-                if (whole) {
-                    const Place here = place;
-                    finish_block<kBF16, kGated, kBack>(args, v, bias, here, ahead, slot, lane, [&]() {
-                        if (c + 2 < chunks) {
-                            at_chunk(c + 2);
-                            fetch_ahead<kGated, kBack>(args, place, slot, lane, ahead);
-                        }
-                    });
-                } else {
-                    float4* const d = reinterpret_cast<float4*>(
-                        args.partial + ((quarter * args.splits + w.split) * blocks + c) * 1024) + lane;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (8 * k < place.valid) {
-                            d[(2 * k) * 32] = make_float4(v[0][2 * k], v[0][2 * k + 1], v[1][2 * k], v[1][2 * k + 1]);
-                            d[(2 * k + 1) * 32] = make_float4(v[2][2 * k], v[2][2 * k + 1], v[3][2 * k], v[3][2 * k + 1]);
-                        }
-                }
-            }
-            if (!whole && turn < chunks) {
-                uint32_t* const counter = args.counters + ((int64_t)w.tile * 2 + rank) * kEpWarps + (warp - 2);
-                __threadfence();  // this lane's pieces are visible before the count
-                __syncwarp();
-                uint32_t before = 0;
-                if (lane == 0) before = atomicAdd(counter, 1u);
-                before = __shfl_sync(0xffffffffu, before, 0);
-                if (before == (uint32_t)args.splits - 1) {
-                    __threadfence();  // and the others' before this warp reads them
-                    if (lane == 0) *counter = 0u;
-#pragma unroll 1
-                    for (int c = turn; c < chunks; c += 2) {
-                        at_chunk(c);
+            while (true) {
+                if (pass == kWhole || pass == kPiece) {
+                    if (pass == kWhole && turn < chunks) {
+                        at_chunk(turn);
                         fetch_ahead<kGated, kBack>(args, place, slot, lane, ahead);
-                        float v[4][8];
+                    }
+                    int ok = 1;
+                    if (lane == 0)
+                        ok = wait_bounded<false, true>(smem_u32(&bar_tfull[b]), aph, abort,
+                                                       args.timeout_ns, args.status, 44);
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (!ok) {
+                        gave_up = true;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    if (turn >= chunks) hand_back();
+                }
+                const int end = pass == kWarm ? turn + 1 : chunks;
+#pragma unroll 1
+                for (int c = turn; c < end; c += 2) {
+                    float v[4][8];
+                    at_chunk(c);
+                    if (pass == kWhole || pass == kPiece) {
+                        tmem_load_fragment32(taddr + c * 32, v);
+                        if (c + 2 >= chunks) hand_back();
+                        if (empty) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i / 8][i % 8] = 0.0f;
+                        }
+                        if (pass == kPiece) {
+                            float4* const d = reinterpret_cast<float4*>(
+                                args.partial + ((quarter * args.splits + w.split) * blocks + c) * 1024) + lane;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (8 * k < place.valid) {
+                                    d[(2 * k) * 32] = make_float4(v[0][2 * k], v[0][2 * k + 1], v[1][2 * k], v[1][2 * k + 1]);
+                                    d[(2 * k + 1) * 32] = make_float4(v[2][2 * k], v[2][2 * k + 1], v[3][2 * k], v[3][2 * k + 1]);
+                                }
+                            continue;
+                        }
+                    } else {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i / 8][i % 8] = 0.0f;
+                        if (pass == kWarm)
+                            place.valid = place.rows = 0;
+                        else
+                            fetch_ahead<kGated, kBack>(args, place, slot, lane, ahead);
                         const float4* d = reinterpret_cast<const float4*>(
                             args.partial + (quarter * args.splits * blocks + c) * 1024) + lane;
+                        const int pieces = pass == kWarm ? 0 : args.splits;
 #pragma unroll 4
-                        for (int s = 0; s < args.splits; ++s, d += blocks * 256) {
+                        for (int s = 0; s < pieces; ++s, d += blocks * 256) {
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 if (8 * k < place.valid) {
@@ -858,10 +863,33 @@ __global__ void __launch_bounds__(ffn::kThreads, 1)
                                     v[3][2 * k + 1] += hi.w;
                                 }
                         }
-                        finish_block<kBF16, kGated, kBack>(args, v, bias, place, ahead, slot, lane, [] {});
                     }
+                    const Place here = place;
+                    finish_block<kBF16, kGated, kBack>(args, v, bias, here, ahead, slot, lane, [&]() {
+                        if (pass == kWhole && c + 2 < chunks) {
+                            at_chunk(c + 2);
+                            fetch_ahead<kGated, kBack>(args, place, slot, lane, ahead);
+                        }
+                    });
                 }
+                if (pass == kWarm) {
+                    warm = false;
+                    pass = main_pass;
+                    continue;
+                }
+                if (pass != kPiece || turn >= chunks) break;
+                uint32_t* const counter = args.counters + ((int64_t)w.tile * 2 + rank) * kEpWarps + (warp - 2);
+                __threadfence();  // this lane's pieces are visible before the count
+                __syncwarp();
+                uint32_t before = 0;
+                if (lane == 0) before = atomicAdd(counter, 1u);
+                before = __shfl_sync(0xffffffffu, before, 0);
+                if (before != (uint32_t)args.splits - 1) break;
+                __threadfence();  // and the others' before this warp reads them
+                if (lane == 0) *counter = 0u;
+                pass = kJoin;
             }
+            if (gave_up) break;
         }
     }
 

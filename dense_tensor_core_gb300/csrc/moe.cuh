@@ -526,13 +526,20 @@ __device__ __forceinline__ void plan_count(const PlanArgs& a, const PlanRun& r, 
     }
 }
 
-// Counts per warp to exclusive prefixes over the warps; the block's count of the thread's expert.
-__device__ __forceinline__ int plan_prefix(const PlanArgs& a, int* hist) {
+// Warps of the block that have choices.
+__device__ __forceinline__ int plan_warps(const PlanArgs& a, int block) {
+    const int64_t left = (int64_t)a.n - (int64_t)block * kPlanWarps * a.run;
+    return left <= 0 || a.run == 0 ? 0 : (int)min((int64_t)kPlanWarps, (left + a.run - 1) / a.run);
+}
+
+// Counts per warp to exclusive prefixes over the first `warps` warps; the block's count of the
+// thread's expert.
+__device__ __forceinline__ int plan_prefix(const PlanArgs& a, int warps, int* hist) {
     const int e = threadIdx.x;
     int s = 0;
     if (e < a.E) {
 #pragma unroll 8
-        for (int w = 0; w < kPlanWarps; ++w) {
+        for (int w = 0; w < warps; ++w) {
             const int c = hist[w * a.E + e];
             hist[w * a.E + e] = s;
             s += c;
@@ -609,7 +616,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_kernel(const PlanArg
     __shared__ int2 warp_sums[kPlanWarps];
     const int rank = (int)cluster_ctarank(), ctas = (int)gridDim.x;
     grid_launch_dependents();
-    for (int i = threadIdx.x; i < kPlanWarps * a.E; i += kPlanThreads) hist[i] = 0;
+    const int warps = plan_warps(a, rank);
+    for (int i = threadIdx.x; i < warps * a.E; i += kPlanThreads) hist[i] = 0;
     __syncthreads();
     grid_dependency_wait();
     const PlanRun run(a, rank);
@@ -617,7 +625,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_kernel(const PlanArg
     plan_count(a, run, my);
     __syncthreads();
     const int e = threadIdx.x;
-    const int mine = plan_prefix(a, hist);
+    const int mine = plan_prefix(a, warps, hist);
     if (e < a.E) totals[e] = mine;
     cluster_sync();
     int count = 0, below = 0;
@@ -653,7 +661,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_place_kernel(const P
     int* const base = hist + kPlanWarps * a.E;  // [E]
     int* const sums = base + a.E;               // [2][E]
     __shared__ int2 warp_sums[kPlanWarps];
-    for (int i = threadIdx.x; i < kPlanWarps * a.E; i += kPlanThreads) hist[i] = 0;
+    const int warps = plan_warps(a, blockIdx.x);
+    for (int i = threadIdx.x; i < warps * a.E; i += kPlanThreads) hist[i] = 0;
     for (int i = threadIdx.x; i < 2 * a.E; i += kPlanThreads) sums[i] = 0;
     __syncthreads();
     grid_launch_dependents();
@@ -662,7 +671,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_place_kernel(const P
     int* const my = hist + (threadIdx.x >> 5) * a.E;
     plan_count(a, run, my);
     __syncthreads();
-    plan_prefix(a, hist);
+    plan_prefix(a, warps, hist);
     // each expert's choices in all blocks and in those before this one: threads e, e + E, ... share
     // an expert's blocks
     const int e = threadIdx.x;
