@@ -190,9 +190,9 @@ def moe_route_backward(dweights, logits, indices, scoring="softmax", renormalize
 
 @functools.lru_cache(maxsize=256)
 def _plan_layout(T, k, E):
-    info = moe_plan_info()
-    _check(_L().moe_plan_layout(T, k, E, ctypes.byref(info)))
-    return info
+    i = moe_plan_info()
+    _check(_L().moe_plan_layout(T, k, E, ctypes.byref(i)))
+    return i.words, i.offsets, i.counts, i.slots, i.rows, i.capacity
 
 
 class MoePlan:
@@ -205,26 +205,10 @@ class MoePlan:
     * rows [capacity]: the choice t * k + j in each row, -1 in gap rows (past offsets[E]: unset).
     """
 
-    def __init__(self, data, layout, tokens, top_k, experts):
-        self.data, self._layout = data, layout
+    def __init__(self, arrays, tokens, top_k, experts):
+        self.data, self.offsets, self.counts, self.slots, self.rows = arrays
         self.tokens, self.top_k, self.experts = tokens, top_k, experts
-        self.capacity = layout.capacity
-
-    @property
-    def offsets(self):
-        return _N().plan_view(self.data, self._layout.offsets, self.experts + 1, 0)
-
-    @property
-    def counts(self):
-        return _N().plan_view(self.data, self._layout.counts, self.experts, 0)
-
-    @property
-    def slots(self):
-        return _N().plan_view(self.data, self._layout.slots, self.tokens, self.top_k)
-
-    @property
-    def rows(self):
-        return _N().plan_view(self.data, self._layout.rows, self.capacity, 0)
+        self.capacity = self.rows.shape[0]
 
 
 def moe_plan(indices, experts, stream=None):
@@ -233,9 +217,8 @@ def moe_plan(indices, experts, stream=None):
     if indices.dim() != 2:
         raise ValueError("indices must be [T, k]")
     T, k = indices.shape
-    layout = _plan_layout(T, k, experts)
-    data = _N().moe_plan(indices, experts, layout.words, _handle(stream))
-    return MoePlan(data, layout, T, k, experts)
+    return MoePlan(_N().moe_plan(indices, experts, *_plan_layout(T, k, experts), _handle(stream)), T, k,
+                   experts)
 
 
 # ------------------------------------------------------------------------------------------------

@@ -8,6 +8,7 @@
 // and GemmError (what the library answers).
 #include <Python.h>
 
+#include <ATen/core/LegacyTypeDispatch.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -157,6 +158,8 @@ template <typename F>
 PyObject* entry(Py_ssize_t got, Py_ssize_t want, F f) {
     try {
         if (got != want) refuse(PyExc_TypeError, "expected " + std::to_string(want) + " arguments");
+        // outputs and views are made without torch's gradient bookkeeping (a microsecond or two each)
+        const at::AutoDispatchBelowADInplaceOrView guard;
         return f();
     } catch (const Refusal& r) {
         PyErr_SetString(r.type, r.what.c_str());
@@ -355,30 +358,30 @@ PyObject* py_moe_route_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// (indices, experts, words of the plan, stream)
+// (indices, experts, words of the plan, its first words of offsets, counts, slots and rows, rows,
+// stream) to (plan, offsets, counts, slots, rows). The views are made before the launch: tensor
+// bookkeeping right behind a launch costs several microseconds here, before it a fraction of one.
 PyObject* py_moe_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return entry(n, 4, [&]() -> PyObject* {
+    return entry(n, 9, [&]() -> PyObject* {
         const at::Tensor& idx = tensor(a[0], "indices");
         const c10::Device dev = device_of(idx, at::kInt, "indices");
         dense(idx, at::kInt, "indices", dev);
         if (idx.dim() != 2) refuse(PyExc_ValueError, "indices must be [T, k]");
-        const int64_t E = integer(a[1]);
+        const int64_t E = integer(a[1]), T = idx.size(0), k = idx.size(1);
         const at::Tensor data = empty({integer(a[2])}, at::kInt, dev);
-        call(dev, a[3], [&](dtc_stream_t st) {
-            return moe_plan(static_cast<const int*>(address(idx)), idx.size(0), (int)idx.size(1), E,
-                            data.data_ptr(), st);
-        });
-        return wrap(data);
-    });
-}
-
-// (plan, first word, rows, columns): a view of the plan as [rows, columns], or [rows] for columns 0
-PyObject* py_plan_view(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return entry(n, 4, [&]() -> PyObject* {
-        const at::Tensor& data = tensor(a[0], "plan");
-        const int64_t at = integer(a[1]), rows = integer(a[2]), cols = integer(a[3]);
-        return wrap(cols ? data.as_strided({rows, cols}, {cols, 1}, data.storage_offset() + at)
-                         : data.as_strided({rows}, {1}, data.storage_offset() + at));
+        PyObject* const r = tuple({data, data.as_strided({E + 1}, {1}, integer(a[3])),
+                                   data.as_strided({E}, {1}, integer(a[4])),
+                                   data.as_strided({T, k}, {k, 1}, integer(a[5])),
+                                   data.as_strided({integer(a[7])}, {1}, integer(a[6]))});
+        try {
+            call(dev, a[8], [&](dtc_stream_t st) {
+                return moe_plan(static_cast<const int*>(address(idx)), T, (int)k, E, data.data_ptr(), st);
+            });
+        } catch (...) {
+            Py_DECREF(r);
+            throw;
+        }
+        return r;
     });
 }
 
@@ -490,8 +493,7 @@ PyObject* py_set_error(PyObject*, PyObject* type) {
 #define DTC_FN(name) {#name, (PyCFunction)(void*)py_##name, METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {DTC_FN(gemm_act),      DTC_FN(gemm_act_backward),
                           DTC_FN(moe_route),     DTC_FN(moe_route_backward),
-                          DTC_FN(moe_plan),      DTC_FN(plan_view),
-                          DTC_FN(moe_experts),
+                          DTC_FN(moe_plan),      DTC_FN(moe_experts),
                           DTC_FN(moe_experts_backward),
                           {"set_error", py_set_error, METH_O, nullptr},
                           {nullptr, nullptr, 0, nullptr}};
