@@ -134,8 +134,7 @@ __device__ __forceinline__ void load_run(const void* p, int64_t i, float (&v)[kN
 template <int kType, int kVPL, bool kRun>
 __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const RouteArgs a) {
     __shared__ uint32_t group_keys[kRouteWarps][kRun ? 1 : kVPL * 32];
-    __shared__ uint32_t cands[kRouteWarps][32];
-    __shared__ uint16_t cands_at[kRouteWarps][32];
+    __shared__ uint2 cands[kRouteWarps][32];  // key and expert
     grid_launch_dependents();
     grid_dependency_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -221,11 +220,11 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
             if (sub == 0 && m1)
                 score = order_key(__fadd_rn(from_key(m1), a.sigmoid && m2 ? from_key(m2) : 0.0f));
             // a group stays if fewer than top_groups groups come before it (the lower one on ties)
+            // (o > score, or o == score from a lower lane: o > score - 1)
             int rank = 0;
-            for (int i = 0; i < 32; i += lanes_per) {
-                const uint32_t o = __shfl_sync(kFull, score, i);
-                rank += o > score || (o == score && i < lane) ? 1 : 0;
-            }
+#pragma unroll 4
+            for (int i = 0; i < 32; i += lanes_per)
+                rank += __shfl_sync(kFull, score, i) > (i < lane ? score - 1u : score) ? 1 : 0;
             const unsigned heads = __ballot_sync(kFull, score != 0 && rank < a.top_groups);
             if constexpr (kRun) {
                 if (!((heads >> (lane - sub)) & 1u)) {
@@ -275,30 +274,32 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
                 for (int j = 0; j < kVPL; ++j) {
                     if (key[j] >= bound) {
                         const int to = kRun ? at : at + __popc(in[j] & below_me);
-                        cands[warp][to] = key[j];
-                        cands_at[warp][to] = (uint16_t)expert(j);
+                        cands[warp][to] = make_uint2(key[j], (uint32_t)expert(j));
                         if (kRun) ++at;
                     }
                     if (!kRun) at += __popc(in[j]);
                 }
             }
             __syncwarp();
-            cand = lane < n ? cands[warp][lane] : 0u;
-            cand_at = cands_at[warp][lane];
+            const uint2 c = cands[warp][lane];
+            cand = lane < n ? c.x : 0u;
+            cand_at = (int)c.y;
         }
         if (few) {
-            // a candidate's place: how many come before it (they stand in the order of their index)
-            const unsigned live = __ballot_sync(kFull, cand != 0);
+            // a candidate's place: how many come before it (they stand in the order of their index,
+            // so an equal one in a lower lane does); seldom are there more than 16
             int rank = 0;
-            for (unsigned left = live; left; left &= left - 1) {
-                const int i = __ffs(left) - 1;
-                const uint32_t o = __shfl_sync(kFull, cand, i);
-                rank += o > cand || (o == cand && i < lane) ? 1 : 0;
-            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                rank += __shfl_sync(kFull, cand, i) > (i < lane ? cand - 1u : cand) ? 1 : 0;
+            const unsigned live = __ballot_sync(kFull, cand != 0);
+            if (live >> 16)
+                for (int i = 16; i < 32; ++i)
+                    rank += __shfl_sync(kFull, cand, i) > (i < lane ? cand - 1u : cand) ? 1 : 0;
             __syncwarp();
-            if (cand != 0 && rank < a.k) cands_at[warp][rank] = (uint16_t)cand_at;
+            if (cand != 0 && rank < a.k) cands[warp][rank].y = (uint32_t)cand_at;
             __syncwarp();
-            if (lane < min(__popc(live), a.k)) mine = cands_at[warp][lane];
+            if (lane < min(__popc(live), a.k)) mine = (int)cands[warp][lane].y;
         } else {
             for (int i = 0; i < a.k; ++i) {
                 uint32_t m = key[0];
@@ -319,7 +320,6 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
         }
         const bool got = mine >= 0;
         const float zi = got ? load_f<kType>(a.logits, row + mine) : -CUDART_INF_F;
-        // (divisions only in lanes that hold a choice: a zero numerator takes the slow path)
         float w = 0.0f;
         if (a.sigmoid) {
             if (got) w = sigmoid_exact(zi);
@@ -514,12 +514,13 @@ struct PlanRun {
     }
 };
 
-// Counts the warp's run into `hist` (shared memory, [E], zero before).
-__device__ __forceinline__ void plan_count(const PlanArgs& a, const PlanRun& r, int* hist) {
+// Counts the warp's run into `hist` (shared memory, [E], zero before). Here and below, not `live`:
+// the same instructions on choices that are none, nothing read from or written to global memory.
+__device__ __forceinline__ void plan_count(const PlanArgs& a, const PlanRun& r, int* hist, bool live = true) {
     for (int64_t i = r.r0 + (threadIdx.x & 31); i < r.r1; i += 128) {
         int e[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) e[j] = i + 32 * j < r.r1 ? a.indices[i + 32 * j] : -1;
+        for (int j = 0; j < 4; ++j) e[j] = live && i + 32 * j < r.r1 ? a.indices[i + 32 * j] : -1;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if (e[j] >= 0 && e[j] < a.E) atomicAdd(hist + e[j], 1);
@@ -577,7 +578,8 @@ __device__ __forceinline__ void plan_offsets(const PlanArgs& a, int count, int b
 }
 
 // Rows of the warp's run; `my`: the warp's prefixes, advanced as it goes.
-__device__ __forceinline__ void plan_place(const PlanArgs& a, const PlanRun& run, const int* base, int* my) {
+__device__ __forceinline__ void plan_place(const PlanArgs& a, const PlanRun& run, const int* base, int* my,
+                                           bool live = true) {
     const int lane = threadIdx.x & 31;
     const unsigned below_me = (1u << lane) - 1u;
     constexpr int kAhead = 8;  // loads in flight
@@ -586,7 +588,7 @@ __device__ __forceinline__ void plan_place(const PlanArgs& a, const PlanRun& run
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
             const int64_t i = i0 + 32 * j + lane;
-            ahead[j] = i < run.r1 ? a.indices[i] : -1;
+            ahead[j] = live && i < run.r1 ? a.indices[i] : -1;
             if (ahead[j] >= a.E) ahead[j] = -1;
         }
 #pragma unroll
@@ -600,7 +602,7 @@ __device__ __forceinline__ void plan_place(const PlanArgs& a, const PlanRun& run
             __syncwarp();
             if (x >= 0 && (same & below_me) == 0) my[x] += __popc(same);
             __syncwarp();
-            if (i < run.r1) {
+            if (live && i < run.r1) {
                 a.slots[i] = at;
                 if (x >= 0) a.rows[at] = (int)i;
             }
@@ -619,28 +621,33 @@ __global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_kernel(const PlanArg
     const int warps = plan_warps(a, rank);
     for (int i = threadIdx.x; i < warps * a.E; i += kPlanThreads) hist[i] = 0;
     __syncthreads();
-    grid_dependency_wait();
     const PlanRun run(a, rank);
     int* const my = hist + (threadIdx.x >> 5) * a.E;
-    plan_count(a, run, my);
-    __syncthreads();
     const int e = threadIdx.x;
-    const int mine = plan_prefix(a, warps, hist);
-    if (e < a.E) totals[e] = mine;
-    cluster_sync();
-    int count = 0, below = 0;
-    if (e < a.E) {
-        const uint32_t at = smem_u32(totals + e);
-        for (int c = 0; c < ctas; ++c) {
-            const int v = ld_shared_cluster_s32(map_to_cta(at, c));
-            if (c < rank) below += v;
-            count += v;
+    // A first pass on no choices brings the instructions into the caches while the kernel before
+    // (usually the router) still runs: a token's plan is bound by fetching them.
+    for (int pass = 0; pass < 2; ++pass) {
+        const bool live = pass == 1;
+        if (live) grid_dependency_wait();
+        plan_count(a, run, my, live);
+        __syncthreads();
+        const int mine = plan_prefix(a, warps, hist);
+        if (e < a.E) totals[e] = mine;
+        cluster_sync();
+        int count = 0, below = 0;
+        if (e < a.E) {
+            const uint32_t at = smem_u32(totals + e);
+            for (int c = 0; c < ctas; ++c) {
+                const int v = ld_shared_cluster_s32(map_to_cta(at, c));
+                if (c < rank) below += v;
+                count += v;
+            }
         }
+        plan_offsets(a, count, below, live && rank == 0, base, warp_sums);
+        __syncthreads();
+        plan_place(a, run, base, my, live);
+        cluster_sync();  // no CTA goes on or leaves while another may still read its totals
     }
-    plan_offsets(a, count, below, rank == 0, base, warp_sums);
-    __syncthreads();
-    plan_place(a, run, base, my);
-    cluster_sync();  // no CTA leaves while another may still read its totals
 }
 
 __global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_count_kernel(const PlanArgs a) {
