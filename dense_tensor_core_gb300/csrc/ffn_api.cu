@@ -14,6 +14,19 @@ constexpr int64_t kMaxSize = 2147483647;
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 uint64_t up256(uint64_t v) { return (v + 255) & ~(uint64_t)255; }
 
+// Up to this many rows a product with K-major operands runs on the kernel without tiles, where its
+// blocks (16 features; gated, 8 and their gates) fill the SMs or K is short; else the K splits of the
+// tiles win (us, without tiles against tiles: 8 x 4096 x 4096 10.8 and 13.7, 16 x 8192 x 8192 27.6
+// and 30.4, 16 x 1032 x 4104 13.6 and 13.8; 8 x 1024 x 8192 14.6 and 14.3, 16 x 1024 x 8192 23.5 and
+// 15.9). Its 32-bit indexes run a little past K and N, hence the limit on both.
+constexpr int kSkinnyRows = 16, kSkinnyShortK = 4104;
+bool skinny(int64_t M, int64_t N, int64_t K, bool gated, bool k_major, int sms) {
+    constexpr int64_t most = (int64_t)1 << 30;
+    const int64_t blocks = ceil_div(N, gated ? 8 : 16);
+    return M <= kSkinnyRows && k_major && K > 0 && K % 8 == 0 && K <= most && N <= most &&
+           (blocks >= sms || K <= kSkinnyShortK);
+}
+
 // ------------------------------------------------------------------------------------------------
 // Launch plan of a feed-forward product
 // ------------------------------------------------------------------------------------------------
@@ -39,7 +52,10 @@ void size_split(FfnPlan* p) {
 // per 128-byte row piece that a CTA fetches (256 of the features, one per row of the tile); a piece
 // of rows that do not start on 128-byte lines spans two lines and costs 2.4 times that (the 2.4 is
 // measured: 1111 x 4112 x 2040 at 3.9 cycles a piece). An item costs 200 more; the last tile's
-// epilogue shows. Split items write their sums and the last of a tile reads them all back.
+// epilogue shows. Split items write their sums and the last of a tile reads them all back. What
+// that adds is not timed by itself but set so that the choice follows whole launches, apart for
+// rows that do not start on 128-byte lines (the smaller term there: 777 x 1032 x 1544 17.1 us in 3
+// pieces, 12.0 whole; the larger term on aligned rows: 64 x 4096 x 4096 16.6 us against 14.4).
 struct Delivery {
     double p = 1, q = 1;  // cost of a 128-byte piece of the features' and of the rows' operand
 };
@@ -49,7 +65,8 @@ double item_cost(const FfnPlan& p, int kb, int pairs, Delivery d) {
     double cost = 16.0 * p.tile_n;
     if (p.splits > 1) {
         const double item = p.kb_per_split * block + 200.0 + 6.0 * p.tile_n;
-        cost += (double)((split_items + pairs - 1) / pairs) * item + 2000.0 + 6.0 * p.tile_n * p.splits;
+        cost += (double)((split_items + pairs - 1) / pairs) * item;
+        cost += std::max(d.p, d.q) > 1 ? 4000.0 + 25.0 * p.tile_n * p.splits : 2000.0 + 6.0 * p.tile_n * p.splits;
         cost += (double)((whole + pairs - 1) / pairs) * (kb * block + 200.0);
     } else {
         cost += (double)((p.tiles + pairs - 1) / pairs) * (kb * block + 200.0);
@@ -248,6 +265,29 @@ int gemm_act(int dtype, const void* A, const void* B, void* C, int64_t M, int64_
     if (o.bias && (rc = check_device_ptr(o.bias, dev, "bias"))) return rc;
     if (o.residual && (rc = check_device_ptr(o.residual, dev, "residual"))) return rc;
     if (o.preact && (rc = check_device_ptr(o.preact, dev, "preact"))) return rc;
+    if (skinny(M, N, K, gated, !amn && !bmn, 2 * pairs_of(info))) {
+        SkinnyCall c;
+        c.bf16 = dtype == 0;
+        c.gated = gated;
+        c.wide = M > 8;
+        c.P = B;
+        c.ldp = o.ldb;
+        c.Q = A;
+        c.ldq = o.lda;
+        dtc::FfnArgs& a = c.args;
+        a.feats = (int)N;
+        a.rows = (int)M;
+        a.red = (int)K;
+        a.act = o.activation;
+        a.out = C;
+        a.ld_out = o.ldc;
+        a.bias = o.bias;
+        a.residual = o.residual;
+        a.ld_res = o.ld_residual;
+        a.preact = o.preact;
+        a.ld_pre = o.ld_preact;
+        return launch_skinny(c, (cudaStream_t)stream);
+    }
     const FfnPlan p = plan_rows(M, N, gated, K, amn, pairs_of(info), o.workspace ? o.workspace_bytes : 0,
                                 Delivery{piece_cost(B, o.ldb), piece_cost(A, o.lda)});
     if (p.num_ft == 0) return fail(GEMM_ERR_UNSUPPORTED, "too many tiles");
@@ -298,6 +338,8 @@ int gemm_act_workspace_size(int dtype, int64_t M, int64_t N, int64_t K, int layo
     int dev;
     DeviceInfo* info;
     if ((rc = current_device(&dev, &info))) return rc;
+    if (skinny(M, N, K, dtc::act_gated(activation), !a_is_mn(layout) && !b_is_mn(layout), 2 * pairs_of(info)))
+        return GEMM_OK;
     // for dense operands; other row pitches are planned within this size
     const Delivery d{piece_cost(nullptr, b_is_mn(layout) ? N : K), piece_cost(nullptr, a_is_mn(layout) ? M : K)};
     *bytes = plan_rows(M, N, dtc::act_gated(activation), K, a_is_mn(layout), pairs_of(info), ~0ull, d).bytes;
@@ -722,6 +764,36 @@ int red_product(const ExpertSizes& s, bool bf16, const int32_t* plan, const moe_
     return launch_ffn_experts(c, info, st);
 }
 
+// Whether the tokens are few enough for the kernel without tiles (us, without tiles against tiles:
+// 64 experts, 8 each, H 2048, F 1024: 1 token 28 and 36, 8 tokens 99 to 107 and 107, 16 tokens 159 to
+// 165 and 132 to 144; 128 experts, 4 each, F 768: 1 token 16 and 25, 8 tokens 58 to 64 and 67 to 70,
+// 16 tokens 116 and 96 to 104). An expert chosen more than 8 times by one plan, as only repeated
+// choices can, reads its weights again, from the L2.
+constexpr int kFewTokens = 8;
+bool few_rows(const ExpertSizes& s) { return s.T <= kFewTokens; }
+
+SkinnyCall skinny_call(const ExpertSizes& s, bool bf16, const int32_t* plan, const void* weights, int64_t red,
+                       int64_t feats, bool gated) {
+    SkinnyCall c;
+    c.bf16 = bf16;
+    c.seg = true;
+    c.gated = gated;
+    c.P = weights;
+    c.ldp = red;
+    c.k = s.k;
+    c.choices = s.T * s.k;
+    dtc::FfnArgs& a = c.args;
+    a.feats = (int)feats;
+    a.rows = (int)s.plan.capacity;
+    a.red = (int)red;
+    a.experts = (int)s.E;
+    a.p_expert_rows = (int)(gated ? 2 * feats : feats);
+    a.tiles = reinterpret_cast<const dtc::FfnTile*>(plan + s.plan.tiles);
+    a.num_tiles = plan;
+    a.max_tiles = (int)s.plan.max_tiles;
+    return c;
+}
+
 int experts_layout(const ExpertSizes& s, int train, int pairs, moe_experts_info* l) {
     const uint64_t R = s.plan.capacity;
     l->x = 0;
@@ -796,6 +868,39 @@ int moe_experts(int dtype, const void* x, const void* w_in, const void* w_out, c
     const int32_t* const pl = static_cast<const int32_t*>(plan);
     const cudaStream_t st = (cudaStream_t)stream;
     const bool bf16 = dtype == 0;
+    if (few_rows(s)) {
+        // weights are read for a handful of rows each: no tiles, and (without train, which keeps the
+        // rows) no gathering
+        if (train) {
+            const GatherCall g{x, b + l.x, weights, o.weights_dtype, reinterpret_cast<float*>(b + l.scale),
+                               nullptr, 0};
+            if ((rc = launch_moe_gather(g, pl, s.plan, k, E, H, s.ldH, info, st))) return rc;
+        }
+        SkinnyCall c = skinny_call(s, bf16, pl, w_in, H, F, s.gated);
+        c.Q = train ? static_cast<const void*>(b + l.x) : x;
+        c.ldq = train ? s.ldH : H;
+        if (train) {
+            c.args.row_scale = reinterpret_cast<const float*>(b + l.scale);
+        } else {
+            c.choice = pl + s.plan.rows;
+            c.weights = weights;
+            c.wtype = o.weights_dtype;
+        }
+        c.args.act = s.act;
+        c.args.out = b + l.h;
+        c.args.ld_out = s.ldF;
+        c.args.preact = train ? b + l.z : nullptr;
+        c.args.ld_pre = s.ldFz;
+        if ((rc = launch_skinny(c, st))) return rc;
+        c = skinny_call(s, bf16, pl, w_out, F, H, false);
+        c.Q = b + l.h;
+        c.ldq = s.ldF;
+        c.args.out = b + l.y;
+        c.args.ld_out = s.ldH;
+        if ((rc = launch_skinny(c, st))) return rc;
+        const JoinCall j{b + l.y, o.residual, y, nullptr, 0, nullptr, 0};
+        return launch_moe_join(bf16, j, pl, s.plan, T, k, E, H, s.ldH, info, st);
+    }
     const GatherCall g{x, b + l.x, weights, o.weights_dtype, reinterpret_cast<float*>(b + l.scale),
                        reinterpret_cast<uint32_t*>(split), (int)(sc.partial / 4)};
     if ((rc = launch_moe_gather(g, pl, s.plan, k, E, H, s.ldH, info, st))) return rc;

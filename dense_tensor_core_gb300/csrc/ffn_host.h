@@ -38,6 +38,23 @@ int launch_ffn(const FfnCall& c, DeviceInfo* dev, cudaStream_t stream) {
                         stream, tp, tq, c.args);
 }
 
+// A product of gemm16_skinny.cuh: K-major operands, red a multiple of 8; args carries the sizes, the
+// plan and the epilogue. wide (one matrix): 16 rows at a time
+// instead of 8.
+struct SkinnyCall {
+    bool bf16 = true, seg = false, gated = false, wide = false;
+    const void* P = nullptr;
+    const void* Q = nullptr;
+    int64_t ldp = 0, ldq = 0;
+    const int* choice = nullptr;  // rows straight from the tokens (the plan's rows)
+    int k = 1;
+    int64_t choices = 0;
+    const void* weights = nullptr;
+    int wtype = 2;
+    dtc::FfnArgs args = {};
+};
+int launch_skinny(const SkinnyCall& c, cudaStream_t stream);
+
 // dZ of gemm_act and its column sums (act_backward.cuh). dz may be NULL (sums only), dbias too.
 struct ActBackwardCall {
     bool bf16;
