@@ -4,6 +4,9 @@ operands, fp32 accumulation.
 The compute runs in the CUDA library ``libdtc_gemm.so`` (C ABI in ``include/dtc_gemm.h``). This
 package is a thin ctypes binding with the same function names: it checks and marshals torch
 tensors (device pointers, sizes, the current stream) and raises ``GemmError`` on a non-OK status.
+The feed-forward operators (``include/dtc_ffn.h``) run in the same library and are called through
+the native module ``_ffn_native``: gemm_act (product, bias, activation or gate, residual) and its
+gradient, moe_route and its gradient, moe_plan, moe_experts and its gradient.
 There is no CPU fallback: if the library is missing, every call raises.
 """
 from ._binding import (  # noqa: F401

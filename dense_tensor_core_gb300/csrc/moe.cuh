@@ -38,7 +38,8 @@ __device__ __forceinline__ float warp_max(float v) {
 // ties leave more than 32, k rounds over all keys do.
 //
 // Bound by the issue of instructions, not by HBM: for 256 experts a third of them are the 8 exact
-// logistic functions a lane computes.
+// logistic functions a lane computes. Measured (launch duration): 65536 x 256 fp32 logits, sigmoid, 8
+// of 256 in 8 groups 68 us, 1 TB/s of logits.
 // ------------------------------------------------------------------------------------------------
 struct RouteArgs {
     const void* logits;
@@ -425,7 +426,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_backward_kernel(co
 // Few choices (up to kPlanFew): one launch of one cluster, whose blocks read each other's counts
 // through distributed shared memory: for few tokens a second launch would take longer than the
 // work. Many: a counting launch and a placing launch on up to 128 blocks, the counts in the plan's
-// scratch (524288 choices, 256 experts: 78 us on one cluster).
+// scratch (524288 choices, 256 experts: 78 us on one cluster; launch durations of the two 4 and 18
+// us). 8 choices take 6 us, latency.
 // ------------------------------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024, kPlanWarps = 32, kPlanMaxCtas = 8;
 constexpr int kPlanFew = 8192, kPlanBlocks = 128;
@@ -685,7 +687,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_place_kernel(const P
 }
 
 // ------------------------------------------------------------------------------------------------
-// Movement of rows, bound by HBM. A warp per row, 16 bytes a lane.
+// Movement of rows, bound by HBM. A warp per row, 16 bytes a lane. Measured (launch durations, 4096
+// tokens by 8 of 64 experts, H 2048, bf16): gather 25 us (151 MB, 6.0 TB/s), join 31 to 33 us (168
+// MB, 5.1 to 5.4 TB/s).
 // ------------------------------------------------------------------------------------------------
 struct RowsArgs {
     const uint16_t* in;   // [T,H]
