@@ -47,42 +47,31 @@ void size_split(FfnPlan* p) {
     p->bytes = p->counter_bytes + (uint64_t)p->split_tiles * p->splits * p->tile_n * 1024;
 }
 
-// Modelled time of a launch in SM cycles. A K-block of 128 costs 4 cycles per row of the tile (the
-// tensor core's rate for 256 features) or the delivery of its operands, measured as about 1.6 cycles
-// per 128-byte row piece that a CTA fetches (256 of the features, one per row of the tile); a piece
-// of rows that do not start on 128-byte lines spans two lines and costs 2.4 times that (the 2.4 is
-// measured: 1111 x 4112 x 2040 at 3.9 cycles a piece). An item costs 200 more; the last tile's
-// epilogue shows. Split items write their sums and the last of a tile reads them all back. What
-// that adds is not timed by itself but set so that the choice follows whole launches, apart for
-// rows that do not start on 128-byte lines (the smaller term there: 777 x 1032 x 1544 17.1 us in 3
-// pieces, 12.0 whole; the larger term on aligned rows: 64 x 4096 x 4096 16.6 us against 14.4).
-struct Delivery {
-    double p = 1, q = 1;  // cost of a 128-byte piece of the features' and of the rows' operand
-};
-double item_cost(const FfnPlan& p, int kb, int pairs, Delivery d) {
-    const double block = std::max(4.0 * p.tile_n, 1.6 * (256 * d.p + p.tile_n * d.q));
+// Modelled time of a launch in us, less what every launch costs. The constants are fitted to the
+// measured times of every tile height and split of 46 sizes (K 176 to 8192, 32 to 8192 rows, plain
+// and gated, aligned and not; root mean square error 9 %). A K-block of 128 takes 0.43 us and little
+// more for more rows: three stages cover the latency of their loads and no more, so a tall tile is
+// cheaper per row until it leaves pairs idle (2048 x 4096 x 4096: 57 us in tiles of 160 rows, 47 in
+// 256; 1280 x 4096 x 4096: 41 and 34, the tail of 256 split in 4). Rows that do not start on 128-byte
+// lines add 6 %. Split items write their sums and the last of a tile reads them all back, which shows
+// in full where all tiles are split and little where whole tiles follow.
+bool off_lines(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 127) || ld % 64; }
+double item_cost(const FfnPlan& p, int kb, int pairs, bool off) {
+    const double block = (0.43 + 0.0005 * p.tile_n) * (off ? 1.06 : 1.0), item = 1.3;
     const int64_t split_items = (int64_t)p.split_tiles * p.splits, whole = p.tiles - p.split_tiles;
-    double cost = 16.0 * p.tile_n;
+    double cost = 0.0114 * p.tile_n + (double)((whole + pairs - 1) / pairs) * (kb * block + item);
     if (p.splits > 1) {
-        const double item = p.kb_per_split * block + 200.0 + 6.0 * p.tile_n;
-        cost += (double)((split_items + pairs - 1) / pairs) * item;
-        cost += std::max(d.p, d.q) > 1 ? 4000.0 + 25.0 * p.tile_n * p.splits : 2000.0 + 6.0 * p.tile_n * p.splits;
-        cost += (double)((whole + pairs - 1) / pairs) * (kb * block + 200.0);
-    } else {
-        cost += (double)((p.tiles + pairs - 1) / pairs) * (kb * block + 200.0);
+        cost += (double)((split_items + pairs - 1) / pairs) * (p.kb_per_split * block + item);
+        cost += whole > 0 ? 0.0062 * p.tile_n * p.splits : 2.2 + 0.01 * p.tile_n * p.splits;
     }
     return cost;
-}
-
-double piece_cost(const void* p, int64_t ld) {
-    return (reinterpret_cast<uintptr_t>(p) & 127) || ld % 64 ? 2.4 : 1.0;
 }
 
 // Tile rows and K splits of one matrix's product: the cheapest by item_cost, among whole tiles, all
 // tiles split (when they are fewer than two waves) and the tiles beyond whole waves split over the
 // pairs.
 FfnPlan plan_rows(int64_t rows, int64_t feats, bool gated, int64_t red, bool q_mn, int pairs,
-                  uint64_t ws_bytes, Delivery d) {
+                  uint64_t ws_bytes, bool off) {
     FfnPlan best;
     double cost = 0;
     const int ft = num_feature_tiles(feats, gated);
@@ -103,7 +92,7 @@ FfnPlan plan_rows(int64_t rows, int64_t feats, bool gated, int64_t red, bool q_m
             p.split_tiles = splits > 1 ? (int)split_tiles : 0;
             size_split(&p);
             if (p.bytes > ws_bytes || p.bytes > (64ull << 20)) return;
-            const double c = item_cost(p, kb, pairs, d);
+            const double c = item_cost(p, kb, pairs, off);
             if (best.num_ft == 0 || c < cost) {
                 best = p;
                 cost = c;
@@ -141,7 +130,7 @@ FfnPlan plan_seg(int64_t T, int k, int64_t E, int64_t max_tiles, int64_t feats, 
         q.kb_per_split = ceil_div(kb, s);
         if (s > 1 && ceil_div(kb, q.kb_per_split) != s) continue;
         q.split_tiles = s > 1 ? (int)q.tiles : 0;
-        const double c = item_cost(q, kb, pairs, Delivery());
+        const double c = item_cost(q, kb, pairs, false);
         if (s == 1 || c < cost) {
             cost = c;
             p.splits = s;
@@ -289,7 +278,7 @@ int gemm_act(int dtype, const void* A, const void* B, void* C, int64_t M, int64_
         return launch_skinny(c, (cudaStream_t)stream);
     }
     const FfnPlan p = plan_rows(M, N, gated, K, amn, pairs_of(info), o.workspace ? o.workspace_bytes : 0,
-                                Delivery{piece_cost(B, o.ldb), piece_cost(A, o.lda)});
+                                off_lines(B, o.ldb) || off_lines(A, o.lda));
     if (p.num_ft == 0) return fail(GEMM_ERR_UNSUPPORTED, "too many tiles");
     if (p.splits > 1 && (rc = check_device_ptr(o.workspace, dev, "the workspace"))) return rc;
     FfnCall c;
@@ -341,8 +330,8 @@ int gemm_act_workspace_size(int dtype, int64_t M, int64_t N, int64_t K, int layo
     if (skinny(M, N, K, dtc::act_gated(activation), !a_is_mn(layout) && !b_is_mn(layout), 2 * pairs_of(info)))
         return GEMM_OK;
     // for dense operands; other row pitches are planned within this size
-    const Delivery d{piece_cost(nullptr, b_is_mn(layout) ? N : K), piece_cost(nullptr, a_is_mn(layout) ? M : K)};
-    *bytes = plan_rows(M, N, dtc::act_gated(activation), K, a_is_mn(layout), pairs_of(info), ~0ull, d).bytes;
+    const bool off = off_lines(nullptr, b_is_mn(layout) ? N : K) || off_lines(nullptr, a_is_mn(layout) ? M : K);
+    *bytes = plan_rows(M, N, dtc::act_gated(activation), K, a_is_mn(layout), pairs_of(info), ~0ull, off).bytes;
     return GEMM_OK;
 }
 
