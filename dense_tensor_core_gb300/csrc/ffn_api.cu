@@ -753,12 +753,12 @@ int red_product(const ExpertSizes& s, bool bf16, const int32_t* plan, const moe_
     return launch_ffn_experts(c, info, st);
 }
 
-// Whether the tokens are few enough for the kernel without tiles (us, without tiles against tiles:
-// 64 experts, 8 each, H 2048, F 1024: 1 token 28 and 36, 8 tokens 99 to 107 and 107, 16 tokens 159 to
-// 165 and 132 to 144; 128 experts, 4 each, F 768: 1 token 16 and 25, 8 tokens 58 to 64 and 67 to 70,
-// 16 tokens 116 and 96 to 104). An expert chosen more than 8 times by one plan, as only repeated
-// choices can, reads its weights again, from the L2.
-constexpr int kFewTokens = 8;
+// Whether the tokens are few enough for the kernel without tiles (us with the same routes, without
+// tiles against tiles. 64 experts, 8 each, H 2048, F 1024: 1 token 28 and 36, 16 tokens 127 and 128,
+// 48 157 and 151. 8 experts, 2 each, H and F 4096: 43 and 55, 16 tokens 133 and 153, 32 177 and 155.
+// 128 experts, 4 each, H 2048, F 768: 16 and 25, 16 tokens 93 and 91, 24 136 and 129). An expert with
+// more than 8 rows reads its weights again, from the L2.
+constexpr int kFewTokens = 16;
 bool few_rows(const ExpertSizes& s) { return s.T <= kFewTokens; }
 
 SkinnyCall skinny_call(const ExpertSizes& s, bool bf16, const int32_t* plan, const void* weights, int64_t red,

@@ -86,3 +86,30 @@ def test_experts(T, kind, H, F, name, one):
     dtc.gemm_stream_status()
     R.check(got, y, bound, "y")
     assert torch.equal(dtc.moe_experts(kind, x, wi, wo, w, plan, activation=name, residual=res, save=True)[0], got)
+
+
+# the number of tokens from which tiles take over, with experts of several turns of 8 rows
+@pytest.mark.parametrize("T", [10, 15, 16, 17])
+@pytest.mark.parametrize("kind,E,k,H,F,name", [("bf16", 3, 2, 520, 264, "geglu"), ("f16", 40, 8, 72, 136, "silu")])
+def test_experts_around_the_change(T, kind, E, k, H, F, name):
+    import dense_tensor_core_gb300 as dtc
+    Fz = 2 * F if name in R.GATED else F
+    x = rand((T, H), kind, 1)
+    wi, wo = rand((E, Fz, H), kind, 3, H ** -0.5), rand((E, H, F), kind, 4, F ** -0.5)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    idx = torch.rand((T, E), generator=g, device="cuda").topk(k, 1).indices.to(torch.int32)
+    w = torch.softmax(torch.randn((T, k), generator=g, device="cuda"), 1)
+    plan = dtc.moe_plan(idx, E)
+    y, bound = R.experts_bound(kind, x.double(), wi.double(), wo.double(), w.double(), idx, name)
+    got = dtc.moe_experts(kind, x, wi, wo, w, plan, activation=name)
+    dtc.gemm_stream_status()
+    R.check(got, y, bound, "y")
+    # kept rows of a training call give a gradient
+    y2, saved = dtc.moe_experts(kind, x, wi, wo, w, plan, activation=name, save=True)
+    assert torch.equal(y2, got)
+    dy = rand((T, H), kind, 9)
+    grads = dtc.moe_experts_backward(kind, dy, wi, wo, w, plan, saved, activation=name)
+    leaf = [t.double().requires_grad_() for t in (x, wi, wo, w)]
+    want = torch.autograd.grad(R.experts(*leaf, idx, name), leaf, dy.double())
+    for a, r, n, what in zip(grads, want, (4, 3, 2, 2), ("dx", "dw_in", "dw_out", "dweights")):
+        R.close(a, r, 1.1 * n * R.U[kind], what)
