@@ -14,17 +14,19 @@ constexpr int64_t kMaxSize = 2147483647;
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 uint64_t up256(uint64_t v) { return (v + 255) & ~(uint64_t)255; }
 
-// Up to this many rows a product with K-major operands runs on the kernel without tiles, where its
-// blocks (16 features; gated, 8 and their gates) fill the SMs or K is short; else the K splits of the
-// tiles win (us, without tiles against tiles: 8 x 4096 x 4096 10.8 and 13.7, 16 x 8192 x 8192 27.6
-// and 30.4, 16 x 1032 x 4104 13.6 and 13.8; 8 x 1024 x 8192 14.6 and 14.3, 16 x 1024 x 8192 23.5 and
-// 15.9). Its 32-bit indexes run a little past K and N, hence the limit on both.
-constexpr int kSkinnyRows = 16, kSkinnyShortK = 4104;
+// Up to this many rows a product with K-major operands runs on the kernel without tiles. A block of it
+// (16 features; gated, 8 and their gates) walks the whole K, so a long K needs several blocks an SM to
+// fill the HBM, else the K splits of the tiles win. Measured (K up to 16384; gated not apart), us, without tiles and with:
+//   K short           8 x 1024 x 4096 8.3, 11.5; 16 x 1024 x 5120 12.4, 13.2; 16 x 1024 x 6144 14.4, 13.7
+//   2 blocks an SM    16 x 4864 x 8192 20.7, 22.0; 8 x 4864 x 16384 36.6, 33.4
+//   3 blocks an SM    8 x 7296 x 16384 44.6, 48.2; 16 x 8192 x 8192 26.6, 30.6
+// Its 32-bit indexes run a little past K and N, hence the limit on both.
+constexpr int kSkinnyRows = 16, kSkinnyShortK = 5120, kSkinnyLongK = 8192;
 bool skinny(int64_t M, int64_t N, int64_t K, bool gated, bool k_major, int sms) {
     constexpr int64_t most = (int64_t)1 << 30;
     const int64_t blocks = ceil_div(N, gated ? 8 : 16);
     return M <= kSkinnyRows && k_major && K > 0 && K % 8 == 0 && K <= most && N <= most &&
-           (blocks >= sms || K <= kSkinnyShortK);
+           (K <= kSkinnyShortK || (blocks >= 2 * sms && K <= kSkinnyLongK) || blocks >= 3 * sms);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -754,9 +756,9 @@ int red_product(const ExpertSizes& s, bool bf16, const int32_t* plan, const moe_
 }
 
 // Whether the tokens are few enough for the kernel without tiles (us with the same routes, without
-// tiles against tiles. 64 experts, 8 each, H 2048, F 1024: 1 token 28 and 36, 16 tokens 127 and 128,
+// tiles against tiles. 64 experts, 8 each, H 2048, F 1024: 1 token 28 and 36, 16 tokens 124 and 128,
 // 48 157 and 151. 8 experts, 2 each, H and F 4096: 43 and 55, 16 tokens 133 and 153, 32 177 and 155.
-// 128 experts, 4 each, H 2048, F 768: 16 and 25, 16 tokens 93 and 91, 24 136 and 129). An expert with
+// 128 experts, 4 each, H 2048, F 768: 16 and 25, 16 tokens 90 and 91, 24 136 and 129). An expert with
 // more than 8 rows reads its weights again, from the L2.
 constexpr int kFewTokens = 16;
 bool few_rows(const ExpertSizes& s) { return s.T <= kFewTokens; }

@@ -46,7 +46,7 @@
 // Measured: 4096 x 4096 x 8192 with GELU, bias, residual and the kept sum 181 us (1515 TFLOP/s);
 // launch durations of 4096 tokens by 8 of 64 experts, H 2048, F 1024, bf16: the gated product 180 to
 // 190 us (1447 to 1527 TFLOP/s), the second 105 to 109 us (1261 to 1309). Large products are bound
-// by the tensor pipe and the waits of its ring, narrow ones by the delivery of operands.
+// by the tensor pipe and the waits of its ring, narrow ones by the latency of the loads.
 #pragma once
 
 #include "activation.cuh"
