@@ -131,8 +131,8 @@ def gemm_act(kind, A, B, C=None, layout="NT", bias=None, residual=None, activati
     activation: none, relu, gelu, gelu_tanh, silu, or the gated swiglu / geglu (layout "NT", B
     [2N, K] with the gate rows first, bias [2N]). preact (optional, [M,N], gated [M,2N]) receives
     the sum before the activation, for gemm_act_backward. workspace: a zero-filled CUDA tensor of
-    gemm_act_workspace_size bytes, reusable by later calls of the same stream. C may be the
-    residual."""
+    gemm_act_workspace_size bytes, reusable by later calls of the same stream, of other sizes too.
+    C may be the residual."""
     return _N().gemm_act(_code(_KIND, kind, "kind"), _code(_ACT, activation, "activation"),
                          _layout(layout), A, B, C, bias, residual, preact, workspace, timeout_ns,
                          fault_inject, _handle(stream))

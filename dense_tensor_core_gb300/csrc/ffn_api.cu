@@ -42,10 +42,20 @@ struct FfnPlan {
 
 int num_feature_tiles(int64_t feats, bool gated) { return ceil_div(feats, gated ? 128 : 256); }
 
-void size_split(FfnPlan* p) {
+// Counters of a split tile, and of a plan of `tiles` split ones.
+constexpr uint64_t kTileCounterBytes = 2 * dtc::ffn::kEpWarps * 4;
+uint64_t counters_of(int64_t tiles) { return up256((uint64_t)tiles * kTileCounterBytes); }
+// Head of a caller's workspace that holds the words which are zero between calls: the same bytes
+// whatever the sizes, row pitches and alignment of a call are, so that one workspace serves calls of
+// different plans (a plan's partial sums must not reach where a later plan counts). Plans split fewer
+// than 2 * pairs tiles.
+uint64_t zero_words_bytes(int pairs) { return counters_of(2 * pairs); }
+
+// `counters`: bytes of the region before the partial sums.
+void size_split(FfnPlan* p, uint64_t counters) {
     p->counter_bytes = p->bytes = 0;
     if (p->splits <= 1) return;
-    p->counter_bytes = up256((uint64_t)p->split_tiles * 2 * dtc::ffn::kEpWarps * 4);
+    p->counter_bytes = counters;
     p->bytes = p->counter_bytes + (uint64_t)p->split_tiles * p->splits * p->tile_n * 1024;
 }
 
@@ -92,7 +102,7 @@ FfnPlan plan_rows(int64_t rows, int64_t feats, bool gated, int64_t red, bool q_m
             if (splits > 1 && ceil_div(kb, p.kb_per_split) != splits) return;
             p.splits = splits;
             p.split_tiles = splits > 1 ? (int)split_tiles : 0;
-            size_split(&p);
+            size_split(&p, zero_words_bytes(pairs));
             if (p.bytes > ws_bytes || p.bytes > (64ull << 20)) return;
             const double c = item_cost(p, kb, pairs, off);
             if (best.num_ft == 0 || c < cost) {
@@ -140,7 +150,7 @@ FfnPlan plan_seg(int64_t T, int k, int64_t E, int64_t max_tiles, int64_t feats, 
         }
     }
     if (p.splits > 1) p.split_tiles = (int)p.tiles;
-    size_split(&p);
+    size_split(&p, counters_of(p.split_tiles));  // (cleared by each call: no need for a fixed place)
     p.grid = 2 * (int)std::min<int64_t>(p.items(), pairs);
     return p;
 }
