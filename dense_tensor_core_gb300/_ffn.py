@@ -151,7 +151,8 @@ def gemm_act_backward(kind, dC, A, B, preact=None, layout="NT", activation="none
     """(dA, dB, dbias) of gemm_act from dC [M,N] and the preact it kept (not needed for "none"):
     dA and dB stored as A and B are, dbias fp32. need: which of the three to compute (the others
     are None). The gradient of a residual is dC. workspace: a zero-filled CUDA tensor of
-    gemm_act_backward_workspace_size bytes; allocated here when not given."""
+    gemm_act_backward_workspace_size bytes, reusable like gemm_act's, also by calls of gemm_act;
+    allocated here when not given."""
     act, code = _code(_ACT, activation, "activation"), _layout(layout)
     if workspace is None and dC.is_cuda and A.dim() == 2 and B.dim() == 2:
         K = A.shape[1 - code // 2]

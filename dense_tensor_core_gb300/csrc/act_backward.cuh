@@ -25,7 +25,7 @@ struct ActBackArgs {
     int64_t M, N, ldc, ldz;
     int act;
     int rows_per_block;
-    uint32_t* counters;
+    uint32_t* counters;  // one a strip; neither is used with one row block
     float* partial;      // [gridDim.y][width]
 };
 
@@ -116,9 +116,10 @@ __global__ void __launch_bounds__(kActBackThreads) act_backward_kernel(const Act
             float t = 0.0f;
 #pragma unroll
             for (int j = 0; j < kActBackLanes; ++j) t += sums[j][k * kActBackCols + threadIdx.x];
-            a.partial[(int64_t)blockIdx.y * width + k * a.N + c0] = t;
+            (gridDim.y == 1 ? a.dbias : a.partial + (int64_t)blockIdx.y * width)[k * a.N + c0] = t;
         }
     }
+    if (gridDim.y == 1) return;
     __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) {

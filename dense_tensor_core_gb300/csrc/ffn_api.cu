@@ -45,11 +45,13 @@ int num_feature_tiles(int64_t feats, bool gated) { return ceil_div(feats, gated 
 // Counters of a split tile, and of a plan of `tiles` split ones.
 constexpr uint64_t kTileCounterBytes = 2 * dtc::ffn::kEpWarps * 4;
 uint64_t counters_of(int64_t tiles) { return up256((uint64_t)tiles * kTileCounterBytes); }
-// Head of a caller's workspace that holds the words which are zero between calls: the same bytes
-// whatever the sizes, row pitches and alignment of a call are, so that one workspace serves calls of
-// different plans (a plan's partial sums must not reach where a later plan counts). Plans split fewer
-// than 2 * pairs tiles.
-uint64_t zero_words_bytes(int pairs) { return counters_of(2 * pairs); }
+// Head of a caller's workspace that holds the words which are zero between calls: the same bytes for
+// gemm_act and gemm_act_backward, whatever the sizes, row pitches and alignment of a call are, so that
+// one workspace serves calls of both (what one call leaves in the rest must not reach where another
+// counts). First the counters of split tiles (plans split fewer than 2 * pairs of them) and of the
+// column sums' strips, then the stream-K flags of the gradient's products.
+uint64_t flags_offset(int pairs) { return std::max<uint64_t>(counters_of(2 * pairs), kActBackwardStrips * 4); }
+uint64_t zero_words_bytes(int pairs) { return flags_offset(pairs) + kSkFlagBytes; }
 
 // `counters`: bytes of the region before the partial sums.
 void size_split(FfnPlan* p, uint64_t counters) {
@@ -374,12 +376,13 @@ BackProduct grad_b(int64_t M, int64_t Nb, int64_t K, int layout) {
     }
 }
 
-// Workspace of gemm_act_backward: counters of the column sums, the stream-K workspace of the
-// products (both zero between calls), dZ, the column sums' pieces.
+// Workspace of gemm_act_backward: the words that are zero between calls, which end with the flags at
+// the start of the products' stream-K workspace; the pieces of that; dZ; the column sums' pieces.
 struct BackLayout {
     uint64_t sk, sk_bytes, dz, partial, bytes;
 };
-int back_layout(int dtype, int64_t M, int64_t N, int64_t K, int layout, int act, int sms, BackLayout* l) {
+int back_layout(int dtype, int64_t M, int64_t N, int64_t K, int layout, int act, int sms, int pairs,
+                BackLayout* l) {
     const int64_t Nb = dtc::act_gated(act) ? 2 * N : N;
     uint64_t sk = 0;
     for (const BackProduct& p : {grad_a(M, Nb, K, layout), grad_b(M, Nb, K, layout)}) {
@@ -390,9 +393,9 @@ int back_layout(int dtype, int64_t M, int64_t N, int64_t K, int layout, int act,
         }
         sk = std::max(sk, b);
     }
-    l->sk = up256((uint64_t)act_backward_col_blocks(N) * 4);
+    l->sk = flags_offset(pairs);
     l->sk_bytes = sk;
-    l->dz = l->sk + up256(sk);
+    l->dz = l->sk + up256(std::max(sk, kSkFlagBytes));
     l->partial = l->dz + (act != GEMM_ACT_NONE ? up256((uint64_t)M * Nb * 2) : 0);
     l->bytes = l->partial + up256((uint64_t)act_backward_partial_floats(M, N, sms) * 4);
     return GEMM_OK;
@@ -413,7 +416,7 @@ int gemm_act_backward_workspace_size(int dtype, int64_t M, int64_t N, int64_t K,
     DeviceInfo* info;
     if ((rc = current_device(&dev, &info))) return rc;
     BackLayout l;
-    if ((rc = back_layout(dtype, M, N, K, layout, activation, info->model.sms, &l))) return rc;
+    if ((rc = back_layout(dtype, M, N, K, layout, activation, info->model.sms, pairs_of(info), &l))) return rc;
     *bytes = l.bytes;
     return GEMM_OK;
 }
@@ -440,7 +443,7 @@ int gemm_act_backward(int dtype, const void* dC, const void* A, const void* B, v
     DeviceInfo* info;
     if ((rc = current_device(&dev, &info))) return rc;
     BackLayout l;
-    if ((rc = back_layout(dtype, M, N, K, layout, o.activation, info->model.sms, &l))) return rc;
+    if ((rc = back_layout(dtype, M, N, K, layout, o.activation, info->model.sms, pairs_of(info), &l))) return rc;
     if (!o.workspace || o.workspace_bytes < l.bytes)
         return fail(GEMM_ERR_INVALID_ARG, "gemm_act_backward needs a workspace of %llu bytes",
                     (unsigned long long)l.bytes);

@@ -64,10 +64,10 @@ struct ActBackwardCall {
     float* dbias;
     int64_t M, N, ldc, ldz;
     int act;
-    uint32_t* counters;  // act_backward_col_blocks words, zero between calls
+    uint32_t* counters;  // kActBackwardStrips words, zero between calls
     float* partial;      // act_backward_partial_floats
 };
-int64_t act_backward_col_blocks(int64_t width);
+constexpr int kActBackwardStrips = 1024;  // column strips whose pieces meet through a counter, at most
 int64_t act_backward_partial_floats(int64_t M, int64_t width, int sms);
 int launch_act_backward(const ActBackwardCall& c, DeviceInfo* dev, cudaStream_t stream);
 

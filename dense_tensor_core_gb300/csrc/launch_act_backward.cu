@@ -5,20 +5,21 @@
 namespace dtc_host {
 
 namespace {
+int64_t strips(int64_t N) { return (N + dtc::kActBackCols - 1) / dtc::kActBackCols; }
+
 // Row blocks: about 2 blocks per SM in all (enough loads in flight for the copy bandwidth; more row
-// blocks only lengthen the last block's sum over them), each with at least 32 rows.
+// blocks only lengthen the last block's sum over them), each with at least 32 rows. Above
+// kActBackwardStrips strips (more than SMs) there is one.
 int row_blocks(int64_t M, int64_t N, int sms) {
-    const int64_t gx = (N + dtc::kActBackCols - 1) / dtc::kActBackCols;
+    const int64_t gx = strips(N);
+    if (gx > kActBackwardStrips) return 1;
     return (int)std::max<int64_t>(1, std::min<int64_t>((M + 31) / 32, (int64_t)sms * 2 / gx));
 }
 }  // namespace
 
-int64_t act_backward_col_blocks(int64_t N) {
-    return (N + dtc::kActBackCols - 1) / dtc::kActBackCols;
-}
-
 int64_t act_backward_partial_floats(int64_t M, int64_t N, int sms) {
-    return 2 * N * row_blocks(M, N, sms);
+    const int blocks = row_blocks(M, N, sms);
+    return blocks > 1 ? 2 * N * blocks : 0;
 }
 
 int launch_act_backward(const ActBackwardCall& c, DeviceInfo* dev, cudaStream_t stream) {
@@ -37,7 +38,7 @@ int launch_act_backward(const ActBackwardCall& c, DeviceInfo* dev, cudaStream_t 
     a.rows_per_block = (int)((c.M + gy - 1) / gy);
     a.counters = c.counters;
     a.partial = c.partial;
-    const dim3 grid((unsigned)act_backward_col_blocks(c.N), gy);
+    const dim3 grid((unsigned)strips(c.N), gy);
     auto kern = c.bf16 ? (gated ? dtc::act_backward_kernel<true, true> : dtc::act_backward_kernel<true, false>)
                        : (gated ? dtc::act_backward_kernel<false, true> : dtc::act_backward_kernel<false, false>);
     return launch_chain(kern, grid, dtc::kActBackThreads, 0, 1, true, stream, a);

@@ -43,11 +43,11 @@ typedef struct {
     int64_t lda, ldb, ldc; /* elements between stored rows; 0 = dense. ldc: of C or of dC */
     int64_t ld_residual, ld_preact;
     void* workspace;       /* device scratch, 16-byte aligned, all zero before the first call that
-                              uses it. Its head holds counters, in the same place for every size;
-                              every completed call leaves them zero, so one workspace serves
-                              gemm_act calls of any sizes (after a GEMM_ERR_TIMEOUT, zero it
-                              before reuse). Calls that may run at the same time must not share
-                              it, nor may calls of gemm_ex. */
+                              uses it. Its head holds counters and flags, in the same place for
+                              every size; every completed call leaves them zero, so one workspace
+                              serves calls of gemm_act and gemm_act_backward of any sizes (after a
+                              GEMM_ERR_TIMEOUT, zero it before reuse). Calls that may run at the
+                              same time must not share it, nor may calls of gemm_ex. */
     uint64_t workspace_bytes;
     uint64_t timeout_ns;   /* limit of every device-side wait; 0 = the default (2 s) */
     int fault_inject;      /* test hook, 0 in normal use (see gemm_options) */
