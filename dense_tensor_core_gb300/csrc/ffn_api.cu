@@ -383,6 +383,8 @@ struct BackLayout {
 };
 int back_layout(int dtype, int64_t M, int64_t N, int64_t K, int layout, int act, int sms, int pairs,
                 BackLayout* l) {
+    *l = {};
+    if (M == 0 || N == 0) return GEMM_OK;  // no dZ, no sums over it, no pieces
     const int64_t Nb = dtc::act_gated(act) ? 2 * N : N;
     uint64_t sk = 0;
     for (const BackProduct& p : {grad_a(M, Nb, K, layout), grad_b(M, Nb, K, layout)}) {
@@ -412,6 +414,7 @@ int gemm_act_backward_workspace_size(int dtype, int64_t M, int64_t N, int64_t K,
     *bytes = 0;
     int rc = check_act(dtype, M, N, K, layout, activation);
     if (rc) return rc;
+    if (M == 0 || N == 0) return GEMM_OK;
     int dev;
     DeviceInfo* info;
     if ((rc = current_device(&dev, &info))) return rc;
@@ -444,10 +447,12 @@ int gemm_act_backward(int dtype, const void* dC, const void* A, const void* B, v
     if ((rc = current_device(&dev, &info))) return rc;
     BackLayout l;
     if ((rc = back_layout(dtype, M, N, K, layout, o.activation, info->model.sms, pairs_of(info), &l))) return rc;
-    if (!o.workspace || o.workspace_bytes < l.bytes)
-        return fail(GEMM_ERR_INVALID_ARG, "gemm_act_backward needs a workspace of %llu bytes",
-                    (unsigned long long)l.bytes);
-    if ((rc = check_device_ptr(o.workspace, dev, "the workspace"))) return rc;
+    if (l.bytes) {
+        if (!o.workspace || o.workspace_bytes < l.bytes)
+            return fail(GEMM_ERR_INVALID_ARG, "gemm_act_backward needs a workspace of %llu bytes",
+                        (unsigned long long)l.bytes);
+        if ((rc = check_device_ptr(o.workspace, dev, "the workspace"))) return rc;
+    }
     char* const ws = static_cast<char*>(o.workspace);
     const cudaStream_t s = (cudaStream_t)stream;
     const void* dz = dC;
@@ -489,7 +494,7 @@ int gemm_act_backward(int dtype, const void* dC, const void* A, const void* B, v
         if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(dbias)");
     }
     if (act) {
-        dz = ws + l.dz;
+        if (l.bytes) dz = ws + l.dz;
         ldz = Nb;
     }
     ga.timeout_ns = gb.timeout_ns = o.timeout_ns;

@@ -12,7 +12,7 @@ int64_t strips(int64_t N) { return (N + dtc::kActBackCols - 1) / dtc::kActBackCo
 // kActBackwardStrips strips (more than SMs) there is one.
 int row_blocks(int64_t M, int64_t N, int sms) {
     const int64_t gx = strips(N);
-    if (gx > kActBackwardStrips) return 1;
+    if (gx == 0 || gx > kActBackwardStrips) return 1;
     return (int)std::max<int64_t>(1, std::min<int64_t>((M + 31) / 32, (int64_t)sms * 2 / gx));
 }
 }  // namespace

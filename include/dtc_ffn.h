@@ -82,13 +82,14 @@ int gemm_act_workspace_size(int dtype, int64_t M, int64_t N, int64_t K, int layo
  * The workspace (gemm_act_backward_workspace_size bytes) holds dZ, the column sums' pieces and the
  * products' stream-K pieces. opts->bias, residual and fault_inject are not read. INVALID_ARG as
  * gemm_act, when preact is NULL where it is needed, or when the workspace is missing or too small.
- * The pages have no counterpart.
+ * Degenerate sizes: with M == 0 or N == 0 there is no dZ, what it would be summed into is zero, and no
+ * workspace is needed; with K == 0 only dbias is left. The pages have no counterpart.
  */
 int gemm_act_backward(int dtype, const void* dC, const void* A, const void* B, void* dA, void* dB,
                       float* dbias, int64_t M, int64_t N, int64_t K, int layout,
                       const gemm_act_options* opts, dtc_stream_t stream);
 
-/* Bytes of workspace gemm_act_backward needs. The pages have no counterpart. */
+/* Bytes of workspace gemm_act_backward needs (0 for M == 0 or N == 0). The pages have no counterpart. */
 int gemm_act_backward_workspace_size(int dtype, int64_t M, int64_t N, int64_t K, int layout,
                                      int activation, uint64_t* bytes);
 

@@ -55,6 +55,14 @@ def test_gated_takes_nt_only(L, layout, back):
     assert _act(L, layout=layout, activation=5, preact=0x4000, back=back) == UNSUPPORTED
 
 
+@pytest.mark.parametrize("M,N", [(16, 0), (0, 16), (0, 0)])
+@pytest.mark.parametrize("act", [0, 1, 5])
+def test_empty_gradient_needs_no_workspace(L, M, N, act):
+    out = ctypes.c_uint64(7)
+    assert L.gemm_act_backward_workspace_size(0, M, N, 64, 0, act, ctypes.byref(out)) == 0
+    assert out.value == 0
+
+
 def test_empty_results_are_no_ops(L):
     assert _act(L, A=0, B=0, C=0, M=0) == 0
     assert _act(L, A=0, B=0, C=0, N=0) == 0

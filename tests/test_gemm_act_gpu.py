@@ -288,3 +288,25 @@ def test_gradient_parts_strides_and_empty():
     e = lambda *s: torch.empty(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
     dA, dB, db = dtc.gemm_act_backward(kind, e(0, N), e(0, K), B, preact=e(0, N), activation="gelu")
     assert dA.shape == (0, K) and bool((dB == 0).all()) and bool((db == 0).all())
+
+
+@pytest.mark.parametrize("layout", ["NT", "NN", "TN", "TT"])
+@pytest.mark.parametrize("name", ["none", "silu", "swiglu"])
+@pytest.mark.parametrize("M,N,K", [(40, 0, 64), (0, 24, 64), (40, 24, 0), (40, 0, 0), (0, 0, 64)])
+def test_gradient_of_empty_operands(M, N, K, name, layout):
+    import dense_tensor_core_gb300 as dtc
+    if name in R.GATED and layout != "NT":
+        pytest.skip("gated activations take NT")
+    A, B, Nb = operands("bf16", layout, M, N, K, name)
+    dC, z = rand((M, N), "bf16", 5), rand((M, Nb), "bf16", 6)
+    dA, dB, db = dtc.gemm_act_backward("bf16", dC, A, B, preact=z, layout=layout, activation=name)
+    dtc.gemm_stream_status()
+    assert dA.shape == A.shape and dB.shape == B.shape and db.shape == (Nb,)
+    assert bool((dA == 0).all()) and bool((dB == 0).all())  # sums over nothing
+    if K:
+        assert bool((db == 0).all())
+    else:
+        _, _, dz = reference_gradient("bf16", dC, A, B, z, layout, name)
+        # at most 40 fp32 additions of terms within 2^-16
+        R.check(db, dz.sum(0), (2.0 ** -16 + 40 * 2.0 ** -24) * 1.2 *
+                (dC.double().abs().sum(0).repeat(Nb // max(N, 1)) * (1 + z.double().abs().max())), "dbias")
