@@ -305,8 +305,8 @@ def test_gradient_of_empty_operands(M, N, K, name, layout):
     assert bool((dA == 0).all()) and bool((dB == 0).all())  # sums over nothing
     if K:
         assert bool((db == 0).all())
-    else:
+    elif N:
         _, _, dz = reference_gradient("bf16", dC, A, B, z, layout, name)
         # at most 40 fp32 additions of terms within 2^-16
         R.check(db, dz.sum(0), (2.0 ** -16 + 40 * 2.0 ** -24) * 1.2 *
-                (dC.double().abs().sum(0).repeat(Nb // max(N, 1)) * (1 + z.double().abs().max())), "dbias")
+                (dC.double().abs().sum(0).repeat(Nb // N) * (1 + z.double().abs().max())), "dbias")
