@@ -157,10 +157,12 @@ def gemm_act_backward(kind, dC, A, B, preact=None, layout="NT", activation="none
     if workspace is None and dC.is_cuda and A.dim() == 2 and B.dim() == 2:
         K = A.shape[1 - code // 2]
         Nb = B.shape[0 if code in (0, 3) else 1]
-        with torch.cuda.device(dC.device):
+        # the fill is ordered before the kernels, and the memory not reused before them, only on their
+        # own stream
+        with torch.cuda.device(dC.device), torch.cuda.stream(stream):
             n = gemm_act_backward_workspace_size(kind, dC.shape[0], Nb // 2 if act >= 5 else Nb, K,
                                                  layout, activation)
-        workspace = torch.zeros(max(n, 16), dtype=torch.uint8, device=dC.device)
+            workspace = torch.zeros(max(n, 16), dtype=torch.uint8, device=dC.device)
     return _N().gemm_act_backward(_code(_KIND, kind, "kind"), act, code, dC, A, B, preact,
                                   bool(need[0]), bool(need[1]), bool(need[2]), workspace, timeout_ns,
                                   _handle(stream))
