@@ -2,6 +2,10 @@
 allocation and the calls are in the native module ``_ffn_native`` (csrc/ffn_binding.cpp), which
 raises TypeError, ValueError or GemmError; sizes and layouts go through ctypes. Every arithmetic
 step runs in the library's kernels.
+
+stream: None for the current stream. A call allocates its outputs and buffers as under
+``torch.cuda.stream(stream)``, so tensors it returns belong to that stream (``record_stream`` is for the
+caller who uses them on another).
 """
 import ctypes
 import functools

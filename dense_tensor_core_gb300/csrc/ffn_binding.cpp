@@ -117,20 +117,35 @@ int float_code(const at::Tensor& t, const char* name) {
 }
 bool gated(int64_t act) { return act >= GEMM_ACT_SWIGLU; }
 
-// Calls the library with `dev` current, on the given stream (an integer handle) or the current one,
-// without the interpreter lock (a launch may wait for room in the stream's queue).
-template <typename F>
-void call(c10::Device dev, PyObject* stream, F f) {
-    const c10::cuda::OptionalCUDAGuard guard(dev);
-    const dtc_stream_t s = stream == Py_None
-                               ? (dtc_stream_t)c10::cuda::getCurrentCUDAStream(dev.index()).stream()
-                               : (dtc_stream_t)(uintptr_t)integer(stream);
-    int status;
-    Py_BEGIN_ALLOW_THREADS;
-    status = f(s);
-    Py_END_ALLOW_THREADS;
-    if (status) throw LibraryError{status};
-}
+// Makes `dev` current, and with it the given stream (an integer handle; None: the current one), for as
+// long as it lives. Set up before anything is allocated: the allocator hands memory that is freed on a
+// stream to that stream's next request, so buffers that die when the call returns must have come from
+// the stream their kernels run on, and so must outputs, whose memory earlier work of another stream may
+// still be using.
+class OnStream {
+public:
+    OnStream(c10::Device dev, PyObject* stream) {
+        device_.set_device(dev);
+        if (stream != Py_None)
+            stream_.reset_stream(c10::cuda::getStreamFromExternal(
+                (cudaStream_t)(uintptr_t)integer(stream), dev.index()));
+        handle_ = (dtc_stream_t)c10::cuda::getCurrentCUDAStream(dev.index()).stream();
+    }
+    // Calls the library, without the interpreter lock (a launch may wait for room in the queue).
+    template <typename F>
+    void call(F f) const {
+        int status;
+        Py_BEGIN_ALLOW_THREADS;
+        status = f(handle_);
+        Py_END_ALLOW_THREADS;
+        if (status) throw LibraryError{status};
+    }
+
+private:
+    c10::cuda::OptionalCUDAGuard device_;
+    c10::cuda::OptionalCUDAStreamGuard stream_;
+    dtc_stream_t handle_ = nullptr;
+};
 
 PyObject* wrap(const at::Tensor& t) {
     PyObject* o = THPVariable_Wrap(t);
@@ -216,6 +231,7 @@ PyObject* py_gemm_act(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor *Cin = maybe(a[5], "C"), *bias = maybe(a[6], "bias"),
                          *res = maybe(a[7], "residual"), *pre = maybe(a[8], "preact");
         const c10::Device dev = device_of(A, dt, "A");
+        const OnStream on(dev, a[12]);
         gemm_act_options o = {};
         o.activation = (int)act;
         o.lda = matrix(A, dt, "A", dev);
@@ -247,7 +263,7 @@ PyObject* py_gemm_act(PyObject*, PyObject* const* a, Py_ssize_t n) {
         } else {
             C = empty({s.M, s.N}, dt, dev);
         }
-        call(dev, a[12], [&](dtc_stream_t st) {
+        on.call([&](dtc_stream_t st) {
             return gemm_act((int)kind, address(A), address(B), address(C), s.M, s.N, s.K, (int)layout, &o, st);
         });
         return wrap(C);
@@ -262,6 +278,7 @@ PyObject* py_gemm_act_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor &dC = tensor(a[3], "dC"), &A = tensor(a[4], "A"), &B = tensor(a[5], "B");
         const at::Tensor* pre = maybe(a[6], "preact");
         const c10::Device dev = device_of(dC, dt, "dC");
+        const OnStream on(dev, a[12]);
         gemm_act_options o = {};
         o.activation = (int)act;
         o.ldc = matrix(dC, dt, "dC", dev);
@@ -282,7 +299,7 @@ PyObject* py_gemm_act_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (a[8] == Py_True) dB = empty(B.sizes(), dt, dev);
         if (a[9] == Py_True) db = empty({s.Nb}, at::kFloat, dev);
         auto out = [](const at::Tensor& t) { return t.defined() ? address(t) : nullptr; };
-        call(dev, a[12], [&](dtc_stream_t st) {
+        on.call([&](dtc_stream_t st) {
             return gemm_act_backward((int)kind, address(dC), address(A), address(B), out(dA), out(dB),
                                      static_cast<float*>(out(db)), s.M, s.N, s.K, (int)layout, &o, st);
         });
@@ -309,6 +326,7 @@ PyObject* py_moe_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor *bias = maybe(a[2], "bias"), *win = maybe(a[8], "weights"), *iin = maybe(a[9], "indices");
         const int code = float_code(z, "logits");
         const c10::Device dev = device_of(z, z.scalar_type(), "logits");
+        const OnStream on(dev, a[10]);
         const int64_t ld = matrix(z, z.scalar_type(), "logits", dev);
         const moe_route_options o = route_options(a[1], a[3], a[4], a[5], a[6], a[7]);
         const int64_t T = z.size(0), E = z.size(1), k = o.top_k;
@@ -327,7 +345,7 @@ PyObject* py_moe_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (k < 0) refuse(PyExc_ValueError, "top_k must not be negative");
         const at::Tensor w = win ? *win : empty({T, k}, at::kFloat, dev);
         const at::Tensor i = iin ? *iin : empty({T, k}, at::kInt, dev);
-        call(dev, a[10], [&](dtc_stream_t st) {
+        on.call([&](dtc_stream_t st) {
             return moe_route(code, address(z), ld, static_cast<const float*>(address(bias)), T, E, &o,
                              static_cast<float*>(address(w)), static_cast<int*>(address(i)), st);
         });
@@ -341,6 +359,7 @@ PyObject* py_moe_route_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor &dw = tensor(a[0], "dweights"), &z = tensor(a[1], "logits"), &idx = tensor(a[2], "indices");
         const int code = float_code(z, "logits");
         const c10::Device dev = device_of(z, z.scalar_type(), "logits");
+        const OnStream on(dev, a[6]);
         const int64_t ld = matrix(z, z.scalar_type(), "logits", dev);
         dense(idx, at::kInt, "indices", dev);
         dense(dw, at::kFloat, "dweights", dev);
@@ -350,7 +369,7 @@ PyObject* py_moe_route_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         shape(dw, {T, k}, "dweights");
         moe_route_options o = {(int)k, (int)integer(a[3]), 1, 1, PyObject_IsTrue(a[4]) == 1, (float)real(a[5])};
         const at::Tensor out = empty({T, E}, z.scalar_type(), dev);
-        call(dev, a[6], [&](dtc_stream_t st) {
+        on.call([&](dtc_stream_t st) {
             return moe_route_backward(code, static_cast<const float*>(address(dw)), address(z), ld,
                                       static_cast<const int*>(address(idx)), T, E, &o, address(out), st);
         });
@@ -365,6 +384,7 @@ PyObject* py_moe_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return entry(n, 9, [&]() -> PyObject* {
         const at::Tensor& idx = tensor(a[0], "indices");
         const c10::Device dev = device_of(idx, at::kInt, "indices");
+        const OnStream on(dev, a[8]);
         dense(idx, at::kInt, "indices", dev);
         if (idx.dim() != 2) refuse(PyExc_ValueError, "indices must be [T, k]");
         const int64_t E = integer(a[1]), T = idx.size(0), k = idx.size(1);
@@ -374,7 +394,7 @@ PyObject* py_moe_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                    data.as_strided({T, k}, {k, 1}, integer(a[5])),
                                    data.as_strided({integer(a[7])}, {1}, integer(a[6]))});
         try {
-            call(dev, a[8], [&](dtc_stream_t st) {
+            on.call([&](dtc_stream_t st) {
                 return moe_plan(static_cast<const int*>(address(idx)), T, (int)k, E, data.data_ptr(), st);
             });
         } catch (...) {
@@ -432,6 +452,7 @@ ExpertsArgs experts_args(PyObject* const* a, const char* name) {
 PyObject* py_moe_experts(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return entry(n, 17, [&]() -> PyObject* {
         ExpertsArgs e = experts_args(a, "x");
+        const OnStream on(e.dev, a[16]);
         const at::Tensor *res = maybe(a[10], "residual"), *oin = maybe(a[11], "out");
         if (res) {
             dense(*res, e.dt, "residual", e.dev);
@@ -447,7 +468,7 @@ PyObject* py_moe_experts(PyObject*, PyObject* const* a, Py_ssize_t n) {
         e.o.fault_inject = (int)integer(a[15]);
         const at::Tensor out = oin ? *oin : empty({e.T, e.H}, e.dt, e.dev);
         const at::Tensor buffer = empty({integer(a[13])}, at::kByte, e.dev);
-        call(e.dev, a[16], [&](dtc_stream_t st) {
+        on.call([&](dtc_stream_t st) {
             return moe_experts((int)e.kind, address(e.x), address(e.w_in), address(e.w_out), address(e.w),
                                e.plan->data_ptr(), address(out), e.T, (int)e.k, e.E, e.H, e.F, &e.o, save,
                                address(buffer), st);
@@ -460,6 +481,7 @@ PyObject* py_moe_experts(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* py_moe_experts_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return entry(n, 17, [&]() -> PyObject* {
         ExpertsArgs e = experts_args(a, "dy");
+        const OnStream on(e.dev, a[16]);
         const at::Tensor& saved = tensor(a[10], "saved");
         if (saved.scalar_type() != at::kByte || saved.numel() != integer(a[11]) || saved.device() != e.dev ||
             !saved.is_contiguous())
@@ -475,7 +497,7 @@ PyObject* py_moe_experts_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int64_t bytes = integer(a[12]);
         const at::Tensor ws = empty({bytes}, at::kByte, e.dev);
         auto out = [](const at::Tensor& t) { return t.defined() ? address(t) : nullptr; };
-        call(e.dev, a[16], [&](dtc_stream_t st) {
+        on.call([&](dtc_stream_t st) {
             return moe_experts_backward((int)e.kind, address(e.x), address(e.w_in), address(e.w_out), address(e.w),
                                         e.plan->data_ptr(), address(saved), out(dx), out(dwi), out(dwo), address(dw),
                                         e.T, (int)e.k, e.E, e.H, e.F, &e.o, address(ws), (uint64_t)bytes, st);
