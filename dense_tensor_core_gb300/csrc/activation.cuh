@@ -5,9 +5,19 @@
 //   silu(z) = z s(z), s(z) = 1 / (1 + e^-z)  gelu_tanh(z) = 0.5 z (1 + tanh u)
 //                                            u = sqrt(2/pi) (z + 0.044715 z^3)
 // 0.5 (1 + tanh u) = s(2u), so silu and gelu_tanh are z times a logistic function of z: one
-// exponential and one reciprocal. The exponential and the division are the fast forms (a few ulp),
-// which stays two decimal digits below what the 16-bit outputs can hold and below the fp32
-// column sums' own rounding. gelu's derivative Phi(z) + z phi(z) needs erff and one exponential.
+// exponential and one reciprocal. The exponential and the division are the fast forms: a few ulp, and
+// an ulp per unit of the exponent's argument, at most 2^-15 of the result over the range of fp32, which
+// is far below half an ulp of the 16-bit outputs.
+//
+// gelu needs Phi(z) to that relative error too, down its negative tail, where 0.5 + 0.5 erf(z / sqrt 2)
+// cancels (4 % off at z = -5). Phi(-a) = e^(-a^2/2) m(a) for a >= 0 with m(a) = e^(a^2/2) Phi(-a), the
+// normal distribution's Mills ratio times its density at 0: smooth, 1/2 at 0 and like 1 / (a sqrt(2 pi))
+// far out. With t = 1 / (1 + 0.3 a), m = t P(t), P a polynomial of degree 7 fitted to the least largest
+// relative error over a in [0, 14] (weighted least squares at Chebyshev nodes): 1.5e-7, 5e-7 as computed
+// in fp32. Phi(z) for z >= 0 is 1 - Phi(-z). The derivative Phi(z) + z phi(z) has the same exponential.
+// Measured with GELU, bias, residual and the kept sum, us, this and erfcf: 4096 x 4096 x 8192 183 and
+// 187; 4096 x 4096 x 1024, where the epilogue shows, 58 and 83.
+//
 // The gated forms take a pair (g, u): swiglu = silu(g) u, geglu = gelu(g) u.
 #pragma once
 
@@ -26,12 +36,28 @@ __host__ __device__ constexpr int act_of_gate(int a) {
 
 constexpr float kGeluC1 = 0.7978845608028654f;      // sqrt(2/pi)
 constexpr float kGeluC3 = 0.044715f;
-constexpr float kRsqrt2 = 0.7071067811865476f;
 constexpr float kRsqrt2Pi = 0.3989422804014327f;    // 1/sqrt(2 pi)
 
-// 1 / (1 + e^-v). For v below about -88 the exponential overflows to infinity and the quotient is
-// 0; both are the limits of the exact value.
+// 1 / (1 + e^-v). For v below about -87.3 the fast division gives 0 (its divisor is above 2^126), the
+// limit of the exact value: an absolute error below 2^-125.
 __device__ __forceinline__ float logistic(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
+
+// Phi(z), the normal distribution function; e receives e^(-z^2/2).
+__device__ __forceinline__ float normal_cdf(float z, float& e) {
+    const float a = fabsf(z);
+    const float t = __fdividef(1.0f, fmaf(0.3f, a, 1.0f));
+    e = __expf(-0.5f * z * z);
+    float p = 0.03567477688193321f;
+    p = fmaf(p, t, -0.15720310807228088f);
+    p = fmaf(p, t, 0.20635353028774261f);
+    p = fmaf(p, t, -0.05368367210030556f);
+    p = fmaf(p, t, 0.12856164574623108f);
+    p = fmaf(p, t, 0.09991348534822464f);
+    p = fmaf(p, t, 0.12075395882129669f);
+    p = fmaf(p, t, 0.11962930113077164f);
+    const float h = p * t * e;
+    return z < 0.0f ? h : 1.0f - h;
+}
 
 // z * s for s = logistic(v) in [0, 1]: 0 at z = -infinity, the limit, instead of -inf * 0.
 __device__ __forceinline__ float times_logistic(float z, float s) { return s == 0.0f ? 0.0f : z * s; }
@@ -51,7 +77,8 @@ __device__ __forceinline__ void act_forward(float (&z)[N], int act) {
         case kActGelu:
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const float p = 0.5f + 0.5f * erff(z[i] * kRsqrt2);
+                float e;
+                const float p = normal_cdf(z[i], e);
                 z[i] = times_logistic(z[i], p);
             }
             break;
@@ -81,8 +108,9 @@ __device__ __forceinline__ void act_both(float (&z)[N], float (&d)[N], int act) 
         case kActGelu:
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const float p = 0.5f + 0.5f * erff(z[i] * kRsqrt2);
-                const float q = kRsqrt2Pi * __expf(-0.5f * z[i] * z[i]);
+                float e;
+                const float p = normal_cdf(z[i], e);
+                const float q = kRsqrt2Pi * e;
                 d[i] = q == 0.0f ? p : fmaf(z[i], q, p);
                 z[i] = times_logistic(z[i], p);
             }
