@@ -810,7 +810,7 @@ int experts_layout(const ExpertSizes& s, int train, int pairs, moe_experts_info*
     l->h = l->z + (train ? up256(R * s.ldFz * 2) : 0);
     l->scale = l->h + up256(R * s.ldF * 2);
     l->y = l->scale + up256(R * 4);
-    l->split = l->y + up256(R * s.ldH * 2);
+    l->split = l->y + up256(R * s.ldH * 4);
     const SplitScratch x = split_scratch(seg_plan(s, s.F, s.gated, s.H, pairs),
                                          seg_plan(s, s.H, false, s.F, pairs));
     l->bytes = l->split + up256(x.bytes);
@@ -905,9 +905,10 @@ int moe_experts(int dtype, const void* x, const void* w_in, const void* w_out, c
         c.Q = b + l.h;
         c.ldq = s.ldF;
         c.args.out = b + l.y;
+        c.args.out_f32 = true;
         c.args.ld_out = s.ldH;
         if ((rc = launch_skinny(c, st))) return rc;
-        const JoinCall j{b + l.y, o.residual, y, nullptr, 0, nullptr, 0};
+        const JoinCall j{reinterpret_cast<const float*>(b + l.y), o.residual, y, nullptr, 0, nullptr, 0};
         return launch_moe_join(bf16, j, pl, s.plan, T, k, E, H, s.ldH, info, st);
     }
     const GatherCall g{x, b + l.x, weights, o.weights_dtype, reinterpret_cast<float*>(b + l.scale),
@@ -927,11 +928,12 @@ int moe_experts(int dtype, const void* x, const void* w_in, const void* w_out, c
         return rc;
     e = {};
     e.out = b + l.y;
+    e.out_f32 = true;
     e.ld_out = s.ldH;
     if ((rc = seg_product(s, bf16, pl, o, info, p2, split + sc.second, split + sc.partial, b + l.h, s.ldF, F,
                           w_out, false, H, false, false, e, st)))
         return rc;
-    const JoinCall j{b + l.y, o.residual, y, nullptr, 0, nullptr, 0};
+    const JoinCall j{reinterpret_cast<const float*>(b + l.y), o.residual, y, nullptr, 0, nullptr, 0};
     return launch_moe_join(bf16, j, pl, s.plan, T, k, E, H, s.ldH, info, st);
 }
 
@@ -950,7 +952,7 @@ void experts_back_layout(const ExpertSizes& s, int pairs, ExpertsBackLayout* l) 
     l->dy = 0;
     l->dz = up256(R * s.ldH * 2);
     l->dx = l->dz + up256(R * s.ldFz * 2);
-    l->dots = l->dx + up256(R * s.ldH * 2);
+    l->dots = l->dx + up256(R * s.ldH * 4);
     l->parts = num_feature_tiles(s.F, false) * 8;
     l->split = l->dots + up256(R * l->parts * 4);
     const SplitScratch x = split_scratch(seg_plan(s, s.F, false, s.H, pairs),
@@ -1062,12 +1064,13 @@ int moe_experts_backward(int dtype, const void* dy, const void* w_in, const void
     if (dx) {
         e = {};
         e.out = ws + w.dx;
+        e.out_f32 = true;
         e.ld_out = s.ldH;
         if ((rc = seg_product(s, bf16, pl, o, info, px, split + sc.second, split + sc.partial, ws + w.dz,
                               s.ldFz, s.Fz, w_in, true, H, false, false, e, st)))
             return rc;
     }
-    const JoinCall j{ws + w.dx, nullptr, dx, reinterpret_cast<const float*>(ws + w.dots), w.parts, dweights,
+    const JoinCall j{reinterpret_cast<const float*>(ws + w.dx), nullptr, dx, reinterpret_cast<const float*>(ws + w.dots), w.parts, dweights,
                      o.weights_dtype};
     return launch_moe_join(bf16, j, pl, s.plan, T, k, E, H, s.ldH, info, st);
 }

@@ -106,7 +106,7 @@ int launch_moe_gather(const GatherCall& c, const int32_t* plan, const moe_plan_i
 // out[t] = residual[t] + sum_j rows[slot[t,j]] (out NULL: no join); dweights from the pieces of the
 // rows' dot products (dweights NULL: none).
 struct JoinCall {
-    const void* rows;
+    const float* rows;
     const void* residual;
     void* out;
     const float* dots;

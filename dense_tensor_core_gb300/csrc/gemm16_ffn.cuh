@@ -31,7 +31,9 @@
 // features x 8 rows), finished in fp32, packed, and transposed to rows of consecutive features by
 // four stmatrix.trans into 2 KB of the warp's own shared memory, from where it leaves as 16-byte
 // stores (64 contiguous bytes per row). Residuals and kept activations come in the opposite way
-// (16-byte loads issued a block ahead, ldmatrix.trans). No value is rounded before the one store.
+// (16-byte loads issued a block ahead, ldmatrix.trans). No value is rounded before the one store. Rows
+// that a later kernel adds up (the experts' outputs) are stored as the fp32 sums they are, through both
+// of the warp's slots (128 contiguous bytes per row).
 // Against an earlier form that passed fp32 blocks through shared memory with 4 warps this halves
 // the shared-memory traffic, which the MMA's operand reads compete for, and it is what bounds the
 // products with a short reduction.
@@ -107,6 +109,7 @@ struct FfnArgs {
     // epilogue
     int act;
     void* out;
+    bool out_f32;                // kSeg, ungated: `out` is fp32, unfinished sums of the valid rows
     int64_t ld_out, expert_out;  // elements between rows, and (kRed) between experts' matrices
     const float* row_scale;      // factor of each row, after the activation
     float* row_dot;              // backward: [num_ft * 8][row_dot_ld] pieces of sum_f x act(z)
@@ -370,13 +373,42 @@ __device__ __forceinline__ void fetch_ahead(const FfnArgs& a, const Place& p, ui
     }
 }
 
+// A 32 x 32 block of fp32 sums to memory through 4 KB of shared memory: a row is 128 bytes, its 16-byte
+// piece j stands at j ^ (row % 8), so that the fragments' scalar stores and the pieces' loads cover all
+// banks.
+__device__ __forceinline__ void store_sums(const float (&v)[4][8], uint32_t slot, int lane, float* out, int64_t ld,
+                                           int rows, int feats) {
+    __syncwarp();  // the slots have been read
+#pragma unroll
+    for (int o = 0; o < 4; ++o)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int r = 8 * (k >> 1) + 2 * (lane & 3) + (k & 1), f = 8 * o + (lane >> 2);
+            st_shared_f32(slot + r * 128 + (((f >> 2) ^ (r & 7)) << 4) + (f & 3) * 4, v[o][k]);
+        }
+    __syncwarp();
+    const int j = lane & 7;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = 4 * i + (lane >> 3);
+        const uint4 x = ld_shared_u4(slot + r * 128 + ((j ^ (r & 7)) << 4));
+        if (r < rows && 4 * j < feats) *reinterpret_cast<uint4*>(out + r * ld + 4 * j) = x;
+    }
+}
+
 // Finishes one block: v holds the sums. `bias`: of the thread's 4 accumulator lanes. `x` goes into
 // the slots first, then `refill` may fetch the next block's into it.
-template <bool kBF16, bool kGated, bool kBack, typename Refill>
+template <bool kBF16, bool kGated, bool kBack, bool kSums, typename Refill>
 __device__ __forceinline__ void finish_block(const FfnArgs& a, float (&v)[4][8], const float (&bias)[4],
                                              const Place& p, Ahead<kGated, kBack>& x, uint32_t slot,
                                              int lane, Refill refill) {
     const int left = a.feats - p.f;
+    if constexpr (kSums) {
+        if (a.out_f32) {
+            store_sums(v, slot, lane, static_cast<float*>(a.out) + p.row * a.ld_out + p.f, a.ld_out, p.valid, left);
+            return;
+        }
+    }
     uint16_t* const out = static_cast<uint16_t*>(a.out) + p.out_base + p.row * a.ld_out + p.f;
     const int tr = 2 * (lane & 3);  // the thread's rows: 8 b + tr + i
     __syncwarp();  // the slots have been read
@@ -870,7 +902,8 @@ __global__ void __launch_bounds__(ffn::kThreads, 1)
                         }
                     }
                     const Place here = place;
-                    finish_block<kBF16, kGated, kBack>(args, v, bias, here, ahead, slot, lane, [&]() {
+                    finish_block<kBF16, kGated, kBack, kMode == kSeg && !kGated && !kBack>(
+                        args, v, bias, here, ahead, slot, lane, [&]() {
                         if (pass == kWhole && c + 2 < chunks) {
                             at_chunk(c + 2);
                             fetch_ahead<kGated, kBack>(args, place, slot, lane, ahead);

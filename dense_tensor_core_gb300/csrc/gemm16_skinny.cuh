@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(skinny::kThreads) gemm16_skinny_kernel(const S
         expert = rec.x;
         row0 = rec.y;
         valid = rec.z;
-        if (rec.w) zeros = min((kSegAlign - (rec.z & (kSegAlign - 1))) & (kSegAlign - 1), a.rows - rec.y - rec.z);
+        if (rec.w && !a.out_f32) zeros = min((kSegAlign - (rec.z & (kSegAlign - 1))) & (kSegAlign - 1), a.rows - rec.y - rec.z);
     }
     // this lane's rows of P: features f0 + g and f0 + g + 8 (gated: gate and up of f0 + g)
     const int fa = f0 + g, fb = kGated ? fa : f0 + g + 8;
@@ -210,7 +210,10 @@ __global__ void __launch_bounds__(skinny::kThreads) gemm16_skinny_kernel(const S
                 v[0] *= a.row_scale[row];
             }
             if (a.residual) v[0] += load(a.residual, row * a.ld_res + f);
-            store(a.out, row * a.ld_out + f, v[0]);
+            if (kSegRows && !kGated && a.out_f32)
+                static_cast<float*>(a.out)[row * a.ld_out + f] = v[0];
+            else
+                store(a.out, row * a.ld_out + f, v[0]);
         }
     }
     // gap rows beyond the last chunk of rows

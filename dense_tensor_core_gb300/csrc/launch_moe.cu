@@ -150,15 +150,15 @@ int launch_moe_gather(const GatherCall& c, const int32_t* plan, const moe_plan_i
 int launch_moe_join(bool bf16, const JoinCall& c, const int32_t* plan, const moe_plan_info& l, int64_t T,
                     int k, int64_t E, int64_t H, int64_t ld_rows, DeviceInfo* dev, cudaStream_t stream) {
     dtc::JoinArgs a;
-    a.rows = static_cast<const uint16_t*>(c.rows);
+    a.rows = c.rows;
     a.slots = plan + l.slots;
     a.residual = static_cast<const uint16_t*>(c.residual);
     a.out = static_cast<uint16_t*>(c.out);
     a.T = T;
     a.k = k;
-    a.H8 = (int)(H / 8);
-    a.ld8 = (int)(ld_rows / 8);
-    a.items = c.out ? T * ((a.H8 + 31) / 32) : 0;
+    a.H = (int)H;
+    a.ld_rows = (int)ld_rows;
+    a.items = c.out ? T * ((H + 255) / 256) : 0;
     a.dots = c.dots;
     a.parts = c.parts;
     a.ld = l.capacity;

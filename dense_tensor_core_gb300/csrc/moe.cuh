@@ -740,14 +740,14 @@ __global__ void __launch_bounds__(kRowsThreads) moe_gather_kernel(const RowsArgs
 }
 
 struct JoinArgs {
-    const uint16_t* rows;
+    const float* rows;  // fp32: the sum over a token's choices is rounded once, when it is stored
     const int* slots;
     const uint16_t* residual;
     uint16_t* out;
     int64_t T;
     int64_t items;   // 256-column pieces of all tokens; 0: no join
     int k;
-    int H8, ld8;     // 16-byte pieces of a row, and between the rows of `rows`
+    int H, ld_rows;  // columns, and elements between the rows of `rows`
     // gradient of the weights: pieces of each row's dot product, [parts][ld]
     const float* dots;
     int parts;
@@ -760,8 +760,8 @@ struct JoinArgs {
 };
 
 // out[t] = residual[t] + sum_j rows[slot_j], in the order of j, fp32, one rounding. A warp takes
-// 256 columns of a token; lane j holds choice j's row and hands it round. Four rows' pieces are in
-// flight at a time. In the backward pass the kernel also adds up the weights' gradients, whose
+// 256 columns of a token, a lane 4 of the first and 4 of the second 128; lane j holds choice j's row and
+// hands it round. Four rows' pieces are in flight at a time. In the backward pass the kernel also adds up the weights' gradients, whose
 // pieces the products' epilogues left per row.
 template <bool kBF16>
 __global__ void __launch_bounds__(kRowsThreads) moe_join_kernel(const JoinArgs a) {
@@ -769,7 +769,7 @@ __global__ void __launch_bounds__(kRowsThreads) moe_join_kernel(const JoinArgs a
     grid_launch_dependents();
     grid_dependency_wait();
     const int lane = threadIdx.x & 31;
-    const int pieces = (a.H8 + 31) / 32;
+    const int pieces = (a.H + 255) / 256;
     const int64_t tid = (int64_t)blockIdx.x * kRowsThreads + threadIdx.x;
     const int64_t threads = (int64_t)gridDim.x * kRowsThreads;
     if (a.dweights) {
@@ -787,30 +787,47 @@ __global__ void __launch_bounds__(kRowsThreads) moe_join_kernel(const JoinArgs a
     }
     for (int64_t it = tid >> 5; it < a.items; it += threads >> 5) {
         const int64_t t = it / pieces;
-        const int c = (int)(it - t * pieces) * 32 + lane;
+        const int c0 = (int)(it - t * pieces) * 256 + 4 * lane;
         const int slot = lane < a.k ? a.slots[t * a.k + lane] : -1;
-        float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (a.residual && c < a.H8)
-            unpack8<kBF16>(reinterpret_cast<const uint4*>(a.residual)[t * a.H8 + c], s);
+        float s[2][4] = {};
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (a.residual && c0 + 128 * h < a.H) {
+                const uint2 u = *reinterpret_cast<const uint2*>(a.residual + t * a.H + c0 + 128 * h);
+                const float2 lo = unpack2<kBF16>(u.x), hi = unpack2<kBF16>(u.y);
+                s[h][0] = lo.x;
+                s[h][1] = lo.y;
+                s[h][2] = hi.x;
+                s[h][3] = hi.y;
+            }
         for (int j0 = 0; j0 < a.k; j0 += 4) {
-            uint4 v[4];
-            bool on[4];
+            float4 v[4][2];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int src = __shfl_sync(kFull, slot, (j0 + j) & 31);
-                on[j] = j0 + j < a.k && src >= 0 && src < a.capacity && c < a.H8;
-                if (on[j]) v[j] = reinterpret_cast<const uint4*>(a.rows)[(int64_t)src * a.ld8 + c];
+                const bool on = j0 + j < a.k && src >= 0 && src < a.capacity;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    v[j][h] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (on && c0 + 128 * h < a.H)
+                        v[j][h] = *reinterpret_cast<const float4*>(a.rows + (int64_t)src * a.ld_rows + c0 + 128 * h);
+                }
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (!on[j]) continue;
-                float x[8];
-                unpack8<kBF16>(v[j], x);
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) s[i] += x[i];
-            }
+                for (int h = 0; h < 2; ++h) {
+                    s[h][0] += v[j][h].x;
+                    s[h][1] += v[j][h].y;
+                    s[h][2] += v[j][h].z;
+                    s[h][3] += v[j][h].w;
+                }
         }
-        if (c < a.H8) reinterpret_cast<uint4*>(a.out)[t * a.H8 + c] = pack8<kBF16>(s);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (c0 + 128 * h < a.H)
+                *reinterpret_cast<uint2*>(a.out + t * a.H + c0 + 128 * h) =
+                    make_uint2(packf2<kBF16>(s[h][0], s[h][1]), packf2<kBF16>(s[h][2], s[h][3]));
     }
 }
 

@@ -176,7 +176,7 @@ typedef struct {
     uint64_t z;      /* [capacity, F or 2F]: the first product (training only) */
     uint64_t h;      /* [capacity, F]: its activation times the row's weight */
     uint64_t scale;  /* [capacity] fp32: each row's weight */
-    uint64_t y;      /* [capacity, H]: the second product */
+    uint64_t y;      /* [capacity, H] fp32: the second product */
     uint64_t split;  /* counters and partial sums of split products */
 } moe_experts_info;
 
@@ -194,8 +194,8 @@ int moe_experts_layout(int dtype, int64_t T, int k, int64_t E, int64_t H, int64_
  * products run over each expert's rows (experts without rows cost nothing), and the join sums a
  * token's k rows in the order of j. `buffer` (moe_experts_layout bytes, 16-byte aligned, no initial
  * contents needed) holds the rows; with train non-zero moe_experts_backward reads it. A choice's
- * weight multiplies its activation in fp32; that product and the rows of the second product are
- * rounded to the operands' type (the tensor cores' operand, and half the bytes of fp32 rows).
+ * weight multiplies its activation in fp32; that product is rounded to the operands' type, as the
+ * tensor cores' operand. The rows of the second product stay fp32 until the join has added them up.
  * A choice with index -1 adds nothing; T == 0 does nothing. INVALID_ARG as moe_experts_layout, for
  * missing or misaligned pointers. The pages have no counterpart.
  */
@@ -212,7 +212,9 @@ int moe_experts_backward_workspace_size(int dtype, int64_t T, int k, int64_t E, 
  * zero for experts without rows) and dweights [T,k] (weights_dtype; 0 for choices with index -1).
  * `buffer` as moe_experts with train left it; workspace: device scratch, 16-byte aligned, no initial
  * contents needed. dw_in and dw_out may both be NULL (not computed), so may dx. The gradient of the
- * residual is dy itself. The pages have no counterpart.
+ * residual is dy itself. The gradient of z is rounded to the operands' type, as the tensor cores'
+ * operand; it is taken at the z that the forward pass kept, rounded likewise (half the memory held
+ * between the passes). All sums are fp32. The pages have no counterpart.
  */
 int moe_experts_backward(int dtype, const void* dy, const void* w_in, const void* w_out,
                          const void* weights, const void* plan, const void* buffer, void* dx,
