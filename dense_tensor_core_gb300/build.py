@@ -3,10 +3,12 @@ native part of the Python binding, dense_tensor_core_gb300/_ffn_native.so.
 
 One translation unit per kernel family plus the API unit, compiled in parallel with nvcc (one
 -gencode), then linked into one shared library. The CUDA runtime is linked statically so the
-library loads without a GPU (the CPU tests check its exports) and carries no rpath. The binding
-module is host code against torch's headers, compiled beside the kernels (about 10 s) and linked
-against the library in its own folder.
+library loads without a GPU (the CPU tests check its exports) and carries no rpath. The library needs
+neither torch nor Python's headers. The binding module is host code against torch's headers, compiled
+beside the kernels (about 10 s) and linked against the library in its own folder; where torch is not
+installed it is left out, and where it does not compile the library is in place all the same.
 """
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -35,10 +37,13 @@ def nvcc() -> str:
     return p if os.path.exists(p) else (shutil.which("nvcc") or "nvcc")
 
 
-def _inputs():
-    files = sources() + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
-    files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h", ".cpp"))]
-    return files
+def _headers(folder, *kinds):
+    return [os.path.join(folder, f) for f in os.listdir(folder) if f.endswith(kinds)]
+
+
+def _due(target, inputs):
+    """Whether `target` is missing or older than one of its inputs."""
+    return not os.path.exists(target) or os.path.getmtime(target) < max(map(os.path.getmtime, inputs))
 
 
 def _compile_native(obj_dir):
@@ -79,23 +84,27 @@ def _compile(src, obj_dir, verbose_ptxas):
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    if not force and os.path.exists(LIB) and os.path.exists(NATIVE):
-        newest = max(os.path.getmtime(f) for f in _inputs())
-        if min(os.path.getmtime(LIB), os.path.getmtime(NATIVE)) >= newest:
-            return LIB
-    os.makedirs(OBJ_DIR, exist_ok=True)
     srcs = sources()
+    headers = _headers(INCLUDE, ".h")
+    library = force or _due(LIB, srcs + headers + _headers(CSRC, ".cuh", ".h"))
+    native = importlib.util.find_spec("torch") is not None and (
+        force or _due(NATIVE, headers + [os.path.join(CSRC, "ffn_binding.cpp")]))
+    if not library and not native:
+        return LIB
+    os.makedirs(OBJ_DIR, exist_ok=True)
     # objects in a directory of this build's own, so concurrent builds cannot mix their files
-    with tempfile.TemporaryDirectory(dir=OBJ_DIR) as obj_dir:
-        with ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
-            native = ex.submit(_compile_native, obj_dir)
+    with tempfile.TemporaryDirectory(dir=OBJ_DIR) as obj_dir, \
+            ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        binding = ex.submit(_compile_native, obj_dir) if native else None
+        if library:
             objs = list(ex.map(lambda s: _compile(s, obj_dir, verbose_ptxas), srcs))
-        tmp = LIB + ".tmp%d" % os.getpid()
-        subprocess.check_call([nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs])
-        os.replace(tmp, LIB)
-        tmp = NATIVE + ".tmp%d" % os.getpid()
-        _link_native(native.result(), tmp)
-        os.replace(tmp, NATIVE)
+            tmp = LIB + ".tmp%d" % os.getpid()
+            subprocess.check_call([nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs])
+            os.replace(tmp, LIB)
+        if native:
+            tmp = NATIVE + ".tmp%d" % os.getpid()
+            _link_native(binding.result(), tmp)
+            os.replace(tmp, NATIVE)
     return LIB
 
 
