@@ -440,11 +440,18 @@ ExpertsArgs experts_args(PyObject* const* a, const char* name) {
         refuse(PyExc_ValueError, "the plan is for " + std::to_string(integer(a[7])) + " tokens and " +
                                      std::to_string(integer(a[9])) + " experts, not " + std::to_string(e.T) +
                                      " and " + std::to_string(e.E));
+    // (the kernels read the plan where its layout for these sizes says)
+    moe_plan_info layout;
+    const int status = moe_plan_layout(e.T, (int)e.k, e.E, &layout);
+    if (status) throw LibraryError{status};
+    dense(*e.plan, at::kInt, "the plan", e.dev);
+    if (e.plan->numel() != layout.words)
+        refuse(PyExc_ValueError, "the plan holds " + std::to_string(e.plan->numel()) + " words, not the " +
+                                     std::to_string(layout.words) + " of a plan for these sizes");
     e.o.activation = (int)act;
     e.o.weights_dtype = float_code(*e.w, "weights");
     dense(*e.w, e.w->scalar_type(), "weights", e.dev);
     shape(*e.w, {e.T, e.k}, "weights");
-    dense(*e.plan, at::kInt, "the plan", e.dev);
     return e;
 }
 

@@ -1,0 +1,34 @@
+"""Arguments that the binding refuses with tensors on the GPU."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from dense_tensor_core_gb300 import build
+
+    build.build()
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+def experts():
+    e = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    idx = torch.zeros((20, 2), dtype=torch.int32, device="cuda")
+    return idx, (e(20, 64), e(4, 64, 64), e(4, 64, 64), torch.zeros((20, 2), device="cuda"))
+
+
+@pytest.mark.parametrize("spoil", [lambda d: d[:-1], lambda d: d[:16], lambda d: d[:0], lambda d: torch.cat([d, d]),
+                                   lambda d: d[::2], lambda d: d.long(), lambda d: d.cpu()])
+def test_plans_of_another_size(spoil):
+    import dense_tensor_core_gb300 as dtc
+    idx, args = experts()
+    plan = dtc.moe_plan(idx, 4)
+    _, saved = dtc.moe_experts("bf16", *args, plan, activation="silu", save=True)
+    plan.data = spoil(plan.data)
+    with pytest.raises((ValueError, TypeError)):
+        dtc.moe_experts("bf16", *args, plan, activation="silu")
+    with pytest.raises((ValueError, TypeError)):
+        dtc.moe_experts_backward("bf16", *args, plan, saved, activation="silu")
