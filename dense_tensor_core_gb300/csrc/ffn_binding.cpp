@@ -48,6 +48,17 @@ int64_t integer(PyObject* o) {
     if (v == -1 && PyErr_Occurred()) throw PythonError{};
     return v;
 }
+// A number of a C int, and a wait's limit.
+int small(PyObject* o, const char* name) {
+    const int64_t v = integer(o);
+    if (v != (int)v) refuse(PyExc_ValueError, std::string(name) + " is out of range: " + std::to_string(v));
+    return (int)v;
+}
+uint64_t timeout(PyObject* o) {
+    const int64_t v = integer(o);
+    if (v < 0) refuse(PyExc_ValueError, "timeout_ns must not be negative");
+    return (uint64_t)v;
+}
 double real(PyObject* o) {
     const double v = PyFloat_AsDouble(o);
     if (v == -1.0 && PyErr_Occurred()) throw PythonError{};
@@ -253,8 +264,8 @@ PyObject* py_gemm_act(PyObject*, PyObject* const* a, Py_ssize_t n) {
             o.preact = address(pre);
         }
         set_workspace(&o, maybe(a[9], "workspace"), dev);
-        o.timeout_ns = (uint64_t)integer(a[10]);
-        o.fault_inject = (int)integer(a[11]);
+        o.timeout_ns = timeout(a[10]);
+        o.fault_inject = small(a[11], "fault_inject");
         at::Tensor C;
         if (Cin) {
             o.ldc = matrix(*Cin, dt, "C", dev);
@@ -293,7 +304,7 @@ PyObject* py_gemm_act_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
             o.preact = address(pre);
         }
         set_workspace(&o, maybe(a[10], "workspace"), dev);
-        o.timeout_ns = (uint64_t)integer(a[11]);
+        o.timeout_ns = timeout(a[11]);
         at::Tensor dA, dB, db;
         if (a[7] == Py_True) dA = empty(A.sizes(), dt, dev);
         if (a[8] == Py_True) dB = empty(B.sizes(), dt, dev);
@@ -310,10 +321,10 @@ PyObject* py_gemm_act_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 moe_route_options route_options(PyObject* k, PyObject* scoring, PyObject* groups, PyObject* top,
                                 PyObject* renorm, PyObject* scale) {
     moe_route_options o;
-    o.top_k = (int)integer(k);
-    o.scoring = (int)integer(scoring);
-    o.groups = (int)integer(groups);
-    o.top_groups = (int)integer(top);
+    o.top_k = small(k, "top_k");
+    o.scoring = small(scoring, "scoring");
+    o.groups = small(groups, "groups");
+    o.top_groups = small(top, "top_groups");
     o.renormalize = PyObject_IsTrue(renorm) == 1;
     o.scale = (float)real(scale);
     return o;
@@ -367,7 +378,7 @@ PyObject* py_moe_route_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int64_t T = z.size(0), E = z.size(1), k = idx.size(1);
         shape(idx, {T, k}, "indices");
         shape(dw, {T, k}, "dweights");
-        moe_route_options o = {(int)k, (int)integer(a[3]), 1, 1, PyObject_IsTrue(a[4]) == 1, (float)real(a[5])};
+        moe_route_options o = {(int)k, small(a[3], "scoring"), 1, 1, PyObject_IsTrue(a[4]) == 1, (float)real(a[5])};
         const at::Tensor out = empty({T, E}, z.scalar_type(), dev);
         on.call([&](dtc_stream_t st) {
             return moe_route_backward(code, static_cast<const float*>(address(dw)), address(z), ld,
@@ -471,8 +482,8 @@ PyObject* py_moe_experts(PyObject*, PyObject* const* a, Py_ssize_t n) {
             shape(*oin, {e.T, e.H}, "out");
         }
         const bool save = a[12] == Py_True;
-        e.o.timeout_ns = (uint64_t)integer(a[14]);
-        e.o.fault_inject = (int)integer(a[15]);
+        e.o.timeout_ns = timeout(a[14]);
+        e.o.fault_inject = small(a[15], "fault_inject");
         const at::Tensor out = oin ? *oin : empty({e.T, e.H}, e.dt, e.dev);
         const at::Tensor buffer = empty({integer(a[13])}, at::kByte, e.dev);
         on.call([&](dtc_stream_t st) {
@@ -493,7 +504,7 @@ PyObject* py_moe_experts_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (saved.scalar_type() != at::kByte || saved.numel() != integer(a[11]) || saved.device() != e.dev ||
             !saved.is_contiguous())
             refuse(PyExc_ValueError, "saved is not what moe_experts returned for these sizes with save=True");
-        e.o.timeout_ns = (uint64_t)integer(a[15]);
+        e.o.timeout_ns = timeout(a[15]);
         at::Tensor dx, dwi, dwo;
         if (a[13] == Py_True) dx = empty({e.T, e.H}, e.dt, e.dev);
         if (a[14] == Py_True) {
