@@ -16,17 +16,24 @@ uint64_t up256(uint64_t v) { return (v + 255) & ~(uint64_t)255; }
 
 // Up to this many rows a product with K-major operands runs on the kernel without tiles. A block of it
 // (16 features; gated, 8 and their gates) walks the whole K, so a long K needs several blocks an SM to
-// fill the HBM, else the K splits of the tiles win. Measured (K up to 16384; gated not apart), us, without tiles and with:
+// fill the HBM, else the K splits of the tiles win. Measured (K up to 16384), us, without tiles and with:
 //   K short           8 x 1024 x 4096 8.3, 11.5; 16 x 1024 x 5120 12.4, 13.2; 16 x 1024 x 6144 14.4, 13.7
 //   2 blocks an SM    16 x 4864 x 8192 20.7, 22.0; 8 x 4864 x 16384 36.6, 33.4
 //   3 blocks an SM    8 x 7296 x 16384 44.6, 48.2; 16 x 8192 x 8192 26.6, 30.6
+// and gated (N of the result; whole calls between events, a few us more each):
+//   K short           8 x 1024 x 5120 17.0, 19.1; 16 x 1024 x 5120 21.1, 19.1; 16 x 256 x 4096 17.0, 17.0
+//   less than 2       8 x 512 x 8192 21.1, 19.1; 16 x 1216 x 8192 29.3, 23.2
+//   2 blocks an SM    8 x 2432 x 8192 25.3, 31.4; 16 the same 31.4, 31.4; 1216 x 16384 37.5, 31.4
+//   3 blocks an SM    8 x 3648 x 16384 55.9, 62.2; 16 the same 66.2, 64.1
+// so that more than 8 gated rows take a shorter K for short.
 // Its 32-bit indexes run a little past K and N, hence the limit on both.
-constexpr int kSkinnyRows = 16, kSkinnyShortK = 5120, kSkinnyLongK = 8192;
+constexpr int kSkinnyRows = 16, kSkinnyShortK = 5120, kSkinnyShortKWideGated = 4096, kSkinnyLongK = 8192;
 bool skinny(int64_t M, int64_t N, int64_t K, bool gated, bool k_major, int sms) {
     constexpr int64_t most = (int64_t)1 << 30;
     const int64_t blocks = ceil_div(N, gated ? 8 : 16);
+    const int short_k = gated && M > 8 ? kSkinnyShortKWideGated : kSkinnyShortK;
     return M <= kSkinnyRows && k_major && K > 0 && K % 8 == 0 && K <= most && N <= most &&
-           (K <= kSkinnyShortK || (blocks >= 2 * sms && K <= kSkinnyLongK) || blocks >= 3 * sms);
+           (K <= short_k || (blocks >= 2 * sms && K <= kSkinnyLongK) || blocks >= 3 * sms);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -777,9 +784,19 @@ int red_product(const ExpertSizes& s, bool bf16, const int32_t* plan, const moe_
 // tiles against tiles. 64 experts, 8 each, H 2048, F 1024: 1 token 28 and 36, 16 tokens 124 and 128,
 // 48 157 and 151. 8 experts, 2 each, H and F 4096: 43 and 55, 16 tokens 133 and 153, 32 177 and 155.
 // 128 experts, 4 each, H 2048, F 768: 16 and 25, 16 tokens 90 and 91, 24 136 and 129). An expert with
-// more than 8 rows reads its weights again, from the L2.
+// more than 8 rows reads its weights again, from the L2. As for one matrix, a reduction above 8192 has
+// to have its blocks (over the experts that the tokens can reach) fill the HBM; below, few blocks win
+// too (8 experts, F 256 and H 8192: 1 of 1 token 27 and 32, 2 of 16 tokens 44 and 53). Above (8 experts,
+// whole calls between events): H 512, F 16384, 2 of 1 token 59 and 53, of 16 tokens 118 and 102; H 1024, F 16384,
+// 1 of 1 token 54 and 51, of 16 tokens 145 and 151; H 16384, F 512, 2 of 16 tokens 98 and 110.
 constexpr int kFewTokens = 16;
-bool few_rows(const ExpertSizes& s) { return s.T <= kFewTokens; }
+bool few_rows(const ExpertSizes& s, int sms) {
+    const int64_t reached = std::min(s.T * s.k, s.E);
+    auto fills = [&](int64_t red, int64_t feats, bool gated) {
+        return red <= kSkinnyLongK || reached * ceil_div(feats, gated ? 8 : 16) >= 2 * sms;
+    };
+    return s.T <= kFewTokens && fills(s.H, s.F, s.gated) && fills(s.F, s.H, false);
+}
 
 SkinnyCall skinny_call(const ExpertSizes& s, bool bf16, const int32_t* plan, const void* weights, int64_t red,
                        int64_t feats, bool gated) {
@@ -877,7 +894,7 @@ int moe_experts(int dtype, const void* x, const void* w_in, const void* w_out, c
     const int32_t* const pl = static_cast<const int32_t*>(plan);
     const cudaStream_t st = (cudaStream_t)stream;
     const bool bf16 = dtype == 0;
-    if (few_rows(s)) {
+    if (few_rows(s, 2 * pairs)) {
         // weights are read for a handful of rows each: no tiles, and (without train, which keeps the
         // rows) no gathering
         if (train) {

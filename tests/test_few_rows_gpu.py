@@ -113,3 +113,22 @@ def test_experts_around_the_change(T, kind, E, k, H, F, name):
     want = torch.autograd.grad(R.experts(*leaf, idx, name), leaf, dy.double())
     for a, r, n, what in zip(grads, want, (4, 3, 2, 2), ("dx", "dw_in", "dw_out", "dweights")):
         R.close(a, r, 1.1 * n * R.U[kind], what)
+
+
+# few tokens with a reduction at and past the length from which few blocks no longer do
+@pytest.mark.parametrize("H,F", [(64, 8192), (64, 8200), (8192, 72), (8200, 72), (16384, 1024)])
+@pytest.mark.parametrize("T,E,k", [(1, 4, 1), (3, 8, 2), (16, 8, 8)])
+@pytest.mark.parametrize("kind,name", [("bf16", "swiglu"), ("f16", "gelu")])
+def test_experts_with_a_long_reduction(kind, name, T, E, k, H, F):
+    import dense_tensor_core_gb300 as dtc
+    Fz = 2 * F if name in R.GATED else F
+    x, wi, wo = rand((T, H), kind, 1), rand((E, Fz, H), kind, 2, H ** -0.5), rand((E, H, F), kind, 3, F ** -0.5)
+    g = torch.Generator(device="cuda").manual_seed(T + k)
+    idx = torch.rand((T, E), generator=g, device="cuda").topk(k, 1).indices.to(torch.int32)
+    w = torch.softmax(torch.randn((T, k), generator=g, device="cuda"), 1)
+    y, bound = R.experts_bound(kind, x.double(), wi.double(), wo.double(), w.double(), idx, name)
+    plan = dtc.moe_plan(idx, E)
+    got = dtc.moe_experts(kind, x, wi, wo, w, plan, activation=name)
+    dtc.gemm_stream_status()
+    R.check(got, y, bound, "y")
+    assert torch.equal(dtc.moe_experts(kind, x, wi, wo, w, plan, activation=name, save=True)[0], got)
