@@ -34,7 +34,7 @@ int launch_ffn(const FfnCall& c, DeviceInfo* dev, cudaStream_t stream) {
     if (rc) return rc;
     auto kern = dtc::gemm16_ffn_kernel<kBF16, kMode, kPMN, kQMN, kGated, kBack>;
     if ((rc = ensure_smem_attr(kern, dtc::ffn::kSmemBytes, dev))) return rc;
-    return launch_chain(kern, dim3(c.grid), dtc::ffn::kThreads, dtc::ffn::kSmemBytes, 2, true,
+    return launch_chain(kern, dim3(c.grid), dtc::ffn::kThreads, dtc::ffn::kSmemBytes, 2,
                         stream, tp, tq, c.args);
 }
 

@@ -191,11 +191,11 @@ int launch_dependent(Kern kern, int grid, int threads, int smem, cudaStream_t st
     return GEMM_OK;
 }
 
-// A cluster launch that may also begin early behind the stream's previous kernel (`dependent`; the
-// kernel then waits in griddepcontrol.wait before it touches what that kernel reads or writes).
+// A cluster launch that begins early behind the stream's previous kernel (the kernel waits in
+// griddepcontrol.wait before it touches what that kernel reads or writes).
 template <typename Kern, typename... Params>
-int launch_chain(Kern kern, dim3 grid, int threads, int smem, int cluster, bool dependent,
-                 cudaStream_t stream, const Params&... params) {
+int launch_chain(Kern kern, dim3 grid, int threads, int smem, int cluster, cudaStream_t stream,
+                 const Params&... params) {
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -209,10 +209,8 @@ int launch_chain(Kern kern, dim3 grid, int threads, int smem, int cluster, bool 
         attr[cfg.numAttrs].val.clusterDim.y = 1;
         attr[cfg.numAttrs++].val.clusterDim.z = 1;
     }
-    if (dependent) {
-        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
-    }
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, kern, params...);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "kernel launch");

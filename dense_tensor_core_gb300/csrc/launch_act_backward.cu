@@ -41,7 +41,7 @@ int launch_act_backward(const ActBackwardCall& c, DeviceInfo* dev, cudaStream_t 
     const dim3 grid((unsigned)strips(c.N), gy);
     auto kern = c.bf16 ? (gated ? dtc::act_backward_kernel<true, true> : dtc::act_backward_kernel<true, false>)
                        : (gated ? dtc::act_backward_kernel<false, true> : dtc::act_backward_kernel<false, false>);
-    return launch_chain(kern, grid, dtc::kActBackThreads, 0, 1, true, stream, a);
+    return launch_chain(kern, grid, dtc::kActBackThreads, 0, 1, stream, a);
 }
 
 }  // namespace dtc_host

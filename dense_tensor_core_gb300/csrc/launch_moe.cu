@@ -1,4 +1,4 @@
-// launch_moe.cu -- launchers of the routing, plan, gather, spread and join kernels.
+// launch_moe.cu -- launchers of the routing, plan, gather and join kernels.
 #include "ffn_host.h"
 #include "moe.cuh"
 
@@ -39,7 +39,7 @@ int route_by_size(const dtc::RouteArgs& a, DeviceInfo* dev, cudaStream_t s) {
     // the forward kernel walks over tokens with the bias in registers: blocks for the device's
     // threads; the backward one takes a token a warp
     const dim3 grid((unsigned)(kBack ? want : std::min<int64_t>(want, (int64_t)dev->model.sms * 16)));
-    auto go = [&](auto kern) { return launch_chain(kern, grid, threads, 0, 1, true, s, a); };
+    auto go = [&](auto kern) { return launch_chain(kern, grid, threads, 0, 1, s, a); };
     const int v = (a.E + 31) / 32;
     const uintptr_t lane_bytes = std::min<uintptr_t>(16, (uintptr_t)v * (kType == 2 ? 4 : 2));
     const bool run = a.E == 32 * v && (v & (v - 1)) == 0 && a.per_group % v == 0 &&
@@ -112,13 +112,13 @@ int launch_moe_plan(const int* indices, int64_t T, int k, int64_t E, int32_t* pl
     if (few) {
         if ((rc = ensure_smem_attr(dtc::moe_plan_kernel, words * dtc::ffn::kMaxExperts * 4, dev))) return rc;
         return launch_chain(dtc::moe_plan_kernel, dim3(blocks), dtc::kPlanThreads, words * (int)E * 4, blocks,
-                            true, stream, a);
+                            stream, a);
     }
     if ((rc = ensure_smem_attr(dtc::moe_plan_place_kernel, words * dtc::ffn::kMaxExperts * 4, dev))) return rc;
-    if ((rc = launch_chain(dtc::moe_plan_count_kernel, dim3(blocks), dtc::kPlanThreads, (int)E * 4, 1, true,
+    if ((rc = launch_chain(dtc::moe_plan_count_kernel, dim3(blocks), dtc::kPlanThreads, (int)E * 4, 1,
                            stream, a)))
         return rc;
-    return launch_chain(dtc::moe_plan_place_kernel, dim3(blocks), dtc::kPlanThreads, words * (int)E * 4, 1, true,
+    return launch_chain(dtc::moe_plan_place_kernel, dim3(blocks), dtc::kPlanThreads, words * (int)E * 4, 1,
                         stream, a);
 }
 
@@ -144,7 +144,7 @@ int launch_moe_gather(const GatherCall& c, const int32_t* plan, const moe_plan_i
     a.zero = c.zero;
     a.zero_words = c.zero_words;
     return launch_chain(dtc::moe_gather_kernel, dim3(rows_grid(l.capacity, dev)), dtc::kRowsThreads, 0,
-                        1, true, stream, a);
+                        1, stream, a);
 }
 
 int launch_moe_join(bool bf16, const JoinCall& c, const int32_t* plan, const moe_plan_info& l, int64_t T,
@@ -168,8 +168,8 @@ int launch_moe_join(bool bf16, const JoinCall& c, const int32_t* plan, const moe
     a.dweights = c.dweights;
     a.wtype = c.wtype;
     const dim3 grid(rows_grid(std::max<int64_t>(a.items, c.dweights ? (l.capacity + 31) / 32 : 0), dev));
-    return bf16 ? launch_chain(dtc::moe_join_kernel<true>, grid, dtc::kRowsThreads, 0, 1, true, stream, a)
-                : launch_chain(dtc::moe_join_kernel<false>, grid, dtc::kRowsThreads, 0, 1, true, stream, a);
+    return bf16 ? launch_chain(dtc::moe_join_kernel<true>, grid, dtc::kRowsThreads, 0, 1, stream, a)
+                : launch_chain(dtc::moe_join_kernel<false>, grid, dtc::kRowsThreads, 0, 1, stream, a);
 }
 
 }  // namespace dtc_host

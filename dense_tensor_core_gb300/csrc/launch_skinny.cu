@@ -20,7 +20,7 @@ int by_rows(const SkinnyCall& c, cudaStream_t s) {
     a.weights = c.weights;
     a.wtype = c.wtype;
     const dim3 grid((unsigned)ceil_div(c.args.feats, kGated ? 8 : 16), kSegRows ? (unsigned)c.args.max_tiles : 1u);
-    auto go = [&](auto kern) { return launch_chain(kern, grid, dtc::skinny::kThreads, 0, 1, true, s, a); };
+    auto go = [&](auto kern) { return launch_chain(kern, grid, dtc::skinny::kThreads, 0, 1, s, a); };
     if constexpr (!kSegRows)
         if (c.wide) return go(dtc::gemm16_skinny_kernel<kBF16, kSegRows, kGated, 2>);
     return go(dtc::gemm16_skinny_kernel<kBF16, kSegRows, kGated, 1>);
