@@ -824,7 +824,7 @@ int experts_layout(const ExpertSizes& s, int train, int pairs, moe_experts_info*
     const uint64_t R = s.plan.capacity;
     l->x = 0;
     l->z = up256(R * s.ldH * 2);
-    l->h = l->z + (train ? up256(R * s.ldFz * 2) : 0);
+    l->h = l->z + (train ? up256(R * s.ldFz * 4) : 0);
     l->scale = l->h + up256(R * s.ldF * 2);
     l->y = l->scale + up256(R * 4);
     l->split = l->y + up256(R * s.ldH * 4);

@@ -117,7 +117,7 @@ struct FfnArgs {
     const void* bias;            // [feats] (gated [2 feats])
     const void* residual;
     int64_t ld_res;
-    void* preact;  // forward: receives z; backward: the z that act' is taken at
+    void* preact;  // forward: receives z; backward: the z that act' is taken at (kSeg: fp32)
     int64_t ld_pre;
     // split-K
     uint32_t* counters;
@@ -299,10 +299,11 @@ struct Block {
         __syncwarp();
         flush(out, ld, rows, feats);
     }
-    // the slot's rows to memory
+    // the slot's rows to memory (as many passes of kPerPass rows)
+    template <int kCount = kPasses>
     __device__ __forceinline__ void flush(uint16_t* out, int64_t ld, int rows, int feats) const {
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
+        for (int i = 0; i < kCount; ++i) {
             const int r = row + i * kPerPass;
             const uint4 x = ld_shared_u4(piece + i * kPerPass * kRowBytes);
             if (r < rows && col < feats) *reinterpret_cast<uint4*>(out + r * ld + col) = x;
@@ -341,11 +342,70 @@ struct Block {
     }
 };
 
+// 32-row blocks of 8 kOct features in fp32. A row takes 32 kOct bytes of shared memory and the lines of 128
+// bytes (one row of 32 features, two of 16) hold their 16-byte pieces in an order that depends on the
+// row, so that the fragments' scalars and the pieces of a 16-byte access each cover all banks.
+template <int kOct>
+struct Sums {
+    static_assert(kOct == 4 || kOct == 2, "32 or 16 features");
+    static constexpr int kPieces = 2 * kOct;          // of a row
+    static constexpr int kPerPass = 32 / kPieces;     // rows per 16-byte access of the warp
+    // where piece j of row r stands
+    static __device__ __forceinline__ uint32_t at(int r, int j) {
+        if constexpr (kOct == 4)
+            return r * 128 + ((j ^ (r & 7)) << 4);
+        else
+            return (r >> 1) * 128 + (((4 * (r & 1) + j) ^ (2 * ((r >> 1) & 3))) << 4);
+    }
+    // where the thread's element of fragment v[o][k] stands: feature 8 o + lane / 4, row
+    // 8 (k / 2) + 2 (lane % 4) + k % 2
+    static __device__ __forceinline__ uint32_t element(int o, int k, int lane) {
+        const int r = 8 * (k >> 1) + 2 * (lane & 3) + (k & 1), f = 8 * o + (lane >> 2);
+        return at(r, f >> 2) + (f & 3) * 4;
+    }
+    // fragments v(o, k) to memory at `out` (the block's first row and feature) through kOct KB
+    template <typename V>
+    static __device__ __forceinline__ void store(V v, uint32_t slot, int lane, float* out, int64_t ld, int rows,
+                                                 int feats) {
+        __syncwarp();  // the slot has been read
+#pragma unroll
+        for (int o = 0; o < kOct; ++o)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) st_shared_f32(slot + element(o, k, lane), v(o, k));
+        __syncwarp();
+        const int j = lane % kPieces;
+#pragma unroll
+        for (int i = 0; i < 32 / kPerPass; ++i) {
+            const int r = kPerPass * i + lane / kPieces;
+            const uint4 x = ld_shared_u4(slot + at(r, j));
+            if (r < rows && 4 * j < feats) *reinterpret_cast<uint4*>(out + r * ld + 4 * j) = x;
+        }
+    }
+    // The other way for 32 features: fetch issues the loads, put writes the 16 rows of one half to 2 KB.
+    static __device__ __forceinline__ void fetch(uint4 (&x)[8], int lane, const float* in, int64_t ld, int rows,
+                                                 int feats) {
+        const int j = lane & 7;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3);
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (r < rows && 4 * j < feats) x[i] = *reinterpret_cast<const uint4*>(in + r * ld + 4 * j);
+        }
+    }
+    static __device__ __forceinline__ void put(const uint4 (&x)[8], int half, uint32_t slot, int lane) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint4 u = half ? x[4 + i] : x[i];
+            st_shared_u4(slot + at(4 * i + (lane >> 3), lane & 7), u.x, u.y, u.z, u.w);
+        }
+    }
+};
+
 // What a block's epilogue reads from memory, fetched ahead of its sums: the residual, or in the
-// backward form z.
+// backward form z (fp32; gated: both halves).
 template <bool kGated, bool kBack>
 struct Ahead {
-    uint4 a[kGated ? 2 : 4], b[kBack ? 4 : 1];
+    uint4 a[kBack ? 8 : kGated ? 2 : 4], b[kBack ? 8 : 1];
 };
 
 // Where a warp's block lies: first row of the result, first feature, rows that hold sums, rows that
@@ -361,65 +421,40 @@ template <bool kGated, bool kBack>
 __device__ __forceinline__ void fetch_ahead(const FfnArgs& a, const Place& p, uint32_t slot, int lane,
                                             Ahead<kGated, kBack>& x) {
     const int left = a.feats - p.f;
-    const Block<kGated ? 2 : 4> blk(slot, lane);
     if constexpr (!kBack) {
+        const Block<kGated ? 2 : 4> blk(slot, lane);
         if (a.residual)
             blk.fetch(x.a, static_cast<const uint16_t*>(a.residual) + p.row * a.ld_res + p.f, a.ld_res,
                       p.valid, left);
     } else {
-        const uint16_t* const z = static_cast<const uint16_t*>(a.preact) + p.row * a.ld_pre + p.f;
-        blk.fetch(x.a, z, a.ld_pre, p.valid, left);
-        if (act_gated(a.act)) blk.fetch(x.b, z + a.feats, a.ld_pre, p.valid, left);
-    }
-}
-
-// A 32 x 32 block of fp32 sums to memory through 4 KB of shared memory: a row is 128 bytes, its 16-byte
-// piece j stands at j ^ (row % 8), so that the fragments' scalar stores and the pieces' loads cover all
-// banks.
-__device__ __forceinline__ void store_sums(const float (&v)[4][8], uint32_t slot, int lane, float* out, int64_t ld,
-                                           int rows, int feats) {
-    __syncwarp();  // the slots have been read
-#pragma unroll
-    for (int o = 0; o < 4; ++o)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int r = 8 * (k >> 1) + 2 * (lane & 3) + (k & 1), f = 8 * o + (lane >> 2);
-            st_shared_f32(slot + r * 128 + (((f >> 2) ^ (r & 7)) << 4) + (f & 3) * 4, v[o][k]);
-        }
-    __syncwarp();
-    const int j = lane & 7;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = 4 * i + (lane >> 3);
-        const uint4 x = ld_shared_u4(slot + r * 128 + ((j ^ (r & 7)) << 4));
-        if (r < rows && 4 * j < feats) *reinterpret_cast<uint4*>(out + r * ld + 4 * j) = x;
+        const float* const z = static_cast<const float*>(a.preact) + p.row * a.ld_pre + p.f;
+        Sums<4>::fetch(x.a, lane, z, a.ld_pre, p.valid, left);
+        if (act_gated(a.act)) Sums<4>::fetch(x.b, lane, z + a.feats, a.ld_pre, p.valid, left);
     }
 }
 
 // Finishes one block: v holds the sums. `bias`: of the thread's 4 accumulator lanes. `x` goes into
 // the slots first, then `refill` may fetch the next block's into it.
-template <bool kBF16, bool kGated, bool kBack, bool kSums, typename Refill>
+template <bool kBF16, int kMode, bool kGated, bool kBack, typename Refill>
 __device__ __forceinline__ void finish_block(const FfnArgs& a, float (&v)[4][8], const float (&bias)[4],
                                              const Place& p, Ahead<kGated, kBack>& x, uint32_t slot,
                                              int lane, Refill refill) {
     const int left = a.feats - p.f;
-    if constexpr (kSums) {
+    if constexpr (kMode == kSeg && !kGated && !kBack) {
         if (a.out_f32) {
-            store_sums(v, slot, lane, static_cast<float*>(a.out) + p.row * a.ld_out + p.f, a.ld_out, p.valid, left);
+            Sums<4>::store([&](int o, int k) { return v[o][k]; }, slot, lane,
+                           static_cast<float*>(a.out) + p.row * a.ld_out + p.f, a.ld_out, p.valid, left);
             return;
         }
     }
     uint16_t* const out = static_cast<uint16_t*>(a.out) + p.out_base + p.row * a.ld_out + p.f;
     const int tr = 2 * (lane & 3);  // the thread's rows: 8 b + tr + i
-    __syncwarp();  // the slots have been read
-    if constexpr (kBack) {
-        Block<4>(slot, lane).put(x.a);
-        if (act_gated(a.act)) Block<4>(slot + kSlot, lane).put(x.b);
-    } else if (a.residual) {
-        Block<kGated ? 2 : 4>(slot + kSlot, lane).put(x.a);
+    if constexpr (!kBack) {
+        __syncwarp();  // the slots have been read
+        if (a.residual) Block<kGated ? 2 : 4>(slot + kSlot, lane).put(x.a);
+        refill();
+        __syncwarp();
     }
-    refill();
-    __syncwarp();
     float scale[8];
     if (a.row_scale) {
 #pragma unroll
@@ -439,10 +474,17 @@ __device__ __forceinline__ void finish_block(const FfnArgs& a, float (&v)[4][8],
         if constexpr (kGated) {
             const Block<2> blk(slot, lane);
             if (a.preact) {
-                uint16_t* const z = static_cast<uint16_t*>(a.preact) + p.row * a.ld_pre + p.f;
-                blk.template store<kBF16>([&](int o, int k) { return v[2 * o][k]; }, z, a.ld_pre, p.valid, left);
-                blk.template store<kBF16>([&](int o, int k) { return v[2 * o + 1][k]; }, z + a.feats, a.ld_pre,
-                                 p.valid, left);
+                auto gate = [&](int o, int k) { return v[2 * o][k]; };
+                auto up = [&](int o, int k) { return v[2 * o + 1][k]; };
+                if constexpr (kMode == kSeg) {
+                    float* const z = static_cast<float*>(a.preact) + p.row * a.ld_pre + p.f;
+                    Sums<2>::store(gate, slot, lane, z, a.ld_pre, p.valid, left);
+                    Sums<2>::store(up, slot + kSlot, lane, z + a.feats, a.ld_pre, p.valid, left);
+                } else {
+                    uint16_t* const z = static_cast<uint16_t*>(a.preact) + p.row * a.ld_pre + p.f;
+                    blk.template store<kBF16>(gate, z, a.ld_pre, p.valid, left);
+                    blk.template store<kBF16>(up, z + a.feats, a.ld_pre, p.valid, left);
+                }
             }
 #pragma unroll
             for (int o = 0; o < 4; o += 2) {
@@ -467,9 +509,14 @@ __device__ __forceinline__ void finish_block(const FfnArgs& a, float (&v)[4][8],
         } else {
             const Block<4> blk(slot, lane);
             auto val = [&](int o, int k) { return v[o][k]; };
-            if (a.preact)
-                blk.template store<kBF16>(val, static_cast<uint16_t*>(a.preact) + p.row * a.ld_pre + p.f, a.ld_pre,
-                                 p.valid, left);
+            if (a.preact) {
+                if constexpr (kMode == kSeg)
+                    Sums<4>::store(val, slot, lane, static_cast<float*>(a.preact) + p.row * a.ld_pre + p.f,
+                                   a.ld_pre, p.valid, left);
+                else
+                    blk.template store<kBF16>(val, static_cast<uint16_t*>(a.preact) + p.row * a.ld_pre + p.f,
+                                              a.ld_pre, p.valid, left);
+            }
 #pragma unroll
             for (int o = 0; o < 4; ++o) act_forward(v[o], a.act);
             if (a.row_scale) {
@@ -493,51 +540,57 @@ __device__ __forceinline__ void finish_block(const FfnArgs& a, float (&v)[4][8],
         // v is the gradient of the activation's output without the row's factor; the result is that
         // of z (gated: both halves, feats apart), and the row's dot product with the activation is
         // the gradient of its factor
-        // (gated: both halves' slots). Eight rows at a time, each slot rewritten in place.
+        // (gated: both halves' slots). Sixteen rows of z at a time, which fill a slot; the 16-bit results of
+        // eight of them take the place of what was read.
         const Block<4> blk(slot, lane), blk2(slot + kSlot, lane);
         const bool gated = act_gated(a.act);
         float dot[8];
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            uint32_t rz[4], ru[4] = {0, 0, 0, 0};
-            ldmatrix_x4_trans(blk.matrix + b * 512, rz);
-            if (gated) ldmatrix_x4_trans(blk2.matrix + b * 512, ru);
-            float z[8], d[8], up[8];  // [2 o + i]
+        for (int half = 0; half < 2; ++half) {
+            __syncwarp();  // the slots have been read
+            Sums<4>::put(x.a, half, slot, lane);
+            if (gated) Sums<4>::put(x.b, half, slot + kSlot, lane);
+            if (half == 1) refill();
+            __syncwarp();
 #pragma unroll
-            for (int o = 0; o < 4; ++o) {
-                const float2 zz = unpack2<kBF16>(rz[o]), uu = unpack2<kBF16>(ru[o]);
-                z[2 * o] = zz.x;
-                z[2 * o + 1] = zz.y;
-                up[2 * o] = uu.x;
-                up[2 * o + 1] = uu.y;
-            }
-            act_both(z, d, act_of_gate(a.act));
-            dot[2 * b] = dot[2 * b + 1] = 0.0f;
+            for (int b2 = 0; b2 < 2; ++b2) {
+                const int b = 2 * half + b2;
+                float z[8], d[8], up[8];  // [2 o + i]
 #pragma unroll
-            for (int n = 0; n < 8; ++n) {
-                const int k = 2 * b + (n & 1);
-                const float g = v[n >> 1][k];
-                const float t = p.rows > p.valid && past(k) ? 0.0f : a.row_scale ? g * scale[k] : g;
-                if (gated) {
-                    dot[k] = fmaf(g, z[n] * up[n], dot[k]);
-                    d[n] = t * up[n] * d[n];
-                    up[n] = t * z[n];
-                } else {
-                    dot[k] = fmaf(g, z[n], dot[k]);
-                    d[n] = t * d[n];
+                for (int n = 0; n < 8; ++n) {
+                    const uint32_t at = Sums<4>::element(n >> 1, 2 * b2 + (n & 1), lane);
+                    z[n] = ld_shared_f32(slot + at);
+                    up[n] = gated ? ld_shared_f32(slot + kSlot + at) : 0.0f;
                 }
+                act_both(z, d, act_of_gate(a.act));
+                dot[2 * b] = dot[2 * b + 1] = 0.0f;
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    const int k = 2 * b + (n & 1);
+                    const float g = v[n >> 1][k];
+                    const float t = p.rows > p.valid && past(k) ? 0.0f : a.row_scale ? g * scale[k] : g;
+                    if (gated) {
+                        dot[k] = fmaf(g, z[n] * up[n], dot[k]);
+                        d[n] = t * up[n] * d[n];
+                        up[n] = t * z[n];
+                    } else {
+                        dot[k] = fmaf(g, z[n], dot[k]);
+                        d[n] = t * d[n];
+                    }
+                }
+                __syncwarp();
+                stmatrix_x4_trans(blk.matrix + b2 * 512, packf2<kBF16>(d[0], d[1]), packf2<kBF16>(d[2], d[3]),
+                                  packf2<kBF16>(d[4], d[5]), packf2<kBF16>(d[6], d[7]));
+                if (gated)
+                    stmatrix_x4_trans(blk2.matrix + b2 * 512, packf2<kBF16>(up[0], up[1]),
+                                      packf2<kBF16>(up[2], up[3]), packf2<kBF16>(up[4], up[5]),
+                                      packf2<kBF16>(up[6], up[7]));
             }
             __syncwarp();
-            stmatrix_x4_trans(blk.matrix + b * 512, packf2<kBF16>(d[0], d[1]), packf2<kBF16>(d[2], d[3]),
-                              packf2<kBF16>(d[4], d[5]), packf2<kBF16>(d[6], d[7]));
-            if (gated)
-                stmatrix_x4_trans(blk2.matrix + b * 512, packf2<kBF16>(up[0], up[1]),
-                                  packf2<kBF16>(up[2], up[3]), packf2<kBF16>(up[4], up[5]),
-                                  packf2<kBF16>(up[6], up[7]));
+            uint16_t* const rows = out + (int64_t)(16 * half) * a.ld_out;
+            blk.template flush<2>(rows, a.ld_out, p.rows - 16 * half, left);
+            if (gated) blk2.template flush<2>(rows + a.feats, a.ld_out, p.rows - 16 * half, left);
         }
-        __syncwarp();
-        blk.flush(out, a.ld_out, p.rows, left);
-        if (gated) blk2.flush(out + a.feats, a.ld_out, p.rows, left);
         if (a.row_dot) {
             // sum over the 8 lanes that hold other features of the same rows, halving the rows a
             // lane keeps at each step: lane bits 4, 3, 2 end up selecting bits 2, 1, 0 of k
@@ -902,7 +955,7 @@ __global__ void __launch_bounds__(ffn::kThreads, 1)
                         }
                     }
                     const Place here = place;
-                    finish_block<kBF16, kGated, kBack, kMode == kSeg && !kGated && !kBack>(
+                    finish_block<kBF16, kMode, kGated, kBack>(
                         args, v, bias, here, ahead, slot, lane, [&]() {
                         if (pass == kWhole && c + 2 < chunks) {
                             at_chunk(c + 2);

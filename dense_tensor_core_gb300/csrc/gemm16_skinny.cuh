@@ -198,8 +198,14 @@ __global__ void __launch_bounds__(skinny::kThreads) gemm16_skinny_kernel(const S
                 if constexpr (kGated) up += load(a.bias, a.feats + f);
             }
             if (a.preact) {
-                store(a.preact, row * a.ld_pre + f, v[0]);
-                if constexpr (kGated) store(a.preact, row * a.ld_pre + a.feats + f, up);
+                auto keep = [&](int64_t at, float z) {
+                    if constexpr (kSegRows)
+                        static_cast<float*>(a.preact)[at] = z;  // (as the tiles do, for the backward pass)
+                    else
+                        store(a.preact, at, z);
+                };
+                keep(row * a.ld_pre + f, v[0]);
+                if constexpr (kGated) keep(row * a.ld_pre + a.feats + f, up);
             }
             act_forward(v, act_of_gate(a.act));
             if constexpr (kGated) v[0] *= up;

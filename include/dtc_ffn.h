@@ -173,7 +173,7 @@ typedef struct {
 typedef struct {
     uint64_t bytes;  /* size of the buffer */
     uint64_t x;      /* [capacity, H]: the tokens' rows */
-    uint64_t z;      /* [capacity, F or 2F]: the first product (training only) */
+    uint64_t z;      /* [capacity, F or 2F] fp32: the first product (training only) */
     uint64_t h;      /* [capacity, F]: its activation times the row's weight */
     uint64_t scale;  /* [capacity] fp32: each row's weight */
     uint64_t y;      /* [capacity, H] fp32: the second product */
@@ -213,8 +213,8 @@ int moe_experts_backward_workspace_size(int dtype, int64_t T, int k, int64_t E, 
  * `buffer` as moe_experts with train left it; workspace: device scratch, 16-byte aligned, no initial
  * contents needed. dw_in and dw_out may both be NULL (not computed), so may dx. The gradient of the
  * residual is dy itself. The gradient of z is rounded to the operands' type, as the tensor cores'
- * operand; it is taken at the z that the forward pass kept, rounded likewise (half the memory held
- * between the passes). All sums are fp32. The pages have no counterpart.
+ * operand; it is taken at the fp32 z that the forward pass kept. All sums are fp32. The pages have no
+ * counterpart.
  */
 int moe_experts_backward(int dtype, const void* dy, const void* w_in, const void* w_out,
                          const void* weights, const void* plan, const void* buffer, void* dx,

@@ -74,3 +74,33 @@ def test_wide_rows():
     y = dtc.moe_experts("bf16", x.bfloat16(), wi.bfloat16(), wo.bfloat16(), w, dtc.moe_plan(idx, E), activation="none")
     exact = torch.einsum("tkij,tj->tki", wo[idx.clamp(min=0).long()], x[:, torch.arange(F) * 18])
     assert torch.equal(y, (exact * (idx >= 0)[..., None]).sum(1).bfloat16())
+
+
+# the gradient of a weight is taken at the unrounded first product: with fp32 weights nothing on the way
+# to it is rounded to 16 bits
+@pytest.mark.parametrize("T,F", [(1, 136), (12, 136), (40, 72), (300, 136)])
+@pytest.mark.parametrize("kind,name", [("bf16", "swiglu"), ("bf16", "silu"), ("f16", "geglu"), ("bf16", "gelu")])
+def test_gradient_at_the_unrounded_product(kind, name, T, F):
+    import dense_tensor_core_gb300 as dtc
+    dt, H, E, k = R.DT[kind], 64, 8, 3
+    g = torch.Generator(device="cuda").manual_seed(T)
+    r = lambda std, *s: (torch.randn(s, generator=g, device="cuda") * std).to(dt)  # noqa: E731
+    x, dy = r(1, T, H), r(1, T, H)
+    wi, wo = r(H ** -0.5, E, 2 * F if name in R.GATED else F, H), r(F ** -0.5, E, H, F)
+    idx, w = choices(T, E, k, T), torch.rand((T, k), generator=g, device="cuda")
+    plan = dtc.moe_plan(idx, E)
+    _, saved = dtc.moe_experts(kind, x, wi, wo, w, plan, activation=name, save=True)
+    dw = dtc.moe_experts_backward(kind, dy, wi, wo, w, plan, saved, activation=name)[3]
+    got, at = idx >= 0, idx.clamp(min=0).long()
+    xd, dyd, wi, wo = x.double(), dy.double(), wi.double()[at], wo.double()[at]
+    z = torch.einsum("tkfh,th->tkf", wi, xd)
+    ez = (H + 2) * 2.0 ** -23 * torch.einsum("tkfh,th->tkf", wi.abs(), xd.abs())
+    dh = torch.einsum("tkhf,th->tkf", wo, dyd)
+    edh = (H + 2) * 2.0 ** -23 * torch.einsum("tkhf,th->tkf", wo.abs(), dyd.abs())
+    h, eh = R.act(z, name), R.act_bound(z, ez, name)
+    want = (dh * h).sum(2) * got
+    bound = (edh * (h.abs() + eh) + dh.abs() * eh).sum(2) + (F + 2) * 2.0 ** -23 * (dh * h).abs().sum(2)
+    R.check(dw, want, bound * got, "dweights")
+    if T > 5 and kind == "bf16":  # a rounded product would show
+        off = ((dh * R.act(z.to(dt).double(), name)).sum(2) * got - want).abs() > bound
+        assert bool(off.any())
