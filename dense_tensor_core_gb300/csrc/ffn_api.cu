@@ -780,15 +780,15 @@ int red_product(const ExpertSizes& s, bool bf16, const int32_t* plan, const moe_
     return launch_ffn_experts(c, info, st);
 }
 
-// Whether the tokens are few enough for the kernel without tiles (us with the same routes, without
-// tiles against tiles. 64 experts, 8 each, H 2048, F 1024: 1 token 28 and 36, 16 tokens 124 and 128,
-// 48 157 and 151. 8 experts, 2 each, H and F 4096: 43 and 55, 16 tokens 133 and 153, 32 177 and 155.
-// 128 experts, 4 each, H 2048, F 768: 16 and 25, 16 tokens 90 and 91, 24 136 and 129). An expert with
-// more than 8 rows reads its weights again, from the L2. As for one matrix, a reduction above 8192 has
-// to have its blocks (over the experts that the tokens can reach) fill the HBM; below, few blocks win
+// Whether the tokens are few enough for the kernel without tiles (plan, products and join, us, without
+// tiles and with them; same routes. 64 experts, 8 each, H 2048, F 1024: 1 token 31 and 39, 16 tokens 131
+// and 141, 48 160 and 156. 8 experts, 2 each, H and F 4096: 46 and 59, 16 tokens 138 and 159, 32 161 to 186
+// and 160. 128 experts, 4 each, H 2048, F 768: 20 and 29, 16 tokens 97 and 104, 24 130 and 132, 32 152 and
+// 149). An expert with more than 8 rows reads its weights again, from the L2. As for one matrix, a
+// reduction above 8192 has to have its blocks (over the experts that the tokens can reach) fill the HBM; below, few blocks win
 // too (8 experts, F 256 and H 8192: 1 of 1 token 27 and 32, 2 of 16 tokens 44 and 53). Above (8 experts,
-// whole calls between events): H 512, F 16384, 2 of 1 token 59 and 53, of 16 tokens 118 and 102; H 1024, F 16384,
-// 1 of 1 token 54 and 51, of 16 tokens 145 and 151; H 16384, F 512, 2 of 16 tokens 98 and 110.
+// whole calls between events): H 512, F 16384, 2 of 1 token 59 and 53, of 16 tokens 118 and 102; H 1024,
+// F 16384, 1 of 1 token 54 and 51, of 16 tokens 145 and 151; H 16384, F 512, 2 of 16 tokens 98 and 110.
 constexpr int kFewTokens = 16;
 bool few_rows(const ExpertSizes& s, int sms) {
     const int64_t reached = std::min(s.T * s.k, s.E);

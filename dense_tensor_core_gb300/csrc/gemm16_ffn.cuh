@@ -45,10 +45,12 @@
 // is, so results repeat bit for bit), finishes the tile and sets the counter back to zero. No warp
 // waits for another.
 //
-// Measured: 4096 x 4096 x 8192 with GELU, bias, residual and the kept sum 181 us (1515 TFLOP/s);
-// launch durations of 4096 tokens by 8 of 64 experts, H 2048, F 1024, bf16: the gated product 180 to
-// 190 us (1447 to 1527 TFLOP/s), the second 105 to 109 us (1261 to 1309). Large products are bound
-// by the tensor pipe and the waits of its ring, narrow ones by the latency of the loads.
+// Measured: 4096 x 4096 x 8192 with GELU, bias, residual and the kept sum 174 to 188 us (1460 to 1580
+// TFLOP/s); launch durations of 4096 tokens by 8 of 64 experts, H 2048, F 1024, bf16: the gated product
+// 191 us (1440 TFLOP/s), the second 122 us (1120; with rows of 16 bits 105 to 109). Large products are
+// bound by the tensor pipe (4096^3: 69 % of the cycles) and the waits of its ring, narrow ones by the
+// latency of the loads, the backward form by its epilogue, which reads z in fp32 (5000 tokens by 6 of 48
+// experts, H 2048, F 1000: 186 us, with z of 16 bits 144).
 #pragma once
 
 #include "activation.cuh"

@@ -18,7 +18,7 @@
 //
 // Measured, weights not in the L2 (us, this kernel and the tcgen05 form): 1 x 8192 x 8192 23.9 and
 // 29.7 (5.6 TB/s of weights), 1 x 4096 x 4096 10.0 and 13.6, one token's experts (8 of 64, H 2048,
-// F 1024; both products and the join) 28 and 36. Loads under a condition each, in place of rows that
+// F 1024; plan, both products and the join) 31 and 39. Loads under a condition each, in place of rows that
 // exist, cost 25.9 and 10.7 for the first two.
 #pragma once
 
