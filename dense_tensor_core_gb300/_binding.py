@@ -185,9 +185,19 @@ def _ld(t):
     return t.stride(0)
 
 
-def _out(C, M, N, dtype, device, rows_of_larger=False):
+def _empty(shape, dtype, device, stream):
+    """Memory that belongs to the stream the kernels run on: the allocator hands what is freed on a
+    stream to that stream's next request, so a buffer that dies when the call returns, or that the
+    current stream's queued work still uses, must not come from another stream's memory."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _out(C, M, N, dtype, device, stream, rows_of_larger=False):
     if C is None:
-        return torch.empty((M, N), dtype=dtype, device=device)
+        return _empty((M, N), dtype, device, stream)
     _check_tensor(C, dtype, "C", rows_of_larger)
     if tuple(C.shape) != (M, N):
         raise ValueError(f"C must be {(M, N)}, got {tuple(C.shape)}")
@@ -212,7 +222,7 @@ def _gemm16(name, dtype, A, B, C, layout, stream):
     _check_tensor(A, dtype, "A")
     _check_tensor(B, dtype, "B")
     M, N, K = _shapes16(A, B, layout)
-    C = _out(C, M, N, dtype, A.device)
+    C = _out(C, M, N, dtype, A.device, stream)
     dev = _same_device(A, B, C)
     with torch.cuda.device(dev):
         _check(getattr(lib(), name)(_ptr(A), _ptr(B), _ptr(C), M, N, K, _layout_code(layout),
@@ -261,7 +271,7 @@ def gemm_mxfp8(A, B, sfA, sfB, C=None, stream=None):
     """Block-scaled e4m3 NT GEMM. A [M,K], B [N,K] e4m3 codes (uint8 tensors), sfA [M,ceil(K/128)],
     sfB [N,ceil(K/128)] E8M0 codes (uint8); C bf16 [M,N]."""
     M, N, K = _check_mxfp8(A, B, sfA, sfB)
-    C = _out(C, M, N, torch.bfloat16, A.device)
+    C = _out(C, M, N, torch.bfloat16, A.device, stream)
     dev = _same_device(A, B, sfA, sfB, C)
     with torch.cuda.device(dev):
         _check(lib().gemm_mxfp8(_ptr(A), _ptr(B), _ptr(sfA), _ptr(sfB), _ptr(C), M, N, K,
@@ -287,14 +297,14 @@ def gemm_ex(kind, A, B, C=None, layout="NT", sfA=None, sfB=None, variant=0, spli
         M, N, K = _check_mxfp8(A, B, sfA, sfB, rows_of_larger=True,
                                scale_block=scale_block or 128, a_format=a_format,
                                b_format=b_format)
-        C = _out(C, M, N, torch.bfloat16, A.device, rows_of_larger=True)
+        C = _out(C, M, N, torch.bfloat16, A.device, stream, rows_of_larger=True)
         lda, ldb = _ld_elems(A, a_format), _ld_elems(B, b_format)
     else:
         dt = torch.bfloat16 if kind == "bf16" else torch.float16
         _check_tensor(A, dt, "A", rows_of_larger=True)
         _check_tensor(B, dt, "B", rows_of_larger=True)
         M, N, K = _shapes16(A, B, layout)
-        C = _out(C, M, N, dt, A.device, rows_of_larger=True)
+        C = _out(C, M, N, dt, A.device, stream, rows_of_larger=True)
         lda, ldb = _ld(A), _ld(B)
     opts = _options(variant, split_k, timeout_ns, fault_inject, tile_n, tile_k,
                     lda, ldb, _ld(C), a_format, b_format, scale_block, workspace, stream_k)
@@ -362,14 +372,14 @@ def gemm_ex_static_workspace(kind, A, B, C=None, layout="NT", variant=0, tile_n=
         M, N, K = _check_mxfp8(A, B, sfA, sfB, rows_of_larger=True,
                                scale_block=scale_block or 128, a_format=a_format,
                                b_format=b_format)
-        C = _out(C, M, N, torch.bfloat16, A.device, rows_of_larger=True)
+        C = _out(C, M, N, torch.bfloat16, A.device, stream, rows_of_larger=True)
         lda, ldb = _ld_elems(A, a_format), _ld_elems(B, b_format)
     else:
         dt = torch.bfloat16 if kind == "bf16" else torch.float16
         _check_tensor(A, dt, "A", rows_of_larger=True)
         _check_tensor(B, dt, "B", rows_of_larger=True)
         M, N, K = _shapes16(A, B, layout)
-        C = _out(C, M, N, dt, A.device, rows_of_larger=True)
+        C = _out(C, M, N, dt, A.device, stream, rows_of_larger=True)
         lda, ldb = _ld(A), _ld(B)
     opts = _options(variant, 0, 0, 0, tile_n, tile_k, lda, ldb, _ld(C), a_format, b_format,
                     scale_block, stream_k=stream_k)
@@ -408,10 +418,9 @@ def gemm_nvfp4(A, B, sfA, sfB, C=None, workspace=None, variant=0, split_k=0, til
     if tuple(sfA.shape) != (M, K // 16) or tuple(sfB.shape) != (N, K // 16):
         raise ValueError(f"sfA / sfB must be {(M, K // 16)} / {(N, K // 16)}, got "
                          f"{tuple(sfA.shape)} / {tuple(sfB.shape)}")
-    C = _out(C, M, N, torch.bfloat16, A.device, rows_of_larger=True)
+    C = _out(C, M, N, torch.bfloat16, A.device, stream, rows_of_larger=True)
     if workspace is None:
-        workspace = torch.empty(max(1, gemm_nvfp4_workspace_size(M, N, K)), dtype=torch.uint8,
-                                device=A.device)
+        workspace = _empty(max(1, gemm_nvfp4_workspace_size(M, N, K)), torch.uint8, A.device, stream)
     opts = _options(variant, split_k, timeout_ns, 0, tile_n, tile_k, 0, 0, _ld(C),
                     workspace=sk_workspace, stream_k=stream_k)
     dev = _same_device(A, B, sfA, sfB, C, workspace, sk_workspace)
@@ -449,9 +458,9 @@ def gemm_sp(kind, vals, meta, B, C=None, layout="NT", workspace=None, variant=0,
     N, Kb = (B.shape if name == "NT" else B.shape[::-1])
     if Kb != K:
         raise ValueError(f"B {tuple(B.shape)} does not match K = {K} ({name})")
-    C = _out(C, M, N, dt, vals.device, rows_of_larger=True)
+    C = _out(C, M, N, dt, vals.device, stream, rows_of_larger=True)
     if workspace is None:
-        workspace = torch.empty(max(1, M * K * 2), dtype=torch.uint8, device=vals.device)
+        workspace = _empty(max(1, M * K * 2), torch.uint8, vals.device, stream)
     opts = _options(variant, split_k, 0, 0, tile_n, tile_k, 0, _ld(B), _ld(C),
                     workspace=sk_workspace, stream_k=stream_k)
     dev = _same_device(vals, meta, B, C, workspace, sk_workspace)
