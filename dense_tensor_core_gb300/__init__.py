@@ -7,6 +7,8 @@ tensors (device pointers, sizes, the current stream) and raises ``GemmError`` on
 The feed-forward operators (``include/dtc_ffn.h``) run in the same library and are called through
 the native module ``_ffn_native``: gemm_act (product, bias, activation or gate, residual) and its
 gradient, moe_route and its gradient, moe_plan, moe_experts and its gradient.
+The 4-bit operators (``include/dtc_fp4.h``) are called the same way: quantize_fp4, dequantize_fp4,
+pack_fp4, gemm_fp4, moe_experts_fp4, on matrices held as ``Fp4``.
 There is no CPU fallback: if the library is missing, every call raises.
 """
 from ._binding import (  # noqa: F401
@@ -48,4 +50,13 @@ from ._ffn import (  # noqa: F401
     moe_plan,
     moe_route,
     moe_route_backward,
+)
+from ._fp4 import (  # noqa: F401
+    Fp4,
+    dequantize_fp4,
+    gemm_fp4,
+    gemm_fp4_workspace_size,
+    moe_experts_fp4,
+    pack_fp4,
+    quantize_fp4,
 )

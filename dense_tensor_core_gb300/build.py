@@ -46,29 +46,38 @@ def _due(target, inputs):
     return not os.path.exists(target) or os.path.getmtime(target) < max(map(os.path.getmtime, inputs))
 
 
+def _native_sources():
+    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cpp"))
+
+
 def _compile_native(obj_dir):
-    """The binding module's object (no GPU code; torch's own headers and ABI)."""
+    """The binding module's objects (no GPU code; torch's own headers and ABI), compiled side by side."""
     import torch
 
     root = os.path.dirname(torch.__file__)
     cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
     dirs = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
             cuda, sysconfig.get_paths()["include"], INCLUDE]
-    obj = os.path.join(obj_dir, "ffn_binding.o")
-    subprocess.check_call(
-        [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
-         "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch.compiled_with_cxx11_abi()]
-        + [x for d in dirs for x in ("-isystem" if "torch" in d else "-I", d)]
-        + ["-c", os.path.join(CSRC, "ffn_binding.cpp"), "-o", obj])
-    return obj
+    flags = ["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+             "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch.compiled_with_cxx11_abi()]
+    flags += [x for d in dirs for x in ("-isystem" if "torch" in d else "-I", d)]
+
+    def one(src):
+        obj = os.path.join(obj_dir, os.path.basename(src)[:-4] + ".o")
+        subprocess.check_call([shutil.which("g++") or "g++", *flags, "-c", src, "-o", obj])
+        return obj
+
+    srcs = _native_sources()
+    with ThreadPoolExecutor(max_workers=len(srcs)) as ex:
+        return list(ex.map(one, srcs))
 
 
-def _link_native(obj, tmp):
+def _link_native(objs, tmp):
     import torch
 
     torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     subprocess.check_call(
-        [shutil.which("g++") or "g++", "-shared", obj, "-o", tmp, "-L" + HERE, "-ldtc_gemm",
+        [shutil.which("g++") or "g++", "-shared", *objs, "-o", tmp, "-L" + HERE, "-ldtc_gemm",
          "-Wl,-rpath,$ORIGIN", "-L" + torch_lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
          "-lc10_cuda"])
 
@@ -88,7 +97,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     headers = _headers(INCLUDE, ".h")
     library = force or _due(LIB, srcs + headers + _headers(CSRC, ".cuh", ".h"))
     native = importlib.util.find_spec("torch") is not None and (
-        force or _due(NATIVE, headers + [os.path.join(CSRC, "ffn_binding.cpp")]))
+        force or _due(NATIVE, headers + _native_sources() + [os.path.join(CSRC, "binding.h")]))
     if not library and not native:
         return LIB
     os.makedirs(OBJ_DIR, exist_ok=True)

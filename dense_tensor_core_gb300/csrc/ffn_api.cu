@@ -9,11 +9,6 @@ namespace {
 using namespace dtc_host;
 using dtc::ffn::kBK;
 
-constexpr int64_t kMaxSize = 2147483647;
-
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-uint64_t up256(uint64_t v) { return (v + 255) & ~(uint64_t)255; }
-
 // Up to this many rows a product with K-major operands runs on the kernel without tiles. A block of it
 // (16 features; gated, 8 and their gates) walks the whole K, so a long K needs several blocks an SM to
 // fill the HBM, else the K splits of the tiles win. Measured (K up to 16384), us, without tiles and with:
@@ -46,19 +41,6 @@ struct FfnPlan {
     uint64_t counter_bytes = 0, bytes = 0;  // split-K workspace: counters, then partial sums
     int64_t items() const { return tiles + (int64_t)split_tiles * (splits - 1); }
 };
-
-int num_feature_tiles(int64_t feats, bool gated) { return ceil_div(feats, gated ? 128 : 256); }
-
-// Counters of a split tile, and of a plan of `tiles` split ones.
-constexpr uint64_t kTileCounterBytes = 2 * dtc::ffn::kEpWarps * 4;
-uint64_t counters_of(int64_t tiles) { return up256((uint64_t)tiles * kTileCounterBytes); }
-// Head of a caller's workspace that holds the words which are zero between calls: the same bytes for
-// gemm_act and gemm_act_backward, whatever the sizes, row pitches and alignment of a call are, so that
-// one workspace serves calls of both (what one call leaves in the rest must not reach where another
-// counts). First the counters of split tiles (plans split fewer than 2 * pairs of them) and of the
-// column sums' strips, then the stream-K flags of the gradient's products.
-uint64_t flags_offset(int pairs) { return std::max<uint64_t>(counters_of(2 * pairs), kActBackwardStrips * 4); }
-uint64_t zero_words_bytes(int pairs) { return flags_offset(pairs) + kSkFlagBytes; }
 
 // `counters`: bytes of the region before the partial sums.
 void size_split(FfnPlan* p, uint64_t counters) {
@@ -176,11 +158,6 @@ FfnPlan plan_red(int64_t E, int64_t rows, int64_t feats, int pairs) {
     return p;
 }
 
-int pairs_of(DeviceInfo* d) {
-    const DevModel& m = device_model(d);
-    return m.pairs > 0 ? m.pairs : std::max(1, m.sms / 2);
-}
-
 void apply_plan(const FfnPlan& p, void* ws, FfnCall* c) {
     c->grid = p.grid;
     c->args.tile_n = p.tile_n;
@@ -216,31 +193,6 @@ int check_act(int dtype, int64_t M, int64_t N, int64_t K, int layout, int act) {
                     (long long)M, (long long)N, (long long)K);
     return GEMM_OK;
 }
-
-// A matrix of `rows` rows of `len` 16-bit elements at `p`, `ld` (0: dense) apart. `whole`: it is
-// read or written in 16-byte pieces, so its rows must be whole ones (the product's operands go
-// through tensor maps, which only ask that rows start 16 bytes apart).
-int check_rows(const char* name, const void* p, int64_t rows, int64_t len, int64_t* ld,
-               bool whole = true) {
-    if (*ld < 0) return fail(GEMM_ERR_INVALID_ARG, "the leading dimension of %s is negative", name);
-    if (*ld == 0) *ld = len;
-    if (rows == 0 || len == 0) return GEMM_OK;
-    if (!p) return fail(GEMM_ERR_INVALID_ARG, "%s is NULL", name);
-    if (!aligned(p, 16)) return fail(GEMM_ERR_INVALID_ARG, "%s is not 16-byte aligned", name);
-    if (*ld < len || *ld > kMaxSize || *ld % 8 || (whole && len % 8))
-        return fail(GEMM_ERR_INVALID_ARG, "%s: rows of %lld elements, %lld apart, must %sstart 16 "
-                    "bytes apart and not overlap", name, (long long)len, (long long)*ld,
-                    whole ? "be whole multiples of 16 bytes, " : "");
-    return GEMM_OK;
-}
-
-int check_workspace(const void* ws) {
-    if (ws && !aligned(ws, 16))
-        return fail(GEMM_ERR_INVALID_ARG, "the workspace is not 16-byte aligned");
-    return GEMM_OK;
-}
-
-uint64_t timeout_of(uint64_t ns) { return ns ? ns : kDefaultTimeoutNs; }
 
 }  // namespace
 
@@ -832,12 +784,6 @@ int experts_layout(const ExpertSizes& s, int train, int pairs, moe_experts_info*
                                          seg_plan(s, s.H, false, s.F, pairs));
     l->bytes = l->split + up256(x.bytes);
     return GEMM_OK;
-}
-
-int check_ptr16(const void* p, int dev, const char* name) {
-    if (!p || !aligned(p, 16))
-        return fail(GEMM_ERR_INVALID_ARG, "%s is NULL or not 16-byte aligned", name);
-    return dev < 0 ? GEMM_OK : check_device_ptr(p, dev, name);
 }
 
 }  // namespace

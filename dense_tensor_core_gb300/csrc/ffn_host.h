@@ -117,4 +117,59 @@ struct JoinCall {
 int launch_moe_join(bool bf16, const JoinCall& c, const int32_t* plan, const moe_plan_info& l, int64_t T,
                     int k, int64_t E, int64_t H, int64_t ld_rows, DeviceInfo* dev, cudaStream_t stream);
 
+// ------------------------------------------------------------------------------------------------
+// Pieces of the entry points
+// ------------------------------------------------------------------------------------------------
+constexpr int64_t kMaxSize = 2147483647;
+
+inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+inline uint64_t up256(uint64_t v) { return (v + 255) & ~(uint64_t)255; }
+inline uint64_t timeout_of(uint64_t ns) { return ns ? ns : kDefaultTimeoutNs; }
+inline int pairs_of(DeviceInfo* d) {
+    const DevModel& m = device_model(d);
+    return m.pairs > 0 ? m.pairs : std::max(1, m.sms / 2);
+}
+
+inline int num_feature_tiles(int64_t feats, bool gated) { return ceil_div(feats, gated ? 128 : 256); }
+
+// Counters of a split tile, and of a plan of `tiles` split ones.
+constexpr uint64_t kTileCounterBytes = 2 * dtc::ffn::kEpWarps * 4;
+inline uint64_t counters_of(int64_t tiles) { return up256((uint64_t)tiles * kTileCounterBytes); }
+// Head of a caller's workspace that holds the words which are zero between calls: the same bytes for
+// gemm_act and gemm_act_backward, whatever the sizes, row pitches and alignment of a call are, so that
+// one workspace serves calls of both (what one call leaves in the rest must not reach where another
+// counts). First the counters of split tiles (plans split fewer than 2 * pairs of them) and of the
+// column sums' strips, then the stream-K flags of the gradient's products.
+inline uint64_t flags_offset(int pairs) { return std::max<uint64_t>(counters_of(2 * pairs), kActBackwardStrips * 4); }
+inline uint64_t zero_words_bytes(int pairs) { return flags_offset(pairs) + kSkFlagBytes; }
+
+// A matrix of `rows` rows of `len` 16-bit elements at `p`, `ld` (0: dense) apart. `whole`: it is
+// read or written in 16-byte pieces, so its rows must be whole ones (the product's operands go
+// through tensor maps, which only ask that rows start 16 bytes apart).
+inline int check_rows(const char* name, const void* p, int64_t rows, int64_t len, int64_t* ld,
+               bool whole = true) {
+    if (*ld < 0) return fail(GEMM_ERR_INVALID_ARG, "the leading dimension of %s is negative", name);
+    if (*ld == 0) *ld = len;
+    if (rows == 0 || len == 0) return GEMM_OK;
+    if (!p) return fail(GEMM_ERR_INVALID_ARG, "%s is NULL", name);
+    if (!aligned(p, 16)) return fail(GEMM_ERR_INVALID_ARG, "%s is not 16-byte aligned", name);
+    if (*ld < len || *ld > kMaxSize || *ld % 8 || (whole && len % 8))
+        return fail(GEMM_ERR_INVALID_ARG, "%s: rows of %lld elements, %lld apart, must %sstart 16 "
+                    "bytes apart and not overlap", name, (long long)len, (long long)*ld,
+                    whole ? "be whole multiples of 16 bytes, " : "");
+    return GEMM_OK;
+}
+
+inline int check_workspace(const void* ws) {
+    if (ws && !aligned(ws, 16))
+        return fail(GEMM_ERR_INVALID_ARG, "the workspace is not 16-byte aligned");
+    return GEMM_OK;
+}
+
+inline int check_ptr16(const void* p, int dev, const char* name) {
+    if (!p || !aligned(p, 16))
+        return fail(GEMM_ERR_INVALID_ARG, "%s is NULL or not 16-byte aligned", name);
+    return dev < 0 ? GEMM_OK : check_device_ptr(p, dev, name);
+}
+
 }  // namespace dtc_host

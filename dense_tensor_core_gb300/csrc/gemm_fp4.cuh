@@ -1,0 +1,492 @@
+// gemm_fp4.cuh -- the product of 4-bit operands (NVFP4 or MXFP4, include/dtc_fp4.h) on CTA pairs (cluster
+// 2x1, tcgen05 cta_group::2), with the epilogue of the feed-forward products, over one matrix or over the
+// row segments of many experts:
+//   out[r, f] = epilogue( gq[r] gp[f] sum_k q[r, k] sq[r, k / b] p[f, k] sp[f, k / b] )
+// The tensor core multiplies codes and block scales (kind::mxf4nvf4, kind::mxf4: K = 64 an instruction, twice
+// the rate of 8-bit elements) and sums in fp32; the factors of rows and features are applied to the sum.
+//
+// Frame, roles and epilogue are those of gemm16_ffn.cuh: features are the M side (256 per pair), rows the N
+// side (32 to 256), warp 0 loads, warp 1 of the leader issues, warps 2-9 finish one tile while the next is
+// multiplied. What is different:
+//   - A stage is 256 elements deep: one 128-byte swizzled row per operand row, 16 KB of P and up to 16 KB of
+//     Q per CTA, and the scales of both: 2 KB for the CTA's 128 features and 2 KB for each 128 rows of the
+//     whole tile (each CTA's datapath computes all rows of its features), in chunks that one tcgen05.cp each
+//     puts into four Tensor Memory columns. Five stages.
+//   - Tensor Memory: accumulators take the columns below args.acc_top, by turns from the left end and up to
+//     acc_top, so that tiles of up to acc_top / 2 rows do not touch; behind them lie 48 columns of scales per
+//     stage in flight (4 for P and 8 for Q per set, up to 4 sets). A tile that does touch its predecessor's
+//     columns waits until those are read.
+//   - The scales of a stage may be overwritten when the MMAs that read them are done: the barrier that frees
+//     that stage's shared memory says so too, and the issuing thread waits for it, sf_stages stages behind.
+#pragma once
+
+#include "gemm16_ffn.cuh"
+
+namespace dtc {
+
+struct Fp4Args {
+    FfnArgs e;            // sizes, plan and epilogue; red = K / 4 (16-bit words of a row)
+    bool mx;              // MXFP4
+    int sets;             // scale sets of a row
+    int p_groups;         // scale groups of an expert's matrix of P
+    const float* p_scale; // [experts][feats], gated [2 feats]; NULL = 1
+    const float* q_scale; // rows; NULL = 1
+    int acc_top;          // Tensor Memory columns of the accumulators
+    int sf_stages;        // stages whose scales fit behind them
+};
+
+namespace gf4 {
+using ffn::kEpBytes;
+using ffn::kEpWarps;
+using ffn::kSlot;
+using ffn::kThreads;
+constexpr int kBK = 64;  // 16-bit words (256 elements) per stage
+constexpr int kStages = 5;
+constexpr int kPBytes = 128 * 128;
+constexpr int kQBytes = 128 * 128;
+constexpr int kSfGroup = 4 * 512;  // the sets of a stage of 128 rows (MXFP4: two of them)
+constexpr int kSfBytes = 3 * kSfGroup;
+constexpr int kStageBytes = kPBytes + kQBytes + kSfBytes;
+constexpr int kSmemBytes = kStages * kStageBytes + kEpBytes + 1024;
+constexpr int kTmemCols = 512;
+constexpr int kSfSet = 12, kSfStage = 4 * kSfSet;
+constexpr int kNarrow = 160;  // tiles of up to so many rows leave four stages of scales, others two
+static_assert(kSmemBytes <= 227 * 1024 - 512, "shared memory budget");
+static_assert(2 * kNarrow + 4 * kSfStage <= kTmemCols, "Tensor Memory budget");
+constexpr int kWideTop = kTmemCols - 2 * kSfStage;
+
+// The t-th item of the launch (see ffn::get_item).
+template <int kMode, bool kGated>
+__device__ __forceinline__ bool item_of(const FfnArgs& a, int t, int seg_tiles, ffn::Item& w) {
+    constexpr int kFeats = kGated ? 128 : 256;
+    int tile = t, split = -1;
+    if (a.splits > 1) {
+        tile = t / a.splits;
+        if (tile < a.split_tiles)
+            split = t - tile * a.splits;
+        else
+            tile = t - a.split_tiles * (a.splits - 1);
+    }
+    w.tile = tile;
+    w.split = split;
+    w.expert = 0;
+    w.zeros = 0;
+    if constexpr (kMode == ffn::kRows) {
+        if (tile >= a.num_ft * a.num_rt) return false;
+        int ft, rt;
+        tile_coords(tile, a.num_ft, a.num_rt, ffn::kGroupF, ft, rt);
+        w.f0 = ft * kFeats;
+        w.r0 = rt * a.tile_n;
+        w.valid = min(a.tile_n, a.rows - w.r0);
+        w.n = a.tile_n;
+        w.krow = w.r0 >> 7;  // first scale group of the rows
+    } else {
+        const int rt = tile / a.num_ft;
+        if (rt >= a.max_tiles) return false;
+        const int4 s = reinterpret_cast<const int4*>(a.tiles)[rt];
+        if (rt >= seg_tiles) return false;
+        // a record that no plan of these sizes holds ends the walk
+        if ((unsigned)s.x >= (unsigned)a.experts || s.z < 1 || s.z > a.tile_n || s.y < 0 ||
+            s.y > a.rows - s.z || (s.y & (ffn::kSegAlign - 1)))
+            return false;
+        w.f0 = (tile - rt * a.num_ft) * kFeats;
+        w.expert = s.x;
+        w.r0 = s.y;
+        w.valid = s.z;
+        w.n = ffn::round32(s.z);
+        w.krow = 2 * rt;  // the rows' scales stand tile by tile
+    }
+    const int kb = (a.red + kBK - 1) / kBK;
+    w.kb0 = split >= 0 ? min(kb, split * a.kb_per_split) : 0;
+    w.kb1 = split >= 0 ? min(kb, w.kb0 + a.kb_per_split) : kb;
+    return true;
+}
+}  // namespace gf4
+
+template <bool kBF16, int kMode, bool kGated>
+__global__ void __launch_bounds__(ffn::kThreads, 1)
+    gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ FfnQMaps tmQ,
+                    const __grid_constant__ CUtensorMap tmSP, const __grid_constant__ CUtensorMap tmSQ,
+                    const Fp4Args fargs) {
+    using namespace gf4;
+    using ffn::Ahead;
+    using ffn::Item;
+    using ffn::Place;
+    constexpr bool kSegRows = kMode == ffn::kSeg;
+    const FfnArgs& args = fargs.e;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bar_full[kStages];
+    __shared__ __align__(8) uint64_t bar_empty[kStages];
+    __shared__ __align__(8) uint64_t bar_tfull[2];
+    __shared__ __align__(8) uint64_t bar_tempty[2];
+    __shared__ __align__(8) uint64_t bar_drain;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t sP = base;
+    const uint32_t sQ = base + kStages * kPBytes;
+    const uint32_t sSF = base + kStages * (kPBytes + kQBytes);
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int pair = blockIdx.x >> 1;
+    const int num_pairs = gridDim.x >> 1;
+    volatile int* abort = &abort_flag;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(smem_u32(&bar_full[s]), 1);
+            mbar_init(smem_u32(&bar_empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&bar_tfull[b]), 1);
+            mbar_init(smem_u32(&bar_tempty[b]), 2 * kEpWarps);  // of both CTAs
+        }
+        mbar_init(smem_u32(&bar_drain), 1);
+        abort_flag = 0;
+        fence_barrier_init();
+        fence_proxy_async_smem();
+    }
+    if (warp == 0 && lane == 0 && args.red > 0) {  // (a product with K = 0 has no tensor maps)
+        tma_prefetch_desc(&tmP);
+        tma_prefetch_desc(&tmQ.m[0]);
+        tma_prefetch_desc(&tmSP);
+        tma_prefetch_desc(&tmSQ);
+    }
+    if (warp == 1) {
+        tmem_alloc<2>(smem_u32(&tmem_slot), kTmemCols);
+        tmem_relinquish<2>();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers exist before any copy or arrival targets them
+    tc_fence_after_sync();
+    const uint32_t tmem_base = tmem_slot;
+    grid_launch_dependents();
+    grid_dependency_wait();  // the set-up above overlaps the tail of the kernel before
+    const int seg_tiles = kSegRows ? min(*args.num_tiles, args.max_tiles) : 0;
+    const int sf_sets = fargs.mx ? 2 : 4;  // of a stage
+    const uint32_t sf_bytes = (uint32_t)sf_sets * 512u;
+    // columns of an accumulator of n rows that the turn b takes
+    auto acc_col = [&](uint32_t b, int n) { return b ? (uint32_t)(fargs.acc_top - n) : 0u; };
+
+    if (warp == 0) {
+        // ------------------------------ TMA producer (both CTAs) ------------------------------
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            Item w;
+            for (int t = pair; ok && item_of<kMode, kGated>(args, t, seg_tiles, w); t += num_pairs) {
+                const int nh = w.n / 2;  // rows of Q per CTA
+                const int q_row = w.r0 + (int)rank * nh;
+                const int f_row = kGated ? w.f0 + (int)rank * 64 : w.f0 + (int)rank * 128;
+                const int qi = kSegRows ? ffn::box_of(nh) : 0;
+                const CUtensorMap* const q_map = &tmQ.m[qi];
+                const int q_rows = kSegRows ? ffn::box_rows(qi) : args.q_box;
+                // scale groups: of the CTA's features (one that the matrix does not have repeats its last:
+                // those features are not stored), and of the rows
+                const int pg = w.expert * fargs.p_groups + min(f_row / (kGated ? 64 : 128), fargs.p_groups - 1);
+                const int q_groups = (w.n + (kSegRows ? 0 : w.r0 & 127) + 127) >> 7;
+                const uint32_t bytes = 2u * (kPBytes + (uint32_t)q_rows * 128u + (uint32_t)(1 + q_groups) * sf_bytes);
+                for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+                    const uint32_t s = it % kStages, ph = (it / kStages) & 1u;
+                    if (!wait_bounded(smem_u32(&bar_empty[s]), ph ^ 1u, abort, args.timeout_ns, args.status, 41)) {
+                        ok = false;
+                        break;
+                    }
+                    if (args.fault == 1 && it == 0) continue;  // test hook: stage never filled
+                    const uint32_t full_local = smem_u32(&bar_full[s]);
+                    const uint32_t full = map_to_cta(full_local, 0);
+                    if (leader) mbar_arrive_expect_tx(full_local, bytes);
+                    const uint32_t sf = sSF + s * kSfBytes;
+                    if constexpr (kGated)
+                        tma_load_4d_pair(sP + s * kPBytes, &tmP, full, kb * kBK, 0, 0,
+                                         (w.expert * args.p_expert_rows + f_row) / 8);
+                    else
+                        tma_load_2d_pair(sP + s * kPBytes, &tmP, full, kb * kBK,
+                                         w.expert * args.p_expert_rows + f_row);
+                    tma_load_2d_pair(sQ + s * kQBytes, q_map, full, kb * kBK, q_row);
+                    // rows of 128 bytes, four to a chunk
+                    tma_load_2d_pair(sf, &tmSP, full, 0, (pg * fargs.sets + kb * sf_sets) * 4);
+                    for (int h = 0; h < q_groups; ++h)
+                        tma_load_2d_pair(sf + (1 + h) * kSfGroup, &tmSQ, full, 0,
+                                         ((w.krow + h) * fargs.sets + kb * sf_sets) * 4);
+                }
+            }
+            if (!ok && leader) {
+                // The leader's full barriers count both CTAs' copies: let those in flight land.
+                const uint32_t first = it > (uint32_t)kStages ? it - kStages : 0;
+                for (uint32_t i = first; i < it; ++i) {
+                    if (args.fault == 1 && i == 0) continue;
+                    wait_drain(smem_u32(&bar_full[i % kStages]), (i / kStages) & 1u, ffn::kDrainNs);
+                }
+            } else if (!ok) {
+                // The peer's copies complete on the leader's barriers, which it cannot observe:
+                // give them a fixed, bounded time to land before this CTA may exit.
+                const uint64_t t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < ffn::kPeerSettleNs) __nanosleep(1000);
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------ MMA issuer (leader CTA) ------------------------------
+        if (lane == 0 && leader) {
+            const uint64_t p_desc0 = smem_desc_sw128(sP, 16, 1024);
+            const uint64_t q_desc0 = smem_desc_sw128(sQ, 16, 1024);
+            const uint32_t p_hi = (uint32_t)(p_desc0 >> 32), q_hi = (uint32_t)(q_desc0 >> 32);
+            const uint32_t sf_ring = (uint32_t)fargs.sf_stages;
+            uint32_t it = 0, acc = 0, sf_slot = 0;
+            int before = 0;  // rows of the tile before
+            bool ok = true, issued = false;
+            Item w;
+            for (int t = pair; ok && item_of<kMode, kGated>(args, t, seg_tiles, w); t += num_pairs) {
+                const uint32_t b = acc & 1u, aph = (acc >> 1) & 1u;
+                ok = wait_bounded(smem_u32(&bar_tempty[b]), aph ^ 1u, abort, args.timeout_ns, args.status, 42);
+                if (ok && before + w.n > fargs.acc_top) {  // the columns of the tile before: wait until they are read
+                    const uint32_t j = acc - 1;
+                    ok = wait_bounded(smem_u32(&bar_tempty[j & 1u]), (j >> 1) & 1u, abort, args.timeout_ns,
+                                      args.status, 45);
+                }
+                if (!ok) break;
+                before = w.n;
+                tc_fence_after_sync();
+                const uint32_t idesc = idesc_f4(fargs.mx, 256, w.n, 0);
+                const uint32_t d_tmem = tmem_base + acc_col(b, w.n);
+                // the tile's first row may be the 64th of its scale group: two columns in
+                const uint32_t q_off = kSegRows ? 0u : (uint32_t)((w.r0 & 127) >> 5);
+                const int q_groups = (w.n + (int)q_off * 32 + 127) >> 7;
+                for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+                    const uint32_t s = it % kStages;
+                    if (!wait_bounded(smem_u32(&bar_full[s]), (it / kStages) & 1u, abort, args.timeout_ns,
+                                      args.status, 43)) {
+                        ok = false;
+                        break;
+                    }
+                    if (it >= sf_ring) {  // the MMAs that read this stage's scale columns are done
+                        const uint32_t o = it - sf_ring;
+                        if (!wait_bounded(smem_u32(&bar_empty[o % kStages]), (o / kStages) & 1u, abort,
+                                          args.timeout_ns, args.status, 47)) {
+                            ok = false;
+                            break;
+                        }
+                    }
+                    tc_fence_after_sync();
+                    const uint32_t sf = sSF + s * kSfBytes;
+                    const uint32_t col = tmem_base + (uint32_t)fargs.acc_top + sf_slot * kSfStage;
+                    if (++sf_slot == sf_ring) sf_slot = 0;
+                    const uint32_t p_lo = (uint32_t)p_desc0 + s * (uint32_t)(kPBytes >> 4);
+                    const uint32_t q_lo = (uint32_t)q_desc0 + s * (uint32_t)(kQBytes >> 4);
+                    const int steps = min(4, (args.red - kb * kBK + 15) / 16);  // 64-element steps that hold data
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        if (c < sf_sets) {
+                            tmem_cp_32x128b_x4_cta2(col + c * kSfSet, smem_desc_plain(sf + c * 512, 128, 128));
+                            tmem_cp_32x128b_x4_cta2(col + c * kSfSet + 4,
+                                                    smem_desc_plain(sf + kSfGroup + c * 512, 128, 128));
+                            if (q_groups > 1)
+                                tmem_cp_32x128b_x4_cta2(col + c * kSfSet + 8,
+                                                        smem_desc_plain(sf + 2 * kSfGroup + c * 512, 128, 128));
+                        }
+                    }
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        if (kk < steps) {
+                            const uint64_t pd = ((uint64_t)p_hi << 32) | (p_lo + 2u * kk);
+                            const uint64_t qd = ((uint64_t)q_hi << 32) | (q_lo + 2u * kk);
+                            const uint32_t more = (kb != w.kb0 || kk != 0) ? 1u : 0u;
+                            if (fargs.mx) {
+                                const uint32_t id = (uint32_t)(kk & 1) * 2u;
+                                const uint32_t sfp = col + (kk >> 1) * kSfSet;
+                                mma_mxf4_cta2(d_tmem, pd, qd, idesc | (id << 4) | (id << 29), sfp,
+                                              sfp + 4 + q_off, more);
+                            } else {
+                                const uint32_t sfp = col + kk * kSfSet;
+                                mma_nvf4_cta2(d_tmem, pd, qd, idesc, sfp, sfp + 4 + q_off, more);
+                            }
+                        }
+                    }
+                    issued = true;
+                    mma_commit_cta2_both(smem_u32(&bar_empty[s]));  // stage free in both CTAs
+                }
+                if (!ok) break;
+                mma_commit_cta2_both(smem_u32(&bar_tfull[b]));
+                ++acc;
+            }
+            if (!ok && issued) {
+                mma_commit_cta2(smem_u32(&bar_drain));
+                wait_drain(smem_u32(&bar_drain), 0, ffn::kDrainNs);
+            }
+        }
+    } else {
+        // ------------------------------ epilogue (warps 2..9, both CTAs) ---------------------
+        const int q = warp & 3, turn = (warp - 2) >> 2;
+        const uint32_t slot = base + kStages * kStageBytes + (uint32_t)(warp - 2) * (2 * kSlot);
+        uint32_t acc = 0;
+        bool warm = true;
+        Item w;
+        for (int t = pair; item_of<kMode, kGated>(args, t, seg_tiles, w); t += num_pairs) {
+            const uint32_t b = acc & 1u, aph = (acc >> 1) & 1u;
+            ++acc;
+            const int total = w.valid + w.zeros;
+            const int chunks = (total + 31) / 32;
+            Place place;
+            place.f = kGated ? w.f0 + (int)rank * 64 + q * 16 : w.f0 + (int)rank * 128 + q * 32;
+            place.out_base = 0;
+            place.piece = 0;
+            auto at_chunk = [&](int c) {
+                place.row = (int64_t)w.r0 + c * 32;
+                place.valid = min(32, w.valid - c * 32);
+                place.rows = min(32, total - c * 32);
+            };
+            // bias and factor of the thread's 4 lanes (feats is a multiple of 8, so octets are whole)
+            float bias[4], gp[4];
+#pragma unroll
+            for (int o = 0; o < 4; ++o) {
+                bias[o] = 0.0f;
+                gp[o] = 1.0f;
+                const int f = place.f + (lane >> 2) + (kGated ? (o >> 1) * 8 : o * 8);
+                if (f < args.feats) {
+                    const int64_t at = f + (kGated && (o & 1) ? args.feats : 0);
+                    if (args.bias) bias[o] = ffn::unpack2<kBF16>(static_cast<const uint16_t*>(args.bias)[at]).x;
+                    if (fargs.p_scale) gp[o] = fargs.p_scale[(int64_t)w.expert * args.p_expert_rows + at];
+                }
+            }
+            Ahead<kGated, false> ahead;
+            auto hand_back = [&]() {  // accumulator read: back to the MMA issuer
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(map_to_cta(smem_u32(&bar_tempty[b]), 0));
+            };
+            const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + acc_col(b, w.n);
+            const bool empty = w.kb0 == w.kb1;  // no K-block: the sum is zero
+            const int blocks = args.tile_n / 32;
+            const int64_t quarter = ((int64_t)w.tile * 2 + rank) * 4 + q;
+            // the passes of gemm16_ffn.cuh's epilogue: a first one of no rows that fetches its instructions,
+            // the sums of a whole tile, those of a piece, and all pieces' sums
+            constexpr int kWarm = 0, kWhole = 1, kPiece = 2, kJoin = 3;
+            const int main_pass = w.split < 0 ? kWhole : kPiece;
+            int pass = warm ? kWarm : main_pass;
+            bool gave_up = false;
+#pragma unroll 1
+            while (true) {
+                if (pass == kWhole || pass == kPiece) {
+                    if (pass == kWhole && turn < chunks) {
+                        at_chunk(turn);
+                        ffn::fetch_ahead<kGated, false>(args, place, slot, lane, ahead);
+                    }
+                    int ok = 1;
+                    if (lane == 0)
+                        ok = wait_bounded<false, true>(smem_u32(&bar_tfull[b]), aph, abort, args.timeout_ns,
+                                                       args.status, 44);
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (!ok) {
+                        gave_up = true;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    if (turn >= chunks) hand_back();
+                }
+                const int end = pass == kWarm ? turn + 1 : chunks;
+#pragma unroll 1
+                for (int c = turn; c < end; c += 2) {
+                    float v[4][8];
+                    at_chunk(c);
+                    if (pass == kWhole || pass == kPiece) {
+                        tmem_load_fragment32(taddr + c * 32, v);
+                        if (c + 2 >= chunks) hand_back();
+                        if (empty) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i / 8][i % 8] = 0.0f;
+                        }
+                        if (pass == kPiece) {
+                            float4* const d = reinterpret_cast<float4*>(
+                                args.partial + ((quarter * args.splits + w.split) * blocks + c) * 1024) + lane;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (8 * k < place.valid) {
+                                    d[(2 * k) * 32] = make_float4(v[0][2 * k], v[0][2 * k + 1], v[1][2 * k], v[1][2 * k + 1]);
+                                    d[(2 * k + 1) * 32] = make_float4(v[2][2 * k], v[2][2 * k + 1], v[3][2 * k], v[3][2 * k + 1]);
+                                }
+                            continue;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i / 8][i % 8] = 0.0f;
+                        if (pass == kWarm)
+                            place.valid = place.rows = 0;
+                        else
+                            ffn::fetch_ahead<kGated, false>(args, place, slot, lane, ahead);
+                        const float4* d = reinterpret_cast<const float4*>(
+                            args.partial + (quarter * args.splits * blocks + c) * 1024) + lane;
+                        const int pieces = pass == kWarm ? 0 : args.splits;
+#pragma unroll 4
+                        for (int s = 0; s < pieces; ++s, d += blocks * 256) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (8 * k < place.valid) {
+                                    const float4 lo = ld_global_cg_f4(d + (2 * k) * 32);
+                                    const float4 hi = ld_global_cg_f4(d + (2 * k + 1) * 32);
+                                    v[0][2 * k] += lo.x;
+                                    v[0][2 * k + 1] += lo.y;
+                                    v[1][2 * k] += lo.z;
+                                    v[1][2 * k + 1] += lo.w;
+                                    v[2][2 * k] += hi.x;
+                                    v[2][2 * k + 1] += hi.y;
+                                    v[3][2 * k] += hi.z;
+                                    v[3][2 * k + 1] += hi.w;
+                                }
+                        }
+                    }
+                    // the factors of features and rows
+                    {
+                        const int tr = 2 * (lane & 3);  // the thread's rows: 8 b + tr + i
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int r = 8 * (k >> 1) + tr + (k & 1);
+                            const float gq = fargs.q_scale && r < place.valid ? fargs.q_scale[place.row + r] : 1.0f;
+#pragma unroll
+                            for (int o = 0; o < 4; ++o) v[o][k] = v[o][k] * gp[o] * gq;
+                        }
+                    }
+                    const Place here = place;
+                    ffn::finish_block<kBF16, kMode, kGated, false>(args, v, bias, here, ahead, slot, lane, [&]() {
+                        if (pass == kWhole && c + 2 < chunks) {
+                            at_chunk(c + 2);
+                            ffn::fetch_ahead<kGated, false>(args, place, slot, lane, ahead);
+                        }
+                    });
+                }
+                if (pass == kWarm) {
+                    warm = false;
+                    pass = main_pass;
+                    continue;
+                }
+                if (pass != kPiece || turn >= chunks) break;
+                uint32_t* const counter = args.counters + ((int64_t)w.tile * 2 + rank) * kEpWarps + (warp - 2);
+                __threadfence();  // this lane's pieces are visible before the count
+                __syncwarp();
+                uint32_t before = 0;
+                if (lane == 0) before = atomicAdd(counter, 1u);
+                before = __shfl_sync(0xffffffffu, before, 0);
+                if (before != (uint32_t)args.splits - 1) break;
+                __threadfence();  // and the others' before this warp reads them
+                if (lane == 0) *counter = 0u;
+                pass = kJoin;
+            }
+            if (gave_up) break;
+        }
+    }
+
+    // ------------------------------ teardown ------------------------------
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_sync();  // no CTA leaves while its peer may still signal its barriers
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after_sync();
+        tmem_dealloc<2>(tmem_base, kTmemCols);
+    }
+}
+
+}  // namespace dtc

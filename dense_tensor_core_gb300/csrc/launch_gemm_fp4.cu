@@ -1,0 +1,45 @@
+// launch_gemm_fp4.cu -- the 4-bit products (gemm_fp4.cuh): one matrix and experts' rows, plain and gated.
+#include "fp4_host.h"
+
+namespace dtc_host {
+
+namespace {
+
+// Chunks of scales as rows of 128 bytes; a box: the sets of a stage of one group.
+int scales_tmap(CUtensorMap* m, const void* p, uint64_t chunks, int sets, const char* name) {
+    return make_tmap(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p, 128, chunks * 4, 128, 128, 4 * sets,
+                     CU_TENSOR_MAP_SWIZZLE_NONE, name);
+}
+
+template <bool kBF16, int kMode, bool kGated>
+int go(const Fp4Call& c, DeviceInfo* dev, cudaStream_t stream) {
+    CUtensorMap tp = {}, sp = {}, sq = {};
+    dtc::FfnQMaps tq = {};
+    const int sets = c.args.mx ? 2 : 4;
+    int rc = ffn_tmaps(c.ffn, &tp, &tq);
+    if (rc) return rc;
+    if (c.ffn.red > 0 && ((rc = scales_tmap(&sp, c.p_scales, c.p_chunks, sets, "scales of the features")) ||
+                          (rc = scales_tmap(&sq, c.q_scales, c.q_chunks, sets, "scales of the rows"))))
+        return rc;
+    auto kern = dtc::gemm_fp4_kernel<kBF16, kMode, kGated>;
+    if ((rc = ensure_smem_attr(kern, dtc::gf4::kSmemBytes, dev))) return rc;
+    dtc::Fp4Args a = c.args;
+    a.e = c.ffn.args;
+    return launch_chain(kern, dim3(c.ffn.grid), dtc::ffn::kThreads, dtc::gf4::kSmemBytes, 2, stream, tp, tq, sp,
+                        sq, a);
+}
+
+template <bool kBF16>
+int mode_of(const Fp4Call& c, DeviceInfo* dev, cudaStream_t s) {
+    using namespace dtc::ffn;
+    if (c.ffn.mode == kRows) return c.ffn.gated ? go<kBF16, kRows, true>(c, dev, s) : go<kBF16, kRows, false>(c, dev, s);
+    return c.ffn.gated ? go<kBF16, kSeg, true>(c, dev, s) : go<kBF16, kSeg, false>(c, dev, s);
+}
+
+}  // namespace
+
+int launch_gemm_fp4(const Fp4Call& c, DeviceInfo* dev, cudaStream_t stream) {
+    return c.ffn.bf16 ? mode_of<true>(c, dev, stream) : mode_of<false>(c, dev, stream);
+}
+
+}  // namespace dtc_host

@@ -477,6 +477,30 @@ __device__ __forceinline__ void mma_mxf8_cta2(uint32_t d_tmem, uint64_t adesc, u
         : "memory");
 }
 
+// Packed e2m1 operands at the 4-bit rate, M = 256 over the CTA pair, K = 64 (32 bytes of a row): NVFP4 with
+// a UE4M3 scale per 16 elements (scale_vec::4X: a set's four bytes), and MXFP4 with an E8M0 scale per 32
+// (scale_vec::2X: the half of a set that the instruction descriptor's scale id 0 or 2 names).
+__device__ __forceinline__ void mma_nvf4_cta2(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_mxf4_cta2(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+}
+
 // Arrive once on `bar` (own CTA) when every tcgen05 op issued so far by this thread completes.
 __device__ __forceinline__ void mma_commit_cta1(uint32_t bar) {
     asm volatile(
@@ -665,6 +689,14 @@ __host__ __device__ constexpr uint32_t idesc_f16(bool bf16, bool b_mn_major, int
 __host__ __device__ constexpr uint32_t idesc_mxf8(int M, int N, uint32_t sfa_id, uint32_t sfb_id) {
     return ((sfb_id & 3u) << 4) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
            ((uint32_t)(M >> 4) << 24) | ((sfa_id & 3u) << 29);
+}
+
+// Instruction descriptor, kind::mxf4 and kind::mxf4nvf4: B scale id (bits 4-5: 0 or 2), A/B format e2m1 = 1
+// (bits 7-9, 10-11), K-major A and B, N >> 3 (bits 17-22), scale format (bit 23: 0 = UE4M3, 1 = UE8M0),
+// M >> 7 (bits 27-28), A scale id (bits 29-30), K = 64 (bit 31 = 0).
+__host__ __device__ constexpr uint32_t idesc_f4(bool ue8m0, int M, int N, uint32_t sf_id) {
+    return ((sf_id & 3u) << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((ue8m0 ? 1u : 0u) << 23) |
+           ((uint32_t)(M >> 7) << 27) | ((sf_id & 3u) << 29);
 }
 
 }  // namespace dtc
