@@ -17,7 +17,11 @@
 //     stage in flight (4 for P and 8 for Q per set, up to 4 sets). A tile that does touch its predecessor's
 //     columns waits until those are read.
 //   - The scales of a stage may be overwritten when the MMAs that read them are done: the barrier that frees
-//     that stage's shared memory says so too, and the issuing thread waits for it, sf_stages stages behind.
+//     that stage's shared memory says so too. An eleventh warp waits for it, sf_stages stages behind, and then
+//     arrives on the full barrier of the stage that takes the columns, so that the issuing thread waits once
+//     a stage. That thread is what bounds tiles of few rows: four MMAs of 128 rows take 256 cycles, and a stage
+//     350 to 400 of issue (a wait is about 115, a copy of scales 7 to 14, an MMA 43), so two stages are
+//     unrolled and the next stage's barrier is looked at before the MMAs of this one.
 #pragma once
 
 #include "gemm16_ffn.cuh"
@@ -39,7 +43,7 @@ namespace gf4 {
 using ffn::kEpBytes;
 using ffn::kEpWarps;
 using ffn::kSlot;
-using ffn::kThreads;
+constexpr int kThreads = ffn::kThreads + 32;
 constexpr int kBK = 64;  // 16-bit words (256 elements) per stage
 constexpr int kStages = 5;
 constexpr int kPBytes = 128 * 128;
@@ -101,15 +105,110 @@ __device__ __forceinline__ bool item_of(const FfnArgs& a, int t, int seg_tiles, 
     w.kb1 = split >= 0 ? min(kb, w.kb0 + a.kb_per_split) : kb;
     return true;
 }
+// What a block's epilogue reads from memory, fetched ahead of its sums: the residual, and the factors of the
+// thread's 8 rows.
+template <bool kGated>
+struct Ahead {
+    uint4 res[kGated ? 2 : 4];
+    float gq[8];
+};
+template <bool kGated>
+__device__ __forceinline__ void fetch_ahead(const Fp4Args& f, const ffn::Place& p, uint32_t slot, int lane,
+                                            Ahead<kGated>& x) {
+    if (f.e.residual)
+        ffn::Block<kGated ? 2 : 4>(slot, lane).fetch(
+            x.res, static_cast<const uint16_t*>(f.e.residual) + p.row * f.e.ld_res + p.f, f.e.ld_res, p.valid,
+            f.e.feats - p.f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const int r = 8 * (k >> 1) + 2 * (lane & 3) + (k & 1);
+        x.gq[k] = f.q_scale && r < p.valid ? f.q_scale[p.row + r] : 1.0f;
+    }
+}
+
+// act() of all of a thread's values (gated: of the gates, each times its up value), one branch for all: the
+// epilogue's instructions of one activation lie together.
+template <bool kGated, int kAct>
+__device__ __forceinline__ void act_block(float (&v)[4][8]) {
+#pragma unroll
+    for (int o = 0; o < 4; o += kGated ? 2 : 1) {
+        act_forward(v[o], kAct);
+        if constexpr (kGated) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[o][k] *= v[o + 1][k];
+        }
+    }
+}
+
+// Finishes one 32-row block of sums v: factors and bias of the thread's 4 accumulator lanes, activation,
+// residual, store. `x` goes into the slots first, then `refill` may fetch the next block's into it.
+template <bool kBF16, int kMode, bool kGated, typename Refill>
+__device__ __forceinline__ void finish_block(const Fp4Args& fa, float (&v)[4][8], const float (&gp)[4],
+                                             const float (&bias)[4], const ffn::Place& p, Ahead<kGated>& x,
+                                             uint32_t slot, int lane, Refill refill) {
+    using ffn::Block;
+    const FfnArgs& a = fa.e;
+    const int left = a.feats - p.f;
+    const int tr = 2 * (lane & 3);  // the thread's rows: 8 b + tr + i
+#pragma unroll
+    for (int o = 0; o < 4; ++o)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[o][k] = fmaf(v[o][k], gp[o] * x.gq[k], bias[o]);
+    if constexpr (kMode == ffn::kSeg && !kGated) {
+        if (a.out_f32) {
+            refill();
+            ffn::Sums<4>::store([&](int o, int k) { return v[o][k]; }, slot, lane,
+                                static_cast<float*>(a.out) + p.row * a.ld_out + p.f, a.ld_out, p.valid, left);
+            return;
+        }
+    }
+    uint16_t* const out = static_cast<uint16_t*>(a.out) + p.row * a.ld_out + p.f;
+    if (a.residual) {
+        __syncwarp();  // the slot has been read
+        Block<kGated ? 2 : 4>(slot + kSlot, lane).put(x.res);
+        __syncwarp();
+    }
+    refill();
+    if constexpr (kGated) {
+        if (a.act == kActSwiglu)
+            act_block<true, kActSilu>(v);
+        else
+            act_block<true, kActGelu>(v);
+    } else if (a.act != kActNone) {
+        if (a.act == kActRelu)
+            act_block<false, kActRelu>(v);
+        else if (a.act == kActGelu)
+            act_block<false, kActGelu>(v);
+        else if (a.act == kActGeluTanh)
+            act_block<false, kActGeluTanh>(v);
+        else
+            act_block<false, kActSilu>(v);
+    }
+    constexpr int kStep = kGated ? 2 : 1;
+    if (a.residual)
+        Block<kGated ? 2 : 4>(slot + kSlot, lane).template take<kBF16>([&](int o, int k, float r) {
+            v[kStep * o][k] += r;
+        });
+    if constexpr (kMode == ffn::kSeg) {
+        if (p.rows > p.valid) {  // an expert's gap rows: zeros
+#pragma unroll
+            for (int o = 0; o < 4; o += kStep)
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (8 * (k >> 1) + tr + (k & 1) >= p.valid) v[o][k] = 0.0f;
+        }
+    }
+    Block<kGated ? 2 : 4>(slot, lane).template store<kBF16>([&](int o, int k) { return v[kStep * o][k]; }, out,
+                                                            a.ld_out, p.rows, left);
+}
 }  // namespace gf4
 
 template <bool kBF16, int kMode, bool kGated>
-__global__ void __launch_bounds__(ffn::kThreads, 1)
+__global__ void __launch_bounds__(gf4::kThreads, 1)
     gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ FfnQMaps tmQ,
                     const __grid_constant__ CUtensorMap tmSP, const __grid_constant__ CUtensorMap tmSQ,
                     const Fp4Args fargs) {
     using namespace gf4;
-    using ffn::Ahead;
     using ffn::Item;
     using ffn::Place;
     constexpr bool kSegRows = kMode == ffn::kSeg;
@@ -137,7 +236,7 @@ __global__ void __launch_bounds__(ffn::kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(smem_u32(&bar_full[s]), 1);
+            mbar_init(smem_u32(&bar_full[s]), 2);  // the leader's: its producer, the scales' columns
             mbar_init(smem_u32(&bar_empty[s]), 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -174,7 +273,7 @@ __global__ void __launch_bounds__(ffn::kThreads, 1)
 
     if (warp == 0) {
         // ------------------------------ TMA producer (both CTAs) ------------------------------
-        if (lane == 0) {
+        if (elect_one()) {
             uint32_t it = 0;
             bool ok = true;
             Item w;
@@ -231,12 +330,12 @@ __global__ void __launch_bounds__(ffn::kThreads, 1)
         }
     } else if (warp == 1) {
         // ------------------------------ MMA issuer (leader CTA) ------------------------------
-        if (lane == 0 && leader) {
+        if (leader && elect_one()) {
             const uint64_t p_desc0 = smem_desc_sw128(sP, 16, 1024);
             const uint64_t q_desc0 = smem_desc_sw128(sQ, 16, 1024);
             const uint32_t p_hi = (uint32_t)(p_desc0 >> 32), q_hi = (uint32_t)(q_desc0 >> 32);
             const uint32_t sf_ring = (uint32_t)fargs.sf_stages;
-            uint32_t it = 0, acc = 0, sf_slot = 0;
+            uint32_t acc = 0, sf_slot = 0, s = 0, ph = 0;
             int before = 0;  // rows of the tile before
             bool ok = true, issued = false;
             Item w;
@@ -256,20 +355,12 @@ __global__ void __launch_bounds__(ffn::kThreads, 1)
                 // the tile's first row may be the 64th of its scale group: two columns in
                 const uint32_t q_off = kSegRows ? 0u : (uint32_t)((w.r0 & 127) >> 5);
                 const int q_groups = (w.n + (int)q_off * 32 + 127) >> 7;
-                for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
-                    const uint32_t s = it % kStages;
-                    if (!wait_bounded(smem_u32(&bar_full[s]), (it / kStages) & 1u, abort, args.timeout_ns,
-                                      args.status, 43)) {
+                bool ready = mbar_test_wait(smem_u32(&bar_full[s]), ph);
+#pragma unroll 2
+                for (int kb = w.kb0; kb < w.kb1; ++kb) {
+                    if (!ready && !wait_bounded(smem_u32(&bar_full[s]), ph, abort, args.timeout_ns, args.status, 43)) {
                         ok = false;
                         break;
-                    }
-                    if (it >= sf_ring) {  // the MMAs that read this stage's scale columns are done
-                        const uint32_t o = it - sf_ring;
-                        if (!wait_bounded(smem_u32(&bar_empty[o % kStages]), (o / kStages) & 1u, abort,
-                                          args.timeout_ns, args.status, 47)) {
-                            ok = false;
-                            break;
-                        }
                     }
                     tc_fence_after_sync();
                     const uint32_t sf = sSF + s * kSfBytes;
@@ -289,6 +380,8 @@ __global__ void __launch_bounds__(ffn::kThreads, 1)
                                                         smem_desc_plain(sf + 2 * kSfGroup + c * 512, 128, 128));
                         }
                     }
+                    const uint32_t ns = s + 1 == kStages ? 0 : s + 1, nph = s + 1 == kStages ? ph ^ 1u : ph;
+                    ready = mbar_test_wait(smem_u32(&bar_full[ns]), nph);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
                         if (kk < steps) {
@@ -306,8 +399,10 @@ __global__ void __launch_bounds__(ffn::kThreads, 1)
                             }
                         }
                     }
-                    issued = true;
                     mma_commit_cta2_both(smem_u32(&bar_empty[s]));  // stage free in both CTAs
+                    issued = true;
+                    s = ns;
+                    ph = nph;
                 }
                 if (!ok) break;
                 mma_commit_cta2_both(smem_u32(&bar_tfull[b]));
@@ -317,6 +412,29 @@ __global__ void __launch_bounds__(ffn::kThreads, 1)
                 mma_commit_cta2(smem_u32(&bar_drain));
                 wait_drain(smem_u32(&bar_drain), 0, ffn::kDrainNs);
             }
+        }
+    } else if (warp == 2 + kEpWarps) {
+        // ------------------------------ scales' columns (leader CTA) ---------------------------
+        if (leader && elect_one()) {
+            const uint32_t ring = (uint32_t)fargs.sf_stages;
+            uint32_t it = 0, s = 0, os = 0, oph = 0;
+            bool ok = true;
+            Item w;
+            for (int t = pair; ok && item_of<kMode, kGated>(args, t, seg_tiles, w); t += num_pairs)
+                for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+                    if (it >= ring) {
+                        if (!wait_bounded(smem_u32(&bar_empty[os]), oph, abort, args.timeout_ns, args.status, 47)) {
+                            ok = false;
+                            break;
+                        }
+                        if (++os == kStages) {
+                            os = 0;
+                            oph ^= 1u;
+                        }
+                    }
+                    mbar_arrive(smem_u32(&bar_full[s]));
+                    if (++s == kStages) s = 0;
+                }
         }
     } else {
         // ------------------------------ epilogue (warps 2..9, both CTAs) ---------------------
@@ -352,11 +470,11 @@ __global__ void __launch_bounds__(ffn::kThreads, 1)
                     if (fargs.p_scale) gp[o] = fargs.p_scale[(int64_t)w.expert * args.p_expert_rows + at];
                 }
             }
-            Ahead<kGated, false> ahead;
+            Ahead<kGated> ahead;
             auto hand_back = [&]() {  // accumulator read: back to the MMA issuer
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(map_to_cta(smem_u32(&bar_tempty[b]), 0));
+                if (lane == 0) mbar_arrive_remote(map_to_cta(smem_u32(&bar_tempty[b]), 0));
             };
             const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + acc_col(b, w.n);
             const bool empty = w.kb0 == w.kb1;  // no K-block: the sum is zero
@@ -373,7 +491,7 @@ __global__ void __launch_bounds__(ffn::kThreads, 1)
                 if (pass == kWhole || pass == kPiece) {
                     if (pass == kWhole && turn < chunks) {
                         at_chunk(turn);
-                        ffn::fetch_ahead<kGated, false>(args, place, slot, lane, ahead);
+                        fetch_ahead<kGated>(fargs, place, slot, lane, ahead);
                     }
                     int ok = 1;
                     if (lane == 0)
@@ -416,7 +534,7 @@ __global__ void __launch_bounds__(ffn::kThreads, 1)
                         if (pass == kWarm)
                             place.valid = place.rows = 0;
                         else
-                            ffn::fetch_ahead<kGated, false>(args, place, slot, lane, ahead);
+                            fetch_ahead<kGated>(fargs, place, slot, lane, ahead);
                         const float4* d = reinterpret_cast<const float4*>(
                             args.partial + (quarter * args.splits * blocks + c) * 1024) + lane;
                         const int pieces = pass == kWarm ? 0 : args.splits;
@@ -438,22 +556,11 @@ __global__ void __launch_bounds__(ffn::kThreads, 1)
                                 }
                         }
                     }
-                    // the factors of features and rows
-                    {
-                        const int tr = 2 * (lane & 3);  // the thread's rows: 8 b + tr + i
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int r = 8 * (k >> 1) + tr + (k & 1);
-                            const float gq = fargs.q_scale && r < place.valid ? fargs.q_scale[place.row + r] : 1.0f;
-#pragma unroll
-                            for (int o = 0; o < 4; ++o) v[o][k] = v[o][k] * gp[o] * gq;
-                        }
-                    }
                     const Place here = place;
-                    ffn::finish_block<kBF16, kMode, kGated, false>(args, v, bias, here, ahead, slot, lane, [&]() {
+                    finish_block<kBF16, kMode, kGated>(fargs, v, gp, bias, here, ahead, slot, lane, [&]() {
                         if (pass == kWhole && c + 2 < chunks) {
                             at_chunk(c + 2);
-                            ffn::fetch_ahead<kGated, false>(args, place, slot, lane, ahead);
+                            fetch_ahead<kGated>(fargs, place, slot, lane, ahead);
                         }
                     });
                 }

@@ -25,7 +25,7 @@ int go(const Fp4Call& c, DeviceInfo* dev, cudaStream_t stream) {
     if ((rc = ensure_smem_attr(kern, dtc::gf4::kSmemBytes, dev))) return rc;
     dtc::Fp4Args a = c.args;
     a.e = c.ffn.args;
-    return launch_chain(kern, dim3(c.ffn.grid), dtc::ffn::kThreads, dtc::gf4::kSmemBytes, 2, stream, tp, tq, sp,
+    return launch_chain(kern, dim3(c.ffn.grid), dtc::gf4::kThreads, dtc::gf4::kSmemBytes, 2, stream, tp, tq, sp,
                         sq, a);
 }
 

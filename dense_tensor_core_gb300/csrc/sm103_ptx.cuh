@@ -30,6 +30,19 @@ __device__ __forceinline__ uint32_t lane_id() {
     return l;
 }
 
+// One thread of a warp whose lanes all run this (true in that thread). Code under it may issue tcgen05 and
+// TMA instructions with one operand set: under a test of the lane number the compiler cannot know that one
+// thread is left, and wraps each in a loop over the threads (some 100 cycles an instruction).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(p));
+    return p != 0;
+}
+
 // ---------------------------------------------------------------------------------------------
 // Clusters
 // ---------------------------------------------------------------------------------------------
@@ -144,11 +157,31 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
                  : "memory");
 }
 
+// The same with the default ordering (this CTA's): for arrivals that publish no memory, such as that a
+// Tensor Memory accumulator has been read (the loads are complete, see tcgen05.wait::ld). The form above
+// waits until the thread's earlier global stores are visible to the cluster, some 1500 cycles.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// A look at the barrier that does not suspend the thread.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}\n"
         : "=r"(ok)
         : "r"(bar), "r"(parity)
