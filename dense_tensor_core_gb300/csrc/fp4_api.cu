@@ -267,7 +267,7 @@ void apply_plan(const Fp4Plan& p, void* counters, void* partial, Fp4Call* c) {
         a.counters = static_cast<uint32_t*>(counters);
         a.partial = static_cast<float*>(partial);
     }
-    const bool narrow = p.tile_n <= dtc::gf4::kNarrow;
+    const bool narrow = p.tile_n <= dtc::gf4::kNarrow || 2 * p.tile_n > dtc::gf4::kWideTop;
     c->args.acc_top = narrow ? 2 * dtc::gf4::kNarrow : dtc::gf4::kWideTop;
     c->args.sf_stages = narrow ? 4 : 2;
 }
@@ -350,7 +350,7 @@ int gemm_fp4(int dtype, const fp4_matrix* A, const fp4_matrix* B, void* C, const
     a.timeout_ns = timeout_of(o.timeout_ns);
     a.fault = o.fault_inject;
     a.status = info->status;
-    c.args.mx = A->format == FP4_MXFP4;
+    c.mx = A->format == FP4_MXFP4;
     c.args.sets = (int)la.sets;
     c.args.p_groups = (int)lb.groups;
     c.args.p_scale = B->row_scale;
@@ -561,7 +561,7 @@ int moe_experts_fp4(int dtype, const void* x, const fp4_matrix* w_in, const fp4_
         a.timeout_ns = timeout_of(o.timeout_ns);
         a.fault = o.fault_inject;
         a.status = info->status;
-        c.args.mx = !nv;
+        c.mx = !nv;
         c.args.sets = (int)sets;
         c.args.p_groups = (int)l.groups;
         c.args.p_scale = w->row_scale;

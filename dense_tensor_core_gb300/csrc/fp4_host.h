@@ -19,6 +19,7 @@ int launch_fp4_pack(const dtc::fp4::PackArgs& a, DeviceInfo* dev, cudaStream_t s
 // A product of gemm_fp4.cuh: `ffn` describes the codes as 16-bit words (four elements each).
 struct Fp4Call {
     FfnCall ffn;
+    bool mx = false;
     dtc::Fp4Args args = {};  // (its e is ffn.args)
     const void* p_scales = nullptr;
     const void* q_scales = nullptr;

@@ -30,7 +30,6 @@ namespace dtc {
 
 struct Fp4Args {
     FfnArgs e;            // sizes, plan and epilogue; red = K / 4 (16-bit words of a row)
-    bool mx;              // MXFP4
     int sets;             // scale sets of a row
     int p_groups;         // scale groups of an expert's matrix of P
     const float* p_scale; // [experts][feats], gated [2 feats]; NULL = 1
@@ -54,7 +53,9 @@ constexpr int kStageBytes = kPBytes + kQBytes + kSfBytes;
 constexpr int kSmemBytes = kStages * kStageBytes + kEpBytes + 1024;
 constexpr int kTmemCols = 512;
 constexpr int kSfSet = 12, kSfStage = 4 * kSfSet;
-constexpr int kNarrow = 160;  // tiles of up to so many rows leave four stages of scales, others two
+// Tiles of up to so many rows leave four stages of scales beside two accumulators, and so do tiles whose
+// accumulators touch in any case; those between leave two.
+constexpr int kNarrow = 160;
 static_assert(kSmemBytes <= 227 * 1024 - 512, "shared memory budget");
 static_assert(2 * kNarrow + 4 * kSfStage <= kTmemCols, "Tensor Memory budget");
 constexpr int kWideTop = kTmemCols - 2 * kSfStage;
@@ -203,7 +204,7 @@ __device__ __forceinline__ void finish_block(const Fp4Args& fa, float (&v)[4][8]
 }
 }  // namespace gf4
 
-template <bool kBF16, int kMode, bool kGated>
+template <bool kMx, bool kBF16, int kMode, bool kGated>
 __global__ void __launch_bounds__(gf4::kThreads, 1)
     gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ FfnQMaps tmQ,
                     const __grid_constant__ CUtensorMap tmSP, const __grid_constant__ CUtensorMap tmSQ,
@@ -266,8 +267,8 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
     grid_launch_dependents();
     grid_dependency_wait();  // the set-up above overlaps the tail of the kernel before
     const int seg_tiles = kSegRows ? min(*args.num_tiles, args.max_tiles) : 0;
-    const int sf_sets = fargs.mx ? 2 : 4;  // of a stage
-    const uint32_t sf_bytes = (uint32_t)sf_sets * 512u;
+    constexpr int sf_sets = kMx ? 2 : 4;  // of a stage
+    constexpr uint32_t sf_bytes = sf_sets * 512u;
     // columns of an accumulator of n rows that the turn b takes
     auto acc_col = [&](uint32_t b, int n) { return b ? (uint32_t)(fargs.acc_top - n) : 0u; };
 
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
                 if (!ok) break;
                 before = w.n;
                 tc_fence_after_sync();
-                const uint32_t idesc = idesc_f4(fargs.mx, 256, w.n, 0);
+                const uint32_t idesc = idesc_f4(kMx, 256, w.n, 0);
                 const uint32_t d_tmem = tmem_base + acc_col(b, w.n);
                 // the tile's first row may be the 64th of its scale group: two columns in
                 const uint32_t q_off = kSegRows ? 0u : (uint32_t)((w.r0 & 127) >> 5);
@@ -370,15 +371,13 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
                     const uint32_t q_lo = (uint32_t)q_desc0 + s * (uint32_t)(kQBytes >> 4);
                     const int steps = min(4, (args.red - kb * kBK + 15) / 16);  // 64-element steps that hold data
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        if (c < sf_sets) {
-                            tmem_cp_32x128b_x4_cta2(col + c * kSfSet, smem_desc_plain(sf + c * 512, 128, 128));
-                            tmem_cp_32x128b_x4_cta2(col + c * kSfSet + 4,
-                                                    smem_desc_plain(sf + kSfGroup + c * 512, 128, 128));
-                            if (q_groups > 1)
-                                tmem_cp_32x128b_x4_cta2(col + c * kSfSet + 8,
-                                                        smem_desc_plain(sf + 2 * kSfGroup + c * 512, 128, 128));
-                        }
+                    for (int c = 0; c < sf_sets; ++c) {
+                        tmem_cp_32x128b_x4_cta2(col + c * kSfSet, smem_desc_plain(sf + c * 512, 128, 128));
+                        tmem_cp_32x128b_x4_cta2(col + c * kSfSet + 4,
+                                                smem_desc_plain(sf + kSfGroup + c * 512, 128, 128));
+                        if (q_groups > 1)
+                            tmem_cp_32x128b_x4_cta2(col + c * kSfSet + 8,
+                                                    smem_desc_plain(sf + 2 * kSfGroup + c * 512, 128, 128));
                     }
                     const uint32_t ns = s + 1 == kStages ? 0 : s + 1, nph = s + 1 == kStages ? ph ^ 1u : ph;
                     ready = mbar_test_wait(smem_u32(&bar_full[ns]), nph);
@@ -388,7 +387,7 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
                             const uint64_t pd = ((uint64_t)p_hi << 32) | (p_lo + 2u * kk);
                             const uint64_t qd = ((uint64_t)q_hi << 32) | (q_lo + 2u * kk);
                             const uint32_t more = (kb != w.kb0 || kk != 0) ? 1u : 0u;
-                            if (fargs.mx) {
+                            if constexpr (kMx) {
                                 const uint32_t id = (uint32_t)(kk & 1) * 2u;
                                 const uint32_t sfp = col + (kk >> 1) * kSfSet;
                                 mma_mxf4_cta2(d_tmem, pd, qd, idesc | (id << 4) | (id << 29), sfp,

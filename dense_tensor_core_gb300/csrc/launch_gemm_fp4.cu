@@ -11,22 +11,27 @@ int scales_tmap(CUtensorMap* m, const void* p, uint64_t chunks, int sets, const 
                      CU_TENSOR_MAP_SWIZZLE_NONE, name);
 }
 
-template <bool kBF16, int kMode, bool kGated>
-int go(const Fp4Call& c, DeviceInfo* dev, cudaStream_t stream) {
+template <bool kMx, bool kBF16, int kMode, bool kGated>
+int go_of(const Fp4Call& c, DeviceInfo* dev, cudaStream_t stream) {
     CUtensorMap tp = {}, sp = {}, sq = {};
     dtc::FfnQMaps tq = {};
-    const int sets = c.args.mx ? 2 : 4;
+    constexpr int sets = kMx ? 2 : 4;
     int rc = ffn_tmaps(c.ffn, &tp, &tq);
     if (rc) return rc;
     if (c.ffn.red > 0 && ((rc = scales_tmap(&sp, c.p_scales, c.p_chunks, sets, "scales of the features")) ||
                           (rc = scales_tmap(&sq, c.q_scales, c.q_chunks, sets, "scales of the rows"))))
         return rc;
-    auto kern = dtc::gemm_fp4_kernel<kBF16, kMode, kGated>;
+    auto kern = dtc::gemm_fp4_kernel<kMx, kBF16, kMode, kGated>;
     if ((rc = ensure_smem_attr(kern, dtc::gf4::kSmemBytes, dev))) return rc;
     dtc::Fp4Args a = c.args;
     a.e = c.ffn.args;
     return launch_chain(kern, dim3(c.ffn.grid), dtc::gf4::kThreads, dtc::gf4::kSmemBytes, 2, stream, tp, tq, sp,
                         sq, a);
+}
+
+template <bool kBF16, int kMode, bool kGated>
+int go(const Fp4Call& c, DeviceInfo* dev, cudaStream_t s) {
+    return c.mx ? go_of<true, kBF16, kMode, kGated>(c, dev, s) : go_of<false, kBF16, kMode, kGated>(c, dev, s);
 }
 
 template <bool kBF16>
