@@ -284,6 +284,13 @@ struct Block {
     template <bool kBF16, typename V>
     __device__ __forceinline__ void store(V v, uint16_t* out, int64_t ld, int rows, int feats) const {
         __syncwarp();  // the slot has been read
+        stage<kBF16>(v);
+        __syncwarp();
+        flush(out, ld, rows, feats);
+    }
+    // the fragments into the slot
+    template <bool kBF16, typename V>
+    __device__ __forceinline__ void stage(V v) const {
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
             if constexpr (kOct == 4) {
@@ -298,8 +305,6 @@ struct Block {
                                   packf2<kBF16>(v(1, 2 * b + 2), v(1, 2 * b + 3)));
             }
         }
-        __syncwarp();
-        flush(out, ld, rows, feats);
     }
     // the slot's rows to memory (as many passes of kPerPass rows)
     template <int kCount = kPasses>

@@ -106,12 +106,12 @@ __device__ __forceinline__ bool item_of(const FfnArgs& a, int t, int seg_tiles, 
     w.kb1 = split >= 0 ? min(kb, w.kb0 + a.kb_per_split) : kb;
     return true;
 }
-// What a block's epilogue reads from memory, fetched ahead of its sums: the residual, and the factors of the
-// thread's 8 rows.
+// What a block's epilogue reads from memory, fetched ahead of its sums: the residual, and the factor of the
+// lane's row.
 template <bool kGated>
 struct Ahead {
     uint4 res[kGated ? 2 : 4];
-    float gq[8];
+    float gq;
 };
 template <bool kGated>
 __device__ __forceinline__ void fetch_ahead(const Fp4Args& f, const ffn::Place& p, uint32_t slot, int lane,
@@ -120,11 +120,25 @@ __device__ __forceinline__ void fetch_ahead(const Fp4Args& f, const ffn::Place& 
         ffn::Block<kGated ? 2 : 4>(slot, lane).fetch(
             x.res, static_cast<const uint16_t*>(f.e.residual) + p.row * f.e.ld_res + p.f, f.e.ld_res, p.valid,
             f.e.feats - p.f);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const int r = 8 * (k >> 1) + 2 * (lane & 3) + (k & 1);
-        x.gq[k] = f.q_scale && r < p.valid ? f.q_scale[p.row + r] : 1.0f;
-    }
+    x.gq = f.q_scale && lane < p.valid ? f.q_scale[p.row + lane] : 1.0f;
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
 }
 
 // act() of all of a thread's values (gated: of the gates, each times its up value), one branch for all: the
@@ -142,33 +156,49 @@ __device__ __forceinline__ void act_block(float (&v)[4][8]) {
 }
 
 // Finishes one 32-row block of sums v: factors and bias of the thread's 4 accumulator lanes, activation,
-// residual, store. `x` goes into the slots first, then `refill` may fetch the next block's into it.
+// residual, store. The residual goes through the slot first, then `refill` may fetch the next block's. Whole
+// blocks leave by TMA (the slot's order of 16-byte pieces is the copy's swizzle); blocks that end inside an
+// expert's rows leave piece by piece. The slot may be reused when the copy of two blocks before has read it.
 template <bool kBF16, int kMode, bool kGated, typename Refill>
-__device__ __forceinline__ void finish_block(const Fp4Args& fa, float (&v)[4][8], const float (&gp)[4],
-                                             const float (&bias)[4], const ffn::Place& p, Ahead<kGated>& x,
-                                             uint32_t slot, int lane, Refill refill) {
-    using ffn::Block;
+__device__ __forceinline__ void finish_block(const Fp4Args& fa, const CUtensorMap* tmC, float (&v)[4][8],
+                                             const float (&gp)[4], const float (&bias)[4], const ffn::Place& p,
+                                             Ahead<kGated>& x, uint32_t slot, int lane, Refill refill) {
+    using Block = ffn::Block<kGated ? 2 : 4>;
     const FfnArgs& a = fa.e;
     const int left = a.feats - p.f;
     const int tr = 2 * (lane & 3);  // the thread's rows: 8 b + tr + i
 #pragma unroll
-    for (int o = 0; o < 4; ++o)
+    for (int b = 0; b < 4; ++b) {
+        const float2 gq = make_float2(__shfl_sync(0xffffffffu, x.gq, 8 * b + tr),
+                                      __shfl_sync(0xffffffffu, x.gq, 8 * b + tr + 1));
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[o][k] = fmaf(v[o][k], gp[o] * x.gq[k], bias[o]);
+        for (int o = 0; o < 4; ++o) {
+            const float2 z = fma2(make_float2(v[o][2 * b], v[o][2 * b + 1]), mul2(gq, make_float2(gp[o], gp[o])),
+                                  make_float2(bias[o], bias[o]));
+            v[o][2 * b] = z.x;
+            v[o][2 * b + 1] = z.y;
+        }
+    }
     if constexpr (kMode == ffn::kSeg && !kGated) {
-        if (a.out_f32) {
+        if (a.out_f32) {  // eight lanes hold 32 bytes of a row: whole sectors
             refill();
-            ffn::Sums<4>::store([&](int o, int k) { return v[o][k]; }, slot, lane,
-                                static_cast<float*>(a.out) + p.row * a.ld_out + p.f, a.ld_out, p.valid, left);
+            float* const out = static_cast<float*>(a.out) + (p.row + tr) * a.ld_out + p.f + (lane >> 2);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int r = 8 * (k >> 1) + (k & 1);
+                if (r + tr < p.valid) {
+#pragma unroll
+                    for (int o = 0; o < 4; ++o)
+                        if (8 * o < left) out[r * a.ld_out + 8 * o] = v[o][k];
+                }
+            }
             return;
         }
     }
-    uint16_t* const out = static_cast<uint16_t*>(a.out) + p.row * a.ld_out + p.f;
-    if (a.residual) {
-        __syncwarp();  // the slot has been read
-        Block<kGated ? 2 : 4>(slot + kSlot, lane).put(x.res);
-        __syncwarp();
-    }
+    if (lane == 0) bulk_wait_group_read<1>();
+    __syncwarp();
+    const Block blk(slot, lane);
+    if (a.residual) blk.put(x.res);
     refill();
     if constexpr (kGated) {
         if (a.act == kActSwiglu)
@@ -186,11 +216,14 @@ __device__ __forceinline__ void finish_block(const Fp4Args& fa, float (&v)[4][8]
             act_block<false, kActSilu>(v);
     }
     constexpr int kStep = kGated ? 2 : 1;
-    if (a.residual)
-        Block<kGated ? 2 : 4>(slot + kSlot, lane).template take<kBF16>([&](int o, int k, float r) {
-            v[kStep * o][k] += r;
-        });
+    if (a.residual) {
+        __syncwarp();
+        blk.template take<kBF16>([&](int o, int k, float r) { v[kStep * o][k] += r; });
+        __syncwarp();
+    }
+    bool whole = true;
     if constexpr (kMode == ffn::kSeg) {
+        whole = p.rows == 32;
         if (p.rows > p.valid) {  // an expert's gap rows: zeros
 #pragma unroll
             for (int o = 0; o < 4; o += kStep)
@@ -199,8 +232,18 @@ __device__ __forceinline__ void finish_block(const Fp4Args& fa, float (&v)[4][8]
                     if (8 * (k >> 1) + tr + (k & 1) >= p.valid) v[o][k] = 0.0f;
         }
     }
-    Block<kGated ? 2 : 4>(slot, lane).template store<kBF16>([&](int o, int k) { return v[kStep * o][k]; }, out,
-                                                            a.ld_out, p.rows, left);
+    blk.template stage<kBF16>([&](int o, int k) { return v[kStep * o][k]; });
+    if (whole) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && left > 0 && p.rows > 0) {
+            tma_store_2d(tmC, slot, p.f, (int)p.row);
+            bulk_commit_group();
+        }
+    } else {
+        __syncwarp();
+        blk.flush(static_cast<uint16_t*>(a.out) + p.row * a.ld_out + p.f, a.ld_out, p.rows, left);
+    }
 }
 }  // namespace gf4
 
@@ -208,7 +251,7 @@ template <bool kMx, bool kBF16, int kMode, bool kGated>
 __global__ void __launch_bounds__(gf4::kThreads, 1)
     gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ FfnQMaps tmQ,
                     const __grid_constant__ CUtensorMap tmSP, const __grid_constant__ CUtensorMap tmSQ,
-                    const Fp4Args fargs) {
+                    const __grid_constant__ CUtensorMap tmC, const Fp4Args fargs) {
     using namespace gf4;
     using ffn::Item;
     using ffn::Place;
@@ -438,7 +481,8 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
     } else {
         // ------------------------------ epilogue (warps 2..9, both CTAs) ---------------------
         const int q = warp & 3, turn = (warp - 2) >> 2;
-        const uint32_t slot = base + kStages * kStageBytes + (uint32_t)(warp - 2) * (2 * kSlot);
+        const uint32_t slots = base + kStages * kStageBytes + (uint32_t)(warp - 2) * (2 * kSlot);
+        uint32_t slot = slots;  // by turns
         uint32_t acc = 0;
         bool warm = true;
         Item w;
@@ -556,12 +600,13 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
                         }
                     }
                     const Place here = place;
-                    finish_block<kBF16, kMode, kGated>(fargs, v, gp, bias, here, ahead, slot, lane, [&]() {
+                    finish_block<kBF16, kMode, kGated>(fargs, &tmC, v, gp, bias, here, ahead, slot, lane, [&]() {
                         if (pass == kWhole && c + 2 < chunks) {
                             at_chunk(c + 2);
                             fetch_ahead<kGated>(fargs, place, slot, lane, ahead);
                         }
                     });
+                    slot = 2 * slots + kSlot - slot;
                 }
                 if (pass == kWarm) {
                     warm = false;
@@ -582,6 +627,8 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
             }
             if (gave_up) break;
         }
+        if (lane == 0) bulk_wait_group_read<0>();  // the copies have read their slots
+        __syncwarp();
     }
 
     // ------------------------------ teardown ------------------------------

@@ -21,12 +21,21 @@ int go_of(const Fp4Call& c, DeviceInfo* dev, cudaStream_t stream) {
     if (c.ffn.red > 0 && ((rc = scales_tmap(&sp, c.p_scales, c.p_chunks, sets, "scales of the features")) ||
                           (rc = scales_tmap(&sq, c.q_scales, c.q_chunks, sets, "scales of the rows"))))
         return rc;
+    CUtensorMap tc = {};
+    const dtc::FfnArgs& e = c.ffn.args;
+    if (!e.out_f32) {
+        // blocks of 32 rows and 32 features (gated 16), in the order of the epilogue's slots
+        rc = make_tmap(&tc, kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, e.out, e.feats,
+                       e.rows, e.ld_out, kGated ? 16 : 32, 32,
+                       kGated ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B, "the result");
+        if (rc) return rc;
+    }
     auto kern = dtc::gemm_fp4_kernel<kMx, kBF16, kMode, kGated>;
     if ((rc = ensure_smem_attr(kern, dtc::gf4::kSmemBytes, dev))) return rc;
     dtc::Fp4Args a = c.args;
     a.e = c.ffn.args;
     return launch_chain(kern, dim3(c.ffn.grid), dtc::gf4::kThreads, dtc::gf4::kSmemBytes, 2, stream, tp, tq, sp,
-                        sq, a);
+                        sq, tc, a);
 }
 
 template <bool kBF16, int kMode, bool kGated>
