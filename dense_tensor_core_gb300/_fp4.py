@@ -67,23 +67,29 @@ class Fp4:
     * codes [..., rows, K / 2] uint8: e2m1 codes, element k in the low nibble of byte k / 2 for even k;
     * scales uint8: the blocks' scales in the order in which the tensor cores take them;
     * row_scale [..., rows] fp32: the rows' factors (None: all 1);
-    * format "nvfp4" or "mxfp4"; gated: the scales are ordered for a gated product (gate rows first).
+    * shape; format "nvfp4" or "mxfp4"; gated: the scales are ordered for a gated product (gate rows first).
     """
 
-    __slots__ = ("codes", "scales", "row_scale", "format", "gated", "_parts")
+    __slots__ = ("shape", "format", "gated", "_parts", "_views")
 
     def __init__(self, codes, scales, row_scale, format, gated=False):
         if codes.dim() not in (2, 3):
             raise ValueError("codes must be [rows, K / 2] or [matrices, rows, K / 2]")
-        self.codes, self.scales, self.row_scale = codes, scales, row_scale
+        self.shape = (*codes.shape[:-1], 2 * codes.shape[-1])
         self.format, self.gated = format, bool(gated)
+        self._views = (codes, scales, row_scale)
         self._parts = (codes, scales, row_scale, _code(_FORMAT, format, "format"), int(self.gated),
                        codes.shape[0] if codes.dim() == 3 else 1, codes.shape[-2], 2 * codes.shape[-1])
 
-    @property
-    def shape(self):
-        """Of the matrix or stack that is held."""
-        return (*self.codes.shape[:-1], 2 * self.codes.shape[-1])
+    def _look(self):
+        if self._views is None:
+            data, _, _, fmt, gated, matrices, rows, K = self._parts
+            self._views = _N().fp4_views(data, fmt, gated, matrices, rows, K, len(self.shape) == 3)
+        return self._views
+
+    codes = property(lambda self: self._look()[0])
+    scales = property(lambda self: self._look()[1])
+    row_scale = property(lambda self: self._look()[2])
 
     def __repr__(self):
         return f"Fp4({list(self.shape)}, {self.format!r}{', gated' if self.gated else ''})"
@@ -101,9 +107,15 @@ def quantize_fp4(x, format="nvfp4", gated=False, out=None, stream=None):
     two, per row; "mxfp4": an E8M0 scale per 32. Ties go to even. A block with an infinity or NaN becomes NaN.
     gated: x is the weight of a gated product, gate rows first. out: an Fp4 of this shape, format and order
     whose buffers are written."""
-    parts = _N().quantize_fp4(x, _code(_FORMAT, format, "format"), int(bool(gated)),
-                              None if out is None else _held(out, "out"), _handle(stream))
-    return Fp4(*parts, format, gated) if out is None else out
+    fmt, gated = _code(_FORMAT, format, "format"), bool(gated)
+    data, matrices, rows, K = _N().quantize_fp4(x, fmt, int(gated), None if out is None else _held(out, "out"),
+                                                _handle(stream))
+    if out is not None:
+        return out
+    q = Fp4.__new__(Fp4)
+    q.shape, q.format, q.gated, q._views = tuple(x.shape), format, gated, None
+    q._parts = (data, None, None, fmt, int(gated), matrices, rows, K)
+    return q
 
 
 def dequantize_fp4(q, dtype=torch.bfloat16, out=None, stream=None):
@@ -111,7 +123,7 @@ def dequantize_fp4(q, dtype=torch.bfloat16, out=None, stream=None):
     if dtype not in _DTYPE:
         raise TypeError(f"dtype must be bf16, fp16 or fp32, got {dtype}")
     parts = _held(q, "q")
-    return _N().dequantize_fp4(parts, _DTYPE[dtype], out, q.codes.dim() == 3, _handle(stream))
+    return _N().dequantize_fp4(parts, _DTYPE[dtype], out, len(q.shape) == 3, _handle(stream))
 
 
 def pack_fp4(codes, scales, row_scale=None, format="nvfp4", gated=False, stream=None):

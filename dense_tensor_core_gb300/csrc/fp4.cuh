@@ -7,11 +7,14 @@
 // are whole lines. Magnitudes of 16-bit floats compare as whole numbers, two at a time. Bound by HBM.
 //
 // Exactness. The code is the e2m1 value nearest to x / d, d = s g, a tie to even. t = x * (1 / d) in fp32 is
-// within 2^-22 of it, and ties are the seven numbers b of at most 3 bits. x has at most 11 significant
-// bits and b d at most 7 (g is a power of two), so x / d is b exactly or differs from it by 2^-11 of it or
-// more. So t rounded to 16 bits is b exactly where x / d is, and on x / d's side of b where it is not; the
-// conversion instruction then rounds it as x / d itself would be. (Rounding the fp32 product as it is puts
-// about half of the exact ties of a bf16 row on the wrong side.)
+// within 2^-21 of it, and ties are the seven numbers b from 0.25 to 5 of at most 3 bits. x has at most 11
+// significant bits and b d at most 7 (g is a power of two), so x / d is b exactly or differs from it by 2^-11 of
+// it, 2^-13, or more. So t rounded to a multiple of 2^-14 is b exactly where x / d is, and on x / d's side of b
+// where it is not; the conversion instruction then rounds it as x / d itself would be. (Rounding the fp32
+// product as it is puts about half of the exact ties of a bf16 row on the wrong side.) Adding 768, whose fp32
+// neighbours are 2^-14 apart, and subtracting it does that in the product's own instruction and one more.
+// Scales the same way: max / (6 g) is a tie of the UE4M3 grid, which has at most 5 bits, exactly or differs
+// from it by 2^-11 of it, so the product with 1 / 6 is rounded to 16 significant bits first.
 #pragma once
 
 #include "element.cuh"
@@ -56,6 +59,32 @@ __device__ __forceinline__ float of_ue4m3(uint32_t c) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
     return __half2float(__ushort_as_half((unsigned short)(h & 0xffffu)));
 }
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
 // Eight e2m1 codes, element 0 in the lowest nibble.
 __device__ __forceinline__ uint32_t to_e2m1x8(const float (&v)[8]) {
     uint32_t r;
@@ -94,11 +123,109 @@ __device__ __forceinline__ int factor_exponent(float top) {
     return max(-100, (int)(b >> 23) - 127 - 11 + ((b & 0x7fffffu) > 0x280000u ? 1 : 0));
 }
 
-// Which rows a launch quantises, and where they go.
-enum Source {
-    kPlain = 0,   // row r of x is row r of the stack
-    kTokens = 1,  // row r in expert order is token rows[r] / k of x
-    kOrdered = 2  // row r of x is row r in expert order; its factor takes in its choice's weight
+template <bool kBF16>
+__device__ __forceinline__ float magnitude(uint32_t bits) {
+    if constexpr (kBF16) return __uint_as_float(bits << 16);
+    else return __half2float(__ushort_as_half((unsigned short)bits));
+}
+
+// The scale's code of a block whose largest magnitude is `top` (element bits) in a row with factor 2^e, and the
+// reciprocal of the value its elements are divided by. A block that is not finite has the NaN scale.
+template <bool kBF16, int kFormat>
+__device__ __forceinline__ void block_scale(uint32_t top, int e, uint32_t& s, float& r) {
+    constexpr uint32_t kInf = kBF16 ? 0x7f80u : 0x7c00u;
+    const float t = magnitude<kBF16>(top);
+    if constexpr (kFormat == kNvfp4) {
+        const float v = t * pow2(-e) * (1.0f / 6.0f);
+        s = to_ue4m3(__uint_as_float((__float_as_uint(v) + 0x80u) & 0xffffff00u));
+        const float sv = of_ue4m3(s);
+        r = sv > 0.0f ? __fdividef(pow2(-e), sv) : 0.0f;
+        if (top >= kInf) s = 0x7fu;
+    } else {
+        const int b = max(-126, (int)(__float_as_uint(t) >> 23) - 127 - 2);
+        s = t > 0.0f ? (uint32_t)(b + 127) : 127u;
+        r = t > 0.0f ? pow2(-b) : 1.0f;
+        if (top >= kInf) s = 0xffu;
+    }
+}
+
+// The codes of 8 elements.
+template <bool kBF16, int kFormat>
+__device__ __forceinline__ uint32_t encode(const uint4& u, uint32_t top, float r) {
+    constexpr uint32_t kInf = kBF16 ? 0x7f80u : 0x7c00u;
+    float f[8];
+    ffn::unpack8<kBF16>(u, f);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        float2 t = make_float2(f[i], f[i + 1]);
+        if constexpr (kFormat == kNvfp4) {
+            t = fma2(t, make_float2(r, r), make_float2(768.0f, 768.0f));
+            t = add2(t, make_float2(-768.0f, -768.0f));
+        } else {
+            t = mul2(t, make_float2(r, r));  // (a power of two: exact)
+        }
+        f[i] = t.x;
+        f[i + 1] = t.y;
+    }
+    return top >= kInf ? 0u : to_e2m1x8(f);
+}
+
+// Largest magnitude of the block that a lane's piece of 8 elements belongs to, as the element's bits (a block
+// of 16 is two neighbouring lanes, one of 32 four; rows are whole numbers of blocks of 32).
+template <int kFormat>
+__device__ __forceinline__ uint32_t block_top(const uint4& u) {
+    const uint32_t m01 = __vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu);
+    const uint32_t m23 = __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu);
+    const uint32_t m = __vmaxu2(m01, m23);
+    uint32_t t = max(m & 0xffffu, m >> 16);
+    t = max(t, __shfl_xor_sync(kAll, t, 1));
+    if constexpr (kFormat == kMxfp4) t = max(t, __shfl_xor_sync(kAll, t, 2));
+    return t;
+}
+template <int kFormat>
+constexpr int kBlockLanes = kFormat == kNvfp4 ? 2 : 4;
+// The scales of a set side by side, in the first lane of its four blocks.
+template <int kFormat>
+__device__ __forceinline__ uint32_t set_word(uint32_t s) {
+    s |= __shfl_down_sync(kAll, s, kBlockLanes<kFormat>) << 8;
+    return s | __shfl_down_sync(kAll, s, 2 * kBlockLanes<kFormat>) << 16;
+}
+
+// A row's largest finite block, over the kWarps warps that share it (all threads of the block call it).
+template <int kWarps>
+__device__ __forceinline__ uint32_t row_max(uint32_t top, uint32_t* tops) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) top = max(top, __shfl_xor_sync(kAll, top, o));
+    if constexpr (kWarps > 1) {
+        const int warp = threadIdx.x >> 5;
+        __syncthreads();  // the row before has been read
+        if ((threadIdx.x & 31) == 0) tops[warp] = top;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) top = max(top, tops[warp / kWarps * kWarps + i]);
+    }
+    return top;
+}
+
+constexpr int kThreads = 256;
+constexpr int kVecs = 4;  // 16-byte pieces of the row that a lane keeps
+
+// Which rows a launch quantises: all of a stack, or rows that stand in expert order, whose factors take in
+// their choices' weights and whose scales stand tile by tile (two groups a tile).
+enum Source { kPlain = 0, kOrdered = 1 };
+
+struct ExpertRows {
+    const FfnTile* tiles;
+    const int* num_tiles;
+    int max_tiles, experts, capacity;
+    const int* choice;  // the plan's rows
+    const int* offsets;
+    const int* counts;
+    const int* slots;
+    int64_t choices;
+    int k;
+    const void* weights;
+    int wtype;
 };
 
 struct QuantizeArgs {
@@ -115,27 +242,10 @@ struct QuantizeArgs {
     int64_t rows;   // of a matrix
     int64_t groups;
     bool gated;
-    // expert order
-    const FfnTile* tiles;
-    const int* num_tiles;
-    int max_tiles, experts, capacity;
-    const int* choice;  // the plan's rows
-    int64_t choices;
-    int k;
-    const void* weights;
-    int wtype;
+    ExpertRows x_rows;
     uint32_t* zero;  // counters to clear for the products behind
     int zero_words;
 };
-
-constexpr int kThreads = 256;
-constexpr int kVecs = 4;  // 16-byte pieces of the row that a lane keeps
-
-template <bool kBF16>
-__device__ __forceinline__ float magnitude(uint32_t bits) {
-    if constexpr (kBF16) return __uint_as_float(bits << 16);
-    else return __half2float(__ushort_as_half((unsigned short)bits));
-}
 
 // kWarps warps share a row; kKept: they hold it whole (else it is read a second time).
 template <bool kBF16, int kFormat, int kSource, int kWarps, bool kKept>
@@ -147,61 +257,47 @@ __global__ void __launch_bounds__(kThreads < 32 * kWarps ? 32 * kWarps : kThread
     __shared__ uint32_t tops[kBlockThreads / 32];
     grid_launch_dependents();
     grid_dependency_wait();
-    if constexpr (kSource == kTokens) {
-        for (int64_t i = (int64_t)blockIdx.x * kBlockThreads + threadIdx.x; i < a.zero_words;
-             i += (int64_t)gridDim.x * kBlockThreads)
-            a.zero[i] = 0u;
-    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int part = warp % kWarps;  // of the row
-    // the row: where it is read, where its codes and factor go, and where its scales
-    int64_t src, dst, group;
+    // the row, and where its scales go
+    int64_t row, group;
     int place;
     float weight = 1.0f;
     bool live = true;
     if constexpr (kSource == kPlain) {
-        dst = (int64_t)blockIdx.x * kRowsPer + warp / kWarps;
-        live = dst < a.total;
-        src = dst;
-        const int64_t m = live ? dst / a.rows : 0;
-        place_of(dst - m * a.rows, a.rows, a.gated, group, place);
+        row = (int64_t)blockIdx.x * kRowsPer + warp / kWarps;
+        live = row < a.total;
+        int64_t m = 0, r = row;
+        if (a.rows < a.total) {  // a stack
+            m = live ? row / a.rows : 0;
+            r = row - m * a.rows;
+        }
+        place_of(r, a.rows, a.gated, group, place);
         group += m * a.groups;
     } else {
+        const ExpertRows& x = a.x_rows;
         constexpr int kBlocksPer = ffn::kMaxRows / kRowsPer;  // of a tile
         const int tile = blockIdx.x / kBlocksPer;
         const int r = (blockIdx.x - tile * kBlocksPer) * kRowsPer + warp / kWarps;
-        if (tile >= a.max_tiles || tile >= *a.num_tiles) return;
-        const int4 rec = reinterpret_cast<const int4*>(a.tiles)[tile];
+        if (tile >= x.max_tiles || tile >= *x.num_tiles) return;
+        const int4 rec = reinterpret_cast<const int4*>(x.tiles)[tile];
         // (a record that no plan of these sizes holds, of a stale or foreign plan, is left out)
-        if ((unsigned)rec.x >= (unsigned)a.experts || rec.z < 1 || rec.z > ffn::kMaxRows || rec.y < 0 ||
-            rec.y > a.capacity - rec.z)
+        if ((unsigned)rec.x >= (unsigned)x.experts || rec.z < 1 || rec.z > ffn::kMaxRows || rec.y < 0 ||
+            rec.y > x.capacity - rec.z)
             return;
         live = r < rec.z;
-        dst = rec.y + (live ? r : 0);
-        const int c = a.choice[dst];
-        const bool real = c >= 0 && c < a.choices;
-        src = kSource == kTokens ? (real ? c / a.k : 0) : dst;
-        if constexpr (kSource == kOrdered) weight = real ? load_w(a.weights, c, a.wtype) : 0.0f;
+        row = rec.y + (live ? r : 0);
+        const int c = x.choice[row];
+        weight = c >= 0 && c < x.choices ? load_w(x.weights, c, x.wtype) : 0.0f;
         group = 2 * (int64_t)tile + (r >> 7);
         place = r & 127;
     }
     if (kWarps == 1 && !live) return;
-    const uint4* const x = reinterpret_cast<const uint4*>(a.x + (live ? src : 0) * a.ld);
+    const uint4* const x = reinterpret_cast<const uint4*>(a.x + (live ? row : 0) * a.ld);
     const int pieces = a.K >> 3;  // 16-byte pieces of the row
     const int first = part * 32 + lane;
     constexpr int kStep = 32 * kWarps;
     auto fetch = [&](int p) { return live && p < pieces ? x[p] : make_uint4(0, 0, 0, 0); };
-    // largest magnitude of the block that a lane's piece belongs to, as the element's bits (a block of 16
-    // is two neighbouring lanes, one of 32 four; rows are whole numbers of blocks of 32)
-    auto block_top = [&](const uint4& u) {
-        const uint32_t m01 = __vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu);
-        const uint32_t m23 = __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu);
-        const uint32_t m = __vmaxu2(m01, m23);
-        uint32_t t = max(m & 0xffffu, m >> 16);
-        t = max(t, __shfl_xor_sync(kAll, t, 1));
-        if constexpr (kFormat == kMxfp4) t = max(t, __shfl_xor_sync(kAll, t, 2));
-        return t;
-    };
     uint4 v[kVecs];
     uint32_t tops_of[kVecs];
     uint32_t row_top = 0;
@@ -210,7 +306,7 @@ __global__ void __launch_bounds__(kThreads < 32 * kWarps ? 32 * kWarps : kThread
         for (int i = 0; i < kVecs; ++i) v[i] = fetch(first + i * kStep);
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
-            tops_of[i] = block_top(v[i]);
+            tops_of[i] = block_top<kFormat>(v[i]);
             if (tops_of[i] < kInf) row_top = max(row_top, tops_of[i]);
         }
     } else if constexpr (kFormat == kNvfp4) {
@@ -219,64 +315,28 @@ __global__ void __launch_bounds__(kThreads < 32 * kWarps ? 32 * kWarps : kThread
             for (int i = 0; i < kVecs; ++i) v[i] = fetch(p0 + first + i * kStep);
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) {
-                const uint32_t t = block_top(v[i]);
+                const uint32_t t = block_top<kFormat>(v[i]);
                 if (t < kInf) row_top = max(row_top, t);
             }
         }
     }
     int e = 0;
-    if constexpr (kFormat == kNvfp4) {
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) row_top = max(row_top, __shfl_xor_sync(kAll, row_top, o));
-        if constexpr (kWarps > 1) {
-            if (lane == 0) tops[warp] = row_top;
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < kWarps; ++i) row_top = max(row_top, tops[warp - part + i]);
-        }
-        e = factor_exponent(magnitude<kBF16>(row_top));
-        if (live && part == 0 && lane == 0) a.row_scale[dst] = kSource == kOrdered ? weight * pow2(e) : pow2(e);
-    } else if (kSource == kOrdered && live && part == 0 && lane == 0) {
-        a.row_scale[dst] = weight;
-    }
+    if constexpr (kFormat == kNvfp4) e = factor_exponent(magnitude<kBF16>(row_max<kWarps>(row_top, tops)));
     if (kWarps > 1 && !live) return;  // (nothing behind waits for the block)
-    uint32_t* const codes = reinterpret_cast<uint32_t*>(a.codes + dst * a.ld_codes);
+    if (part == 0 && lane == 0 && (kFormat == kNvfp4 || kSource == kOrdered))
+        a.row_scale[row] = kFormat == kNvfp4 ? weight * pow2(e) : weight;
+    uint32_t* const codes = reinterpret_cast<uint32_t*>(a.codes + row * a.ld_codes);
+    uint8_t* const scales = a.scales + scale_at(group, place, a.sets, 0);
     auto convert = [&](const uint4& u, uint32_t top, int p) {
-        const float t = magnitude<kBF16>(top);
         uint32_t s;
         float r;
-        if constexpr (kFormat == kNvfp4) {
-            s = to_ue4m3(__fdiv_rn(t * pow2(-e), 6.0f));
-            const float sv = of_ue4m3(s);
-            r = sv > 0.0f ? __fdiv_rn(pow2(-e), sv) : 0.0f;
-            if (top >= kInf) s = 0x7fu;
-        } else {
-            const int b = max(-126, (int)(__float_as_uint(t) >> 23) - 127 - 2);
-            s = t > 0.0f ? (uint32_t)(b + 127) : 127u;
-            r = t > 0.0f ? pow2(-b) : 1.0f;
-            if (top >= kInf) s = 0xffu;
-        }
-        float f[8];
-        ffn::unpack8<kBF16>(u, f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            f[i] *= r;
-            if constexpr (kFormat == kNvfp4)  // to 16 significant bits (see above; a power of two is exact)
-                f[i] = __uint_as_float((__float_as_uint(f[i]) + 0x80u) & 0xffffff00u);
-            if (top >= kInf) f[i] = 0.0f;
-        }
-        const uint32_t c = to_e2m1x8(f);
-        // the scales of a set side by side, from the lanes of its blocks (8 lanes of 16-element blocks, 16 of 32)
-        uint32_t w = 0;
-        constexpr int kLanes = kFormat == kNvfp4 ? 2 : 4;  // of a block
-        const int base = lane & ~(4 * kLanes - 1);
-        const bool in = p < pieces;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) w |= __shfl_sync(kAll, in ? s : 0u, base + b * kLanes) << (8 * b);
-        if (in) {
+        block_scale<kBF16, kFormat>(top, e, s, r);
+        const uint32_t c = encode<kBF16, kFormat>(u, top, r);
+        const uint32_t w = set_word<kFormat>(p < pieces ? s : 0u);
+        if (p < pieces) {
             codes[p] = c;
-            if (lane == base)
-                *reinterpret_cast<uint32_t*>(a.scales + scale_at(group, place, a.sets, p / kLanes)) = w;
+            if (lane % (4 * kBlockLanes<kFormat>) == 0)
+                *reinterpret_cast<uint32_t*>(scales + (int64_t)(p / (4 * kBlockLanes<kFormat>)) * 512) = w;
         }
     };
     if constexpr (kKept) {
@@ -290,8 +350,146 @@ __global__ void __launch_bounds__(kThreads < 32 * kWarps ? 32 * kWarps : kThread
 #pragma unroll
             for (int i = 0; i < kVecs; ++i)
                 if (p0 + part * 32 + i * kStep < pieces) {
-                    const uint32_t t = block_top(v[i]);
+                    const uint32_t t = block_top<kFormat>(v[i]);
                     convert(v[i], t, p0 + first + i * kStep);
+                }
+        }
+    }
+}
+
+// Tokens' rows into expert order: a token is quantised once and its row written to each of its choices' places.
+// The plan says the row of each choice; the tile that holds it follows from the experts' counts (tiles of an
+// expert are equal, in steps of 32 rows), which each block adds up first. Lane j finds choice j's place.
+constexpr int kTokenExperts = 1024;  // experts at most
+template <bool kBF16, int kFormat, int kWarps, bool kKept>
+__global__ void __launch_bounds__(kThreads < 32 * kWarps ? 32 * kWarps : kThreads)
+    fp4_quantize_tokens_kernel(const QuantizeArgs a) {
+    constexpr int kBlockThreads = kThreads < 32 * kWarps ? 32 * kWarps : kThreads;
+    constexpr int kRowsPer = kBlockThreads / (32 * kWarps);
+    constexpr uint32_t kInf = kBF16 ? 0x7f80u : 0x7c00u;
+    __shared__ uint32_t tops[kBlockThreads / 32];
+    __shared__ int sums[kBlockThreads / 32];
+    extern __shared__ int by_expert[];  // [E + 1] first rows, [E] first tiles, [E] rows per tile
+    const ExpertRows& x = a.x_rows;
+    const int E = x.experts;
+    int* const first_row = by_expert;
+    int* const first_tile = first_row + E + 1;
+    int* const tile_rows = first_tile + E;
+    grid_launch_dependents();
+    grid_dependency_wait();
+    for (int64_t i = (int64_t)blockIdx.x * kBlockThreads + threadIdx.x; i < a.zero_words;
+         i += (int64_t)gridDim.x * kBlockThreads)
+        a.zero[i] = 0u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int part = warp % kWarps;
+    constexpr int kStep = 32 * kWarps;
+    const int pieces = a.K >> 3, first = part * 32 + lane;
+    const int64_t step = (int64_t)gridDim.x * kRowsPer;
+    int64_t t = (int64_t)blockIdx.x * kRowsPer + warp / kWarps;
+    auto fetch = [&](int64_t row, int p) {
+        return row < a.total && p < pieces ? reinterpret_cast<const uint4*>(a.x + row * a.ld)[p] : make_uint4(0, 0, 0, 0);
+    };
+    uint4 v[kVecs];
+    if constexpr (kKept) {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) v[i] = fetch(t, first + i * kStep);  // (in flight while the counts are added up)
+    }
+    constexpr int kPer = (kTokenExperts + kBlockThreads - 1) / kBlockThreads;
+    int nt[kPer], mine = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int e = threadIdx.x * kPer + i;
+        nt[i] = 0;
+        if (e < E) {
+            const int n = max(0, x.counts[e]);
+            nt[i] = (n + ffn::kMaxRows - 1) / ffn::kMaxRows;
+            first_row[e] = x.offsets[e];
+            tile_rows[e] = nt[i] ? ((n + nt[i] - 1) / nt[i] + 31) & ~31 : 32;
+        }
+        mine += nt[i];
+    }
+    if (threadIdx.x == 0) first_row[E] = x.offsets[E];
+    int before = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kAll, before, o);
+        if (lane >= o) before += y;
+    }
+    if (lane == 31) sums[warp] = before;
+    __syncthreads();
+    before -= mine;
+#pragma unroll
+    for (int w = 0; w < kBlockThreads / 32; ++w)
+        if (w < warp) before += sums[w];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int e = threadIdx.x * kPer + i;
+        if (e < E) first_tile[e] = before;
+        before += nt[i];
+    }
+    __syncthreads();
+    for (; t - warp / kWarps < a.total; t += step) {  // (all threads of the block go round alike)
+        const bool live = t < a.total;
+        // the choices' places: row, scale group and place, -1 where there is none
+        int row = -1, group = 0, place = 0;
+        if (live && lane < x.k) {
+            row = x.slots[t * x.k + lane];
+            if (row >= x.capacity || row >= first_row[E]) row = -1;
+            if (row >= 0) {
+                int e = 0;  // the last expert whose first row is not behind
+                for (int half = 512; half; half >>= 1)
+                    if (e + half < E && first_row[e + half] <= row) e += half;
+                const int r = row - first_row[e], i = r / tile_rows[e];
+                const int tile = first_tile[e] + i;
+                place = r - i * tile_rows[e];
+                group = 2 * tile + (place >> 7);
+                place &= 127;
+                if (r < 0 || place < 0 || tile >= x.max_tiles) row = -1;  // (of a stale or foreign plan)
+            }
+        }
+        uint32_t tops_of[kVecs], row_top = 0;
+        if constexpr (kKept) {
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+                tops_of[i] = block_top<kFormat>(v[i]);
+                if (tops_of[i] < kInf) row_top = max(row_top, tops_of[i]);
+            }
+        } else if constexpr (kFormat == kNvfp4) {
+            for (int p0 = 0; p0 < pieces; p0 += kStep) {
+                const uint32_t top = block_top<kFormat>(fetch(t, p0 + first));
+                if (top < kInf) row_top = max(row_top, top);
+            }
+        }
+        int e = 0;
+        if constexpr (kFormat == kNvfp4) e = factor_exponent(magnitude<kBF16>(row_max<kWarps>(row_top, tops)));
+        if (kFormat == kNvfp4 && part == 0 && row >= 0) a.row_scale[row] = pow2(e);
+        auto write = [&](const uint4& u, uint32_t top, int p) {
+            uint32_t s;
+            float r;
+            block_scale<kBF16, kFormat>(top, e, s, r);
+            const uint32_t c = encode<kBF16, kFormat>(u, top, r);
+            const uint32_t w = set_word<kFormat>(p < pieces ? s : 0u);
+            const bool in = p < pieces;
+            for (int j = 0; j < x.k; ++j) {
+                const int to = __shfl_sync(kAll, row, j), g = __shfl_sync(kAll, group, j), at = __shfl_sync(kAll, place, j);
+                if (to < 0 || !in) continue;
+                reinterpret_cast<uint32_t*>(a.codes + (int64_t)to * a.ld_codes)[p] = c;
+                if (lane % (4 * kBlockLanes<kFormat>) == 0)
+                    *reinterpret_cast<uint32_t*>(a.scales + scale_at(g, at, a.sets, 0) +
+                                                 (int64_t)(p / (4 * kBlockLanes<kFormat>)) * 512) = w;
+            }
+        };
+        if constexpr (kKept) {
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i)
+                if (part * 32 + i * kStep < pieces) write(v[i], tops_of[i], first + i * kStep);
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) v[i] = fetch(t + step, first + i * kStep);
+        } else {
+            for (int p0 = 0; p0 < pieces; p0 += kStep)
+                if (p0 + part * 32 < pieces) {
+                    const uint4 u = fetch(t, p0 + first);
+                    write(u, block_top<kFormat>(u), p0 + first);
                 }
         }
     }
@@ -307,38 +505,57 @@ struct ValuesArgs {
     bool gated;
 };
 
-// 8 elements a lane: 4 bytes of codes, one scale, 16 (32) bytes of values. Bound by HBM.
-template <int kType, int kFormat>
+// 8 elements a lane and step: 4 bytes of codes, one scale, 16 (32) bytes of values; kWarps warps share a row.
+// Bound by HBM.
+template <int kType, int kFormat, int kWarps>
 __global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const ValuesArgs a) {
+    constexpr int kRowsPer = kThreads / (32 * kWarps), kStep = 32 * kWarps, kAhead = 4;
     grid_launch_dependents();
     grid_dependency_wait();
-    const int per = a.K >> 3;
-    const int64_t items = a.total * per, stride = (int64_t)gridDim.x * kThreads;
-    for (int64_t it = (int64_t)blockIdx.x * kThreads + threadIdx.x; it < items; it += stride) {
-        const int64_t row = it / per;
-        const int p = (int)(it - row * per);
-        const int64_t m = row / a.rows;
-        int64_t group;
-        int place;
-        place_of(row - m * a.rows, a.rows, a.gated, group, place);
-        const uint32_t c = reinterpret_cast<const uint32_t*>(a.codes)[it];
-        const uint32_t s = a.scales[scale_at(group + m * a.groups, place, a.sets, kFormat == kNvfp4 ? p >> 1 : p >> 2)];
-        float f;
-        if constexpr (kFormat == kNvfp4)
-            f = of_ue4m3(s);
-        else
-            f = s == 0xffu ? __int_as_float(0x7fffffff) : s == 0 ? __uint_as_float(0x00400000u) : pow2((int)s - 127);
-        if (a.row_scale) f *= a.row_scale[row];
-        float v[8];
-        of_e2m1x8(c, v);
+    const int64_t row = (int64_t)blockIdx.x * kRowsPer + (threadIdx.x >> 5) / kWarps;
+    if (row >= a.total) return;
+    int64_t m = 0, group;
+    if (a.rows < a.total) m = row / a.rows;
+    int place;
+    place_of(row - m * a.rows, a.rows, a.gated, group, place);
+    const uint8_t* const scales = a.scales + scale_at(group + m * a.groups, place, a.sets, 0);
+    const int pieces = a.K >> 3;
+    const uint32_t* const codes = reinterpret_cast<const uint32_t*>(a.codes) + row * pieces;
+    const float g = a.row_scale ? a.row_scale[row] : 1.0f;
+    for (int p0 = threadIdx.x % kStep; p0 < pieces; p0 += kAhead * kStep) {
+        uint32_t c[kAhead], s[kAhead];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= f;
-        if constexpr (kType == 2) {
-            float4* const o = static_cast<float4*>(a.out) + 2 * it;
-            o[0] = make_float4(v[0], v[1], v[2], v[3]);
-            o[1] = make_float4(v[4], v[5], v[6], v[7]);
-        } else {
-            static_cast<uint4*>(a.out)[it] = ffn::pack8<kType == 0>(v);
+        for (int i = 0; i < kAhead; ++i) {
+            const int p = p0 + i * kStep;
+            c[i] = s[i] = 0u;
+            if (p < pieces) {
+                c[i] = codes[p];
+                const int block = p / kBlockLanes<kFormat>;
+                s[i] = scales[(int64_t)(block >> 2) * 512 + (block & 3)];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int p = p0 + i * kStep;
+            if (p >= pieces) break;
+            float f;
+            if constexpr (kFormat == kNvfp4)
+                f = of_ue4m3(s[i]);
+            else
+                f = s[i] == 0xffu ? __int_as_float(0x7fffffff) : s[i] == 0 ? __uint_as_float(0x00400000u) : pow2((int)s[i] - 127);
+            f *= g;
+            float v[8];
+            of_e2m1x8(c[i], v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] *= f;
+            const int64_t it = row * pieces + p;
+            if constexpr (kType == 2) {
+                float4* const o = static_cast<float4*>(a.out) + 2 * it;
+                o[0] = make_float4(v[0], v[1], v[2], v[3]);
+                o[1] = make_float4(v[4], v[5], v[6], v[7]);
+            } else {
+                static_cast<uint4*>(a.out)[it] = ffn::pack8<kType == 0>(v);
+            }
         }
     }
 }

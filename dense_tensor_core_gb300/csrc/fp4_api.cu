@@ -115,7 +115,7 @@ int fp4_dequantize(int dtype, const fp4_matrix* q, void* out, dtc_stream_t strea
     a.K = (int)q->K;
     a.sets = (int)l.sets;
     a.gated = q->gated != 0;
-    return launch_fp4_dequantize(dtype, q->format, a, info, (cudaStream_t)stream);
+    return launch_fp4_dequantize(dtype, q->format, a, (cudaStream_t)stream);
 }
 
 int fp4_pack_scales(const void* scales, const fp4_matrix* q, dtc_stream_t stream) {
@@ -515,14 +515,21 @@ int moe_experts_fp4(int dtype, const void* x, const fp4_matrix* w_in, const fp4_
     const int64_t tiles = s.plan.max_tiles, R = s.plan.capacity;
     // the tokens' rows in expert order, in 4 bits
     dtc::fp4::QuantizeArgs q = {};
-    q.tiles = reinterpret_cast<const dtc::FfnTile*>(pl + s.plan.tiles);
-    q.num_tiles = pl;
-    q.max_tiles = (int)tiles;
-    q.experts = (int)E;
-    q.capacity = (int)R;
-    q.choice = pl + s.plan.rows;
-    q.choices = T * k;
-    q.k = k;
+    dtc::fp4::ExpertRows& xr = q.x_rows;
+    xr.tiles = reinterpret_cast<const dtc::FfnTile*>(pl + s.plan.tiles);
+    xr.num_tiles = pl;
+    xr.max_tiles = (int)tiles;
+    xr.experts = (int)E;
+    xr.capacity = (int)R;
+    xr.choice = pl + s.plan.rows;
+    xr.offsets = pl + s.plan.offsets;
+    xr.counts = pl + s.plan.counts;
+    xr.slots = pl + s.plan.slots;
+    xr.choices = T * k;
+    xr.k = k;
+    xr.weights = weights;
+    xr.wtype = o.weights_dtype;
+    q.total = T;
     q.x = static_cast<const uint16_t*>(x);
     q.ld = H;
     q.K = (int)H;
@@ -533,7 +540,7 @@ int moe_experts_fp4(int dtype, const void* x, const fp4_matrix* w_in, const fp4_
     q.row_scale = reinterpret_cast<float*>(b + s.xg);
     q.zero = reinterpret_cast<uint32_t*>(b + s.split);
     q.zero_words = (int)((s.partial - s.split) / 4);
-    if ((rc = launch_fp4_quantize_experts(bf16, s.format, dtc::fp4::kTokens, q, st))) return rc;
+    if ((rc = launch_fp4_quantize_tokens(bf16, s.format, q, info, st))) return rc;
     // h = act(w_in x), 16 bits
     auto product = [&](const fp4_matrix* w, const fp4_info& l, const Fp4Plan& p, uint64_t counters, uint64_t codes,
                        int64_t ld, uint64_t scales, const float* factors, int64_t K, int64_t sets, int64_t feats,
@@ -554,7 +561,7 @@ int moe_experts_fp4(int dtype, const void* x, const fp4_matrix* w_in, const fp4_
         a.rows = (int)R;
         a.red = (int)(K / 4);
         a.experts = (int)E;
-        a.tiles = q.tiles;
+        a.tiles = xr.tiles;
         a.num_tiles = pl;
         a.max_tiles = (int)tiles;
         a.p_expert_rows = (int)w->rows;
@@ -588,10 +595,7 @@ int moe_experts_fp4(int dtype, const void* x, const fp4_matrix* w_in, const fp4_
     q.ld_codes = s.ldc;
     q.scales = b + s.hs;
     q.row_scale = reinterpret_cast<float*>(b + s.hg);
-    q.weights = weights;
-    q.wtype = o.weights_dtype;
-    q.zero_words = 0;
-    if ((rc = launch_fp4_quantize_experts(bf16, s.format, dtc::fp4::kOrdered, q, st))) return rc;
+    if ((rc = launch_fp4_quantize_ordered(bf16, s.format, q, st))) return rc;
     e = {};
     e.out = b + s.y;
     e.out_f32 = true;

@@ -10,7 +10,8 @@ namespace {
 
 using namespace dtc_py;
 
-// (codes, scales, row_scale or None, format, gated, matrices, rows, K)
+// (codes, scales, row_scale or None, format, gated, matrices, rows, K). With scales None the first tensor
+// holds all three, as buffers_of says: one allocation, and no views of it where nobody looks at them.
 struct Held {
     fp4_matrix m = {};
     const at::Tensor *codes, *scales, *factors;
@@ -21,22 +22,46 @@ fp4_info layout_of(const fp4_matrix& m) {
     if (status) throw LibraryError{status};
     return l;
 }
+struct Buffers {
+    int64_t scales, factors, bytes;  // byte offsets behind the codes
+};
+Buffers buffers_of(const fp4_matrix& m, const fp4_info& l) {
+    auto up = [](uint64_t v) { return (int64_t)((v + 255) & ~(uint64_t)255); };
+    Buffers b;
+    b.scales = up(l.code_bytes);
+    b.factors = b.scales + up(l.scale_bytes);
+    b.bytes = b.factors + (m.format == FP4_NVFP4 ? m.matrices * m.rows * 4 : 0);
+    return b;
+}
+void point_at(fp4_matrix* m, const at::Tensor& data, const Buffers& b) {
+    if (data.numel() == 0) return;
+    char* const p = static_cast<char*>(data.data_ptr());
+    m->codes = p;
+    m->scales = p + b.scales;
+    m->row_scale = m->format == FP4_NVFP4 ? reinterpret_cast<float*>(p + b.factors) : nullptr;
+}
 Held held(PyObject* o, const char* name) {
     const std::string n(name);
     if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 8) refuse(PyExc_TypeError, n + " must be an Fp4");
     auto at = [&](int i) { return PyTuple_GET_ITEM(o, i); };
     Held h;
     h.codes = &tensor(at(0), name);
-    h.scales = &tensor(at(1), name);
+    h.scales = maybe(at(1), name);
     h.factors = maybe(at(2), name);
     h.m.format = small(at(3), "format");
     h.m.gated = small(at(4), "gated");
     h.m.matrices = integer(at(5));
     h.m.rows = integer(at(6));
     h.m.K = integer(at(7));
-    const c10::Device dev = device_of(*h.codes, at::kByte, (n + ".codes").c_str());
+    const c10::Device dev = device_of(*h.codes, at::kByte, name);
     const fp4_info l = layout_of(h.m);
-    dense(*h.codes, at::kByte, (n + ".codes").c_str(), dev);
+    dense(*h.codes, at::kByte, name, dev);
+    if (!h.scales) {
+        const Buffers b = buffers_of(h.m, l);
+        if (h.codes->numel() != b.bytes) refuse(PyExc_ValueError, n + " is not what quantize_fp4 made");
+        point_at(&h.m, *h.codes, b);
+        return h;
+    }
     dense(*h.scales, at::kByte, (n + ".scales").c_str(), dev);
     if ((uint64_t)h.codes->numel() != l.code_bytes || (uint64_t)h.scales->numel() != l.scale_bytes)
         refuse(PyExc_ValueError, n + ": codes and scales hold " + std::to_string(h.codes->numel()) + " and " +
@@ -71,7 +96,7 @@ int64_t stack(const at::Tensor& x, at::ScalarType dt, const char* name, c10::Dev
     return ld;
 }
 
-// (x, format, gated, out or None, stream) to (codes, scales, row_scale)
+// (x, format, gated, out or None, stream) to (the tensor of codes, scales and factors, matrices, rows, K)
 PyObject* py_quantize_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return entry(n, 5, [&]() -> PyObject* {
         const at::Tensor& x = tensor(a[0], "x");
@@ -83,32 +108,50 @@ PyObject* py_quantize_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int64_t ld = stack(x, x.scalar_type(), "x", dev, &m);
         m.format = small(a[1], "format");
         m.gated = small(a[2], "gated");
-        at::Tensor codes, scales, factors;
+        at::Tensor data;
         if (a[3] != Py_None) {
             const Held h = held(a[3], "out");
             on_device(h, "out", dev);
             if (h.m.format != m.format || h.m.gated != m.gated || h.m.matrices != m.matrices || h.m.rows != m.rows ||
                 h.m.K != m.K)
                 refuse(PyExc_ValueError, "out is of another shape, format or order");
-            if ((h.factors != nullptr) != (m.format == FP4_NVFP4))
+            if (h.scales && (h.factors != nullptr) != (m.format == FP4_NVFP4))
                 refuse(PyExc_ValueError, "out must have row factors in NVFP4 and only there");
             m = h.m;
-            codes = *h.codes;
-            scales = *h.scales;
-            if (h.factors) factors = *h.factors;
+            data = *h.codes;
         } else {
-            const fp4_info l = layout_of(m);
-            codes = x.dim() == 3 ? empty({m.matrices, m.rows, m.K / 2}, at::kByte, dev)
-                                 : empty({m.rows, m.K / 2}, at::kByte, dev);
-            scales = empty({(int64_t)l.scale_bytes}, at::kByte, dev);
-            if (m.format == FP4_NVFP4)
-                factors = x.dim() == 3 ? empty({m.matrices, m.rows}, at::kFloat, dev) : empty({m.rows}, at::kFloat, dev);
-            m.codes = address(codes);
-            m.scales = address(scales);
-            m.row_scale = factors.defined() ? static_cast<float*>(address(factors)) : nullptr;
+            const Buffers b = buffers_of(m, layout_of(m));
+            data = empty({b.bytes}, at::kByte, dev);
+            point_at(&m, data, b);
         }
         on.call([&](dtc_stream_t st) { return fp4_quantize(code, address(x), ld, &m, st); });
-        return tuple({codes, scales, factors});
+        PyObject* const t = wrap(data);
+        PyObject* const r = Py_BuildValue("NLLL", t, (long long)m.matrices, (long long)m.rows, (long long)m.K);
+        if (!r) throw PythonError{};
+        return r;
+    });
+}
+
+// (data, format, gated, matrices, rows, K) to the codes, scales and factors in it: views
+PyObject* py_fp4_views(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return entry(n, 7, [&]() -> PyObject* {
+        const at::Tensor& data = tensor(a[0], "data");
+        fp4_matrix m = {};
+        m.format = small(a[1], "format");
+        m.gated = small(a[2], "gated");
+        m.matrices = integer(a[3]);
+        m.rows = integer(a[4]);
+        m.K = integer(a[5]);
+        const fp4_info l = layout_of(m);
+        const Buffers b = buffers_of(m, l);
+        const bool three = a[6] == Py_True;
+        const std::vector<int64_t> rows = three ? std::vector<int64_t>{m.matrices, m.rows} : std::vector<int64_t>{m.rows};
+        std::vector<int64_t> codes = rows;
+        codes.push_back(m.K / 2);
+        at::Tensor f;
+        if (m.format == FP4_NVFP4) f = data.narrow(0, b.factors, b.bytes - b.factors).view(at::kFloat).view(rows);
+        return tuple({data.narrow(0, 0, (int64_t)l.code_bytes).view(codes),
+                      data.narrow(0, b.scales, (int64_t)l.scale_bytes), f});
     });
 }
 
@@ -267,6 +310,6 @@ PyObject* py_moe_experts_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }  // namespace
 
 namespace dtc_py {
-PyMethodDef kFp4Methods[] = {DTC_FN(quantize_fp4), DTC_FN(dequantize_fp4), DTC_FN(pack_fp4),
+PyMethodDef kFp4Methods[] = {DTC_FN(quantize_fp4), DTC_FN(fp4_views), DTC_FN(dequantize_fp4), DTC_FN(pack_fp4),
                              DTC_FN(gemm_fp4),     DTC_FN(moe_experts_fp4), {nullptr, nullptr, 0, nullptr}};
 }  // namespace dtc_py

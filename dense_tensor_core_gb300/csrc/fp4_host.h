@@ -10,10 +10,10 @@ namespace dtc_host {
 
 // fp4.cuh; the arguments carry the source's part.
 int launch_fp4_quantize(bool bf16, int format, const dtc::fp4::QuantizeArgs& a, cudaStream_t stream);
-int launch_fp4_quantize_experts(bool bf16, int format, int source, const dtc::fp4::QuantizeArgs& a,
-                                cudaStream_t stream);
-int launch_fp4_dequantize(int dtype, int format, const dtc::fp4::ValuesArgs& a, DeviceInfo* dev,
-                          cudaStream_t stream);
+int launch_fp4_quantize_tokens(bool bf16, int format, const dtc::fp4::QuantizeArgs& a, DeviceInfo* dev,
+                               cudaStream_t stream);
+int launch_fp4_quantize_ordered(bool bf16, int format, const dtc::fp4::QuantizeArgs& a, cudaStream_t stream);
+int launch_fp4_dequantize(int dtype, int format, const dtc::fp4::ValuesArgs& a, cudaStream_t stream);
 int launch_fp4_pack(const dtc::fp4::PackArgs& a, DeviceInfo* dev, cudaStream_t stream);
 
 // A product of gemm_fp4.cuh: `ffn` describes the codes as 16-bit words (four elements each).
@@ -34,7 +34,7 @@ int launch_quantize_of(const dtc::fp4::QuantizeArgs& a, cudaStream_t stream) {
     auto go = [&](auto kern, int warps) {
         const int threads = std::max(kThreads, 32 * warps), rows = threads / (32 * warps);
         const int64_t blocks = kSource == kPlain ? (a.total + rows - 1) / rows
-                                                 : (int64_t)a.max_tiles * (dtc::ffn::kMaxRows / rows);
+                                                 : (int64_t)a.x_rows.max_tiles * (dtc::ffn::kMaxRows / rows);
         if (blocks > kMaxSize) return fail(GEMM_ERR_UNSUPPORTED, "too many rows");
         return launch_chain(kern, dim3((unsigned)blocks), threads, 0, 1, stream, a);
     };

@@ -24,6 +24,7 @@
 //     unrolled and the next stage's barrier is looked at before the MMAs of this one.
 #pragma once
 
+#include "fp4.cuh"
 #include "gemm16_ffn.cuh"
 
 namespace dtc {
@@ -123,24 +124,6 @@ __device__ __forceinline__ void fetch_ahead(const Fp4Args& f, const ffn::Place& 
     x.gq = f.q_scale && lane < p.valid ? f.q_scale[p.row + lane] : 1.0f;
 }
 
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-        "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-        "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-
 // act() of all of a thread's values (gated: of the gates, each times its up value), one branch for all: the
 // epilogue's instructions of one activation lie together.
 template <bool kGated, int kAct>
@@ -173,7 +156,7 @@ __device__ __forceinline__ void finish_block(const Fp4Args& fa, const CUtensorMa
                                       __shfl_sync(0xffffffffu, x.gq, 8 * b + tr + 1));
 #pragma unroll
         for (int o = 0; o < 4; ++o) {
-            const float2 z = fma2(make_float2(v[o][2 * b], v[o][2 * b + 1]), mul2(gq, make_float2(gp[o], gp[o])),
+            const float2 z = fp4::fma2(make_float2(v[o][2 * b], v[o][2 * b + 1]), fp4::mul2(gq, make_float2(gp[o], gp[o])),
                                   make_float2(bias[o], bias[o]));
             v[o][2 * b] = z.x;
             v[o][2 * b + 1] = z.y;

@@ -1,4 +1,6 @@
 // launch_fp4.cu -- launches of the 4-bit rows' kernels (fp4.cuh) that know no experts.
+#include <type_traits>
+
 #include "fp4_host.h"
 
 namespace dtc_host {
@@ -13,18 +15,27 @@ unsigned strided_grid(int64_t items, const DeviceInfo* dev) {
 }
 }  // namespace
 
-int launch_fp4_dequantize(int dtype, int format, const dtc::fp4::ValuesArgs& a, DeviceInfo* dev,
-                          cudaStream_t stream) {
+int launch_fp4_dequantize(int dtype, int format, const dtc::fp4::ValuesArgs& a, cudaStream_t stream) {
     using namespace dtc::fp4;
-    const dim3 grid(strided_grid(a.total * (a.K / 8), dev));
-    auto go = [&](auto kern) { return launch_chain(kern, grid, kThreads, 0, 1, stream, a); };
-    if (format == FP4_NVFP4)
-        return dtype == 0   ? go(fp4_dequantize_kernel<0, kNvfp4>)
-               : dtype == 1 ? go(fp4_dequantize_kernel<1, kNvfp4>)
-                            : go(fp4_dequantize_kernel<2, kNvfp4>);
-    return dtype == 0   ? go(fp4_dequantize_kernel<0, kMxfp4>)
-           : dtype == 1 ? go(fp4_dequantize_kernel<1, kMxfp4>)
-                        : go(fp4_dequantize_kernel<2, kMxfp4>);
+    auto go = [&](auto kern, int warps) {
+        const int rows = kThreads / (32 * warps);
+        const int64_t blocks = (a.total + rows - 1) / rows;
+        return launch_chain(kern, dim3((unsigned)blocks), kThreads, 0, 1, stream, a);
+    };
+    // a warp takes a few steps of 256 elements
+    auto warps = [&](auto type, auto fmt) {
+        constexpr int kType = decltype(type)::value, kFormat = decltype(fmt)::value;
+        if (a.K <= 1024) return go(fp4_dequantize_kernel<kType, kFormat, 1>, 1);
+        if (a.K <= 4096) return go(fp4_dequantize_kernel<kType, kFormat, 2>, 2);
+        return go(fp4_dequantize_kernel<kType, kFormat, 8>, 8);
+    };
+    auto formats = [&](auto type) {
+        return format == FP4_NVFP4 ? warps(type, std::integral_constant<int, kNvfp4>())
+                                   : warps(type, std::integral_constant<int, kMxfp4>());
+    };
+    return dtype == 0   ? formats(std::integral_constant<int, 0>())
+           : dtype == 1 ? formats(std::integral_constant<int, 1>())
+                        : formats(std::integral_constant<int, 2>());
 }
 
 int launch_fp4_pack(const dtc::fp4::PackArgs& a, DeviceInfo* dev, cudaStream_t stream) {
