@@ -394,48 +394,57 @@ __global__ void __launch_bounds__(kThreads < 32 * kWarps ? 32 * kWarps : kThread
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) v[i] = fetch(t, first + i * kStep);  // (in flight while the counts are added up)
     }
+    // Few tiles (few choices): a lane looks at one, and the experts' counts are not needed.
+    const bool few = x.max_tiles <= 32;
+    int4 tile_of = make_int4(0, 0, 0, 0);
+    if (few && lane < x.max_tiles) {
+        tile_of = reinterpret_cast<const int4*>(x.tiles)[lane];
+        if (lane >= *x.num_tiles) tile_of.z = 0;
+    }
     constexpr int kPer = (kTokenExperts + kBlockThreads - 1) / kBlockThreads;
     int nt[kPer], mine = 0;
+    if (!few) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int e = threadIdx.x * kPer + i;
-        nt[i] = 0;
-        if (e < E) {
-            const int n = max(0, x.counts[e]);
-            nt[i] = (n + ffn::kMaxRows - 1) / ffn::kMaxRows;
-            first_row[e] = x.offsets[e];
-            tile_rows[e] = nt[i] ? ((n + nt[i] - 1) / nt[i] + 31) & ~31 : 32;
+        for (int i = 0; i < kPer; ++i) {
+            const int e = threadIdx.x * kPer + i;
+            nt[i] = 0;
+            if (e < E) {
+                const int n = max(0, x.counts[e]);
+                nt[i] = (n + ffn::kMaxRows - 1) / ffn::kMaxRows;
+                first_row[e] = x.offsets[e];
+                tile_rows[e] = nt[i] ? ((n + nt[i] - 1) / nt[i] + 31) & ~31 : 32;
+            }
+            mine += nt[i];
         }
-        mine += nt[i];
-    }
-    if (threadIdx.x == 0) first_row[E] = x.offsets[E];
-    int before = mine;
+        if (threadIdx.x == 0) first_row[E] = x.offsets[E];
+        int before = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(kAll, before, o);
-        if (lane >= o) before += y;
-    }
-    if (lane == 31) sums[warp] = before;
-    __syncthreads();
-    before -= mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(kAll, before, o);
+            if (lane >= o) before += y;
+        }
+        if (lane == 31) sums[warp] = before;
+        __syncthreads();
+        before -= mine;
 #pragma unroll
-    for (int w = 0; w < kBlockThreads / 32; ++w)
-        if (w < warp) before += sums[w];
+        for (int w = 0; w < kBlockThreads / 32; ++w)
+            if (w < warp) before += sums[w];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int e = threadIdx.x * kPer + i;
-        if (e < E) first_tile[e] = before;
-        before += nt[i];
+        for (int i = 0; i < kPer; ++i) {
+            const int e = threadIdx.x * kPer + i;
+            if (e < E) first_tile[e] = before;
+            before += nt[i];
+        }
+        __syncthreads();
     }
-    __syncthreads();
     for (; t - warp / kWarps < a.total; t += step) {  // (all threads of the block go round alike)
         const bool live = t < a.total;
         // the choices' places: row, scale group and place, -1 where there is none
         int row = -1, group = 0, place = 0;
         if (live && lane < x.k) {
             row = x.slots[t * x.k + lane];
-            if (row >= x.capacity || row >= first_row[E]) row = -1;
-            if (row >= 0) {
+            if (row >= x.capacity || (!few && row >= first_row[E])) row = -1;
+            if (!few && row >= 0) {
                 int e = 0;  // the last expert whose first row is not behind
                 for (int half = 512; half; half >>= 1)
                     if (e + half < E && first_row[e + half] <= row) e += half;
@@ -446,6 +455,18 @@ __global__ void __launch_bounds__(kThreads < 32 * kWarps ? 32 * kWarps : kThread
                 place &= 127;
                 if (r < 0 || place < 0 || tile >= x.max_tiles) row = -1;  // (of a stale or foreign plan)
             }
+        }
+        if (few) {
+            bool found = false;
+            for (int i = 0; i < x.max_tiles; ++i) {
+                const int r = row - __shfl_sync(kAll, tile_of.y, i), n = __shfl_sync(kAll, tile_of.z, i);
+                if (row >= 0 && r >= 0 && r < n && r < ffn::kMaxRows) {
+                    found = true;
+                    group = 2 * i + (r >> 7);
+                    place = r & 127;
+                }
+            }
+            if (!found) row = -1;
         }
         uint32_t tops_of[kVecs], row_top = 0;
         if constexpr (kKept) {

@@ -178,7 +178,7 @@ __device__ __forceinline__ void finish_block(const Fp4Args& fa, const CUtensorMa
             return;
         }
     }
-    if (lane == 0) bulk_wait_group_read<1>();
+    if (elect_one()) bulk_wait_group_read<1>();  // (the same lane each time)
     __syncwarp();
     const Block blk(slot, lane);
     if (a.residual) blk.put(x.res);
@@ -219,7 +219,7 @@ __device__ __forceinline__ void finish_block(const Fp4Args& fa, const CUtensorMa
     if (whole) {
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0 && left > 0 && p.rows > 0) {
+        if (left > 0 && p.rows > 0 && elect_one()) {
             tma_store_2d(tmC, slot, p.f, (int)p.row);
             bulk_commit_group();
         }
@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
             }
             if (gave_up) break;
         }
-        if (lane == 0) bulk_wait_group_read<0>();  // the copies have read their slots
+        if (elect_one()) bulk_wait_group_read<0>();  // the copies have read their slots
         __syncwarp();
     }
 
