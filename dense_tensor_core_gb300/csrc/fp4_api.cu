@@ -272,6 +272,21 @@ void apply_plan(const Fp4Plan& p, void* counters, void* partial, Fp4Call* c) {
     c->args.sf_stages = narrow ? 4 : 2;
 }
 
+// Up to this many rows an NVFP4 product runs on the kernel without tiles, while its conversions take less than a
+// tile's longer start: its time grows with the elements of B (4 TB/s of them; the tiles read faster), more so for
+// more than 8 rows and for a short K, whose blocks do little. Measured, us, without tiles and with (the host's
+// part of a call is 6):
+//   1 x 8192 x 8192    12.7, 13.4     gated (as much again) 22.2, 17.6
+//   1 x 4096 x 4096     6.3, 9.1      gated 8.8, 9.9
+//   16 x 8192 x 8192   17.4, 13.7     16 x 4096 x 4096 6.8, 9.2; gated 10.6, 10.0
+//   16 x 1024 x 8192    8.3, 10.1     16 x 8192 x 1024 gated 8.3, 6.8
+constexpr int kSkinnyRows = 16;
+bool fp4_skinny(int format, int64_t M, int64_t Nb, int64_t K) {
+    if (format != FP4_NVFP4 || M > kSkinnyRows || K == 0) return false;
+    const int64_t most = M <= 8 ? (int64_t)1 << 26 : (int64_t)1 << 24;
+    return Nb <= most / K && (K >= 2048 || Nb <= ((int64_t)1 << 23) / K);
+}
+
 int check_product(int64_t M, int64_t N, int64_t K, int act) {
     if (act < GEMM_ACT_NONE || act > GEMM_ACT_GEGLU)
         return fail(GEMM_ERR_INVALID_ARG, "unknown activation %d", act);
@@ -318,9 +333,10 @@ int gemm_fp4(int dtype, const fp4_matrix* A, const fp4_matrix* B, void* C, const
         return rc;
     if (o.bias && (rc = check_device_ptr(o.bias, dev, "bias"))) return rc;
     if (o.residual && (rc = check_device_ptr(o.residual, dev, "residual"))) return rc;
-    const Fp4Plan p = plan_rows(M, N, gated, K, pairs_of(info), o.workspace ? o.workspace_bytes : 0, o.tile_rows,
-                                o.split_k);
-    if (p.num_ft == 0)
+    const bool few = !o.tile_rows && !o.split_k && fp4_skinny(A->format, M, Nb, K);
+    const Fp4Plan p = few ? Fp4Plan() : plan_rows(M, N, gated, K, pairs_of(info), o.workspace ? o.workspace_bytes : 0,
+                                                  o.tile_rows, o.split_k);
+    if (!few && p.num_ft == 0)
         return o.tile_rows || o.split_k
                    ? fail(GEMM_ERR_INVALID_ARG, "tile_rows %d and split_k %d are not what this call can have",
                           o.tile_rows, o.split_k)
@@ -359,6 +375,7 @@ int gemm_fp4(int dtype, const fp4_matrix* A, const fp4_matrix* B, void* C, const
     c.q_scales = A->scales;
     c.p_chunks = lb.scale_bytes / 512;
     c.q_chunks = la.scale_bytes / 512;
+    if (few) return launch_fp4_skinny(c, M > 8, (cudaStream_t)stream);
     apply_plan(p, o.workspace, static_cast<char*>(o.workspace) + p.counter_bytes, &c);
     return launch_gemm_fp4(c, info, (cudaStream_t)stream);
 }
