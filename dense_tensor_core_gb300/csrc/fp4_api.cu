@@ -167,9 +167,13 @@ void size_split(Fp4Plan* p, uint64_t counters) {
     p->bytes = counters + (uint64_t)p->split_tiles * p->splits * p->tile_n * 1024;
 }
 
-// Modelled time of a launch in us, less what every launch costs.
+// Modelled time of a launch in us, less what every launch costs, after measured times (4096 x 4096 x 1024: 18.3
+// in tiles of 192 rows, 20.3 of 256; x 8192: 69, 59 and 54 of 128, 192 and 256): a stage of 256 elements takes
+// the issuing thread's 0.25 us, above 128 rows the tensor pipe's; a tile whose accumulator touches its
+// predecessor's waits until that is read.
 double item_cost(const Fp4Plan& p, int kb, int pairs) {
-    const double block = 0.2 + 0.0006 * p.tile_n, item = 1.2;
+    const double block = 0.25 + 0.0003 * std::max(0, p.tile_n - 128);
+    const double item = 1.2 + (dtc::gf4::tiles_touch(p.tile_n) ? 1.2 : 0.0);
     const int64_t split_items = (int64_t)p.split_tiles * p.splits, whole = p.tiles - p.split_tiles;
     double cost = 0.0114 * p.tile_n + (double)((whole + pairs - 1) / pairs) * (kb * block + item);
     if (p.splits > 1) {
@@ -224,7 +228,8 @@ Fp4Plan plan_rows(int64_t rows, int64_t feats, bool gated, int64_t K, int pairs,
     return best;
 }
 
-// As moe_experts plans its products: the tiles are known on the device only.
+// As moe_experts plans its products: the tiles are known on the device only. (Tall tiles taken in halves, whose
+// accumulators go by turns, were slower: 4096 tokens by 8 of 64 experts, H 2048, F 1024 293 us against 285.)
 Fp4Plan plan_seg(int64_t T, int k, int64_t E, int64_t max_tiles, int64_t feats, bool gated, int64_t K, int pairs) {
     Fp4Plan p;
     p.num_ft = num_feature_tiles(feats, gated);
@@ -267,7 +272,7 @@ void apply_plan(const Fp4Plan& p, void* counters, void* partial, Fp4Call* c) {
         a.counters = static_cast<uint32_t*>(counters);
         a.partial = static_cast<float*>(partial);
     }
-    const bool narrow = p.tile_n <= dtc::gf4::kNarrow || 2 * p.tile_n > dtc::gf4::kWideTop;
+    const bool narrow = p.tile_n <= dtc::gf4::kNarrow || dtc::gf4::tiles_touch(p.tile_n);
     c->args.acc_top = narrow ? 2 * dtc::gf4::kNarrow : dtc::gf4::kWideTop;
     c->args.sf_stages = narrow ? 4 : 2;
 }
@@ -276,14 +281,14 @@ void apply_plan(const Fp4Plan& p, void* counters, void* partial, Fp4Call* c) {
 // tile's longer start: its time grows with the elements of B (4 TB/s of them; the tiles read faster), more so for
 // more than 8 rows and for a short K, whose blocks do little. Measured, us, without tiles and with (the host's
 // part of a call is 6):
-//   1 x 8192 x 8192    12.7, 13.4     gated (as much again) 22.2, 17.6
+//   1 x 8192 x 8192    12.7, 12.1 to 13.4 (K split)     gated (as much again) 22.2, 17.6
 //   1 x 4096 x 4096     6.3, 9.1      gated 8.8, 9.9
 //   16 x 8192 x 8192   17.4, 13.7     16 x 4096 x 4096 6.8, 9.2; gated 10.6, 10.0
 //   16 x 1024 x 8192    8.3, 10.1     16 x 8192 x 1024 gated 8.3, 6.8
 constexpr int kSkinnyRows = 16;
 bool fp4_skinny(int format, int64_t M, int64_t Nb, int64_t K) {
     if (format != FP4_NVFP4 || M > kSkinnyRows || K == 0) return false;
-    const int64_t most = M <= 8 ? (int64_t)1 << 26 : (int64_t)1 << 24;
+    const int64_t most = M <= 8 ? (int64_t)1 << 25 : (int64_t)1 << 24;
     return Nb <= most / K && (K >= 2048 || Nb <= ((int64_t)1 << 23) / K);
 }
 

@@ -60,6 +60,7 @@ constexpr int kNarrow = 160;
 static_assert(kSmemBytes <= 227 * 1024 - 512, "shared memory budget");
 static_assert(2 * kNarrow + 4 * kSfStage <= kTmemCols, "Tensor Memory budget");
 constexpr int kWideTop = kTmemCols - 2 * kSfStage;
+constexpr bool tiles_touch(int n) { return 2 * n > kWideTop; }
 
 // The t-th item of the launch (see ffn::get_item).
 template <int kMode, bool kGated>
@@ -76,7 +77,6 @@ __device__ __forceinline__ bool item_of(const FfnArgs& a, int t, int seg_tiles, 
     w.tile = tile;
     w.split = split;
     w.expert = 0;
-    w.zeros = 0;
     if constexpr (kMode == ffn::kRows) {
         if (tile >= a.num_ft * a.num_rt) return false;
         int ft, rt;
@@ -99,8 +99,8 @@ __device__ __forceinline__ bool item_of(const FfnArgs& a, int t, int seg_tiles, 
         w.expert = s.x;
         w.r0 = s.y;
         w.valid = s.z;
-        w.n = ffn::round32(s.z);
         w.krow = 2 * rt;  // the rows' scales stand tile by tile
+        w.n = ffn::round32(w.valid);
     }
     const int kb = (a.red + kBK - 1) / kBK;
     w.kb0 = split >= 0 ? min(kb, split * a.kb_per_split) : 0;
@@ -145,7 +145,8 @@ __device__ __forceinline__ void act_block(float (&v)[4][8]) {
 template <bool kBF16, int kMode, bool kGated, typename Refill>
 __device__ __forceinline__ void finish_block(const Fp4Args& fa, const CUtensorMap* tmC, float (&v)[4][8],
                                              const float (&gp)[4], const float (&bias)[4], const ffn::Place& p,
-                                             Ahead<kGated>& x, uint32_t slot, int lane, Refill refill) {
+                                             Ahead<kGated>& x, uint32_t slots, uint32_t slot, int lane,
+                                             Refill refill) {
     using Block = ffn::Block<kGated ? 2 : 4>;
     const FfnArgs& a = fa.e;
     const int left = a.feats - p.f;
@@ -163,17 +164,30 @@ __device__ __forceinline__ void finish_block(const Fp4Args& fa, const CUtensorMa
         }
     }
     if constexpr (kMode == ffn::kSeg && !kGated) {
-        if (a.out_f32) {  // eight lanes hold 32 bytes of a row: whole sectors
+        if (a.out_f32) {  // through both slots, in the order of a 128-byte swizzle
+            using Sums = ffn::Sums<4>;
+            if (elect_one()) bulk_wait_group_read<0>();
+            __syncwarp();
             refill();
-            float* const out = static_cast<float*>(a.out) + (p.row + tr) * a.ld_out + p.f + (lane >> 2);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int r = 8 * (k >> 1) + (k & 1);
-                if (r + tr < p.valid) {
+            for (int o = 0; o < 4; ++o)
 #pragma unroll
-                    for (int o = 0; o < 4; ++o)
-                        if (8 * o < left) out[r * a.ld_out + 8 * o] = v[o][k];
+                for (int k = 0; k < 8; ++k) st_shared_f32(slots + Sums::element(o, k, lane), v[o][k]);
+            if (p.valid == 32) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (left > 0 && elect_one()) {
+                    tma_store_2d(tmC, slots, p.f, (int)p.row);
+                    bulk_commit_group();
                 }
+            } else {
+                __syncwarp();
+                float* const out = static_cast<float*>(a.out) + p.row * a.ld_out + p.f;
+                const int j = lane & 7;
+#pragma unroll 1
+                for (int r = lane >> 3; r < p.valid; r += 4)
+                    if (4 * j < left)
+                        *reinterpret_cast<uint4*>(out + r * a.ld_out + 4 * j) = ld_shared_u4(slots + Sums::at(r, j));
             }
             return;
         }
@@ -204,28 +218,18 @@ __device__ __forceinline__ void finish_block(const Fp4Args& fa, const CUtensorMa
         blk.template take<kBF16>([&](int o, int k, float r) { v[kStep * o][k] += r; });
         __syncwarp();
     }
-    bool whole = true;
-    if constexpr (kMode == ffn::kSeg) {
-        whole = p.rows == 32;
-        if (p.rows > p.valid) {  // an expert's gap rows: zeros
-#pragma unroll
-            for (int o = 0; o < 4; o += kStep)
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (8 * (k >> 1) + tr + (k & 1) >= p.valid) v[o][k] = 0.0f;
-        }
-    }
+    const bool whole = kMode == ffn::kRows || p.valid == 32;
     blk.template stage<kBF16>([&](int o, int k) { return v[kStep * o][k]; });
     if (whole) {
         fence_proxy_async_smem();
         __syncwarp();
-        if (left > 0 && p.rows > 0 && elect_one()) {
+        if (left > 0 && p.valid > 0 && elect_one()) {
             tma_store_2d(tmC, slot, p.f, (int)p.row);
             bulk_commit_group();
         }
     } else {
         __syncwarp();
-        blk.flush(static_cast<uint16_t*>(a.out) + p.row * a.ld_out + p.f, a.ld_out, p.rows, left);
+        blk.flush(static_cast<uint16_t*>(a.out) + p.row * a.ld_out + p.f, a.ld_out, p.valid, left);
     }
 }
 }  // namespace gf4
@@ -445,7 +449,7 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
             uint32_t it = 0, s = 0, os = 0, oph = 0;
             bool ok = true;
             Item w;
-            for (int t = pair; ok && item_of<kMode, kGated>(args, t, seg_tiles, w); t += num_pairs)
+            for (int t = pair; ok && item_of<kMode, kGated>(args, t, seg_tiles, w); t += num_pairs) {
                 for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
                     if (it >= ring) {
                         if (!wait_bounded(smem_u32(&bar_empty[os]), oph, abort, args.timeout_ns, args.status, 47)) {
@@ -460,6 +464,7 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
                     mbar_arrive(smem_u32(&bar_full[s]));
                     if (++s == kStages) s = 0;
                 }
+            }
         }
     } else {
         // ------------------------------ epilogue (warps 2..9, both CTAs) ---------------------
@@ -472,8 +477,7 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
         for (int t = pair; item_of<kMode, kGated>(args, t, seg_tiles, w); t += num_pairs) {
             const uint32_t b = acc & 1u, aph = (acc >> 1) & 1u;
             ++acc;
-            const int total = w.valid + w.zeros;
-            const int chunks = (total + 31) / 32;
+            const int chunks = (w.valid + 31) / 32;
             Place place;
             place.f = kGated ? w.f0 + (int)rank * 64 + q * 16 : w.f0 + (int)rank * 128 + q * 32;
             place.out_base = 0;
@@ -481,7 +485,6 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
             auto at_chunk = [&](int c) {
                 place.row = (int64_t)w.r0 + c * 32;
                 place.valid = min(32, w.valid - c * 32);
-                place.rows = min(32, total - c * 32);
             };
             // bias and factor of the thread's 4 lanes (feats is a multiple of 8, so octets are whole)
             float bias[4], gp[4];
@@ -558,7 +561,7 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i / 8][i % 8] = 0.0f;
                         if (pass == kWarm)
-                            place.valid = place.rows = 0;
+                            place.valid = 0;
                         else
                             fetch_ahead<kGated>(fargs, place, slot, lane, ahead);
                         const float4* d = reinterpret_cast<const float4*>(
@@ -583,7 +586,7 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
                         }
                     }
                     const Place here = place;
-                    finish_block<kBF16, kMode, kGated>(fargs, &tmC, v, gp, bias, here, ahead, slot, lane, [&]() {
+                    finish_block<kBF16, kMode, kGated>(fargs, &tmC, v, gp, bias, here, ahead, slots, slot, lane, [&]() {
                         if (pass == kWhole && c + 2 < chunks) {
                             at_chunk(c + 2);
                             fetch_ahead<kGated>(fargs, place, slot, lane, ahead);

@@ -23,8 +23,12 @@ int go_of(const Fp4Call& c, DeviceInfo* dev, cudaStream_t stream) {
         return rc;
     CUtensorMap tc = {};
     const dtc::FfnArgs& e = c.ffn.args;
-    if (!e.out_f32) {
-        // blocks of 32 rows and 32 features (gated 16), in the order of the epilogue's slots
+    // the result: blocks of 32 rows and 32 features (gated 16), in the order of the epilogue's slots
+    if (e.out_f32) {
+        rc = make_tmap(&tc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, e.out, e.feats, e.rows, e.ld_out, 32, 32,
+                       CU_TENSOR_MAP_SWIZZLE_128B, "the result");
+        if (rc) return rc;
+    } else {
         rc = make_tmap(&tc, kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, e.out, e.feats,
                        e.rows, e.ld_out, kGated ? 16 : 32, 32,
                        kGated ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B, "the result");
