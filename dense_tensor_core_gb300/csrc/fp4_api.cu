@@ -326,6 +326,7 @@ int gemm_fp4(int dtype, const fp4_matrix* A, const fp4_matrix* B, void* C, const
     if ((rc = check_workspace(o.workspace)) || (rc = check_rows("C", C, M, N, &o.ldc))) return rc;
     if (o.tile_rows < 0 || o.tile_rows > 256 || o.tile_rows % 32 || (o.tile_rows && o.tile_rows < M && o.tile_rows % 64))
         return fail(GEMM_ERR_INVALID_ARG, "tile_rows %d is not one that %lld rows can have", o.tile_rows, (long long)M);
+    if (o.split_k < 0) return fail(GEMM_ERR_INVALID_ARG, "split_k is negative");
     if (M == 0 || N == 0) return GEMM_OK;
     if ((rc = check_buffers(A, la, true, false, -1, "A")) || (rc = check_buffers(B, lb, true, false, -1, "B")))
         return rc;
@@ -374,8 +375,10 @@ int gemm_fp4(int dtype, const fp4_matrix* A, const fp4_matrix* B, void* C, const
     c.mx = A->format == FP4_MXFP4;
     c.args.sets = (int)la.sets;
     c.args.p_groups = (int)lb.groups;
-    c.args.p_scale = B->row_scale;
-    c.args.q_scale = A->row_scale;
+    if (K > 0) {  // (without elements there are no factors to apply, nor have they been written)
+        c.args.p_scale = B->row_scale;
+        c.args.q_scale = A->row_scale;
+    }
     c.p_scales = B->scales;
     c.q_scales = A->scales;
     c.p_chunks = lb.scale_bytes / 512;

@@ -53,7 +53,7 @@ typedef struct {
 
 /* Sizes of the buffers of a stack (its pointers are not read). No CUDA call. INVALID_ARG for an unknown
  * format, sizes below 0, K not a multiple of 32, K above 2^24, gated with rows % 16 != 0, matrices * rows
- * or the scales' chunks above 2^31 - 1 - 256, or NULL pointers. */
+ * or the scales' chunks above 2^31 - 1 - 256, or NULL pointers. The pages have no counterpart. */
 int fp4_layout(const fp4_matrix* q, fp4_info* info);
 
 /*
@@ -66,16 +66,18 @@ int fp4_layout(const fp4_matrix* q, fp4_info* info);
  *          to e2m1, 6 where it is above
  * A block that holds an infinity or NaN gets the NaN scale (UE4M3 0x7F, E8M0 0xFF), so its values are NaN;
  * the other blocks are quantised as if it were zero. out->row_scale is required for NVFP4 and not written
- * for MXFP4.
+ * for MXFP4. The pages have no counterpart.
  */
 int fp4_quantize(int dtype, const void* x, int64_t ld, const fp4_matrix* out, dtc_stream_t stream);
 
 /* The values that q stands for, to out [matrices * rows, K] dense (dtype 0 bf16, 1 fp16, 2 fp32; each
- * rounded once: what fp4_quantize made of 16-bit rows is exact in bf16 and fp32). */
+ * rounded once: what fp4_quantize made of 16-bit rows is exact in bf16 and fp32).
+ * The pages have no counterpart. */
 int fp4_dequantize(int dtype, const fp4_matrix* q, void* out, dtc_stream_t stream);
 
 /* Scales as other programs hold them, [matrices * rows, K / block] bytes row-major and dense, into q's
- * order: writes q->scales (its codes and factors are used as they are, and not read). */
+ * order: writes q->scales (its codes and factors are used as they are, and not read).
+ * The pages have no counterpart. */
 int fp4_pack_scales(const void* scales, const fp4_matrix* q, dtc_stream_t stream);
 
 typedef struct {
@@ -98,12 +100,13 @@ typedef struct {
  * The tensor cores multiply codes and scales exactly and sum in fp32; the rows' factors multiply the sum.
  * N % 8 == 0. opts may be NULL. The workspace lets products of few tiles split K over more SMs.
  * Degenerate sizes: M == 0 or N == 0 does nothing; K == 0 gives Z = bias. INVALID_ARG as gemm_act, for
- * matrices of other shapes or formats, and for a tile or split that the call cannot have.
+ * matrices of other shapes or formats, and for a tile or split that the call cannot have. The
+ * pages have no counterpart.
  */
 int gemm_fp4(int dtype, const fp4_matrix* A, const fp4_matrix* B, void* C, const gemm_fp4_options* opts,
              dtc_stream_t stream);
 
-/* Bytes of workspace with which gemm_fp4 would split K (0: it would not). */
+/* Bytes of workspace with which gemm_fp4 would split K (0: it would not). The pages have no counterpart. */
 int gemm_fp4_workspace_size(int64_t M, int64_t N, int64_t K, int activation, uint64_t* bytes);
 
 /*
@@ -112,12 +115,14 @@ int gemm_fp4_workspace_size(int64_t M, int64_t N, int64_t K, int activation, uin
  * q(v): v as fp4_quantize makes it, in the weights' format; h is rounded to dtype first. w_in: a stack of E
  * matrices [F, H], gated [2F, H] and gated; w_out: E of [H, F]; H and F multiples of 32. The rest as
  * moe_experts; the weight multiplies the second product's sum. `buffer`: moe_experts_fp4_buffer_size bytes.
+ * The pages have no counterpart.
  */
 int moe_experts_fp4(int dtype, const void* x, const fp4_matrix* w_in, const fp4_matrix* w_out,
                     const void* weights, const void* plan, void* y, int64_t T, int k,
                     const moe_experts_options* opts, void* buffer, uint64_t buffer_bytes,
                     dtc_stream_t stream);
 
+/* Bytes of the buffer of moe_experts_fp4. The pages have no counterpart. */
 int moe_experts_fp4_buffer_size(int format, int64_t T, int k, int64_t E, int64_t H, int64_t F,
                                 int activation, uint64_t* bytes);
 
