@@ -25,7 +25,15 @@ struct Fp4Call {
     const void* q_scales = nullptr;
     uint64_t p_chunks = 0, q_chunks = 0;
 };
-int launch_gemm_fp4(const Fp4Call& c, DeviceInfo* dev, cudaStream_t stream);
+int launch_gemm_nvfp4_rows(const Fp4Call& c, DeviceInfo* dev, cudaStream_t stream);
+int launch_gemm_mxfp4_rows(const Fp4Call& c, DeviceInfo* dev, cudaStream_t stream);
+int launch_gemm_nvfp4_experts(const Fp4Call& c, DeviceInfo* dev, cudaStream_t stream);
+int launch_gemm_mxfp4_experts(const Fp4Call& c, DeviceInfo* dev, cudaStream_t stream);
+inline int launch_gemm_fp4(const Fp4Call& c, DeviceInfo* dev, cudaStream_t stream) {
+    if (c.ffn.mode == dtc::ffn::kRows)
+        return c.mx ? launch_gemm_mxfp4_rows(c, dev, stream) : launch_gemm_nvfp4_rows(c, dev, stream);
+    return c.mx ? launch_gemm_mxfp4_experts(c, dev, stream) : launch_gemm_nvfp4_experts(c, dev, stream);
+}
 // The same of one matrix for a handful of rows, NVFP4 (gemm_fp4_skinny.cuh). wide: 16 rows at a time instead of 8.
 int launch_fp4_skinny(const Fp4Call& c, bool wide, cudaStream_t stream);
 

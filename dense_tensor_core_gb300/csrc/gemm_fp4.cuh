@@ -62,51 +62,111 @@ static_assert(2 * kNarrow + 4 * kSfStage <= kTmemCols, "Tensor Memory budget");
 constexpr int kWideTop = kTmemCols - 2 * kSfStage;
 constexpr bool tiles_touch(int n) { return 2 * n > kWideTop; }
 
-// The t-th item of the launch (see ffn::get_item).
-template <int kMode, bool kGated>
-__device__ __forceinline__ bool item_of(const FfnArgs& a, int t, int seg_tiles, ffn::Item& w) {
-    constexpr int kFeats = kGated ? 128 : 256;
-    int tile = t, split = -1;
-    if (a.splits > 1) {
-        tile = t / a.splits;
+// The items of a pair, in their order (see ffn::get_item): every role walks its own copy. Each step also
+// prepares the next: without split tiles it goes on from the last by additions (a division takes a thread some
+// 100 cycles, and a tile has three), and the record of an expert's rows is fetched a step ahead.
+template <int kMode, bool kGated, bool kSplit>
+struct Walk {
+    const FfnArgs& a;
+    int seg_tiles, step;
+    int major, minor;  // kRows: group of feature tiles, tile in it; experts: tile of rows, feature tile
+    int major_step, minor_step;
+    int t;
+    int4 rec;
+
+    __device__ __forceinline__ Walk(const FfnArgs& args, int first, int stride, int tiles)
+        : a(args), seg_tiles(tiles), step(stride), major(0), minor(first), major_step(0), minor_step(stride), t(first) {
+        if constexpr (kMode == ffn::kSeg) {
+            major = first / a.num_ft;
+            minor = first - major * a.num_ft;
+            major_step = stride / a.num_ft;
+            minor_step = stride - major_step * a.num_ft;
+        }
+        settle();
+    }
+    // minor into its range, and the record there
+    __device__ __forceinline__ void settle() {
+        if constexpr (kMode == ffn::kSeg) {
+            int rt = major;
+            if constexpr (kSplit) {
+                int split;
+                rt = tile_at(split) / a.num_ft;
+            } else if (minor >= a.num_ft) {
+                minor -= a.num_ft;
+                rt = ++major;
+            }
+            if (rt < seg_tiles) rec = reinterpret_cast<const int4*>(a.tiles)[rt];
+        } else if constexpr (!kSplit) {
+            int in = group_tiles();
+            while (in > 0 && minor >= in) {
+                minor -= in;
+                ++major;
+                in = group_tiles();
+            }
+        }
+    }
+    __device__ __forceinline__ int group_width() const { return min(ffn::kGroupF, a.num_ft - major * ffn::kGroupF); }
+    __device__ __forceinline__ int group_tiles() const { return group_width() * a.num_rt; }
+    __device__ __forceinline__ int tile_at(int& split) const {
+        int tile = t / a.splits;
+        split = -1;
         if (tile < a.split_tiles)
             split = t - tile * a.splits;
         else
             tile = t - a.split_tiles * (a.splits - 1);
+        return tile;
     }
-    w.tile = tile;
-    w.split = split;
-    w.expert = 0;
-    if constexpr (kMode == ffn::kRows) {
-        if (tile >= a.num_ft * a.num_rt) return false;
-        int ft, rt;
-        tile_coords(tile, a.num_ft, a.num_rt, ffn::kGroupF, ft, rt);
-        w.f0 = ft * kFeats;
-        w.r0 = rt * a.tile_n;
-        w.valid = min(a.tile_n, a.rows - w.r0);
-        w.n = a.tile_n;
-        w.krow = w.r0 >> 7;  // first scale group of the rows
-    } else {
-        const int rt = tile / a.num_ft;
-        if (rt >= a.max_tiles) return false;
-        const int4 s = reinterpret_cast<const int4*>(a.tiles)[rt];
-        if (rt >= seg_tiles) return false;
-        // a record that no plan of these sizes holds ends the walk
-        if ((unsigned)s.x >= (unsigned)a.experts || s.z < 1 || s.z > a.tile_n || s.y < 0 ||
-            s.y > a.rows - s.z || (s.y & (ffn::kSegAlign - 1)))
-            return false;
-        w.f0 = (tile - rt * a.num_ft) * kFeats;
-        w.expert = s.x;
-        w.r0 = s.y;
-        w.valid = s.z;
-        w.krow = 2 * rt;  // the rows' scales stand tile by tile
-        w.n = ffn::round32(w.valid);
+    // The item; false past the end.
+    __device__ __forceinline__ bool next(ffn::Item& w) {
+        constexpr int kFeats = kGated ? 128 : 256;
+        w.split = -1;
+        w.expert = 0;
+        if constexpr (kSplit) w.tile = tile_at(w.split);
+        if constexpr (kMode == ffn::kRows) {
+            int ft, rt;
+            if constexpr (kSplit) {
+                if (w.tile >= a.num_ft * a.num_rt) return false;
+                tile_coords(w.tile, a.num_ft, a.num_rt, ffn::kGroupF, ft, rt);
+            } else {
+                const int width = group_width();
+                if (width <= 0) return false;
+                rt = width == ffn::kGroupF ? minor / ffn::kGroupF : minor / width;
+                ft = major * ffn::kGroupF + minor - rt * width;
+            }
+            w.f0 = ft * kFeats;
+            w.r0 = rt * a.tile_n;
+            w.valid = min(a.tile_n, a.rows - w.r0);
+            w.n = a.tile_n;
+            w.krow = w.r0 >> 7;  // first scale group of the rows
+        } else {
+            int rt = major, ft = minor;
+            if constexpr (kSplit) {
+                rt = w.tile / a.num_ft;
+                ft = w.tile - rt * a.num_ft;
+            }
+            if (rt >= seg_tiles) return false;
+            // a record that no plan of these sizes holds ends the walk
+            if ((unsigned)rec.x >= (unsigned)a.experts || rec.z < 1 || rec.z > a.tile_n || rec.y < 0 ||
+                rec.y > a.rows - rec.z || (rec.y & (ffn::kSegAlign - 1)))
+                return false;
+            w.f0 = ft * kFeats;
+            w.expert = rec.x;
+            w.r0 = rec.y;
+            w.valid = rec.z;
+            w.n = ffn::round32(rec.z);
+            w.krow = 2 * rt;  // the rows' scales stand tile by tile
+        }
+        const int kb = (a.red + kBK - 1) / kBK;
+        w.kb0 = kSplit && w.split >= 0 ? min(kb, w.split * a.kb_per_split) : 0;
+        w.kb1 = kSplit && w.split >= 0 ? min(kb, w.kb0 + a.kb_per_split) : kb;
+        t += step;
+        major += major_step;
+        minor += minor_step;
+        settle();
+        return true;
     }
-    const int kb = (a.red + kBK - 1) / kBK;
-    w.kb0 = split >= 0 ? min(kb, split * a.kb_per_split) : 0;
-    w.kb1 = split >= 0 ? min(kb, w.kb0 + a.kb_per_split) : kb;
-    return true;
-}
+};
+
 // What a block's epilogue reads from memory, fetched ahead of its sums: the residual, and the factor of the
 // lane's row.
 template <bool kGated>
@@ -114,12 +174,12 @@ struct Ahead {
     uint4 res[kGated ? 2 : 4];
     float gq;
 };
-// (Experts' rows have neither residual nor bias, and no code for them: what a launch does not use costs it
-// instruction fetches, 9 % of 4096 x 4096 x 2048 with SwiGLU.)
-template <int kMode, bool kGated>
+// (What a launch does not use costs it instruction fetches, with the residual's code 9 % of 4096 x 4096 x 2048
+// with SwiGLU: split tiles and a residual have kernels of their own.)
+template <bool kGated, bool kSplit, bool kResidual>
 __device__ __forceinline__ void fetch_ahead(const Fp4Args& f, const ffn::Place& p, uint32_t slot, int lane,
                                             Ahead<kGated>& x) {
-    if (kMode == ffn::kRows && f.e.residual)
+    if (kResidual && (!kSplit || f.e.residual))
         ffn::Block<kGated ? 2 : 4>(slot, lane).fetch(
             x.res, static_cast<const uint16_t*>(f.e.residual) + p.row * f.e.ld_res + p.f, f.e.ld_res, p.valid,
             f.e.feats - p.f);
@@ -144,7 +204,7 @@ __device__ __forceinline__ void act_block(float (&v)[4][8]) {
 // residual, store. The residual goes through the slot first, then `refill` may fetch the next block's. Whole
 // blocks leave by TMA (the slot's order of 16-byte pieces is the copy's swizzle); blocks that end inside an
 // expert's rows leave piece by piece. The slot may be reused when the copy of two blocks before has read it.
-template <bool kBF16, int kMode, bool kGated, typename Refill>
+template <bool kBF16, int kMode, bool kGated, bool kSplit, bool kResidual, typename Refill>
 __device__ __forceinline__ void finish_block(const Fp4Args& fa, const CUtensorMap* tmC, float (&v)[4][8],
                                              const float (&gp)[4], const float (&bias)[4], const ffn::Place& p,
                                              Ahead<kGated>& x, uint32_t slots, uint32_t slot, int lane,
@@ -197,7 +257,7 @@ __device__ __forceinline__ void finish_block(const Fp4Args& fa, const CUtensorMa
     if (elect_one()) bulk_wait_group_read<1>();  // (the same lane each time)
     __syncwarp();
     const Block blk(slot, lane);
-    const bool residual = kMode == ffn::kRows && a.residual;
+    const bool residual = kResidual && (!kSplit || a.residual);
     if (residual) blk.put(x.res);
     refill();
     if constexpr (kGated) {
@@ -237,7 +297,7 @@ __device__ __forceinline__ void finish_block(const Fp4Args& fa, const CUtensorMa
 }
 }  // namespace gf4
 
-template <bool kMx, bool kBF16, int kMode, bool kGated>
+template <bool kMx, bool kBF16, int kMode, bool kGated, bool kSplit, bool kResidual>
 __global__ void __launch_bounds__(gf4::kThreads, 1)
     gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ FfnQMaps tmQ,
                     const __grid_constant__ CUtensorMap tmSP, const __grid_constant__ CUtensorMap tmSQ,
@@ -311,7 +371,8 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
             uint32_t it = 0;
             bool ok = true;
             Item w;
-            for (int t = pair; ok && item_of<kMode, kGated>(args, t, seg_tiles, w); t += num_pairs) {
+            Walk<kMode, kGated, kSplit> walk(args, pair, num_pairs, seg_tiles);
+            while (ok && walk.next(w)) {
                 const int nh = w.n / 2;  // rows of Q per CTA
                 const int q_row = w.r0 + (int)rank * nh;
                 const int f_row = kGated ? w.f0 + (int)rank * 64 : w.f0 + (int)rank * 128;
@@ -373,7 +434,8 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
             int before = 0;  // rows of the tile before
             bool ok = true, issued = false;
             Item w;
-            for (int t = pair; ok && item_of<kMode, kGated>(args, t, seg_tiles, w); t += num_pairs) {
+            Walk<kMode, kGated, kSplit> walk(args, pair, num_pairs, seg_tiles);
+            while (ok && walk.next(w)) {
                 const uint32_t b = acc & 1u, aph = (acc >> 1) & 1u;
                 ok = wait_bounded(smem_u32(&bar_tempty[b]), aph ^ 1u, abort, args.timeout_ns, args.status, 42);
                 if (ok && before + w.n > fargs.acc_top) {  // the columns of the tile before: wait until they are read
@@ -452,7 +514,8 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
             uint32_t it = 0, s = 0, os = 0, oph = 0;
             bool ok = true;
             Item w;
-            for (int t = pair; ok && item_of<kMode, kGated>(args, t, seg_tiles, w); t += num_pairs) {
+            Walk<kMode, kGated, kSplit> walk(args, pair, num_pairs, seg_tiles);
+            while (ok && walk.next(w)) {
                 for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
                     if (it >= ring) {
                         if (!wait_bounded(smem_u32(&bar_empty[os]), oph, abort, args.timeout_ns, args.status, 47)) {
@@ -477,7 +540,8 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
         uint32_t acc = 0;
         bool warm = true;
         Item w;
-        for (int t = pair; item_of<kMode, kGated>(args, t, seg_tiles, w); t += num_pairs) {
+        Walk<kMode, kGated, kSplit> walk(args, pair, num_pairs, seg_tiles);
+        while (walk.next(w)) {
             const uint32_t b = acc & 1u, aph = (acc >> 1) & 1u;
             ++acc;
             const int chunks = (w.valid + 31) / 32;
@@ -511,19 +575,21 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
             const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + acc_col(b, w.n);
             const bool empty = w.kb0 == w.kb1;  // no K-block: the sum is zero
             const int blocks = args.tile_n / 32;
-            const int64_t quarter = ((int64_t)w.tile * 2 + rank) * 4 + q;
+            const int64_t quarter = kSplit ? ((int64_t)w.tile * 2 + rank) * 4 + q : 0;
             // the passes of gemm16_ffn.cuh's epilogue: a first one of no rows that fetches its instructions,
             // the sums of a whole tile, those of a piece, and all pieces' sums
             constexpr int kWarm = 0, kWhole = 1, kPiece = 2, kJoin = 3;
-            const int main_pass = w.split < 0 ? kWhole : kPiece;
+            const int main_pass = !kSplit || w.split < 0 ? kWhole : kPiece;
             int pass = warm ? kWarm : main_pass;
+            auto is_piece = [&]() { return kSplit && pass == kPiece; };
+            auto is_sum = [&]() { return kSplit ? pass == kWhole || pass == kPiece : pass != kWarm; };
             bool gave_up = false;
 #pragma unroll 1
             while (true) {
-                if (pass == kWhole || pass == kPiece) {
+                if (is_sum()) {
                     if (pass == kWhole && turn < chunks) {
                         at_chunk(turn);
-                        fetch_ahead<kMode, kGated>(fargs, place, slot, lane, ahead);
+                        fetch_ahead<kGated, kSplit, kResidual>(fargs, place, slot, lane, ahead);
                     }
                     int ok = 1;
                     if (lane == 0)
@@ -542,14 +608,14 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
                 for (int c = turn; c < end; c += 2) {
                     float v[4][8];
                     at_chunk(c);
-                    if (pass == kWhole || pass == kPiece) {
+                    if (is_sum()) {
                         tmem_load_fragment32(taddr + c * 32, v);
                         if (c + 2 >= chunks) hand_back();
                         if (empty) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i) v[i / 8][i % 8] = 0.0f;
                         }
-                        if (pass == kPiece) {
+                        if (is_piece()) {
                             float4* const d = reinterpret_cast<float4*>(
                                 args.partial + ((quarter * args.splits + w.split) * blocks + c) * 1024) + lane;
 #pragma unroll
@@ -566,10 +632,10 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
                         if (pass == kWarm)
                             place.valid = 0;
                         else
-                            fetch_ahead<kMode, kGated>(fargs, place, slot, lane, ahead);
+                            fetch_ahead<kGated, kSplit, kResidual>(fargs, place, slot, lane, ahead);
                         const float4* d = reinterpret_cast<const float4*>(
                             args.partial + (quarter * args.splits * blocks + c) * 1024) + lane;
-                        const int pieces = pass == kWarm ? 0 : args.splits;
+                        const int pieces = !kSplit || pass == kWarm ? 0 : args.splits;
 #pragma unroll 4
                         for (int s = 0; s < pieces; ++s, d += blocks * 256) {
 #pragma unroll
@@ -589,12 +655,14 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
                         }
                     }
                     const Place here = place;
-                    finish_block<kBF16, kMode, kGated>(fargs, &tmC, v, gp, bias, here, ahead, slots, slot, lane, [&]() {
-                        if (pass == kWhole && c + 2 < chunks) {
+                    auto refill = [&]() {
+                        if (is_sum() && c + 2 < chunks) {
                             at_chunk(c + 2);
-                            fetch_ahead<kMode, kGated>(fargs, place, slot, lane, ahead);
+                            fetch_ahead<kGated, kSplit, kResidual>(fargs, place, slot, lane, ahead);
                         }
-                    });
+                    };
+                    finish_block<kBF16, kMode, kGated, kSplit, kResidual>(fargs, &tmC, v, gp, bias, here, ahead, slots,
+                                                                          slot, lane, refill);
                     slot = 2 * slots + kSlot - slot;
                 }
                 if (pass == kWarm) {
@@ -602,7 +670,7 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
                     pass = main_pass;
                     continue;
                 }
-                if (pass != kPiece || turn >= chunks) break;
+                if (!is_piece() || turn >= chunks) break;
                 uint32_t* const counter = args.counters + ((int64_t)w.tile * 2 + rank) * kEpWarps + (warp - 2);
                 __threadfence();  // this lane's pieces are visible before the count
                 __syncwarp();

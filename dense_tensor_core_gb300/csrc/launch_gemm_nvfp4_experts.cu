@@ -1,0 +1,10 @@
+// launch_gemm_nvfp4_experts.cu -- the NVFP4 products of experts' rows (gemm_fp4.cuh), plain and gated.
+#include "launch_gemm_fp4.h"
+
+namespace dtc_host {
+
+int launch_gemm_nvfp4_experts(const Fp4Call& c, DeviceInfo* dev, cudaStream_t stream) {
+    return launch_gemm_fp4_experts_any<false>(c, dev, stream);
+}
+
+}  // namespace dtc_host
