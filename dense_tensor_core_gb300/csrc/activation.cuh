@@ -37,6 +37,12 @@ __host__ __device__ constexpr int act_of_gate(int a) {
 constexpr float kGeluC1 = 0.7978845608028654f;      // sqrt(2/pi)
 constexpr float kGeluC3 = 0.044715f;
 constexpr float kRsqrt2Pi = 0.3989422804014327f;    // 1/sqrt(2 pi)
+// P's coefficients, the highest power first.
+__device__ __forceinline__ constexpr float mills(int i) {
+    constexpr float c[8] = {0.03567477688193321f, -0.15720310807228088f, 0.20635353028774261f, -0.05368367210030556f,
+                            0.12856164574623108f, 0.09991348534822464f,  0.12075395882129669f, 0.11962930113077164f};
+    return c[i];
+}
 
 // 1 / (1 + e^-v). For v below about -87.3 the fast division gives 0 (its divisor is above 2^126), the
 // limit of the exact value: an absolute error below 2^-125.
@@ -47,14 +53,9 @@ __device__ __forceinline__ float normal_cdf(float z, float& e) {
     const float a = fabsf(z);
     const float t = __fdividef(1.0f, fmaf(0.3f, a, 1.0f));
     e = __expf(-0.5f * z * z);
-    float p = 0.03567477688193321f;
-    p = fmaf(p, t, -0.15720310807228088f);
-    p = fmaf(p, t, 0.20635353028774261f);
-    p = fmaf(p, t, -0.05368367210030556f);
-    p = fmaf(p, t, 0.12856164574623108f);
-    p = fmaf(p, t, 0.09991348534822464f);
-    p = fmaf(p, t, 0.12075395882129669f);
-    p = fmaf(p, t, 0.11962930113077164f);
+    float p = mills(0);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) p = fmaf(p, t, mills(i));
     const float h = p * t * e;
     return z < 0.0f ? h : 1.0f - h;
 }

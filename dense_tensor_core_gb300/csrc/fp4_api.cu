@@ -167,31 +167,45 @@ void size_split(Fp4Plan* p, uint64_t counters) {
     p->bytes = counters + (uint64_t)p->split_tiles * p->splits * p->tile_n * 1024;
 }
 
-// Modelled time of a launch in us, less what every launch costs, after measured times (4096 x 4096 x 1024: 18.3
-// in tiles of 192 rows, 20.3 of 256; x 8192: 69, 59 and 54 of 128, 192 and 256): a stage of 256 elements takes
-// the issuing thread's 0.25 us, above 128 rows the tensor pipe's; a tile whose accumulator touches its
-// predecessor's waits until that is read.
-double item_cost(const Fp4Plan& p, int kb, int pairs) {
-    const double block = 0.25 + 0.0003 * std::max(0, p.tile_n - 128);
-    const double item = 1.2 + (dtc::gf4::tiles_touch(p.tile_n) ? 1.2 : 0.0);
-    const int64_t split_items = (int64_t)p.split_tiles * p.splits, whole = p.tiles - p.split_tiles;
-    double cost = 0.0114 * p.tile_n + (double)((whole + pairs - 1) / pairs) * (kb * block + item);
+// Modelled time of a launch in us, less what every launch costs, after measured times (4096 x 4096 x 2048: 22, 20
+// and 23 in tiles of 128, 192 and 256 rows; x 8192: 66, 57 and 51): a stage of 256 elements takes the issuing
+// thread's 0.25 us, above 128 rows the tensor pipe's; a tile whose accumulator touches its predecessor's waits until
+// that is read, `epilogue` us more with what its epilogue does.
+double item_cost(const Fp4Plan& p, int kb, int pairs, double epilogue) {
+    const double block = 0.25 + 0.0006 * std::max(0, std::min(p.tile_n, 192) - 128);
+    const int64_t split_items = (int64_t)p.split_tiles * p.splits;
+    const int64_t waves = (p.tiles - p.split_tiles + pairs - 1) / pairs, split_waves = (split_items + pairs - 1) / pairs;
+    double cost = 0.0114 * p.tile_n + (double)waves * (kb * block + 1.2);
     if (p.splits > 1) {
-        cost += (double)((split_items + pairs - 1) / pairs) * (p.kb_per_split * block + item);
-        cost += whole > 0 ? 0.0062 * p.tile_n * p.splits : 2.2 + 0.01 * p.tile_n * p.splits;
+        cost += (double)split_waves * (p.kb_per_split * block + 1.2);
+        cost += waves > 0 ? 0.0062 * p.tile_n * p.splits : 2.2 + 0.01 * p.tile_n * p.splits;
     }
+    if (dtc::gf4::tiles_touch(p.tile_n)) cost += (double)(waves + split_waves - 1) * (1.2 + epilogue);
     return cost;
+}
+
+// What activation and residual add to a tile of 256 rows over one of 192, whose epilogue runs under the next tile's
+// products. Measured in tiles of 192 and 256, us, at 4096 x 4096 x 8192 and 8192 x 8192 x 8192:
+//   neither 58, 51       silu 62, 58 and 219, 212    gelu 63, 63 and 210, 229     gelu_tanh 63, 59   geglu 59, 54
+//   residual 60.5, 60    both 63, 64 and 224, 235    64, 69 and 223, 243          64, 65             61, 58
+double epilogue_cost(int act, bool residual) {
+    double us = residual ? (dtc::act_gated(act) ? 0.6 : 1.5) : 0.0;
+    if (act == GEMM_ACT_GELU) us += 3.0;
+    else if (act == GEMM_ACT_SILU || act == GEMM_ACT_GELU_TANH) us += 1.2;
+    else if (act == GEMM_ACT_GEGLU) us += 0.5;
+    return us;
 }
 
 // Tile rows and K splits of one matrix's product: the cheapest by item_cost. Tiles of part of the rows
 // start at a multiple of 64 (their scales' Tensor Memory columns do at one of two).
 // want_n, want_split: the caller's (0: chosen).
-Fp4Plan plan_rows(int64_t rows, int64_t feats, bool gated, int64_t K, int pairs, uint64_t ws_bytes, int want_n,
-                  int want_split) {
+Fp4Plan plan_rows(int64_t rows, int64_t feats, int act, bool residual, int64_t K, int pairs, uint64_t ws_bytes,
+                  int want_n, int want_split) {
     Fp4Plan best;
     double cost = 0;
-    const int ft = num_feature_tiles(feats, gated);
+    const int ft = num_feature_tiles(feats, dtc::act_gated(act));
     const int kb = ceil_div(K, 4 * kBK);
+    const double epilogue = epilogue_cost(act, residual);
     for (int n = 32; n <= 256; n += 32) {
         if (n < rows && n % 64) continue;
         if (want_n ? n != want_n : n > 32 && n - 32 >= rows) continue;
@@ -208,7 +222,7 @@ Fp4Plan plan_rows(int64_t rows, int64_t feats, bool gated, int64_t K, int pairs,
             p.split_tiles = splits > 1 ? (int)split_tiles : 0;
             size_split(&p, zero_words_bytes(pairs));
             if (p.bytes > ws_bytes || p.bytes > (64ull << 20)) return;
-            const double c = item_cost(p, kb, pairs);
+            const double c = item_cost(p, kb, pairs, epilogue);
             if (best.num_ft == 0 || c < cost) {
                 best = p;
                 cost = c;
@@ -246,7 +260,7 @@ Fp4Plan plan_seg(int64_t T, int k, int64_t E, int64_t max_tiles, int64_t feats, 
         q.kb_per_split = ceil_div(kb, s);
         if (s > 1 && ceil_div(kb, q.kb_per_split) != s) continue;
         q.split_tiles = s > 1 ? (int)q.tiles : 0;
-        const double c = item_cost(q, kb, pairs);
+        const double c = item_cost(q, kb, pairs, 0.0);  // (the tile's rows are not chosen)
         if (s == 1 || c < cost) {
             cost = c;
             p.splits = s;
@@ -340,8 +354,8 @@ int gemm_fp4(int dtype, const fp4_matrix* A, const fp4_matrix* B, void* C, const
     if (o.bias && (rc = check_device_ptr(o.bias, dev, "bias"))) return rc;
     if (o.residual && (rc = check_device_ptr(o.residual, dev, "residual"))) return rc;
     const bool few = !o.tile_rows && !o.split_k && fp4_skinny(A->format, M, Nb, K);
-    const Fp4Plan p = few ? Fp4Plan() : plan_rows(M, N, gated, K, pairs_of(info), o.workspace ? o.workspace_bytes : 0,
-                                                  o.tile_rows, o.split_k);
+    const Fp4Plan p = few ? Fp4Plan() : plan_rows(M, N, o.activation, o.residual, K, pairs_of(info),
+                                                  o.workspace ? o.workspace_bytes : 0, o.tile_rows, o.split_k);
     if (!few && p.num_ft == 0)
         return o.tile_rows || o.split_k
                    ? fail(GEMM_ERR_INVALID_ARG, "tile_rows %d and split_k %d are not what this call can have",
@@ -398,7 +412,9 @@ int gemm_fp4_workspace_size(int64_t M, int64_t N, int64_t K, int activation, uin
     int dev;
     DeviceInfo* info;
     if ((rc = current_device(&dev, &info))) return rc;
-    *bytes = plan_rows(M, N, dtc::act_gated(activation), K, pairs_of(info), ~0ull, 0, 0).bytes;
+    // with a residual or without
+    for (int r = 0; r < 2; ++r)
+        *bytes = std::max(*bytes, plan_rows(M, N, activation, r, K, pairs_of(info), ~0ull, 0, 0).bytes);
     return GEMM_OK;
 }
 

@@ -186,16 +186,117 @@ __device__ __forceinline__ void fetch_ahead(const Fp4Args& f, const ffn::Place& 
     x.gq = f.q_scale && lane < p.valid ? f.q_scale[p.row + lane] : 1.0f;
 }
 
+// The activations of a block. act_forward's forms are bound by the special-function unit, which takes a quarter of
+// a warp's lanes in two cycles: an exponential and a reciprocal per value, 16 cycles. Here the values of a thread
+// that belong to one row share a reciprocal (of their divisors' product), and the rest goes two rows to an
+// instruction. The divisors lie in [1, 2] (gelu: up to 20), so that no product overflows:
+//   1 / (1 + e^-w) = n / (1 + E) with E = e^-|w|, n = E for w < 0, else 1
+// and a NaN, which the bounds on their arguments take out, reaches its own value only, through the factor z.
+// 4096 x 4096 x 2048 with gelu_tanh: 25.6 us, 27.0 with act_forward (19.9 without activation); x 8192 with geglu 54
+// and 56.5.
+__device__ __forceinline__ float exp2_ftz(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_ftz(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// z * s for s in [0, 1]: 0 at z = -infinity, the limit, and NaN at NaN.
+__device__ __forceinline__ float2 times_share(float2 z, float2 s) {
+    float2 x;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(x.x) : "f"(z.x), "f"(-3.0e38f));
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(x.y) : "f"(z.y), "f"(-3.0e38f));
+    return fp4::mul2(x, s);
+}
+// d[i] becomes 1 / d[i]; N is 2 or 4.
+template <int N>
+__device__ __forceinline__ void reciprocals(float2 (&d)[N]) {
+    const float2 a = fp4::mul2(d[0], d[1]);
+    if constexpr (N == 2) {
+        const float2 r = make_float2(rcp_ftz(a.x), rcp_ftz(a.y)), d0 = d[0];
+        d[0] = fp4::mul2(r, d[1]);
+        d[1] = fp4::mul2(r, d0);
+    } else {
+        const float2 b = fp4::mul2(d[2], d[3]), ab = fp4::mul2(a, b);
+        const float2 r = make_float2(rcp_ftz(ab.x), rcp_ftz(ab.y));
+        const float2 ra = fp4::mul2(r, b), rb = fp4::mul2(r, a), d0 = d[0], d2 = d[2];
+        d[0] = fp4::mul2(ra, d[1]);
+        d[1] = fp4::mul2(ra, d0);
+        d[2] = fp4::mul2(rb, d[3]);
+        d[3] = fp4::mul2(rb, d2);
+    }
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// act(z) of two rows' values of N features.
+template <int kAct, int N>
+__device__ __forceinline__ void act_rows(float2 (&z)[N]) {
+    auto both = [](float c) { return make_float2(c, c); };
+    if constexpr (kAct == kActRelu) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            z[i].x = z[i].x < 0.0f ? 0.0f : z[i].x;
+            z[i].y = z[i].y < 0.0f ? 0.0f : z[i].y;
+        }
+    } else if constexpr (kAct == kActGelu) {  // activation.cuh's form
+        float2 t[N], a[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            a[i] = make_float2(fminf(fabsf(z[i].x), 64.0f), fminf(fabsf(z[i].y), 64.0f));
+            t[i] = fp4::fma2(both(0.3f), a[i], both(1.0f));
+        }
+        reciprocals(t);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float2 h = both(mills(0));
+#pragma unroll
+            for (int j = 1; j < 8; ++j) h = fp4::fma2(h, t[i], both(mills(j)));
+            const float2 w = fp4::mul2(fp4::mul2(a[i], a[i]), both(-0.5f * kLog2e));
+            h = fp4::mul2(fp4::mul2(h, t[i]), make_float2(exp2_ftz(w.x), exp2_ftz(w.y)));
+            const float2 up = fp4::fma2(h, both(-1.0f), both(1.0f));
+            z[i] = times_share(z[i], make_float2(z[i].x < 0.0f ? h.x : up.x, z[i].y < 0.0f ? h.y : up.y));
+        }
+    } else {
+        float2 e[N], d[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float2 w;  // in units of log 2
+            if constexpr (kAct == kActGeluTanh)
+                w = fp4::mul2(z[i], fp4::fma2(fp4::mul2(z[i], z[i]), both(2.0f * kGeluC1 * kGeluC3 * kLog2e),
+                                              both(2.0f * kGeluC1 * kLog2e)));
+            else
+                w = fp4::mul2(z[i], both(kLog2e));
+            e[i] = make_float2(exp2_ftz(fmaxf(-fabsf(w.x), -150.0f)), exp2_ftz(fmaxf(-fabsf(w.y), -150.0f)));
+            d[i] = fp4::add2(e[i], both(1.0f));
+        }
+        reciprocals(d);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float2 n = make_float2(z[i].x < 0.0f ? e[i].x : 1.0f, z[i].y < 0.0f ? e[i].y : 1.0f);
+            z[i] = times_share(z[i], fp4::mul2(d[i], n));
+        }
+    }
+}
+
 // act() of all of a thread's values (gated: of the gates, each times its up value), one branch for all: the
 // epilogue's instructions of one activation lie together.
 template <bool kGated, int kAct>
 __device__ __forceinline__ void act_block(float (&v)[4][8]) {
+    constexpr int N = kGated ? 2 : 4, kStep = kGated ? 2 : 1;
 #pragma unroll
-    for (int o = 0; o < 4; o += kGated ? 2 : 1) {
-        act_forward(v[o], kAct);
-        if constexpr (kGated) {
+    for (int k = 0; k < 8; k += 2) {
+        float2 z[N];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[o][k] *= v[o + 1][k];
+        for (int i = 0; i < N; ++i) z[i] = make_float2(v[kStep * i][k], v[kStep * i][k + 1]);
+        act_rows<kAct>(z);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if constexpr (kGated) z[i] = fp4::mul2(z[i], make_float2(v[2 * i + 1][k], v[2 * i + 1][k + 1]));
+            v[kStep * i][k] = z[i].x;
+            v[kStep * i][k + 1] = z[i].y;
         }
     }
 }

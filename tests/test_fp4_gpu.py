@@ -1,5 +1,7 @@
 """The 4-bit operators on the GPU against 64-bit references: quantisation code by code, the product and its
 epilogue, routed experts, and runs of them together."""
+import math
+
 import pytest
 import torch
 
@@ -415,3 +417,43 @@ def test_same_bits_every_time():
     a = dtc.moe_experts_fp4("bf16", x, wi4, wo4, w, plan)
     for _ in range(3):
         assert torch.equal(a, dtc.moe_experts_fp4("bf16", x, wi4, wo4, w, plan))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("act", R.ACTS)
+def test_activations_of_extreme_sums(act, kind):
+    """Sums that are the bias alone, from the type's smallest numbers to its largest, infinities and NaN, each beside
+    ordinary ones: every value is its own sum's and no other's."""
+    import dense_tensor_core_gb300 as dtc
+    gated = act in R.GATED
+    dt, big = R.DT[kind], torch.finfo(R.DT[kind]).max
+    inf, nan = float("inf"), float("nan")
+    gates = [0.0, 1e-7, -1e-7, 1.0, -1.0, 3.0, -3.0, -5.5, 8.0, -9.5, 14.5, -13.0, 30.0, -30.0, -41.0, -60.0, 75.0,
+             -86.0, 90.0, -104.0, 1000.0, -1000.0, big, -big, inf, 0.5, -inf, -0.5, nan, 0.25, 2.0, nan]
+    N, M, K = 64, 37, 64
+    g = torch.tensor(gates + gates[::-1], device="cuda", dtype=torch.float64).to(dt)
+    bias = torch.cat([g, torch.full_like(g, 0.5)]) if gated else g
+    a = torch.zeros((M, K), device="cuda", dtype=dt)
+    b = rand((2 * N if gated else N, K), kind, 5)
+    y = dtc.gemm_fp4(kind, dtc.quantize_fp4(a), dtc.quantize_fp4(b, gated=gated), bias=bias, activation=act)
+    z = bias.double().expand(M, -1)
+    if act == "gelu_tanh":  # (without R.act's 1 + tanh, which cancels)
+        want = z * torch.sigmoid(2 * math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3))
+    else:
+        want = R.act(z, act)
+    # the limits: relu, gelu and silu of -infinity are 0, which 0 times infinity in the formula is not
+    if act != "none":
+        want = torch.where(z[:, :N] == -inf, 0.0, want)
+    # z is exact. The exponential's argument, at most 88, is off by at most 5 roundings of it (gelu_tanh), 88 x 5 x 2^-24,
+    # and the rest by less than 2^-18: 2^-14 of the value. Exponentials below 2^-126 are 0. Then one rounding to the
+    # type (below its smallest normal number: half a subnormal step).
+    top = torch.finfo(dt)
+    assert torch.equal(torch.isnan(y), torch.isnan(want))
+    over = want.abs() > big  # (finite ones beyond the type become infinite or its largest number)
+    ok = ~torch.isnan(want) & ~over
+    err = (y.double() - want).abs()[ok]
+    tol = (top.eps / 2 + 2.0 ** -14) * want.abs()[ok] + top.tiny * top.eps
+    tol += 2.0 ** -126 * z[:, :N].abs().clamp(max=200)[ok]
+    assert (err <= tol).all(), (act, kind, y.double()[ok][err > tol], want[ok][err > tol])
+    assert (y.double()[over].abs() >= big).all()
+    assert torch.equal(y.nan_to_num(), y[:1].nan_to_num().expand(M, -1))
