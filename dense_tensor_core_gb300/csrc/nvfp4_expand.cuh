@@ -4,12 +4,11 @@
 // The block-scaled product of the 05 Blackwell TCGEN05 GEMM tutorial, "Advanced" (gemm_blockscaled,
 // "MXFP8 and other block-scaled formats"), for the NVFP4 member of that family:
 //   C[m,n] = bf16( sum_k e2m1(A[m,k]) ue4m3(sfA[m,k/16]) * e2m1(B[n,k]) ue4m3(sfB[n,k/16]) )
-// The tensor-core kind that takes UE4M3 scales per 16 elements is not used (no document on this
-// machine fixes its instruction-descriptor codes or where its scale vectors sit in Tensor Memory).
-// Instead each element is multiplied by its scale here and written as bf16, and the bf16 tensor-
-// core product runs on the result. The multiplication is exact: an e2m1 value has at most 2
-// significant bits and a UE4M3 value at most 4, so their product has at most 5 (bf16 holds 8),
-// and its magnitude lies in [2^-10, 2688] (bf16 normals reach 2^-126 and 3.4e38). The product
+// The tensor-core kind that takes UE4M3 scales per 16 elements wants them in another order than row
+// by row (gemm_fp4.cuh runs on it). Here each element is multiplied by its scale and written as bf16,
+// and the bf16 tensor-core product runs on the result. The multiplication is exact: an e2m1 value has
+// at most 2 significant bits and a UE4M3 value at most 4, so their product has at most 5 (bf16 holds
+// 8), and its magnitude lies in [2^-10, 2688] (bf16 normals reach 2^-126 and 3.4e38). The product
 // C = A' B'^T of the expanded operands is then the NVFP4 product up to the order of the fp32
 // accumulation.
 //
