@@ -59,6 +59,11 @@ __device__ __forceinline__ float of_ue4m3(uint32_t c) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
     return __half2float(__ushort_as_half((unsigned short)(h & 0xffffu)));
 }
+__device__ __forceinline__ float rcp_ftz(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     float2 d;
@@ -136,10 +141,10 @@ __device__ __forceinline__ void block_scale(uint32_t top, int e, uint32_t& s, fl
     constexpr uint32_t kInf = kBF16 ? 0x7f80u : 0x7c00u;
     const float t = magnitude<kBF16>(top);
     if constexpr (kFormat == kNvfp4) {
-        const float v = t * pow2(-e) * (1.0f / 6.0f);
+        const float v = t * (pow2(-e) * (1.0f / 6.0f));
         s = to_ue4m3(__uint_as_float((__float_as_uint(v) + 0x80u) & 0xffffff00u));
         const float sv = of_ue4m3(s);
-        r = sv > 0.0f ? __fdividef(pow2(-e), sv) : 0.0f;
+        r = sv > 0.0f ? pow2(-e) * rcp_ftz(sv) : 0.0f;  // (2^-9 to 448, and the power of two is exact)
         if (top >= kInf) s = 0x7fu;
     } else {
         const int b = max(-126, (int)(__float_as_uint(t) >> 23) - 127 - 2);
@@ -208,7 +213,7 @@ __device__ __forceinline__ uint32_t row_max(uint32_t top, uint32_t* tops) {
 }
 
 constexpr int kThreads = 256;
-constexpr int kVecs = 4;  // 16-byte pieces of the row that a lane keeps
+constexpr int kKeep = 4;  // 16-byte pieces of the row that a lane keeps (rows little longer than a power of two: 6)
 
 // Which rows a launch quantises: all of a stack, or rows that stand in expert order, whose factors take in
 // their choices' weights and whose scales stand tile by tile (two groups a tile).
@@ -247,9 +252,12 @@ struct QuantizeArgs {
     int zero_words;
 };
 
-// kWarps warps share a row; kKept: they hold it whole (else it is read a second time).
-template <bool kBF16, int kFormat, int kSource, int kWarps, bool kKept>
-__global__ void __launch_bounds__(kThreads < 32 * kWarps ? 32 * kWarps : kThreads)
+// kWarps warps share a row; kKept: they hold it whole, kVecs pieces a lane (else it is read a second time). A block's
+// time is mostly latency, so registers are held down to fit six (8192 x 8192 NVFP4 34.2 to 33.0 us, 2048 x 16384 22.0
+// to 19.3; eight: 8192 x 2048 10.3 to 12.2).
+template <bool kBF16, int kFormat, int kSource, int kWarps, bool kKept, int kVecs>
+__global__ void __launch_bounds__(kThreads < 32 * kWarps ? 32 * kWarps : kThreads,
+                                  (kVecs > kKeep ? 4 : 6) / (kWarps > 8 ? 2 : 1))
     fp4_quantize_kernel(const QuantizeArgs a) {
     constexpr int kBlockThreads = kThreads < 32 * kWarps ? 32 * kWarps : kThreads;
     constexpr int kRowsPer = kBlockThreads / (32 * kWarps);  // rows of a block
@@ -389,10 +397,10 @@ __global__ void __launch_bounds__(kThreads < 32 * kWarps ? 32 * kWarps : kThread
     auto fetch = [&](int64_t row, int p) {
         return row < a.total && p < pieces ? reinterpret_cast<const uint4*>(a.x + row * a.ld)[p] : make_uint4(0, 0, 0, 0);
     };
-    uint4 v[kVecs];
+    uint4 v[kKeep];
     if constexpr (kKept) {
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) v[i] = fetch(t, first + i * kStep);  // (in flight while the counts are added up)
+        for (int i = 0; i < kKeep; ++i) v[i] = fetch(t, first + i * kStep);  // (in flight while the counts are added up)
     }
     // Few tiles (few choices): a lane looks at one, and the experts' counts are not needed.
     const bool few = x.max_tiles <= 32;
@@ -468,10 +476,10 @@ __global__ void __launch_bounds__(kThreads < 32 * kWarps ? 32 * kWarps : kThread
             }
             if (!found) row = -1;
         }
-        uint32_t tops_of[kVecs], row_top = 0;
+        uint32_t tops_of[kKeep], row_top = 0;
         if constexpr (kKept) {
 #pragma unroll
-            for (int i = 0; i < kVecs; ++i) {
+            for (int i = 0; i < kKeep; ++i) {
                 tops_of[i] = block_top<kFormat>(v[i]);
                 if (tops_of[i] < kInf) row_top = max(row_top, tops_of[i]);
             }
@@ -484,33 +492,43 @@ __global__ void __launch_bounds__(kThreads < 32 * kWarps ? 32 * kWarps : kThread
         int e = 0;
         if constexpr (kFormat == kNvfp4) e = factor_exponent(magnitude<kBF16>(row_max<kWarps>(row_top, tops)));
         if (kFormat == kNvfp4 && part == 0 && row >= 0) a.row_scale[row] = pow2(e);
-        auto write = [&](const uint4& u, uint32_t top, int p) {
+        auto convert = [&](const uint4& u, uint32_t top, int p, uint32_t& c, uint32_t& w) {
             uint32_t s;
             float r;
             block_scale<kBF16, kFormat>(top, e, s, r);
-            const uint32_t c = encode<kBF16, kFormat>(u, top, r);
-            const uint32_t w = set_word<kFormat>(p < pieces ? s : 0u);
-            const bool in = p < pieces;
+            c = encode<kBF16, kFormat>(u, top, r);
+            w = set_word<kFormat>(p < pieces ? s : 0u);
+        };
+        // pieces p, p + kStep, ... to every choice's place
+        auto write = [&](const auto& c, const auto& w, int p) {
+            constexpr int n = sizeof(c) / sizeof(uint32_t), kLanes = 4 * kBlockLanes<kFormat>;
             for (int j = 0; j < x.k; ++j) {
                 const int to = __shfl_sync(kAll, row, j), g = __shfl_sync(kAll, group, j), at = __shfl_sync(kAll, place, j);
-                if (to < 0 || !in) continue;
-                reinterpret_cast<uint32_t*>(a.codes + (int64_t)to * a.ld_codes)[p] = c;
-                if (lane % (4 * kBlockLanes<kFormat>) == 0)
-                    *reinterpret_cast<uint32_t*>(a.scales + scale_at(g, at, a.sets, 0) +
-                                                 (int64_t)(p / (4 * kBlockLanes<kFormat>)) * 512) = w;
+                if (to < 0) continue;
+                uint32_t* const codes = reinterpret_cast<uint32_t*>(a.codes + (int64_t)to * a.ld_codes) + p;
+                uint8_t* const scales = a.scales + scale_at(g, at, a.sets, 0) + (int64_t)(p / kLanes) * 512;
+#pragma unroll
+                for (int i = 0; i < n; ++i) {
+                    if (p + i * kStep >= pieces) break;
+                    codes[i * kStep] = c[i];
+                    if (lane % kLanes == 0) *reinterpret_cast<uint32_t*>(scales + i * (kStep / kLanes) * 512) = w[i];
+                }
             }
         };
         if constexpr (kKept) {
+            uint32_t c[kKeep], w[kKeep];
 #pragma unroll
-            for (int i = 0; i < kVecs; ++i)
-                if (part * 32 + i * kStep < pieces) write(v[i], tops_of[i], first + i * kStep);
+            for (int i = 0; i < kKeep; ++i) convert(v[i], tops_of[i], first + i * kStep, c[i], w[i]);
 #pragma unroll
-            for (int i = 0; i < kVecs; ++i) v[i] = fetch(t + step, first + i * kStep);
+            for (int i = 0; i < kKeep; ++i) v[i] = fetch(t + step, first + i * kStep);
+            write(c, w, first);
         } else {
             for (int p0 = 0; p0 < pieces; p0 += kStep)
                 if (p0 + part * 32 < pieces) {
                     const uint4 u = fetch(t, p0 + first);
-                    write(u, block_top<kFormat>(u), p0 + first);
+                    uint32_t c[1], w[1];
+                    convert(u, block_top<kFormat>(u), p0 + first, c[0], w[0]);
+                    write(c, w, p0 + first);
                 }
         }
     }

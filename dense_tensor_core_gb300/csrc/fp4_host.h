@@ -48,13 +48,18 @@ int launch_quantize_of(const dtc::fp4::QuantizeArgs& a, cudaStream_t stream) {
         if (blocks > kMaxSize) return fail(GEMM_ERR_UNSUPPORTED, "too many rows");
         return launch_chain(kern, dim3((unsigned)blocks), threads, 0, 1, stream, a);
     };
-    constexpr int kWarp = 32 * kVecs * 8;  // elements that a warp keeps
-    if (a.K <= kWarp) return go(fp4_quantize_kernel<kBF16, kFormat, kSource, 1, true>, 1);
-    if (a.K <= 2 * kWarp) return go(fp4_quantize_kernel<kBF16, kFormat, kSource, 2, true>, 2);
-    if (a.K <= 4 * kWarp) return go(fp4_quantize_kernel<kBF16, kFormat, kSource, 4, true>, 4);
-    if (a.K <= 8 * kWarp) return go(fp4_quantize_kernel<kBF16, kFormat, kSource, 8, true>, 8);
-    if (a.K <= 16 * kWarp) return go(fp4_quantize_kernel<kBF16, kFormat, kSource, 16, true>, 16);
-    return go(fp4_quantize_kernel<kBF16, kFormat, kSource, 16, false>, 16);
+    constexpr int kMore = 6;
+    constexpr int64_t kWarp = 32 * kKeep * 8, kWide = 32 * kMore * 8;  // elements that a warp keeps
+    if (a.K <= kWarp) return go(fp4_quantize_kernel<kBF16, kFormat, kSource, 1, true, kKeep>, 1);
+    if (a.K <= kWide) return go(fp4_quantize_kernel<kBF16, kFormat, kSource, 1, true, kMore>, 1);
+    if (a.K <= 2 * kWarp) return go(fp4_quantize_kernel<kBF16, kFormat, kSource, 2, true, kKeep>, 2);
+    if (a.K <= 2 * kWide) return go(fp4_quantize_kernel<kBF16, kFormat, kSource, 2, true, kMore>, 2);
+    if (a.K <= 4 * kWarp) return go(fp4_quantize_kernel<kBF16, kFormat, kSource, 4, true, kKeep>, 4);
+    if (a.K <= 4 * kWide) return go(fp4_quantize_kernel<kBF16, kFormat, kSource, 4, true, kMore>, 4);
+    if (a.K <= 8 * kWarp) return go(fp4_quantize_kernel<kBF16, kFormat, kSource, 8, true, kKeep>, 8);
+    if (a.K <= 8 * kWide) return go(fp4_quantize_kernel<kBF16, kFormat, kSource, 8, true, kMore>, 8);
+    if (a.K <= 16 * kWarp) return go(fp4_quantize_kernel<kBF16, kFormat, kSource, 16, true, kKeep>, 16);
+    return go(fp4_quantize_kernel<kBF16, kFormat, kSource, 16, false, kKeep>, 16);
 }
 
 template <int kSource>

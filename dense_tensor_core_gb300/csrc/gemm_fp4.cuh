@@ -199,11 +199,6 @@ __device__ __forceinline__ float exp2_ftz(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ float rcp_ftz(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // z * s for s in [0, 1]: 0 at z = -infinity, the limit, and NaN at NaN.
 __device__ __forceinline__ float2 times_share(float2 z, float2 s) {
     float2 x;
@@ -216,12 +211,12 @@ template <int N>
 __device__ __forceinline__ void reciprocals(float2 (&d)[N]) {
     const float2 a = fp4::mul2(d[0], d[1]);
     if constexpr (N == 2) {
-        const float2 r = make_float2(rcp_ftz(a.x), rcp_ftz(a.y)), d0 = d[0];
+        const float2 r = make_float2(fp4::rcp_ftz(a.x), fp4::rcp_ftz(a.y)), d0 = d[0];
         d[0] = fp4::mul2(r, d[1]);
         d[1] = fp4::mul2(r, d0);
     } else {
         const float2 b = fp4::mul2(d[2], d[3]), ab = fp4::mul2(a, b);
-        const float2 r = make_float2(rcp_ftz(ab.x), rcp_ftz(ab.y));
+        const float2 r = make_float2(fp4::rcp_ftz(ab.x), fp4::rcp_ftz(ab.y));
         const float2 ra = fp4::mul2(r, b), rb = fp4::mul2(r, a), d0 = d[0], d2 = d[2];
         d[0] = fp4::mul2(ra, d[1]);
         d[1] = fp4::mul2(ra, d0);

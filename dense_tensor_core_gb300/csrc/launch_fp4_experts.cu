@@ -14,7 +14,7 @@ int tokens_of(const dtc::fp4::QuantizeArgs& a, DeviceInfo* dev, cudaStream_t str
         const int64_t blocks = std::min<int64_t>((a.total + rows - 1) / rows, 4 * dev->model.sms);
         return launch_chain(kern, dim3((unsigned)blocks), threads, (3 * a.x_rows.experts + 1) * 4, 1, stream, a);
     };
-    constexpr int kWarp = 32 * kVecs * 8;  // elements that a warp keeps
+    constexpr int kWarp = 32 * kKeep * 8;  // elements that a warp keeps
     if (a.K <= kWarp) return go(fp4_quantize_tokens_kernel<kBF16, kFormat, 1, true>, 1);
     if (a.K <= 2 * kWarp) return go(fp4_quantize_tokens_kernel<kBF16, kFormat, 2, true>, 2);
     if (a.K <= 4 * kWarp) return go(fp4_quantize_tokens_kernel<kBF16, kFormat, 4, true>, 4);

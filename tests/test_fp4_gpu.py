@@ -60,7 +60,8 @@ def same_bits(q, x, fmt, gated=False):
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
 @pytest.mark.parametrize("kind", ["bf16", "f16"])
 @pytest.mark.parametrize("M,K", [(1, 32), (1, 8192), (3, 96), (130, 64), (33, 992), (7, 1056), (300, 2080), (5, 4128),
-                                 (4, 8224), (2, 16384), (3, 16416), (2, 40000)])
+                                 (4, 8224), (2, 16384), (3, 16416), (2, 40000), (9, 1536), (9, 1568), (5, 6144), (5, 6176),
+                                 (2, 12288), (2, 12320)])
 def test_quantize(fmt, kind, M, K):
     import dense_tensor_core_gb300 as dtc
     x = rows(M, K, kind, M + K)
