@@ -299,11 +299,13 @@ __device__ __forceinline__ void act_block(float (&v)[4][8]) {
 // Finishes one 32-row block of sums v: factors and bias of the thread's 4 accumulator lanes, activation,
 // residual, store. The residual goes through the slot first, then `refill` may fetch the next block's. Whole
 // blocks leave by TMA (the slot's order of 16-byte pieces is the copy's swizzle); blocks that end inside an
-// expert's rows leave piece by piece. The slot may be reused when the copy of two blocks before has read it.
-template <bool kBF16, int kMode, bool kGated, bool kSplit, bool kResidual, typename Refill>
+// expert's rows leave piece by piece. kSums: the results are fp32 sums (of the experts' second product). slot is
+// the warp's free one of two that add up to `other`. (Two pairs of slots for fp32 blocks and a ring of four stages:
+// 4096 tokens by 8 of 64 experts, H 2048, F 1024 266 us against 270, but 16 experts, H and F 4096 291 against 286.)
+template <bool kBF16, int kMode, bool kGated, bool kSplit, bool kResidual, bool kSums, typename Refill>
 __device__ __forceinline__ void finish_block(const Fp4Args& fa, const CUtensorMap* tmC, float (&v)[4][8],
                                              const float (&gp)[4], const float (&bias)[4], const ffn::Place& p,
-                                             Ahead<kGated>& x, uint32_t slots, uint32_t slot, int lane,
+                                             Ahead<kGated>& x, uint32_t& slot, uint32_t other, int lane,
                                              Refill refill) {
     using Block = ffn::Block<kGated ? 2 : 4>;
     const FfnArgs& a = fa.e;
@@ -321,36 +323,39 @@ __device__ __forceinline__ void finish_block(const Fp4Args& fa, const CUtensorMa
             v[o][2 * b + 1] = z.y;
         }
     }
-    if constexpr (kMode == ffn::kSeg && !kGated) {
-        if (a.out_f32) {  // through both slots, in the order of a 128-byte swizzle
-            using Sums = ffn::Sums<4>;
-            if (elect_one()) bulk_wait_group_read<0>();
+    // A slot is free when the copy of two before has read it. Each use commits a group, an empty one where it has no
+    // copy, so that all groups but the newest are the copies up to that one. (The same lane is elected each time.)
+    if constexpr (kSums) {  // 16 rows a slot, in the order of a 128-byte swizzle
+        using Sums = ffn::Sums<4>;
+        refill();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (elect_one()) bulk_wait_group_read<1>();
             __syncwarp();
-            refill();
 #pragma unroll
             for (int o = 0; o < 4; ++o)
 #pragma unroll
-                for (int k = 0; k < 8; ++k) st_shared_f32(slots + Sums::element(o, k, lane), v[o][k]);
-            if (p.valid == 32) {
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (left > 0 && elect_one()) {
-                    tma_store_2d(tmC, slots, p.f, (int)p.row);
-                    bulk_commit_group();
-                }
-            } else {
-                __syncwarp();
-                float* const out = static_cast<float*>(a.out) + p.row * a.ld_out + p.f;
+                for (int k = 0; k < 4; ++k) st_shared_f32(slot + Sums::element(o, k, lane), v[o][4 * h + k]);
+            const int valid = p.valid - 16 * h;
+            if (valid >= 16) fence_proxy_async_smem();
+            __syncwarp();
+            if (elect_one()) {
+                if (valid >= 16 && left > 0) tma_store_2d(tmC, slot, p.f, (int)p.row + 16 * h);
+                bulk_commit_group();
+            }
+            if (valid < 16) {
+                float* const out = static_cast<float*>(a.out) + (p.row + 16 * h) * a.ld_out + p.f;
                 const int j = lane & 7;
 #pragma unroll 1
-                for (int r = lane >> 3; r < p.valid; r += 4)
+                for (int r = lane >> 3; r < valid; r += 4)
                     if (4 * j < left)
-                        *reinterpret_cast<uint4*>(out + r * a.ld_out + 4 * j) = ld_shared_u4(slots + Sums::at(r, j));
+                        *reinterpret_cast<uint4*>(out + r * a.ld_out + 4 * j) = ld_shared_u4(slot + Sums::at(r, j));
             }
-            return;
+            slot = other - slot;
         }
+        return;
     }
-    if (elect_one()) bulk_wait_group_read<1>();  // (the same lane each time)
+    if (elect_one()) bulk_wait_group_read<1>();
     __syncwarp();
     const Block blk(slot, lane);
     const bool residual = kResidual && (!kSplit || a.residual);
@@ -377,23 +382,20 @@ __device__ __forceinline__ void finish_block(const Fp4Args& fa, const CUtensorMa
         blk.template take<kBF16>([&](int o, int k, float r) { v[kStep * o][k] += r; });
         __syncwarp();
     }
-    const bool whole = kMode == ffn::kRows || p.valid == 32;
     blk.template stage<kBF16>([&](int o, int k) { return v[kStep * o][k]; });
-    if (whole) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (left > 0 && p.valid > 0 && elect_one()) {
-            tma_store_2d(tmC, slot, p.f, (int)p.row);
-            bulk_commit_group();
-        }
-    } else {
-        __syncwarp();
-        blk.flush(static_cast<uint16_t*>(a.out) + p.row * a.ld_out + p.f, a.ld_out, p.valid, left);
+    const bool whole = kMode == ffn::kRows || p.valid == 32;
+    if (whole) fence_proxy_async_smem();
+    __syncwarp();
+    if (elect_one()) {
+        if (whole && left > 0 && p.valid > 0) tma_store_2d(tmC, slot, p.f, (int)p.row);
+        bulk_commit_group();
     }
+    if (!whole) blk.flush(static_cast<uint16_t*>(a.out) + p.row * a.ld_out + p.f, a.ld_out, p.valid, left);
+    slot = other - slot;
 }
 }  // namespace gf4
 
-template <bool kMx, bool kBF16, int kMode, bool kGated, bool kSplit, bool kResidual>
+template <bool kMx, bool kBF16, int kMode, bool kGated, bool kSplit, bool kResidual, bool kSums>
 __global__ void __launch_bounds__(gf4::kThreads, 1)
     gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ FfnQMaps tmQ,
                     const __grid_constant__ CUtensorMap tmSP, const __grid_constant__ CUtensorMap tmSQ,
@@ -757,9 +759,8 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
                             fetch_ahead<kGated, kSplit, kResidual>(fargs, place, slot, lane, ahead);
                         }
                     };
-                    finish_block<kBF16, kMode, kGated, kSplit, kResidual>(fargs, &tmC, v, gp, bias, here, ahead, slots,
-                                                                          slot, lane, refill);
-                    slot = 2 * slots + kSlot - slot;
+                    finish_block<kBF16, kMode, kGated, kSplit, kResidual, kSums>(fargs, &tmC, v, gp, bias, here, ahead,
+                                                                                 slot, 2 * slots + kSlot, lane, refill);
                 }
                 if (pass == kWarm) {
                     warm = false;

@@ -12,7 +12,7 @@ inline int fp4_scales_tmap(CUtensorMap* m, const void* p, uint64_t chunks, int s
                      CU_TENSOR_MAP_SWIZZLE_NONE, name);
 }
 
-template <bool kMx, bool kBF16, int kMode, bool kGated, bool kSplit, bool kResidual>
+template <bool kMx, bool kBF16, int kMode, bool kGated, bool kSplit, bool kResidual, bool kSums = false>
 int launch_gemm_fp4_of(const Fp4Call& c, DeviceInfo* dev, cudaStream_t stream) {
     CUtensorMap tp = {}, sp = {}, sq = {};
     dtc::FfnQMaps tq = {};
@@ -24,9 +24,9 @@ int launch_gemm_fp4_of(const Fp4Call& c, DeviceInfo* dev, cudaStream_t stream) {
         return rc;
     CUtensorMap tc = {};
     const dtc::FfnArgs& e = c.ffn.args;
-    // the result: blocks of 32 rows and 32 features (gated 16), in the order of the epilogue's slots
-    if (e.out_f32) {
-        rc = make_tmap(&tc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, e.out, e.feats, e.rows, e.ld_out, 32, 32,
+    // the result: what an epilogue's slot holds, 32 rows (fp32: 16) of 32 features (gated: 16), in its order
+    if constexpr (kSums) {
+        rc = make_tmap(&tc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, e.out, e.feats, e.rows, e.ld_out, 32, 16,
                        CU_TENSOR_MAP_SWIZZLE_128B, "the result");
         if (rc) return rc;
     } else {
@@ -35,7 +35,7 @@ int launch_gemm_fp4_of(const Fp4Call& c, DeviceInfo* dev, cudaStream_t stream) {
                        kGated ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B, "the result");
         if (rc) return rc;
     }
-    auto kern = dtc::gemm_fp4_kernel<kMx, kBF16, kMode, kGated, kSplit, kResidual>;
+    auto kern = dtc::gemm_fp4_kernel<kMx, kBF16, kMode, kGated, kSplit, kResidual, kSums>;
     if ((rc = ensure_smem_attr(kern, dtc::gf4::kSmemBytes, dev))) return rc;
     dtc::Fp4Args a = c.args;
     a.e = c.ffn.args;
@@ -61,11 +61,17 @@ int launch_gemm_fp4_rows_any(const Fp4Call& c, DeviceInfo* dev, cudaStream_t s) 
                        : launch_gemm_fp4_rows_of<kMx, false, false>(c, dev, s);
 }
 
+// Of an expert's two products the second one's results are fp32 sums.
 template <bool kMx, bool kBF16, bool kGated>
 int launch_gemm_fp4_experts_of(const Fp4Call& c, DeviceInfo* dev, cudaStream_t s) {
     using dtc::ffn::kSeg;
-    return c.ffn.args.split_tiles > 0 ? launch_gemm_fp4_of<kMx, kBF16, kSeg, kGated, true, false>(c, dev, s)
-                                      : launch_gemm_fp4_of<kMx, kBF16, kSeg, kGated, false, false>(c, dev, s);
+    const bool split = c.ffn.args.split_tiles > 0;
+    if constexpr (!kGated)
+        if (c.ffn.args.out_f32)
+            return split ? launch_gemm_fp4_of<kMx, kBF16, kSeg, false, true, false, true>(c, dev, s)
+                         : launch_gemm_fp4_of<kMx, kBF16, kSeg, false, false, false, true>(c, dev, s);
+    return split ? launch_gemm_fp4_of<kMx, kBF16, kSeg, kGated, true, false>(c, dev, s)
+                 : launch_gemm_fp4_of<kMx, kBF16, kSeg, kGated, false, false>(c, dev, s);
 }
 
 template <bool kMx>
