@@ -317,8 +317,9 @@ __device__ __forceinline__ void finish_block(const Fp4Args& fa, const CUtensorMa
                                       __shfl_sync(0xffffffffu, x.gq, 8 * b + tr + 1));
 #pragma unroll
         for (int o = 0; o < 4; ++o) {
-            const float2 z = fp4::fma2(make_float2(v[o][2 * b], v[o][2 * b + 1]), fp4::mul2(gq, make_float2(gp[o], gp[o])),
-                                  make_float2(bias[o], bias[o]));
+            // (the feature's factor first: the product of both may be infinite beside a sum of 0)
+            const float2 z = fp4::fma2(fp4::mul2(make_float2(v[o][2 * b], v[o][2 * b + 1]), make_float2(gp[o], gp[o])),
+                                       gq, make_float2(bias[o], bias[o]));
             v[o][2 * b] = z.x;
             v[o][2 * b + 1] = z.y;
         }

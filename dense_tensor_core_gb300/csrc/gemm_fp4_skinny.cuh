@@ -173,9 +173,9 @@ __global__ void __launch_bounds__(skinny4::kThreads) gemm_fp4_skinny_kernel(cons
             auto load = [](const void* p, int64_t at) { return load_f<kBF16 ? 0 : 1>(p, at); };
             const float gq = s.a.q_scale ? s.a.q_scale[row] : 1.0f;
             const float* const gp = s.a.p_scale;
-            v[0] = fmaf(v[0], gq * (gp ? gp[f] : 1.0f), a.bias ? load(a.bias, f) : 0.0f);
+            v[0] = fmaf(gp ? v[0] * gp[f] : v[0], gq, a.bias ? load(a.bias, f) : 0.0f);
             if constexpr (kGated)
-                up = fmaf(up, gq * (gp ? gp[a.feats + f] : 1.0f), a.bias ? load(a.bias, a.feats + f) : 0.0f);
+                up = fmaf(gp ? up * gp[a.feats + f] : up, gq, a.bias ? load(a.bias, a.feats + f) : 0.0f);
             act_forward(v, act_of_gate(a.act));
             if constexpr (kGated) v[0] *= up;
             if (a.residual) v[0] += load(a.residual, row * a.ld_res + f);

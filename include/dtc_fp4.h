@@ -97,7 +97,8 @@ typedef struct {
 /*
  * C[M,N] = act(Z) + residual, Z = A . B^T + bias (dtype: of C, bias and residual). A is one matrix [M, K]
  * that is not gated, B one of [N, K], or [2N, K] and gated for the gated activations, both of one format.
- * The tensor cores multiply codes and scales exactly and sum in fp32; the rows' factors multiply the sum.
+ * The tensor cores multiply codes and scales exactly and sum in fp32; the factor of B's row multiplies the
+ * sum, then that of A's (at rows of B from about 2^90 on, the first product may be infinite).
  * N % 8 == 0. opts may be NULL. The workspace lets products of few tiles split K over more SMs.
  * Degenerate sizes: M == 0 or N == 0 does nothing; K == 0 gives Z = bias. INVALID_ARG as gemm_act, for
  * matrices of other shapes or formats, and for a tile or split that the call cannot have. The

@@ -458,3 +458,34 @@ def test_activations_of_extreme_sums(act, kind):
     assert (err <= tol).all(), (act, kind, y.double()[ok][err > tol], want[ok][err > tol])
     assert (y.double()[over].abs() >= big).all()
     assert torch.equal(y.nan_to_num(), y[:1].nan_to_num().expand(M, -1))
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("M", [1, 40])
+def test_factors_whose_product_leaves_the_range(fmt, M):
+    """Rows from 2^-60 to 2^100 and features from 2^-60 to 2^76, so that products of two factors reach from below fp32's range to above
+    it: a result that fits is right, one of no common elements 0, one above the range infinite."""
+    import dense_tensor_core_gb300 as dtc
+    K, N = 128, 48
+    exps = [-60, -50, -30, -8, 0, 9, 40, 64, 76, 100]
+    a = rows(M, K, "bf16", 11).double()
+    b = rows(N, K, "bf16", 12).double()
+    ea = torch.tensor([exps[(i + 7) % 10] for i in range(M)], device="cuda")
+    eb = torch.tensor([exps[i % 9] for i in range(N)], device="cuda")
+    a, b = a * Q.pow2(ea)[:, None], b * Q.pow2(eb)[:, None]
+    a[:, :64] = 0  # a feature with nothing behind has no elements in common with any row
+    b[1::3, 64:] = 0
+    a, b = a.bfloat16(), b.bfloat16()
+    y = dtc.gemm_fp4("bf16", dtc.quantize_fp4(a, format=fmt), dtc.quantize_fp4(b, format=fmt))
+    want = Q.rounded(a, fmt) @ Q.rounded(b, fmt).t()
+    size = Q.rounded(a, fmt).abs() @ Q.rounded(b, fmt).abs().t()
+    big = torch.finfo(torch.bfloat16).max
+    fits = size < big * (1 - 2.0 ** -8)  # (MXFP4's scales are inside the sum)
+    assert fits.any() and (want == 0).any()
+    # (a bf16 value has 8 bits: half a step is up to 2^-8 of it)
+    err = (y.double() - want).abs()[fits]
+    tol = (2.0 ** -8 * want.abs() + (K + 2) * 2.0 ** -23 * size + 2.0 ** -133)[fits]
+    assert (err <= tol).all(), (fmt, y.double()[fits][~(err <= tol)], want[fits][~(err <= tol)])
+    over = want.abs() > big * (1 + 2.0 ** -8)
+    assert over.any()
+    assert torch.isinf(y[over]).all()
