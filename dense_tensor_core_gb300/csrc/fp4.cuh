@@ -605,7 +605,7 @@ struct PackArgs {
     uint8_t* scales;
     int64_t matrices, rows, groups;
     int sets, blocks;
-    bool gated;
+    bool gated, ue4m3;
 };
 // (A template so that every translation unit that includes this header may define it.)
 template <int kBlockThreads = kThreads>
@@ -634,6 +634,10 @@ __global__ void __launch_bounds__(kBlockThreads) fp4_pack_scales_kernel(const Pa
 #pragma unroll
             for (int b = 0; b < 4; ++b)
                 if (4 * set + b < a.blocks) w |= (uint32_t)p[4 * set + b] << (8 * b);
+        }
+        if (a.ue4m3) {  // (a UE4M3 byte with the sign bit set is no number: the NaN)
+            const uint32_t bad = ((w >> 7) & 0x01010101u) * 0xffu;
+            w = (w & ~bad) | (bad & 0x7f7f7f7fu);
         }
         reinterpret_cast<uint32_t*>(a.scales)[it] = w;
     }

@@ -141,6 +141,7 @@ int fp4_pack_scales(const void* scales, const fp4_matrix* q, dtc_stream_t stream
     a.sets = (int)l.sets;
     a.blocks = (int)(q->K / block_of(q->format));
     a.gated = q->gated != 0;
+    a.ue4m3 = q->format == FP4_NVFP4;
     return launch_fp4_pack(a, info, (cudaStream_t)stream);
 }
 

@@ -76,7 +76,8 @@ int fp4_quantize(int dtype, const void* x, int64_t ld, const fp4_matrix* out, dt
 int fp4_dequantize(int dtype, const fp4_matrix* q, void* out, dtc_stream_t stream);
 
 /* Scales as other programs hold them, [matrices * rows, K / block] bytes row-major and dense, into q's
- * order: writes q->scales (its codes and factors are used as they are, and not read).
+ * order: writes q->scales (its codes and factors are used as they are, and not read). A UE4M3 byte with the
+ * sign bit set is the NaN, as in gemm_nvfp4.
  * The pages have no counterpart. */
 int fp4_pack_scales(const void* scales, const fp4_matrix* q, dtc_stream_t stream);
 
