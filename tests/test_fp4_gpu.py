@@ -375,6 +375,28 @@ def test_experts(fmt, T, E, k, H, F, act):
                 2 * R.U[kind] + (1 / 3) * (1 / 1600) ** 0.5, f"{kind} {fmt}")
 
 
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("T,E,k,H,F", [(9, 4, 2, 2080, 64), (5, 3, 2, 4128, 96), (6, 2, 1, 8224, 64), (300, 2, 1, 8224, 64),
+                                       (6, 2, 2, 64, 2080), (6, 2, 2, 96, 8224), (60, 1024, 4, 96, 64), (40, 33, 32, 64, 32)])
+def test_experts_of_wide_rows_many_experts_and_many_choices(fmt, T, E, k, H, F):
+    test_experts(fmt, T, E, k, H, F, "swiglu")
+
+
+@pytest.mark.parametrize("T", [3, 60])
+def test_experts_chosen_twice_and_weights_of_any_sign(T):
+    """A token may choose an expert twice; weights may be 0 or negative. Tolerance as in test_experts."""
+    import dense_tensor_core_gb300 as dtc
+    kind, fmt, act, E, k, H, F = "bf16", "nvfp4", "swiglu", 5, 4, 256, 96
+    x, wi, wo, idx, w = experts_case(kind, fmt, T, E, k, H, F, act, masked=False)
+    idx[:, 1] = idx[:, 0]
+    idx[0] = 2
+    w[:, 2], w[:, 3] = 0, -w[:, 3]
+    y = dtc.moe_experts_fp4(kind, x, dtc.quantize_fp4(wi, gated=True), dtc.quantize_fp4(wo), w, dtc.moe_plan(idx, E),
+                            activation=act)
+    R.close(y, experts_reference(kind, fmt, x, wi, wo, idx, w, None, act), 2 * R.U[kind] + (1 / 3) * (1 / 1600) ** 0.5,
+            "twice")
+
+
 def test_experts_equal_their_parts():
     """The call against the same steps through the other operators, expert by expert: equal but for the order of
     fp32 sums."""
@@ -505,3 +527,29 @@ def test_packed_signed_scales_are_nan(M):
     assert torch.equal(torch.isnan(dtc.dequantize_fp4(q)), bad.repeat_interleave(16, 1))
     y = dtc.gemm_fp4("bf16", q, dtc.quantize_fp4(rand((N, K), "bf16", 3)))
     assert torch.equal(torch.isnan(y), bad.any(1)[:, None].expand(M, N))
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_offsets_past_32_bits(fmt):
+    """Rows and results of more than 2^31 elements: the last ones against the same rows by themselves."""
+    import dense_tensor_core_gb300 as dtc
+    M, K, tail = 66000, 32800, 300
+    x = torch.empty((M, K), device="cuda", dtype=torch.bfloat16).normal_(generator=gen(1))
+    q = dtc.quantize_fp4(x, format=fmt)
+    last = dtc.quantize_fp4(x[-tail:].contiguous(), format=fmt)
+    assert torch.equal(q.codes[-tail:], last.codes)
+    back = dtc.dequantize_fp4(q)
+    assert torch.equal(back[-tail:], dtc.dequantize_fp4(last))
+    del x, back
+    b = dtc.quantize_fp4(rand((264, K), "bf16", 2, K ** -0.5), format=fmt)
+    # (the same tiles of rows, so the same order of sums)
+    y = dtc.gemm_fp4("bf16", q, b, tile_rows=256, split_k=1)
+    assert torch.equal(y[-tail:], dtc.gemm_fp4("bf16", last, b, tile_rows=256, split_k=1))
+    del q, y
+    a, w = dtc.quantize_fp4(rand((M, 64), "bf16", 3), format=fmt), rand((K, 64), "bf16", 4)
+    res = torch.empty((M, K), device="cuda", dtype=torch.bfloat16).normal_(generator=gen(5))
+    y = dtc.gemm_fp4("bf16", a, dtc.quantize_fp4(w, format=fmt), residual=res)
+    want = Q.rounded(rand((M, 64), "bf16", 3)[-tail:], fmt) @ Q.rounded(w, fmt).t() + res[-tail:].double()
+    # one rounding, and the fp32 sum of 64 products
+    size = Q.rounded(rand((M, 64), "bf16", 3)[-tail:], fmt).abs() @ Q.rounded(w, fmt).abs().t() + res[-tail:].abs()
+    assert ((y[-tail:].double() - want).abs() <= 2.0 ** -8 * want.abs() + 66 * 2.0 ** -23 * size).all()
