@@ -3,6 +3,7 @@
 #include <algorithm>
 
 #include "fp4_host.h"
+#include "gemm_fp4_skinny.cuh"
 
 namespace {
 
@@ -293,18 +294,20 @@ void apply_plan(const Fp4Plan& p, void* counters, void* partial, Fp4Call* c) {
 }
 
 // Up to this many rows an NVFP4 product runs on the kernel without tiles, while its conversions take less than a
-// tile's longer start: its time grows with the elements of B (4 TB/s of them; the tiles read faster), more so for
-// more than 8 rows and for a short K, whose blocks do little. Measured, us, without tiles and with (the host's
-// part of a call is 6):
-//   1 x 8192 x 8192    12.7, 12.1 to 13.4 (K split)     gated (as much again) 22.2, 17.6
-//   1 x 4096 x 4096     6.3, 9.1      gated 8.8, 9.9
-//   16 x 8192 x 8192   17.4, 13.7     16 x 4096 x 4096 6.8, 9.2; gated 10.6, 10.0
-//   16 x 1024 x 8192    8.3, 10.1     16 x 8192 x 1024 gated 8.3, 6.8
+// tile's longer start. Its time grows with the elements of B, by waves of two blocks an SM or of four with less in
+// flight, which a long K suits badly. Measured one launch behind the other, us, without tiles and with:
+//   1 row  4096 x 4096 4.7, 8.0   4096 x 8192 7.0, 10.1    4096 x 14336 10.9, 12.5   4800 x 16384 12.4, 14.1
+//          8192 x 8192 11.5, 12.6  9600 x 8192 11.7, 13.7   6144 x 10240 13.1, 12.6   5120 x 13824 16.7, 13.5
+//          16384 x 1024 5.2, 5.7   16384 x 2048 7.1, 7.2    32768 x 1024 9.0, 7.6     16384 x 4096 11.1, 10.4
+//   12     4096 x 4096 5.6, 8.0   4096 x 8192 9.0, 10.6    8192 x 4096 9.6, 8.6      8192 x 2048 6.7, 6.2
 constexpr int kSkinnyRows = 16;
-bool fp4_skinny(int format, int64_t M, int64_t Nb, int64_t K) {
+bool fp4_skinny(int format, int64_t M, int64_t Nb, int64_t K, int sms) {
     if (format != FP4_NVFP4 || M > kSkinnyRows || K == 0) return false;
-    const int64_t most = M <= 8 ? (int64_t)1 << 25 : (int64_t)1 << 24;
-    return Nb <= most / K && (K >= 2048 || Nb <= ((int64_t)1 << 23) / K);
+    const int64_t blocks = ceil_div(Nb, 128) * dtc::skinny4::kBlocksPerGroup;
+    auto up_to = [&](int64_t elements) { return Nb <= elements / K; };
+    if (M > 8) return up_to(blocks <= 2 * sms ? 1 << 25 : 1 << 23);
+    if (blocks <= 2 * sms) return up_to(1 << 27);
+    return blocks <= 4 * sms ? K <= 8192 : up_to(1 << 24);
 }
 
 int check_product(int64_t M, int64_t N, int64_t K, int act) {
@@ -354,7 +357,7 @@ int gemm_fp4(int dtype, const fp4_matrix* A, const fp4_matrix* B, void* C, const
         return rc;
     if (o.bias && (rc = check_device_ptr(o.bias, dev, "bias"))) return rc;
     if (o.residual && (rc = check_device_ptr(o.residual, dev, "residual"))) return rc;
-    const bool few = !o.tile_rows && !o.split_k && fp4_skinny(A->format, M, Nb, K);
+    const bool few = !o.tile_rows && !o.split_k && fp4_skinny(A->format, M, Nb, K, info->model.sms);
     const Fp4Plan p = few ? Fp4Plan() : plan_rows(M, N, o.activation, o.residual, K, pairs_of(info),
                                                   o.workspace ? o.workspace_bytes : 0, o.tile_rows, o.split_k);
     if (!few && p.num_ft == 0)
@@ -398,7 +401,7 @@ int gemm_fp4(int dtype, const fp4_matrix* A, const fp4_matrix* B, void* C, const
     c.q_scales = A->scales;
     c.p_chunks = lb.scale_bytes / 512;
     c.q_chunks = la.scale_bytes / 512;
-    if (few) return launch_fp4_skinny(c, M > 8, (cudaStream_t)stream);
+    if (few) return launch_fp4_skinny(c, info, (cudaStream_t)stream);
     apply_plan(p, o.workspace, static_cast<char*>(o.workspace) + p.counter_bytes, &c);
     return launch_gemm_fp4(c, info, (cudaStream_t)stream);
 }

@@ -34,8 +34,8 @@ inline int launch_gemm_fp4(const Fp4Call& c, DeviceInfo* dev, cudaStream_t strea
         return c.mx ? launch_gemm_mxfp4_rows(c, dev, stream) : launch_gemm_nvfp4_rows(c, dev, stream);
     return c.mx ? launch_gemm_mxfp4_experts(c, dev, stream) : launch_gemm_nvfp4_experts(c, dev, stream);
 }
-// The same of one matrix for a handful of rows, NVFP4 (gemm_fp4_skinny.cuh). wide: 16 rows at a time instead of 8.
-int launch_fp4_skinny(const Fp4Call& c, bool wide, cudaStream_t stream);
+// The same of one matrix for a handful of rows, NVFP4 (gemm_fp4_skinny.cuh).
+int launch_fp4_skinny(const Fp4Call& c, const DeviceInfo* dev, cudaStream_t stream);
 
 template <int kSource, bool kBF16, int kFormat>
 int launch_quantize_of(const dtc::fp4::QuantizeArgs& a, cudaStream_t stream) {

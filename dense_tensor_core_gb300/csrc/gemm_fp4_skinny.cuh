@@ -13,6 +13,11 @@
 // (g, t) uses its elements 4 s .. 4 s + 3 as the layout's columns 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of step s, for P
 // and Q alike, which permutes K but not the sum's terms.
 //
+// What bounds it is the issue of those conversions and multiplications, some 190 instructions for 128 elements of 16
+// features, and their latency. One launch behind the other, NVFP4 weights per second: 1 x 8192 x 8192 11.5 us (3.3
+// TB/s), 1 x 4096 x 8192 7.0, 1 x 4096 x 4096 4.7, 1 x 8192 x 512 2.7. (With asynchronous copies to rings in shared
+// memory in place of registers 13.5, 9.4 and 5.5 at best: more instructions.)
+//
 // The block's features are those whose scales share sectors of memory: 4 neighbours of each of a group's four
 // 32-row columns (gated: 2 gate rows and their up rows of each).
 #pragma once
@@ -68,11 +73,11 @@ __device__ __forceinline__ uint4 load_stream(const uint8_t* p) {
 }
 }  // namespace skinny4
 
-template <bool kBF16, bool kGated, int kR8>
-__global__ void __launch_bounds__(skinny4::kThreads) gemm_fp4_skinny_kernel(const Fp4SkinnyArgs s) {
+template <bool kBF16, bool kGated, int kR8, int kBlocks>
+__global__ void __launch_bounds__(skinny4::kThreads, kBlocks) gemm_fp4_skinny_kernel(const Fp4SkinnyArgs s) {
     using namespace skinny4;
     constexpr int kRows = 8 * kR8;
-    constexpr int kAhead = kR8 == 2 ? 2 : 4;  // chunks loaded together
+    constexpr int kAhead = kR8 == 2 || kBlocks > 2 ? 2 : 4;  // chunks loaded together
     __shared__ float sums[kWarps][kFeats][kRows + 1];
     const FfnArgs& a = s.a.e;
     grid_launch_dependents();
@@ -111,11 +116,11 @@ __global__ void __launch_bounds__(skinny4::kThreads) gemm_fp4_skinny_kernel(cons
             q[n] = s.Q + (int64_t)r * s.ldq + t * 16;
             sq[n] = s.q_scales + fp4::scale_at(r >> 7, r & 127, sets, 0) + (t >> 1) * 512 + half;
         }
-        float acc[kR8][4];
+        float acc[kR8][4], odd[kR8][4];  // (two, so that an instruction need not wait for the one before)
 #pragma unroll
         for (int n = 0; n < kR8; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
+            for (int i = 0; i < 4; ++i) acc[n][i] = odd[n][i] = 0.0f;
         constexpr int kStride = kWarps * kChunk;
         for (int k0 = warp * kChunk; k0 < s.K; k0 += kStride * kAhead) {
             uint4 wa[kAhead], wb[kAhead], x[kAhead][kR8];
@@ -148,7 +153,7 @@ __global__ void __launch_bounds__(skinny4::kThreads) gemm_fp4_skinny_kernel(cons
                     decode(x[c][n], cx[c][n], X);
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        skinny::mma16<false>(acc[n], A[2 * j], B[2 * j], A[2 * j + 1], B[2 * j + 1], X[2 * j], X[2 * j + 1]);
+                        skinny::mma16<false>(j & 1 ? odd[n] : acc[n], A[2 * j], B[2 * j], A[2 * j + 1], B[2 * j + 1], X[2 * j], X[2 * j + 1]);
                 }
             }
         }
@@ -157,7 +162,7 @@ __global__ void __launch_bounds__(skinny4::kThreads) gemm_fp4_skinny_kernel(cons
 #pragma unroll
         for (int n = 0; n < kR8; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sums[warp][g + 8 * (i >> 1)][8 * n + 2 * t + (i & 1)] = acc[n][i];
+            for (int i = 0; i < 4; ++i) sums[warp][g + 8 * (i >> 1)][8 * n + 2 * t + (i & 1)] = acc[n][i] + odd[n][i];
         __syncthreads();
         constexpr int kOut = kGated ? 8 : 16;  // features of the result per block
         for (int i = threadIdx.x; i < kOut * kRows; i += kThreads) {

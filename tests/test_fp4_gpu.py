@@ -209,6 +209,14 @@ def test_gemm_shapes(fmt, kind, M, N, K):
     run(kind, fmt, M, N, K, bias=M % 2 == 1, res=N % 16 == 8)
 
 
+@pytest.mark.parametrize("M,N,K,act", [(1, 5000, 288, "none"), (8, 9000, 96, "silu"), (3, 2600, 160, "swiglu"),
+                                       (2, 4400, 1056, "geglu"), (16, 4000, 64, "none"), (9, 5000, 128, "gelu"),
+                                       (1, 10000, 64, "none"), (4, 5136, 8192, "none")])
+def test_gemm_few_rows_many_features(M, N, K, act):
+    for kind in ("bf16", "f16"):
+        run(kind, "nvfp4", M, N, K, act, bias=True, res=M % 2 == 0)
+
+
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
 @pytest.mark.parametrize("act", R.ACTS)
 @pytest.mark.parametrize("M,N,K", [(1, 64, 96), (70, 200, 288), (260, 136, 512)])
