@@ -157,6 +157,7 @@ using dtc::gf4::kBK;
 
 struct Fp4Plan {
     int tile_n = 256, num_ft = 0, num_rt = 0, splits = 1, kb_per_split = 0, grid = 0, split_tiles = 0;
+    int sf_stages = 4;  // of scales in Tensor Memory (gemm_fp4.cuh)
     int64_t tiles = 0;
     uint64_t counter_bytes = 0, bytes = 0;
     int64_t items() const { return tiles + (int64_t)split_tiles * (splits - 1); }
@@ -172,7 +173,7 @@ void size_split(Fp4Plan* p, uint64_t counters) {
 // Modelled time of a launch in us, less what every launch costs, after measured times (4096 x 4096 x 2048: 22, 20
 // and 23 in tiles of 128, 192 and 256 rows; x 8192: 66, 57 and 51): a stage of 256 elements takes the issuing
 // thread's 0.25 us, above 128 rows the tensor pipe's; a tile whose accumulator touches its predecessor's waits until
-// that is read, `epilogue` us more with what its epilogue does.
+// the columns of both are read, `epilogue` us more with what its epilogue does.
 double item_cost(const Fp4Plan& p, int kb, int pairs, double epilogue) {
     const double block = 0.25 + 0.0006 * std::max(0, std::min(p.tile_n, 192) - 128);
     const int64_t split_items = (int64_t)p.split_tiles * p.splits;
@@ -182,18 +183,18 @@ double item_cost(const Fp4Plan& p, int kb, int pairs, double epilogue) {
         cost += (double)split_waves * (p.kb_per_split * block + 1.2);
         cost += waves > 0 ? 0.0062 * p.tile_n * p.splits : 2.2 + 0.01 * p.tile_n * p.splits;
     }
-    if (dtc::gf4::tiles_touch(p.tile_n)) cost += (double)(waves + split_waves - 1) * (1.2 + epilogue);
+    if (dtc::gf4::tiles_touch(p.tile_n)) cost += (double)(waves + split_waves - 1) * (1.1 + epilogue);
     return cost;
 }
 
 // What activation and residual add to a tile of 256 rows over one of 192, whose epilogue runs under the next tile's
-// products. Measured in tiles of 192 and 256, us, at 4096 x 4096 x 8192 and 8192 x 8192 x 8192:
-//   neither 58, 51       silu 62, 58 and 219, 212    gelu 63, 63 and 210, 229     gelu_tanh 63, 59   geglu 59, 54
-//   residual 60.5, 60    both 63, 64 and 224, 235    64, 69 and 223, 243          64, 65             61, 58
+// products from its start. Measured in tiles of 192 and 256, us, at 4096 x 4096 x 8192 and 4096 x 14336 x 4096:
+//   neither  58, 51 and 96, 87     gelu_tanh 63, 57 and 115, 107   gelu 65, 61   swiglu 59, 51   geglu 60, 53
+//   residual 60, 59 and 100, 99    both      63, 64 and 108, 107        64, 67          60, 55         61, 57
 double epilogue_cost(int act, bool residual) {
-    double us = residual ? (dtc::act_gated(act) ? 0.6 : 1.5) : 0.0;
-    if (act == GEMM_ACT_GELU) us += 3.0;
-    else if (act == GEMM_ACT_SILU || act == GEMM_ACT_GELU_TANH) us += 1.2;
+    double us = residual ? (dtc::act_gated(act) ? 0.4 : 1.0) : 0.0;
+    if (act == GEMM_ACT_GELU) us += 1.9;
+    else if (act == GEMM_ACT_SILU || act == GEMM_ACT_GELU_TANH) us += 0.7;
     else if (act == GEMM_ACT_GEGLU) us += 0.5;
     return us;
 }
@@ -241,6 +242,10 @@ Fp4Plan plan_rows(int64_t rows, int64_t feats, int act, bool residual, int64_t K
             for (int s = 2; s <= std::min<int64_t>(most, pairs / tail); ++s) consider(s, tail);
     }
     best.grid = 2 * (int)std::min<int64_t>(best.items(), pairs);
+    // (with a residual the epilogue of a short K is the longer part: 4096 x 14336 x 4096 with gelu_tanh and one 107 us
+    // beside two stages, 115 beside three; gated 98 and 99)
+    if (best.tile_n > dtc::gf4::kNarrow)
+        best.sf_stages = !dtc::gf4::tiles_touch(best.tile_n) || (K <= 4096 && epilogue >= 1.0) ? 2 : 3;
     return best;
 }
 
@@ -251,6 +256,8 @@ Fp4Plan plan_seg(int64_t T, int k, int64_t E, int64_t max_tiles, int64_t feats, 
     p.num_ft = num_feature_tiles(feats, gated);
     p.tile_n = (int)std::min<int64_t>(256, (T * k + 31) / 32 * 32);
     const int expect = (int)std::min<int64_t>(256, (T + 31) / 32 * 32);
+    // (most tiles are low where the experts have few rows)
+    p.sf_stages = T * k <= dtc::gf4::kNarrow * E ? 4 : K <= 4096 ? 2 : 3;
     p.tiles = max_tiles * p.num_ft;
     const int kb = ceil_div(K, 4 * kBK);
     Fp4Plan q = p;
@@ -288,9 +295,8 @@ void apply_plan(const Fp4Plan& p, void* counters, void* partial, Fp4Call* c) {
         a.counters = static_cast<uint32_t*>(counters);
         a.partial = static_cast<float*>(partial);
     }
-    const bool narrow = p.tile_n <= dtc::gf4::kNarrow || dtc::gf4::tiles_touch(p.tile_n);
-    c->args.acc_top = narrow ? 2 * dtc::gf4::kNarrow : dtc::gf4::kWideTop;
-    c->args.sf_stages = narrow ? 4 : 2;
+    c->args.sf_stages = p.sf_stages;
+    c->args.acc_top = dtc::gf4::top_beside(p.sf_stages);
 }
 
 // Up to this many rows an NVFP4 product runs on the kernel without tiles, while its conversions take less than a

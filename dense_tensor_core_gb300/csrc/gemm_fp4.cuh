@@ -14,8 +14,8 @@
 //     puts into four Tensor Memory columns. Five stages.
 //   - Tensor Memory: accumulators take the columns below args.acc_top, by turns from the left end and up to
 //     acc_top, so that tiles of up to acc_top / 2 rows do not touch; behind them lie 48 columns of scales per
-//     stage in flight (4 for P and 8 for Q per set, up to 4 sets). A tile that does touch its predecessor's
-//     columns waits until those are read.
+//     stage in flight (4 for P and 8 for Q per set, up to 4 sets). A tile that does touch its predecessor
+//     waits until the columns that both use are read; the epilogue reads those first.
 //   - The scales of a stage may be overwritten when the MMAs that read them are done: the barrier that frees
 //     that stage's shared memory says so too. An eleventh warp waits for it, sf_stages stages behind, and then
 //     arrives on the full barrier of the stage that takes the columns, so that the issuing thread waits once
@@ -54,13 +54,16 @@ constexpr int kStageBytes = kPBytes + kQBytes + kSfBytes;
 constexpr int kSmemBytes = kStages * kStageBytes + kEpBytes + 1024;
 constexpr int kTmemCols = 512;
 constexpr int kSfSet = 12, kSfStage = 4 * kSfSet;
-// Tiles of up to so many rows leave four stages of scales beside two accumulators, and so do tiles whose
-// accumulators touch in any case; those between leave two.
+// Accumulators' columns beside so many stages of scales. Two tiles of up to top / 2 rows stand side by side; of
+// taller ones the next tile waits for the columns it shares with its predecessor, which the epilogue reads first.
+// Two stages slow a long K (4096 x 4096 x 8192 in tiles of 256 rows 54 us, with three or four 51), but share few
+// columns (4096 tokens by 8 of 64 experts, H 2048, F 1024 249 us, with three 254, with four 258; waiting for all of
+// the predecessor 270).
+__host__ __device__ constexpr int top_beside(int stages) { return (kTmemCols - stages * kSfStage) / 32 * 32; }
 constexpr int kNarrow = 160;
 static_assert(kSmemBytes <= 227 * 1024 - 512, "shared memory budget");
-static_assert(2 * kNarrow + 4 * kSfStage <= kTmemCols, "Tensor Memory budget");
-constexpr int kWideTop = kTmemCols - 2 * kSfStage;
-constexpr bool tiles_touch(int n) { return 2 * n > kWideTop; }
+static_assert(2 * kNarrow <= top_beside(4), "Tensor Memory budget");
+constexpr bool tiles_touch(int n) { return 2 * n > top_beside(2); }
 
 // The items of a pair, in their order (see ffn::get_item): every role walks its own copy. Each step also
 // prepares the next: without split tiles it goes on from the last by additions (a division takes a thread some
@@ -411,6 +414,7 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
     __shared__ __align__(8) uint64_t bar_empty[kStages];
     __shared__ __align__(8) uint64_t bar_tfull[2];
     __shared__ __align__(8) uint64_t bar_tempty[2];
+    __shared__ __align__(8) uint64_t bar_tshared[2];
     __shared__ __align__(8) uint64_t bar_drain;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
@@ -435,6 +439,7 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&bar_tfull[b]), 1);
             mbar_init(smem_u32(&bar_tempty[b]), 2 * kEpWarps);  // of both CTAs
+            mbar_init(smem_u32(&bar_tshared[b]), 2 * kEpWarps);
         }
         mbar_init(smem_u32(&bar_drain), 1);
         abort_flag = 0;
@@ -463,6 +468,7 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
     constexpr uint32_t sf_bytes = sf_sets * 512u;
     // columns of an accumulator of n rows that the turn b takes
     auto acc_col = [&](uint32_t b, int n) { return b ? (uint32_t)(fargs.acc_top - n) : 0u; };
+    const bool touch = 2 * args.tile_n > fargs.acc_top;
 
     if (warp == 0) {
         // ------------------------------ TMA producer (both CTAs) ------------------------------
@@ -537,9 +543,9 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
             while (ok && walk.next(w)) {
                 const uint32_t b = acc & 1u, aph = (acc >> 1) & 1u;
                 ok = wait_bounded(smem_u32(&bar_tempty[b]), aph ^ 1u, abort, args.timeout_ns, args.status, 42);
-                if (ok && before + w.n > fargs.acc_top) {  // the columns of the tile before: wait until they are read
+                if (ok && before + w.n > fargs.acc_top) {  // columns of the tile before: wait until those are read
                     const uint32_t j = acc - 1;
-                    ok = wait_bounded(smem_u32(&bar_tempty[j & 1u]), (j >> 1) & 1u, abort, args.timeout_ns,
+                    ok = wait_bounded(smem_u32(&bar_tshared[j & 1u]), (j >> 1) & 1u, abort, args.timeout_ns,
                                       args.status, 45);
                 }
                 if (!ok) break;
@@ -666,11 +672,20 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
                 }
             }
             Ahead<kGated> ahead;
-            auto hand_back = [&]() {  // accumulator read: back to the MMA issuer
+            auto hand_back = [&](uint64_t* bar) {  // (this part of) the accumulator is read: back to the MMA issuer
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_remote(map_to_cta(smem_u32(&bar_tempty[b]), 0));
+                if (lane == 0) mbar_arrive_remote(map_to_cta(smem_u32(&bar[b]), 0));
             };
+            // This warp's blocks are every second one, those first whose columns the next tile may take: the rightmost
+            // of a tile on the left, and the other way round. `shared` of them; count(n): how many of the first n.
+            auto count = [&](int n) { return n > turn ? (n - turn + 1) >> 1 : 0; };
+            const int own = count(chunks);
+            int shared = 0;
+            if (touch)
+                shared = b ? min(own, count((args.tile_n - fargs.acc_top + w.n) / 32))
+                           : own - min(own, count((fargs.acc_top - args.tile_n) / 32));
+            auto chunk_of = [&](int i) { return turn + 2 * (b ? i : own - 1 - i); };
             const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + acc_col(b, w.n);
             const bool empty = w.kb0 == w.kb1;  // no K-block: the sum is zero
             const int blocks = args.tile_n / 32;
@@ -686,8 +701,8 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
 #pragma unroll 1
             while (true) {
                 if (is_sum()) {
-                    if (pass == kWhole && turn < chunks) {
-                        at_chunk(turn);
+                    if (pass == kWhole && own > 0) {
+                        at_chunk(chunk_of(0));
                         fetch_ahead<kGated, kSplit, kResidual>(fargs, place, slot, lane, ahead);
                     }
                     int ok = 1;
@@ -700,19 +715,22 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
                         break;
                     }
                     tc_fence_after_sync();
-                    if (turn >= chunks) hand_back();
+                    if (touch && shared == 0) hand_back(bar_tshared);
+                    if (own == 0) hand_back(bar_tempty);
                 }
-                const int end = pass == kWarm ? turn + 1 : chunks;
+                const int end = pass == kWarm ? 1 : own;
 #pragma unroll 1
-                for (int c = turn; c < end; c += 2) {
+                for (int i = 0; i < end; ++i) {
+                    const int c = chunk_of(i);
                     float v[4][8];
                     at_chunk(c);
                     if (is_sum()) {
                         tmem_load_fragment32(taddr + c * 32, v);
-                        if (c + 2 >= chunks) hand_back();
+                        if (touch && i + 1 == shared) hand_back(bar_tshared);
+                        if (i + 1 == own) hand_back(bar_tempty);
                         if (empty) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i / 8][i % 8] = 0.0f;
+                            for (int j = 0; j < 32; ++j) v[j / 8][j % 8] = 0.0f;
                         }
                         if (is_piece()) {
                             float4* const d = reinterpret_cast<float4*>(
@@ -727,7 +745,7 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
                         }
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i / 8][i % 8] = 0.0f;
+                        for (int j = 0; j < 32; ++j) v[j / 8][j % 8] = 0.0f;
                         if (pass == kWarm)
                             place.valid = 0;
                         else
@@ -755,8 +773,8 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
                     }
                     const Place here = place;
                     auto refill = [&]() {
-                        if (is_sum() && c + 2 < chunks) {
-                            at_chunk(c + 2);
+                        if (is_sum() && i + 1 < own) {
+                            at_chunk(chunk_of(i + 1));
                             fetch_ahead<kGated, kSplit, kResidual>(fargs, place, slot, lane, ahead);
                         }
                     };
@@ -768,7 +786,7 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
                     pass = main_pass;
                     continue;
                 }
-                if (!is_piece() || turn >= chunks) break;
+                if (!is_piece() || own == 0) break;
                 uint32_t* const counter = args.counters + ((int64_t)w.tile * 2 + rank) * kEpWarps + (warp - 2);
                 __threadfence();  // this lane's pieces are visible before the count
                 __syncwarp();
