@@ -4,7 +4,9 @@
 // quantize. A row's factor needs the row's largest magnitude, its blocks' scales need the factor, and the
 // codes need the scales, but the row is read once: 2^n warps share a row and keep it in registers, 16
 // bytes (8 elements) a lane and load, so that the lanes of a block are neighbours and a warp's accesses
-// are whole lines. Magnitudes of 16-bit floats compare as whole numbers, two at a time. Bound by HBM.
+// are whole lines. Magnitudes of 16-bit floats compare as whole numbers, two at a time. 8192 x 8192 bf16 to NVFP4 33.0
+// us (5.2 TB/s; to MXFP4 29.4) and back 28.4 (6.1 TB/s): quantising issues some 13 instructions an element and waits
+// for its row's loads between two such stretches.
 //
 // Exactness. The code is the e2m1 value nearest to x / d, d = s g, a tie to even. t = x * (1 / d) in fp32 is
 // within 2^-21 of it, and ties are the seven numbers b from 0.25 to 5 of at most 3 bits. x has at most 11
@@ -545,7 +547,7 @@ struct ValuesArgs {
 };
 
 // 8 elements a lane and step: 4 bytes of codes, one scale, 16 (32) bytes of values; kWarps warps share a row.
-// Bound by HBM.
+// Bound by the latency of its loads and by HBM (figures at the head).
 template <int kType, int kFormat, int kWarps>
 __global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const ValuesArgs a) {
     constexpr int kRowsPer = kThreads / (32 * kWarps), kStep = 32 * kWarps, kAhead = 4;

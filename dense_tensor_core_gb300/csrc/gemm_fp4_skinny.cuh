@@ -13,10 +13,10 @@
 // (g, t) uses its elements 4 s .. 4 s + 3 as the layout's columns 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of step s, for P
 // and Q alike, which permutes K but not the sum's terms.
 //
-// What bounds it is the issue of those conversions and multiplications, some 190 instructions for 128 elements of 16
-// features, and their latency. One launch behind the other, NVFP4 weights per second: 1 x 8192 x 8192 11.5 us (3.3
+// What bounds it is latency: a warp loads up to four chunks, then converts and multiplies them, some 190 instructions
+// each (1 x 4096 x 8192: issue slots 21 %, DRAM 23 %). One launch behind the other 1 x 8192 x 8192 takes 11.5 us (3.3
 // TB/s), 1 x 4096 x 8192 7.0, 1 x 4096 x 4096 4.7, 1 x 8192 x 512 2.7. (With asynchronous copies to rings in shared
-// memory in place of registers 13.5, 9.4 and 5.5 at best: more instructions.)
+// memory in place of registers 13.5, 9.4 and 5.5 at best; with neighbouring chunks in one warp 11.7, 7.1 and 4.8.)
 //
 // The block's features are those whose scales share sectors of memory: 4 neighbours of each of a group's four
 // 32-row columns (gated: 2 gate rows and their up rows of each).
