@@ -607,19 +607,23 @@ struct PackArgs {
     uint8_t* scales;
     int64_t matrices, rows, groups;
     int sets, blocks;
-    bool gated, ue4m3;
+    bool gated, ue4m3, words;
 };
+// A block takes kPackSets sets of a group: 32 bytes of each of 128 rows come in whole sectors, and whole chunks leave.
+// (64 matrices of 2048 x 128 scales 59 us with a thread per word of the result, whose reads are 4 bytes of a sector.)
 // (A template so that every translation unit that includes this header may define it.)
+constexpr int kPackSets = 8;
 template <int kBlockThreads = kThreads>
 __global__ void __launch_bounds__(kBlockThreads) fp4_pack_scales_kernel(const PackArgs a) {
+    __shared__ uint32_t chunk[kPackSets][129];
     grid_launch_dependents();
     grid_dependency_wait();
-    const int64_t words = a.matrices * a.groups * a.sets * 128, stride = (int64_t)gridDim.x * kThreads;
-    for (int64_t it = (int64_t)blockIdx.x * kThreads + threadIdx.x; it < words; it += stride) {
-        const int at = (int)(it & 127), place = (at & 3) * 32 + (at >> 2);  // word 4 i + j: place 32 j + i
-        const int64_t chunk = it >> 7, g = chunk / a.sets;
-        const int set = (int)(chunk - g * a.sets);
-        const int64_t m = g / a.groups, group = g - m * a.groups;
+    const int parts = (a.sets + kPackSets - 1) / kPackSets;
+    const int64_t g = blockIdx.x / parts, m = g / a.groups, group = g - m * a.groups;
+    const int set0 = (int)(blockIdx.x - g * parts) * kPackSets;
+#pragma unroll
+    for (int it = threadIdx.x; it < 128 * kPackSets; it += kBlockThreads) {
+        const int s = it % kPackSets, place = it / kPackSets, b0 = 4 * (set0 + s);
         int64_t row;
         bool in;
         if (a.gated) {
@@ -632,17 +636,26 @@ __global__ void __launch_bounds__(kBlockThreads) fp4_pack_scales_kernel(const Pa
         }
         uint32_t w = 0;
         if (in) {
-            const uint8_t* const p = a.in + (m * a.rows + row) * a.blocks;
+            const uint8_t* const p = a.in + (m * a.rows + row) * a.blocks + b0;
+            if (a.words) {  // rows of whole words
+                if (b0 < a.blocks) w = *reinterpret_cast<const uint32_t*>(p);
+            } else {
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
-                if (4 * set + b < a.blocks) w |= (uint32_t)p[4 * set + b] << (8 * b);
+                for (int b = 0; b < 4; ++b)
+                    if (b0 + b < a.blocks) w |= (uint32_t)p[b] << (8 * b);
+            }
         }
         if (a.ue4m3) {  // (a UE4M3 byte with the sign bit set is no number: the NaN)
             const uint32_t bad = ((w >> 7) & 0x01010101u) * 0xffu;
             w = (w & ~bad) | (bad & 0x7f7f7f7fu);
         }
-        reinterpret_cast<uint32_t*>(a.scales)[it] = w;
+        chunk[s][4 * (place & 31) + (place >> 5)] = w;
     }
+    __syncthreads();
+    uint32_t* const out = reinterpret_cast<uint32_t*>(a.scales) + (g * a.sets + set0) * 128;
+#pragma unroll
+    for (int it = threadIdx.x; it < 128 * kPackSets; it += kBlockThreads)
+        if (set0 + it / 128 < a.sets) out[it] = chunk[it / 128][it % 128];
 }
 
 }  // namespace fp4

@@ -143,7 +143,8 @@ int fp4_pack_scales(const void* scales, const fp4_matrix* q, dtc_stream_t stream
     a.blocks = (int)(q->K / block_of(q->format));
     a.gated = q->gated != 0;
     a.ue4m3 = q->format == FP4_NVFP4;
-    return launch_fp4_pack(a, info, (cudaStream_t)stream);
+    a.words = a.blocks % 4 == 0 && aligned(scales, 4);
+    return launch_fp4_pack(a, (cudaStream_t)stream);
 }
 
 }  // extern "C"

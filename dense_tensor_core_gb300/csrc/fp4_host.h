@@ -14,7 +14,7 @@ int launch_fp4_quantize_tokens(bool bf16, int format, const dtc::fp4::QuantizeAr
                                cudaStream_t stream);
 int launch_fp4_quantize_ordered(bool bf16, int format, const dtc::fp4::QuantizeArgs& a, cudaStream_t stream);
 int launch_fp4_dequantize(int dtype, int format, const dtc::fp4::ValuesArgs& a, cudaStream_t stream);
-int launch_fp4_pack(const dtc::fp4::PackArgs& a, DeviceInfo* dev, cudaStream_t stream);
+int launch_fp4_pack(const dtc::fp4::PackArgs& a, cudaStream_t stream);
 
 // A product of gemm_fp4.cuh: `ffn` describes the codes as 16-bit words (four elements each).
 struct Fp4Call {

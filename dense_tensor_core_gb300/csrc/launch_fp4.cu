@@ -9,12 +9,6 @@ int launch_fp4_quantize(bool bf16, int format, const dtc::fp4::QuantizeArgs& a, 
     return launch_quantize_any<dtc::fp4::kPlain>(bf16, format, a, stream);
 }
 
-namespace {
-unsigned strided_grid(int64_t items, const DeviceInfo* dev) {
-    return (unsigned)std::min<int64_t>((items + dtc::fp4::kThreads - 1) / dtc::fp4::kThreads, 16 * dev->model.sms);
-}
-}  // namespace
-
 int launch_fp4_dequantize(int dtype, int format, const dtc::fp4::ValuesArgs& a, cudaStream_t stream) {
     using namespace dtc::fp4;
     auto go = [&](auto kern, int warps) {
@@ -40,8 +34,8 @@ int launch_fp4_dequantize(int dtype, int format, const dtc::fp4::ValuesArgs& a, 
                         : formats(std::integral_constant<int, 2>());
 }
 
-int launch_fp4_pack(const dtc::fp4::PackArgs& a, DeviceInfo* dev, cudaStream_t stream) {
-    const dim3 grid(strided_grid(a.matrices * a.groups * a.sets * 128, dev));
+int launch_fp4_pack(const dtc::fp4::PackArgs& a, cudaStream_t stream) {
+    const dim3 grid((unsigned)(a.matrices * a.groups * ceil_div(a.sets, dtc::fp4::kPackSets)));
     return launch_chain(dtc::fp4::fp4_pack_scales_kernel<>, grid, dtc::fp4::kThreads, 0, 1, stream, a);
 }
 
