@@ -296,8 +296,8 @@ void apply_plan(const Fp4Plan& p, void* counters, void* partial, Fp4Call* c) {
         a.counters = static_cast<uint32_t*>(counters);
         a.partial = static_cast<float*>(partial);
     }
-    c->args.sf_stages = p.sf_stages;
-    c->args.acc_top = dtc::gf4::top_beside(p.sf_stages);
+    c->args.sf_stages = c->mx ? 4 : p.sf_stages;
+    c->args.acc_top = dtc::gf4::top_beside(c->args.sf_stages, c->mx);
 }
 
 // Up to this many rows an NVFP4 product runs on the kernel without tiles, while its conversions take less than a

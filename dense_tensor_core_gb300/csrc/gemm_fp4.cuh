@@ -13,8 +13,8 @@
 //     whole tile (each CTA's datapath computes all rows of its features), in chunks that one tcgen05.cp each
 //     puts into four Tensor Memory columns. Five stages.
 //   - Tensor Memory: accumulators take the columns below args.acc_top, by turns from the left end and up to
-//     acc_top, so that tiles of up to acc_top / 2 rows do not touch; behind them lie 48 columns of scales per
-//     stage in flight (4 for P and 8 for Q per set, up to 4 sets). A tile that does touch its predecessor
+//     acc_top, so that tiles of up to acc_top / 2 rows do not touch; behind them lie 48 (MXFP4 24) columns of scales
+//     per stage in flight (4 for P and 8 for Q per set). A tile that does touch its predecessor
 //     waits until the columns that both use are read; the epilogue reads those first.
 //   - The scales of a stage may be overwritten when the MMAs that read them are done: the barrier that frees
 //     that stage's shared memory says so too. An eleventh warp waits for it, sf_stages stages behind, and then
@@ -53,17 +53,20 @@ constexpr int kSfBytes = 3 * kSfGroup;
 constexpr int kStageBytes = kPBytes + kQBytes + kSfBytes;
 constexpr int kSmemBytes = kStages * kStageBytes + kEpBytes + 1024;
 constexpr int kTmemCols = 512;
-constexpr int kSfSet = 12, kSfStage = 4 * kSfSet;
+constexpr int kSfSet = 12;
+__host__ __device__ constexpr int sf_stage(bool mx) { return (mx ? 2 : 4) * kSfSet; }  // columns of a stage's scales
 // Accumulators' columns beside so many stages of scales. Two tiles of up to top / 2 rows stand side by side; of
 // taller ones the next tile waits for the columns it shares with its predecessor, which the epilogue reads first.
 // Two stages slow a long K (4096 x 4096 x 8192 in tiles of 256 rows 54 us, with three or four 51), but share few
 // columns (4096 tokens by 8 of 64 experts, H 2048, F 1024 249 us, with three 254, with four 258; waiting for all of
-// the predecessor 270).
-__host__ __device__ constexpr int top_beside(int stages) { return (kTmemCols - stages * kSfStage) / 32 * 32; }
+// the predecessor 270). MXFP4 has half the scales, and as many columns left beside four stages.
+__host__ __device__ constexpr int top_beside(int stages, bool mx) {
+    return (kTmemCols - stages * sf_stage(mx)) / 32 * 32;
+}
 constexpr int kNarrow = 160;
 static_assert(kSmemBytes <= 227 * 1024 - 512, "shared memory budget");
-static_assert(2 * kNarrow <= top_beside(4), "Tensor Memory budget");
-constexpr bool tiles_touch(int n) { return 2 * n > top_beside(2); }
+static_assert(2 * kNarrow <= top_beside(4, false) && top_beside(4, true) == top_beside(2, false), "Tensor Memory budget");
+constexpr bool tiles_touch(int n) { return 2 * n > top_beside(2, false); }
 
 // The items of a pair, in their order (see ffn::get_item): every role walks its own copy. Each step also
 // prepares the next: without split tiles it goes on from the last by additions (a division takes a thread some
@@ -565,7 +568,7 @@ __global__ void __launch_bounds__(gf4::kThreads, 1)
                     }
                     tc_fence_after_sync();
                     const uint32_t sf = sSF + s * kSfBytes;
-                    const uint32_t col = tmem_base + (uint32_t)fargs.acc_top + sf_slot * kSfStage;
+                    const uint32_t col = tmem_base + (uint32_t)fargs.acc_top + sf_slot * sf_stage(kMx);
                     if (++sf_slot == sf_ring) sf_slot = 0;
                     const uint32_t p_lo = (uint32_t)p_desc0 + s * (uint32_t)(kPBytes >> 4);
                     const uint32_t q_lo = (uint32_t)q_desc0 + s * (uint32_t)(kQBytes >> 4);
