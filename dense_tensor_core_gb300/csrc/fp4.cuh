@@ -19,6 +19,8 @@
 // from it by 2^-11 of it, so the product with 1 / 6 is rounded to 16 significant bits first.
 #pragma once
 
+#include <type_traits>
+
 #include "element.cuh"
 #include "gemm16_ffn.cuh"
 
@@ -546,8 +548,26 @@ struct ValuesArgs {
     bool gated;
 };
 
+// v * g in fp32, for a result of kType behind it. For one of 16 bits it is rounded to odd (of its two neighbours in
+// fp32 the one whose last bit is set, the product itself where it is a number), which leaves it on its side of every
+// middle of two 16-bit numbers, so that the rounding behind it is the only one.
+template <int kType>
+__device__ __forceinline__ float times_factor(float v, float g) {
+    if constexpr (kType == 2) {
+        return v * g;
+    } else {
+        const float lo = __fmul_rd(v, g), hi = __fmul_ru(v, g);
+        return __float_as_uint(lo) & 1u ? lo : hi;
+    }
+}
+
 // 8 elements a lane and step: 4 bytes of codes, one scale, 16 (32) bytes of values; kWarps warps share a row.
-// Bound by the latency of its loads and by HBM (figures at the head).
+// A code times its scale is exact (NVFP4: 6 significant bits, MXFP4: 2, from 2^-128 on); times the row's factor g it is
+// rounded once. Where s g is exact too the code is multiplied by that: in NVFP4 for a power of two up to 2^119, as
+// quantize_fp4 has them (NVFP4 to bf16, 8192 x 8192 28.4 us, 2048 x 16384 11.8; other factors 28.3 and 12.8), in
+// MXFP4 where there are no factors (26.9 and 11.3; with factors 30.3 and 15.0). With others MXFP4's scales from 2^126 on, which could leave the range before the
+// factor has had its part, go in 2^8 lower, and the product up again (it is a normal number, 2^-32 at least). Bound by
+// the latency of its loads and by HBM (figures at the head).
 template <int kType, int kFormat, int kWarps>
 __global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const ValuesArgs a) {
     constexpr int kRowsPer = kThreads / (32 * kWarps), kStep = 32 * kWarps, kAhead = 4;
@@ -563,42 +583,62 @@ __global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const ValuesAr
     const int pieces = a.K >> 3;
     const uint32_t* const codes = reinterpret_cast<const uint32_t*>(a.codes) + row * pieces;
     const float g = a.row_scale ? a.row_scale[row] : 1.0f;
-    for (int p0 = threadIdx.x % kStep; p0 < pieces; p0 += kAhead * kStep) {
-        uint32_t c[kAhead], s[kAhead];
+    const uint32_t bits = __float_as_uint(g) & 0x7fffffffu;
+    const bool exact = kFormat == kNvfp4 ? (bits & 0x7fffffu) == 0 && bits <= (119u + 127u) << 23 : !a.row_scale;
+    auto values = [&](auto form) {
+        constexpr bool whole = decltype(form)::value;
+        for (int p0 = threadIdx.x % kStep; p0 < pieces; p0 += kAhead * kStep) {
+            uint32_t c[kAhead], s[kAhead];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const int p = p0 + i * kStep;
-            c[i] = s[i] = 0u;
-            if (p < pieces) {
-                c[i] = codes[p];
-                const int block = p / kBlockLanes<kFormat>;
-                s[i] = scales[(int64_t)(block >> 2) * 512 + (block & 3)];
+            for (int i = 0; i < kAhead; ++i) {
+                const int p = p0 + i * kStep;
+                c[i] = s[i] = 0u;
+                if (p < pieces) {
+                    c[i] = codes[p];
+                    const int block = p / kBlockLanes<kFormat>;
+                    s[i] = scales[(int64_t)(block >> 2) * 512 + (block & 3)];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int p = p0 + i * kStep;
+                if (p >= pieces) break;
+                float f, back = 1.0f;
+                if constexpr (kFormat == kNvfp4) {
+                    f = of_ue4m3(s[i]);
+                    if constexpr (whole) f *= g;
+                } else {
+                    f = s[i] == 0xffu ? __int_as_float(0x7fffffff) : s[i] == 0 ? __uint_as_float(0x00400000u) : pow2((int)s[i] - 127);
+                    if (!whole && s[i] >= 253u) {
+                        f *= 0x1p-8f;
+                        back = 0x1p8f;
+                    }
+                }
+                float v[8];
+                of_e2m1x8(c[i], v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    v[j] *= f;
+                    if constexpr (!whole) {
+                        v[j] = times_factor<kType>(v[j], g);
+                        if constexpr (kFormat == kMxfp4) v[j] *= back;
+                    }
+                }
+                const int64_t it = row * pieces + p;
+                if constexpr (kType == 2) {
+                    float4* const o = static_cast<float4*>(a.out) + 2 * it;
+                    o[0] = make_float4(v[0], v[1], v[2], v[3]);
+                    o[1] = make_float4(v[4], v[5], v[6], v[7]);
+                } else {
+                    static_cast<uint4*>(a.out)[it] = ffn::pack8<kType == 0>(v);
+                }
             }
         }
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const int p = p0 + i * kStep;
-            if (p >= pieces) break;
-            float f;
-            if constexpr (kFormat == kNvfp4)
-                f = of_ue4m3(s[i]);
-            else
-                f = s[i] == 0xffu ? __int_as_float(0x7fffffff) : s[i] == 0 ? __uint_as_float(0x00400000u) : pow2((int)s[i] - 127);
-            f *= g;
-            float v[8];
-            of_e2m1x8(c[i], v);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] *= f;
-            const int64_t it = row * pieces + p;
-            if constexpr (kType == 2) {
-                float4* const o = static_cast<float4*>(a.out) + 2 * it;
-                o[0] = make_float4(v[0], v[1], v[2], v[3]);
-                o[1] = make_float4(v[4], v[5], v[6], v[7]);
-            } else {
-                static_cast<uint4*>(a.out)[it] = ffn::pack8<kType == 0>(v);
-            }
-        }
-    }
+    };
+    if (exact)
+        values(std::true_type());
+    else
+        values(std::false_type());
 }
 
 // A set's word of every place of every group from row-major scales; places without a row: 0.

@@ -125,3 +125,18 @@ def product(kind, a, b, bias, residual, act):
         ey = ey + 2.0 ** -23 * y.abs()
     u = R.U[kind]
     return y, ey * (1 + u) + u * y.abs() + R.TINY[kind]
+
+
+# Significand bits and lowest exponent of a normal number.
+FLOAT = {torch.float32: (24, -126), torch.bfloat16: (8, -126), torch.float16: (11, -14)}
+
+
+def nearest_float(v, dtype):
+    """The number of a float type nearest to a 64-bit one, a tie to even, in one rounding (a conversion by torch
+    goes through fp32)."""
+    bits, low = FLOAT[dtype]
+    v = v.cpu()
+    e = torch.where(v != 0, torch.frexp(v)[1] - 1, low).clamp(min=low, max=127)
+    step = pow2(e - bits + 1)  # (a normal number of 64 bits, so that dividing by it is exact)
+    r = torch.round(v / step) * step
+    return torch.where(r.abs() > torch.finfo(dtype).max, torch.copysign(torch.tensor(float("inf")).double(), v), r)
