@@ -68,12 +68,17 @@ int fp4_quantize(int dtype, const void* x, int64_t ld, const fp4_matrix* out, dt
     const int64_t total = out->matrices * out->rows;
     const bool nv = out->format == FP4_NVFP4;
     if ((rc = check_rows("x", x, total, out->K, &ld)) || (rc = check_buffers(out, l, true, nv, -1, "out"))) return rc;
-    if (l.code_bytes == 0) return GEMM_OK;
     int dev;
     DeviceInfo* info;
-    if ((rc = current_device(&dev, &info)) || (rc = check_device_ptr(x, dev, "x")) ||
-        (rc = check_buffers(out, l, true, nv, dev, "out")))
+    if (l.code_bytes == 0) {  // (rows of no elements have factors all the same, where there is room for them)
+        if (total == 0 || !nv || !out->row_scale) return GEMM_OK;
+        if (!aligned(out->row_scale, 4))
+            return fail(GEMM_ERR_INVALID_ARG, "the row factors of out are not 4-byte aligned");
+        if ((rc = current_device(&dev, &info)) || (rc = check_device_ptr(out->row_scale, dev, "out"))) return rc;
+    } else if ((rc = current_device(&dev, &info)) || (rc = check_device_ptr(x, dev, "x")) ||
+               (rc = check_buffers(out, l, true, nv, dev, "out"))) {
         return rc;
+    }
     dtc::fp4::QuantizeArgs a = {};
     a.x = static_cast<const uint16_t*>(x);
     a.ld = ld;
@@ -400,7 +405,7 @@ int gemm_fp4(int dtype, const fp4_matrix* A, const fp4_matrix* B, void* C, const
     c.mx = A->format == FP4_MXFP4;
     c.args.sets = (int)la.sets;
     c.args.p_groups = (int)lb.groups;
-    if (K > 0) {  // (without elements there are no factors to apply, nor have they been written)
+    if (K > 0) {  // (without elements there are no factors to apply)
         c.args.p_scale = B->row_scale;
         c.args.q_scale = A->row_scale;
     }

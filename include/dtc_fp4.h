@@ -60,13 +60,13 @@ int fp4_layout(const fp4_matrix* q, fp4_info* info);
  * Quantises x [matrices * rows, K] (dtype 0 or 1, rows ld elements apart, 0 = dense; 16-byte aligned,
  * ld % 8 == 0) into *out. Every step is exact or rounds as said here; ties go to even (a code of zero may
  * carry either sign):
- *   NVFP4  g = 2^e, e the lowest with max|row| <= 6 * 448 * g, at least -100 (a row of zeros: 0);
+ *   NVFP4  g = 2^e, e the lowest with max|row| <= 6 * 448 * g, at least -100 (a row of zeros or of no elements: 0);
  *          s = max|block| / (6 g) rounded to UE4M3; code = x / (s g) rounded to e2m1 (0 where s is 0)
  *   MXFP4  s = 2^(floor(log2 max|block|) - 2), at least 2^-126 (a block of zeros: 1); code = x / s rounded
  *          to e2m1, 6 where it is above
  * A block that holds an infinity or NaN gets the NaN scale (UE4M3 0x7F, E8M0 0xFF), so its values are NaN;
- * the other blocks are quantised as if it were zero. out->row_scale is required for NVFP4 and not written
- * for MXFP4. The pages have no counterpart.
+ * the other blocks are quantised as if it were zero. out->row_scale is required for NVFP4 (with K == 0 it may be
+ * NULL) and not written for MXFP4. The pages have no counterpart.
  */
 int fp4_quantize(int dtype, const void* x, int64_t ld, const fp4_matrix* out, dtc_stream_t stream);
 
