@@ -53,7 +53,8 @@ typedef struct {
 
 /* Sizes of the buffers of a stack (its pointers are not read). No CUDA call. INVALID_ARG for an unknown
  * format, sizes below 0, K not a multiple of 32, K above 2^24, gated with rows % 16 != 0, matrices * rows
- * or the scales' chunks above 2^31 - 1 - 256, or NULL pointers. The pages have no counterpart. */
+ * or four times the scales' chunks (they are read as rows of 128 bytes) above 2^31 - 1 - 256, or NULL
+ * pointers. The pages have no counterpart. */
 int fp4_layout(const fp4_matrix* q, fp4_info* info);
 
 /*
