@@ -146,7 +146,8 @@ def pack_fp4(codes, scales, row_scale=None, format="nvfp4", gated=False, stream=
 
 
 def gemm_fp4_workspace_size(M, N, K, activation="none"):
-    """Bytes of workspace with which gemm_fp4 would split K over more SMs; 0 when it would not."""
+    """Bytes of workspace with which gemm_fp4 would split K over more SMs; 0 when it would not. A bound over both
+    formats: NVFP4 products of up to 16 rows may take none of it."""
     out = _u64(0)
     _check(_L().gemm_fp4_workspace_size(M, N, K, _code(_ACT, activation, "activation"), ctypes.byref(out)))
     return out.value

@@ -109,7 +109,9 @@ typedef struct {
 int gemm_fp4(int dtype, const fp4_matrix* A, const fp4_matrix* B, void* C, const gemm_fp4_options* opts,
              dtc_stream_t stream);
 
-/* Bytes of workspace with which gemm_fp4 would split K (0: it would not). The pages have no counterpart. */
+/* Bytes of workspace with which gemm_fp4, choosing tiles and splits itself, can split K as it would (0: it
+ * would not). A bound over both formats, with a residual and without: NVFP4 products of up to 16 rows may run
+ * on a kernel that takes no workspace and leaves it alone. The pages have no counterpart. */
 int gemm_fp4_workspace_size(int64_t M, int64_t N, int64_t K, int activation, uint64_t* bytes);
 
 /*
