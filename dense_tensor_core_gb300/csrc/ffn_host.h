@@ -136,9 +136,9 @@ inline int num_feature_tiles(int64_t feats, bool gated) { return ceil_div(feats,
 constexpr uint64_t kTileCounterBytes = 2 * dtc::ffn::kEpWarps * 4;
 inline uint64_t counters_of(int64_t tiles) { return up256((uint64_t)tiles * kTileCounterBytes); }
 // Head of a caller's workspace that holds the words which are zero between calls: the same bytes for
-// gemm_act and gemm_act_backward, whatever the sizes, row pitches and alignment of a call are, so that
-// one workspace serves calls of both (what one call leaves in the rest must not reach where another
-// counts). First the counters of split tiles (plans split fewer than 2 * pairs of them) and of the
+// gemm_act, gemm_act_backward and gemm_fp4, whatever the sizes, row pitches and alignment of a call are,
+// so that one workspace serves calls of all three (what one call leaves in the rest must not reach where
+// another counts). First the counters of split tiles (plans split fewer than 2 * pairs of them) and of the
 // column sums' strips, then the stream-K flags of the gradient's products.
 inline uint64_t flags_offset(int pairs) { return std::max<uint64_t>(counters_of(2 * pairs), kActBackwardStrips * 4); }
 inline uint64_t zero_words_bytes(int pairs) { return flags_offset(pairs) + kSkFlagBytes; }

@@ -562,12 +562,12 @@ __device__ __forceinline__ float times_factor(float v, float g) {
 }
 
 // 8 elements a lane and step: 4 bytes of codes, one scale, 16 (32) bytes of values; kWarps warps share a row.
-// A code times its scale is exact (NVFP4: 6 significant bits, MXFP4: 2, from 2^-128 on); times the row's factor g it is
-// rounded once. Where s g is exact too the code is multiplied by that: in NVFP4 for a power of two up to 2^119, as
-// quantize_fp4 has them (NVFP4 to bf16, 8192 x 8192 28.4 us, 2048 x 16384 11.8; other factors 28.3 and 12.8), in
-// MXFP4 where there are no factors (26.9 and 11.3; with factors 30.3 and 15.0). With others MXFP4's scales from 2^126 on, which could leave the range before the
-// factor has had its part, go in 2^8 lower, and the product up again (it is a normal number, 2^-32 at least). Bound by
-// the latency of its loads and by HBM (figures at the head).
+// A code times its scale s is exact (NVFP4: 6 significant bits, MXFP4: 2, from 2^-128 on); times the row's factor g it
+// is rounded once. Where s g is exact too the code is multiplied by that: in NVFP4 for a power of two up to 2^119, as
+// quantize_fp4 has them (to bf16, 8192 x 8192 28.4 us, 2048 x 16384 11.8; other factors 28.3 and 12.8), in MXFP4
+// without factors (26.9 and 11.3; with factors 30.3 and 15.0). With factors MXFP4's scales from 2^126 on, which could
+// leave the range before the factor has had its part, go in 2^8 lower, and the product up again (it is a normal number,
+// 2^-32 at least). Bound by the latency of its loads and by HBM (figures at the head).
 template <int kType, int kFormat, int kWarps>
 __global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const ValuesArgs a) {
     constexpr int kRowsPer = kThreads / (32 * kWarps), kStep = 32 * kWarps, kAhead = 4;

@@ -176,10 +176,12 @@ void size_split(Fp4Plan* p, uint64_t counters) {
     p->bytes = counters + (uint64_t)p->split_tiles * p->splits * p->tile_n * 1024;
 }
 
-// Modelled time of a launch in us, less what every launch costs, after measured times (4096 x 4096 x 2048: 22, 20
-// and 23 in tiles of 128, 192 and 256 rows; x 8192: 66, 57 and 51): a stage of 256 elements takes the issuing
+// Modelled time of a launch in us, less what every launch costs, after NVFP4's measured times (4096 x 4096 x 2048: 22,
+// 19 and 22 in tiles of 128, 192 and 256 rows; x 8192: 65, 56 and 49): a stage of 256 elements takes the issuing
 // thread's 0.25 us, above 128 rows the tensor pipe's; a tile whose accumulator touches its predecessor's waits until
-// the columns of both are read, `epilogue` us more with what its epilogue does.
+// the columns of both are read, `epilogue` us more with what its epilogue does. It knows neither the format nor
+// sf_stages, and prices pieces of a last wave too low: 4096 x 4096 x 8192 with 28 tiles cut in two should gain 1.4 and
+// takes what it takes without (MXFP4 46.9 and 46.2, NVFP4 49.1 and 48.8).
 double item_cost(const Fp4Plan& p, int kb, int pairs, double epilogue) {
     const double block = 0.25 + 0.0006 * std::max(0, std::min(p.tile_n, 192) - 128);
     const int64_t split_items = (int64_t)p.split_tiles * p.splits;
@@ -194,9 +196,10 @@ double item_cost(const Fp4Plan& p, int kb, int pairs, double epilogue) {
 }
 
 // What activation and residual add to a tile of 256 rows over one of 192, whose epilogue runs under the next tile's
-// products from its start. Measured in tiles of 192 and 256, us, at 4096 x 4096 x 8192 and 4096 x 14336 x 4096:
-//   neither  58, 51 and 96, 87     gelu_tanh 63, 57 and 115, 107   gelu 65, 61   swiglu 59, 51   geglu 60, 53
-//   residual 60, 59 and 100, 99    both      63, 64 and 108, 107        64, 67          60, 55         61, 57
+// products from its start. Measured in tiles of 192 and 256, us, NVFP4 at 4096 x 4096 x 8192 and 4096 x 14336 x 4096:
+//             neither             silu                gelu_tanh           gelu                swiglu              geglu
+//   alone     57, 49; 95, 87      61, 54; 107, 101    62, 55; 114, 104    64, 59; 116, 113    57, 50; 101, 92     59, 52; 103, 97
+//   residual  59, 56; 103, 102                        62, 60; 115, 119    63, 64; 118, 121    59, 52; 105, 101    60, 55; 107, 105
 double epilogue_cost(int act, bool residual) {
     double us = residual ? (dtc::act_gated(act) ? 0.4 : 1.0) : 0.0;
     if (act == GEMM_ACT_GELU) us += 1.9;
@@ -248,8 +251,10 @@ Fp4Plan plan_rows(int64_t rows, int64_t feats, int act, bool residual, int64_t K
             for (int s = 2; s <= std::min<int64_t>(most, pairs / tail); ++s) consider(s, tail);
     }
     best.grid = 2 * (int)std::min<int64_t>(best.items(), pairs);
-    // (with a residual the epilogue of a short K is the longer part: 4096 x 14336 x 4096 with gelu_tanh and one 107 us
-    // beside two stages, 115 beside three; gated 98 and 99)
+    // (with a residual the epilogue of a short K is the longer part. Beside two stages and three, us, NVFP4 with gelu_tanh
+    // and one: 4096 x 14336 x 4096 106 and 112, 2048 x 16384 x 4096 65.6 and 66.9, 8192 x 8192 x 2048 95 and 99, 4096 x
+    // 4096 x 4096 40.2 and 41.1; one alone 100 and 101, 60.1 and 61.1, 84 and 88, but 36.4 and 35.7. Longer K than 4096
+    // has been measured at 8192 only: two stages cost there.)
     if (best.tile_n > dtc::gf4::kNarrow)
         best.sf_stages = !dtc::gf4::tiles_touch(best.tile_n) || (K <= 4096 && epilogue >= 1.0) ? 2 : 3;
     return best;

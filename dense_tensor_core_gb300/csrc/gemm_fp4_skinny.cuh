@@ -1,7 +1,7 @@
 // gemm_fp4_skinny.cuh -- the NVFP4 product of one matrix for a handful of rows: the product and epilogue of
 // gemm_fp4.cuh without tiles, as gemm16_skinny.cuh is to gemm16_ffn.cuh. (Over experts' rows the tiles are
-// faster from one token on: 33 us against 35 for a token's pass through 8 of 64 experts, H 2048, F 1024, and 69
-// against 102 for 16 tokens.)
+// faster from one token on: with the rest of the pass as it was then, 33 us against 35 for a token through 8 of 64
+// experts, H 2048, F 1024, and 69 against 102 for 16 tokens; on tiles the one token takes 28 to 31 since.)
 //
 // With so few rows the product is the reading of P, once; everything else is latency around it. A block takes
 // 16 features (gated: 8 gate rows and their 8 up rows) over the whole K; its 8 warps take 128-element chunks in

@@ -119,7 +119,9 @@ int gemm_fp4_workspace_size(int64_t M, int64_t N, int64_t K, int activation, uin
  *   y[t] = residual[t] + sum_j weights[t,j] * w_out[e] . q(h_j),  h_j = act(w_in[e] . q(x[t]))
  * q(v): v as fp4_quantize makes it, in the weights' format; h is rounded to dtype first. w_in: a stack of E
  * matrices [F, H], gated [2F, H] and gated; w_out: E of [H, F]; H and F multiples of 32. The rest as
- * moe_experts; the weight multiplies the second product's sum. `buffer`: moe_experts_fp4_buffer_size bytes.
+ * moe_experts; the weight multiplies the second product's sum, in NVFP4 as one fp32 number with the factor of
+ * h's row (it leaves the range where max|h| times the weight passes about 2^139). `buffer`:
+ * moe_experts_fp4_buffer_size bytes.
  * The pages have no counterpart.
  */
 int moe_experts_fp4(int dtype, const void* x, const fp4_matrix* w_in, const fp4_matrix* w_out,
